@@ -68,6 +68,7 @@ extern "C" {
 #define RWKV7_ERR_ALGO (-7)      /* unknown algorithm, or one that does not support the arguments */
 #define RWKV7_ERR_HIP (-8)       /* a HIP runtime call or kernel launch failed */
 #define RWKV7_ERR_SCRATCH (-9)   /* rwkv7_wkv_prefill_noalloc: the call does not fit its static scratch array */
+#define RWKV7_ERR_DECAY (-10)    /* linear attention: decay not one of RWKV7_DECAY_* */
 
 /* Input dtype of r, w, k, v, a, b. y is always float32; so is the state except in rwkv7_wkv_step_q. */
 #define RWKV7_DTYPE_F32 0
@@ -425,6 +426,61 @@ int rwkv7_wkv_prefill_noalloc(const void *r, const void *w, const void *k, const
  * queried).
  */
 int rwkv7_wkv_prefill_algo(int64_t B, int64_t T, int64_t H, int64_t N, int dtype);
+
+/*
+ * Linear attention with one decay for each head: the recurrence without the
+ * removal key, as in the models whose heads decay by a scalar. Per batch b and
+ * head h, with the float32 state S (row i = value index, column j = key index)
+ * and w_t = exp(log_w_t):
+ *
+ *     S_t = w_t S_{t-1} + v_t k_t^T
+ *     y_t = S_t r_t                      (read out after the update)
+ *
+ * rwkv7_linattn_prefill takes a prompt in chunks on the matrix cores,
+ * rwkv7_linattn_step one token, rwkv7_linattn_backward the gradients.
+ *
+ *   r, k, v    inputs [B,T,H,N] in `dtype` (RWKV7_DTYPE_F32 or _BF16)
+ *   log_w      float32 natural logs of the decays, at most 0; -infinity is a
+ *              decay of 0 (the state is reset before this token, e.g. where packed
+ *              sequences meet). `decay` gives its layout: RWKV7_DECAY_HEAD [H],
+ *              one decay for all tokens of a head; RWKV7_DECAY_TOKEN [B,T,H]
+ *   state_in   [B,H,N,N] float32 initial state, or NULL for zeros
+ *   lens       [B] int32 lengths of the sequences in device memory, or NULL (all
+ *              have T tokens); values outside [0, T] count as the nearer end. The
+ *              tokens of sequence b from lens[b] on are left out whatever they
+ *              hold: y there is 0 and the state is that after token lens[b] - 1
+ *   y          [B,T,H,N] output in `dtype`
+ *   state_out  [B,H,N,N] float32 final state, or NULL; may equal state_in
+ *   B, T, H    batch, tokens, heads (>= 0); B*H at most 2^23, H at most 2^18
+ *   N          head size; must be 64
+ *
+ * The state and every sum are float32 (sums of log_w float64). bfloat16 inputs
+ * are exact matrix-core operands; scaled intermediates and float32 inputs enter
+ * as sums of two or three bfloat16 pieces, so a float32 output (the state, every
+ * output of a float32 call) is off by about float32 rounding, and a bfloat16 one
+ * by its one rounding. Inputs have to be finite in the tokens that count (a
+ * float32 infinity becomes a NaN). No result depends on the launch or on other
+ * work on the device: the same call gives the same bits.
+ *
+ * Ownership, alignment (every pointer 16 bytes), aliasing, empty work, streams
+ * and error codes are as for rwkv7_wkv_prefill; a `decay` not one of
+ * RWKV7_DECAY_* is RWKV7_ERR_DECAY.
+ */
+#define RWKV7_DECAY_HEAD 0  /* log_w [H] */
+#define RWKV7_DECAY_TOKEN 1 /* log_w [B, T, H] */
+
+int rwkv7_linattn_prefill(const void *r, const float *log_w, const void *k, const void *v, const float *state_in,
+                          const int32_t *lens, void *y, float *state_out, int64_t B, int64_t T, int64_t H, int64_t N,
+                          int dtype, int decay, void *stream);
+
+/*
+ * Single-token step of the linear attention (T == 1, else RWKV7_ERR_SHAPE):
+ * reads the state, writes y and the new state (state_out may be state_in).
+ * float32 arithmetic; log_w is [H] or [B,1,H].
+ */
+int rwkv7_linattn_step(const void *r, const float *log_w, const void *k, const void *v, const float *state_in, void *y,
+                       float *state_out, int64_t B, int64_t T, int64_t H, int64_t N, int dtype, int decay,
+                       void *stream);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *rwkv7_wkv_strerror(int status);

@@ -5,6 +5,7 @@
 
 #include <atomic>
 
+#include "api_checks.hpp"
 #include "rwkv7_wkv.h"
 #include "wkv7_internal.hpp"
 
@@ -37,17 +38,9 @@ namespace {
 
 using rwkv7::WkvCall;
 
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-  bool empty() const { return hi <= lo; }
-};
-
-bool overlap(Range x, Range y) { return !x.empty() && !y.empty() && x.lo < y.hi && y.lo < x.hi; }
-
-Range range_of(const void* p, int64_t bytes) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Range{lo, p ? lo + (uintptr_t)bytes : lo};
-}
+using rwkv7::overlap;
+using rwkv7::Range;
+using rwkv7::range_of;
 
 int validate(const void* const in[6], const void* s_in, const float* y, const void* s_out, int64_t B,
              int64_t T, int64_t H, int64_t N, int dtype, int sdtype) {
@@ -408,6 +401,7 @@ const char* rwkv7_wkv_strerror(int status) {
     case RWKV7_ERR_ALGO: return "unknown or unsupported algorithm for these arguments";
     case RWKV7_ERR_HIP: return "HIP runtime error";
     case RWKV7_ERR_SCRATCH: return "the call needs more than the static scratch array of rwkv7_wkv_prefill_noalloc";
+    case RWKV7_ERR_DECAY: return "unknown kind of decay (one per head or one per token and head)";
     default: return "unknown status";
   }
 }

@@ -30,12 +30,16 @@ RWKV7_ALGO_SEQUENTIAL = 1
 RWKV7_ALGO_CHUNKED = 2
 RWKV7_ALGO_CHUNKED_SPLIT = 3
 RWKV7_ERR_SCRATCH = -9
+RWKV7_ERR_DECAY = -10
+RWKV7_DECAY_HEAD = 0
+RWKV7_DECAY_TOKEN = 1
 RWKV7_NOALLOC_SCRATCH_BYTES = 64 << 20
 
 EXPORTED = ("rwkv7_wkv_prefill", "rwkv7_wkv_step", "rwkv7_wkv_step_q", "rwkv7_wkv_prefill_ex",
             "rwkv7_tmix_prefill", "rwkv7_tmix_prefill_ex", "rwkv7_tmix_step", "rwkv7_wkv_backward",
             "rwkv7_wkv_backward_ex",
             "rwkv7_stack_forward", "rwkv7_wkv_prefill_algo", "rwkv7_wkv_prefill_noalloc",
+            "rwkv7_linattn_prefill", "rwkv7_linattn_step",
             "rwkv7_wkv_strerror")
 
 _lib = None
@@ -78,6 +82,10 @@ def lib() -> ctypes.CDLL:
             L.rwkv7_wkv_backward_ex.argtypes = [vp] * 16 + [i64] * 4 + [ci, ci, vp]
             L.rwkv7_stack_forward.restype = ci
             L.rwkv7_stack_forward.argtypes = [vp] * 5 + [i64] * 5 + [ci, vp]
+            L.rwkv7_linattn_prefill.restype = ci
+            L.rwkv7_linattn_prefill.argtypes = [vp] * 8 + [i64] * 4 + [ci, ci, vp]
+            L.rwkv7_linattn_step.restype = ci
+            L.rwkv7_linattn_step.argtypes = [vp] * 7 + [i64] * 4 + [ci, ci, vp]
             L.rwkv7_wkv_prefill_algo.restype = ci
             L.rwkv7_wkv_prefill_algo.argtypes = [i64] * 4 + [ci]
             L.rwkv7_wkv_strerror.restype = ctypes.c_char_p
@@ -355,3 +363,83 @@ def rwkv7_stack_forward(w_in, w_out, vecs, x, states, stream=None):
     _on_gpu(states, stream)
     args = [_ptr(w_in), _ptr(w_out), _ptr(vecs), _ptr(x), _ptr(states), L, B, T, H, N, _dtype_code(w_in)]
     _check(lib().rwkv7_stack_forward(*args, _stream(stream)))
+
+
+# ---- linear attention with a decay for each head
+
+def _launch(fn, args, like, stream):
+    """Call the library with `like`'s device current (a stream given by the caller may be another device's)."""
+    import torch
+    if like.device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(like.device):
+            _check(fn(*args, _stream(stream)))
+
+
+def _decay_code(log_w, B, T, H) -> int:
+    """Which of the two layouts log_w has."""
+    import torch
+    if not isinstance(log_w, torch.Tensor):
+        raise TypeError("log_w must be a torch.Tensor, not %s" % type(log_w).__name__)
+    if log_w.dim() not in (1, 3):
+        raise ValueError("log_w has shape %s, expected (%d,) or (%d, %d, %d)" % (tuple(log_w.shape), H, B, T, H))
+    return RWKV7_DECAY_HEAD if log_w.dim() == 1 else RWKV7_DECAY_TOKEN
+
+
+def _linattn_inputs(r, log_w, k, v, state_in, lens):
+    """Checks the inputs that the linear attention's calls share; returns (B, T, H, N, decay)."""
+    import torch
+    if not isinstance(r, torch.Tensor) or r.dim() != 4:
+        raise ValueError("r must be a [B, T, H, N] tensor")
+    B, T, H, N = r.shape
+    _expect(r, "r", r.shape, _input_dtypes(), r)
+    decay = _decay_code(log_w, B, T, H)
+    _expect(log_w, "log_w", (H,) if decay == RWKV7_DECAY_HEAD else (B, T, H), _f32(), r)
+    for name, t in (("k", k), ("v", v)):
+        _expect(t, name, r.shape, (r.dtype,), r)
+    _expect(state_in, "state_in", (B, H, N, N), _f32(), r, optional=True)
+    _expect(lens, "lens", (B,), (torch.int32,), r, optional=True)
+    return B, T, H, N, decay
+
+
+def rwkv7_linattn_prefill(r, log_w, k, v, state_in, lens, y, state_out, stream=None):
+    """Linear attention over a prompt. r, k, v, y [B,T,H,64] in one dtype; log_w float32 [H] or [B,T,H];
+    lens int32 [B] or None; states float32 [B,H,64,64] or None."""
+    B, T, H, N, decay = _linattn_inputs(r, log_w, k, v, state_in, lens)
+    _expect(y, "y", (B, T, H, N), (r.dtype,), r)
+    _expect(state_out, "state_out", (B, H, N, N), _f32(), r, optional=True)
+    _on_gpu(r, stream)
+    args = [_ptr(x) for x in (r, log_w, k, v, state_in, lens, y, state_out)] + [B, T, H, N, _dtype_code(r), decay]
+    _launch(lib().rwkv7_linattn_prefill, args, r, stream)
+
+
+def rwkv7_linattn_step(r, log_w, k, v, state_in, y, state_out, stream=None):
+    """Single-token step (T == 1) of the linear attention; state_out may be state_in."""
+    B, T, H, N, decay = _linattn_inputs(r, log_w, k, v, state_in, None)
+    _expect(y, "y", (B, T, H, N), (r.dtype,), r)
+    _expect(state_out, "state_out", (B, H, N, N), _f32(), r, optional=True)
+    _on_gpu(r, stream)
+    args = [_ptr(x) for x in (r, log_w, k, v, state_in, y, state_out)] + [B, T, H, N, _dtype_code(r), decay]
+    _launch(lib().rwkv7_linattn_step, args, r, stream)
+
+
+def linattn(r, log_w, k, v, state_in=None, lens=None, want_state=True, stream=None):
+    """Allocate y ([B,T,H,64] in r's dtype) and the final state, run the prompt, return (y, state_out)."""
+    import torch
+    B, T, H, N = r.shape
+    y = torch.empty_like(r)
+    s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device) if want_state else None
+    rwkv7_linattn_prefill(r, log_w, k, v, state_in, lens, y, s_out, stream=stream)
+    return y, s_out
+
+
+def linattn_step(r, log_w, k, v, state_in=None, stream=None):
+    """Allocate y ([B,1,H,64] in r's dtype) and the new state, run one token, return (y, state_out).
+    rwkv7_linattn_step updates a state in place."""
+    import torch
+    B, T, H, N = r.shape
+    y = torch.empty_like(r)
+    s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
+    rwkv7_linattn_step(r, log_w, k, v, state_in, y, s_out, stream=stream)
+    return y, s_out
