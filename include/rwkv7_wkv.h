@@ -482,6 +482,52 @@ int rwkv7_linattn_step(const void *r, const float *log_w, const void *k, const v
                        float *state_out, int64_t B, int64_t T, int64_t H, int64_t N, int dtype, int decay,
                        void *stream);
 
+/*
+ * Layer norm over groups of channels. Every row of x [M, D] has G groups of
+ * n = D / G consecutive channels; over each of them, with xh = (x - mean) * rstd,
+ *
+ *     mean = sum(x) / n,  rstd = 1 / sqrt(sum((x - mean)^2) / n + eps)
+ *     y    = xh * weight + bias                  (weight and bias per channel, [D])
+ *
+ * G = 1 is the layer norm of a residual stream, G = H with n = 64 the GroupNorm
+ * ln_x behind the recurrence (eps 64e-5, RWKV-7 G0 7.2B notes, section 7.1), here
+ * with its gradient.
+ *
+ *   x       [M, D] in x_dtype (RWKV7_DTYPE_F32 or _BF16)
+ *   weight  [D] float32, or NULL for 1;  bias  [D] float32, or NULL for 0
+ *   y       [M, D] in y_dtype, which may differ from x_dtype (a float32 residual
+ *           stream normalised into bfloat16 for a projection)
+ *   mean, rstd  [M, G] float32 outputs for the backward, each may be NULL
+ *   M, D, G rows, channels (at most 2^24), groups (at least 1, a divisor of D);
+ *           else RWKV7_ERR_SHAPE, as is an eps that is negative, infinite or NaN
+ *
+ * The statistics are float32 from two passes over registers. Contiguous row-major
+ * layouts, 16-byte aligned pointers, outputs that overlap nothing, streams and
+ * error codes as for rwkv7_wkv_prefill; no rows or no channels do nothing.
+ */
+int rwkv7_layernorm_forward(const void *x, const float *weight, const float *bias, void *y, float *mean, float *rstd,
+                            int64_t M, int64_t D, int64_t G, float eps, int x_dtype, int y_dtype, void *stream);
+
+/*
+ * Gradients of rwkv7_layernorm_forward from its x, weight, mean and rstd:
+ *
+ *     g  = dy * weight,  dx = rstd * (g - sum(g) / n - xh * sum(g * xh) / n)
+ *     dweight = sum over rows of dy * xh,  dbias = sum over rows of dy
+ *
+ *   dy       [M, D] in y_dtype;  dx  [M, D] output in x_dtype
+ *   dweight, dbias  [D] float32 outputs, each may be NULL (not computed); with
+ *            M == 0 they are zeros
+ *
+ * The sums over rows are float32, in an order that the sizes alone decide (the
+ * same call gives the same bits). With dweight or dbias the partial sums live in
+ * the per-(device, stream) workspace described for rwkv7_wkv_prefill_ex (at most
+ * 64 MiB, or 8 bytes a channel where that is more), and what is said there about
+ * growth and graph capture holds.
+ */
+int rwkv7_layernorm_backward(const void *x, const float *weight, const float *mean, const float *rstd, const void *dy,
+                             void *dx, float *dweight, float *dbias, int64_t M, int64_t D, int64_t G, int x_dtype,
+                             int y_dtype, void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *rwkv7_wkv_strerror(int status);
 

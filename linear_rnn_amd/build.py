@@ -8,10 +8,12 @@ so the kernels' explicit fmaf calls fix the arithmetic order.
 """
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -41,12 +43,19 @@ def flags() -> list:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source under csrc/ into one shared library (always recompiles)."""
+    """Compile every source under csrc/ into one shared library (always recompiles, a source per process)."""
     tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + flags() + ["-shared", "-o", tmp] + sources() + ["-lrocblas"]
-    if verbose:
-        print(" ".join(cmd), flush=True)
-    subprocess.run(cmd, check=True)
+
+    def run(cmd):
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(src) + ".o") for src in sources()]
+        with concurrent.futures.ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            list(pool.map(lambda so: run([hipcc()] + flags() + ["-c", so[0], "-o", so[1]]), zip(sources(), objs)))
+        run([hipcc(), "--offload-arch=" + ARCH, "-fPIC", "-shared", "-o", tmp] + objs + ["-lrocblas"])
     os.replace(tmp, LIB)
     return LIB
 

@@ -127,9 +127,11 @@ hipError_t launch_stack(const StackCall& c);
 // demand (at least doubling); a replaced buffer stays allocated until the process
 // ends, since a HIP graph captured earlier may still use it. Growing while the
 // stream is being captured returns hipErrorStreamCaptureUnsupported.
-// Two independent buffers per (device, stream): the chunked kernels' records use
+// Independent buffers per (device, stream): the chunked kernels' records use
 // their own, so a caller holding the general one (the layer stack) can run them.
 constexpr int kWorkspaceGeneral = 0, kWorkspaceChunks = 1;
+// The linear attention's states and the layer norm's partial sums (neither calls the other).
+constexpr int kWorkspaceOperators = 2;
 hipError_t device_workspace(hipStream_t stream, size_t bytes, void** out, int slot = kWorkspaceGeneral);
 
 // state_out <- state_in (zeros when state_in is null) for B*H heads.

@@ -40,6 +40,7 @@ EXPORTED = ("rwkv7_wkv_prefill", "rwkv7_wkv_step", "rwkv7_wkv_step_q", "rwkv7_wk
             "rwkv7_wkv_backward_ex",
             "rwkv7_stack_forward", "rwkv7_wkv_prefill_algo", "rwkv7_wkv_prefill_noalloc",
             "rwkv7_linattn_prefill", "rwkv7_linattn_step",
+            "rwkv7_layernorm_forward", "rwkv7_layernorm_backward",
             "rwkv7_wkv_strerror")
 
 _lib = None
@@ -86,6 +87,11 @@ def lib() -> ctypes.CDLL:
             L.rwkv7_linattn_prefill.argtypes = [vp] * 8 + [i64] * 4 + [ci, ci, vp]
             L.rwkv7_linattn_step.restype = ci
             L.rwkv7_linattn_step.argtypes = [vp] * 7 + [i64] * 4 + [ci, ci, vp]
+            cf = ctypes.c_float
+            L.rwkv7_layernorm_forward.restype = ci
+            L.rwkv7_layernorm_forward.argtypes = [vp] * 6 + [i64] * 3 + [cf, ci, ci, vp]
+            L.rwkv7_layernorm_backward.restype = ci
+            L.rwkv7_layernorm_backward.argtypes = [vp] * 8 + [i64] * 3 + [ci, ci, vp]
             L.rwkv7_wkv_prefill_algo.restype = ci
             L.rwkv7_wkv_prefill_algo.argtypes = [i64] * 4 + [ci]
             L.rwkv7_wkv_strerror.restype = ctypes.c_char_p
@@ -443,3 +449,75 @@ def linattn_step(r, log_w, k, v, state_in=None, stream=None):
     s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
     rwkv7_linattn_step(r, log_w, k, v, state_in, y, s_out, stream=stream)
     return y, s_out
+
+
+# ---- layer norm over groups of channels
+
+def _rows(x, groups):
+    """x's rows and channels: the last dimension is normalised, in `groups` groups."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+        raise ValueError("x must be a tensor with the channels in its last dimension")
+    _expect(x, "x", x.shape, _input_dtypes(), x)
+    D, G = x.shape[-1], int(groups)
+    if G < 1 or D % G:
+        raise ValueError("groups is %d, expected a divisor of the %d channels" % (G, D))
+    M = 1
+    for n in x.shape[:-1]:
+        M *= n
+    return M, D, G
+
+
+def rwkv7_layernorm_forward(x, weight, bias, y, mean, rstd, groups=1, eps=1e-5, stream=None):
+    """Layer norm of x's last dimension in `groups` groups. x and y [..., D] in float32 or bfloat16 (each its
+    own), weight and bias [D] float32 or None, mean and rstd [..., groups] float32 or None."""
+    M, D, G = _rows(x, groups)
+    _expect(weight, "weight", (D,), _f32(), x, optional=True)
+    _expect(bias, "bias", (D,), _f32(), x, optional=True)
+    _expect(y, "y", x.shape, _input_dtypes(), x)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _expect(t, name, x.shape[:-1] + (G,), _f32(), x, optional=True)
+    _on_gpu(x, stream)
+    args = [_ptr(t) for t in (x, weight, bias, y, mean, rstd)] + [M, D, G, float(eps), _dtype_code(x), _dtype_code(y)]
+    _launch(lib().rwkv7_layernorm_forward, args, x, stream)
+
+
+def rwkv7_layernorm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, groups=1, stream=None):
+    """Gradients of the layer norm from its x, weight, mean and rstd; dweight and dbias [D] float32 or None."""
+    M, D, G = _rows(x, groups)
+    _expect(weight, "weight", (D,), _f32(), x, optional=True)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        _expect(t, name, x.shape[:-1] + (G,), _f32(), x)
+    _expect(dy, "dy", x.shape, _input_dtypes(), x)
+    _expect(dx, "dx", x.shape, (x.dtype,), x)
+    _expect(dweight, "dweight", (D,), _f32(), x, optional=True)
+    _expect(dbias, "dbias", (D,), _f32(), x, optional=True)
+    _on_gpu(x, stream)
+    args = [_ptr(t) for t in (x, weight, mean, rstd, dy, dx, dweight, dbias)] + \
+        [M, D, G, _dtype_code(x), _dtype_code(dy)]
+    _launch(lib().rwkv7_layernorm_backward, args, x, stream)
+
+
+def layernorm(x, weight=None, bias=None, groups=1, eps=1e-5, out_dtype=None, want_stats=True, stream=None):
+    """Allocate y (in out_dtype, or x's) and the statistics, run the forward, return (y, mean, rstd)."""
+    import torch
+    y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    mean = rstd = None
+    if want_stats:
+        mean = torch.empty(x.shape[:-1] + (groups,), dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    rwkv7_layernorm_forward(x, weight, bias, y, mean, rstd, groups=groups, eps=eps, stream=stream)
+    return y, mean, rstd
+
+
+def layernorm_backward(x, weight, mean, rstd, dy, groups=1, want_dweight=True, stream=None):
+    """Allocate the gradients, run the backward, return dict dx, dweight, dbias (the last two None unless
+    want_dweight)."""
+    import torch
+    out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device), "dweight": None, "dbias": None}
+    if want_dweight:
+        out["dweight"] = torch.empty(x.shape[-1:], dtype=torch.float32, device=x.device)
+        out["dbias"] = torch.empty_like(out["dweight"])
+    rwkv7_layernorm_backward(x, weight, mean, rstd, dy, out["dx"], out["dweight"], out["dbias"], groups=groups,
+                             stream=stream)
+    return out
