@@ -483,6 +483,34 @@ int rwkv7_linattn_step(const void *r, const float *log_w, const void *k, const v
                        void *stream);
 
 /*
+ * Gradients of rwkv7_linattn_prefill. With dy = dL/dy, dstate_out = dL/dS_T and
+ * G = dL/dS_t accumulated from the last token back:
+ *
+ *     G += dy_t r_t^T
+ *     dr_t = S_t^T dy_t,  dk_t = G^T v_t,  dv_t = G k_t
+ *     dlog_w_t = w_t sum_ij S_{t-1}[i,j] G[i,j]
+ *     G <- w_t G                             and finally dstate_in = G
+ *
+ *   r, log_w, k, v, state_in, lens   the forward call's inputs
+ *   dy          [B,T,H,N] in `dtype`
+ *   dstate_out  [B,H,N,N] float32, or NULL (the final state is not used)
+ *   dr, dk, dv  [B,T,H,N] outputs in `dtype`; 0 behind a sequence's length
+ *   dlog_w      float32 output in log_w's layout: [B,T,H], or [H] with the sum
+ *               over all tokens of all sequences; 0 where log_w is -infinity
+ *   dstate_in   [B,H,N,N] float32 output, or NULL; may equal dstate_out
+ *
+ * dr, dk, dv and dlog_w are required. With no tokens (B == 0 or T == 0) dlog_w of
+ * RWKV7_DECAY_HEAD is zeros and dstate_in is dstate_out. The states are formed
+ * again from the inputs: those before each 128 tokens (16 KiB each) live in the
+ * per-(device, stream) workspace described for rwkv7_wkv_prefill_ex, and what is
+ * said there about growth and graph capture holds.
+ */
+int rwkv7_linattn_backward(const void *r, const float *log_w, const void *k, const void *v, const float *state_in,
+                           const int32_t *lens, const void *dy, const float *dstate_out, void *dr, float *dlog_w,
+                           void *dk, void *dv, float *dstate_in, int64_t B, int64_t T, int64_t H, int64_t N,
+                           int dtype, int decay, void *stream);
+
+/*
  * Layer norm over groups of channels. Every row of x [M, D] has G groups of
  * n = D / G consecutive channels; over each of them, with xh = (x - mean) * rstd,
  *

@@ -58,9 +58,37 @@ int run_linattn(const void* r, const float* log_w, const void* k, const void* v,
     if (state_out && state_out != state_in) e = rwkv7::launch_state_copy(state_in, state_out, B * H, s);
     return e == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
   }
-  const LinattnCall c{r, log_w, k, v, state_in, lens, y, state_out, B, T, H, dtype == RWKV7_DTYPE_F32,
-                      decay == RWKV7_DECAY_TOKEN, s};
+  LinattnCall c{};
+  c.r = r, c.log_w = log_w, c.k = k, c.v = v, c.s_in = state_in, c.lens = lens, c.y = y, c.s_out = state_out;
+  c.B = B, c.T = T, c.H = H, c.f32 = dtype == RWKV7_DTYPE_F32, c.per_token = decay == RWKV7_DECAY_TOKEN, c.stream = s;
   e = step ? rwkv7::launch_linattn_step(c) : rwkv7::launch_linattn(c);
+  return e == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
+}
+
+int run_backward(const LinattnCall& c, int64_t N, int dtype, int decay) {
+  Sizes z;
+  const int st = check_sizes(c.B, c.T, c.H, N, dtype, decay, &z);
+  if (st != RWKV7_OK) return st;
+  if (z.tokens > 0 && (!c.r || !c.log_w || !c.k || !c.v || !c.dy || !c.dr || !c.dlog_w || !c.dk || !c.dv))
+    return RWKV7_ERR_NULL;
+  for (const void* q : {c.r, (const void*)c.log_w, c.k, c.v, (const void*)c.s_in, (const void*)c.lens, c.dy,
+                        (const void*)c.ds_out, (const void*)c.dr, (const void*)c.dlog_w, (const void*)c.dk,
+                        (const void*)c.dv, (const void*)c.ds_in})
+    if (rwkv7::misaligned(q)) return RWKV7_ERR_ALIGN;
+  const Range in[8] = {range_of(c.r, z.tokens),   range_of(c.log_w, z.log_w), range_of(c.k, z.tokens),
+                       range_of(c.v, z.tokens),   range_of(c.lens, z.lens),   range_of(c.s_in, z.state),
+                       range_of(c.dy, z.tokens),  range_of(c.ds_out, z.state)};
+  const Range out[5] = {range_of(c.dr, z.tokens), range_of(c.dlog_w, z.log_w), range_of(c.dk, z.tokens),
+                        range_of(c.dv, z.tokens), range_of(c.ds_in, z.state)};
+  if (rwkv7::outputs_overlap(out, 5, in, 8, &in[7])) return RWKV7_ERR_ALIAS;
+  if (c.H == 0) return RWKV7_OK;
+  hipError_t e = hipSuccess;
+  if (c.B == 0 || c.T == 0) {  // no tokens: the state's gradient passes through, a decay's own is 0
+    if (c.B > 0 && c.ds_in && c.ds_in != c.ds_out) e = rwkv7::launch_state_copy(c.ds_out, c.ds_in, c.B * c.H, c.stream);
+    if (e == hipSuccess && !c.per_token && c.dlog_w) e = rwkv7::launch_linattn_zero(c.dlog_w, c.H, c.stream);
+    return e == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
+  }
+  e = rwkv7::launch_linattn_backward(c);
   return e == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
 }
 
@@ -78,6 +106,18 @@ int rwkv7_linattn_step(const void* r, const float* log_w, const void* k, const v
                        float* state_out, int64_t B, int64_t T, int64_t H, int64_t N, int dtype, int decay,
                        void* stream) {
   return run_linattn(r, log_w, k, v, state_in, nullptr, y, state_out, B, T, H, N, dtype, decay, true, stream);
+}
+
+int rwkv7_linattn_backward(const void* r, const float* log_w, const void* k, const void* v, const float* state_in,
+                           const int32_t* lens, const void* dy, const float* dstate_out, void* dr, float* dlog_w, void* dk,
+                           void* dv, float* dstate_in, int64_t B, int64_t T, int64_t H, int64_t N, int dtype, int decay,
+                           void* stream) {
+  LinattnCall c{};
+  c.r = r, c.log_w = log_w, c.k = k, c.v = v, c.s_in = state_in, c.lens = lens, c.dy = dy, c.ds_out = dstate_out;
+  c.dr = dr, c.dlog_w = dlog_w, c.dk = dk, c.dv = dv, c.ds_in = dstate_in;
+  c.B = B, c.T = T, c.H = H, c.f32 = dtype == RWKV7_DTYPE_F32, c.per_token = decay == RWKV7_DECAY_TOKEN;
+  c.stream = static_cast<hipStream_t>(stream);
+  return run_backward(c, N, dtype, decay);
 }
 
 }  // extern "C"

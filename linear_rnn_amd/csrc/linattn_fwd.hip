@@ -115,8 +115,8 @@ __global__ __launch_bounds__(256) void linattn_out_kernel(OutParams p) {
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) a01[i] *= d.d01[i];
-      P[0] = pack<NO>(masked(a00, d.d00, lane), zero4());
-      P[1] = pack<NO>(a01, masked(a11, d.d11, lane));
+      P[0] = pack<NO>(masked_j(a00, d.d00, lane), zero4());
+      P[1] = pack<NO>(a01, masked_j(a11, d.d11, lane));
     }
     if (wave < kWaves - 1) {
 #pragma unroll

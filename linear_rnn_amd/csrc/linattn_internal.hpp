@@ -14,14 +14,42 @@ struct LinattnCall {
   const void* v;
   const float* s_in;    // may be null (zeros)
   const int32_t* lens;  // may be null (every sequence has T tokens)
-  void* y;
-  float* s_out;  // may be null
+  void* y;              // forward
+  float* s_out;         // forward; may be null
   int64_t B, T, H;
-  bool f32;            // element type of r, k, v, y (else bfloat16)
-  int32_t per_token;   // log_w is [B, T, H] (else [H])
+  bool f32;           // element type of r, k, v, y, dy, dr, dk, dv (else bfloat16)
+  int32_t per_token;  // log_w is [B, T, H] (else [H])
   hipStream_t stream;
+  // backward
+  const void* dy;
+  const float* ds_out;  // may be null (zeros)
+  void* dr;
+  float* dlog_w;  // in log_w's layout
+  void* dk;
+  void* dv;
+  float* ds_in;  // may be null
 };
 hipError_t launch_linattn(const LinattnCall& c);
 hipError_t launch_linattn_step(const LinattnCall& c);
+hipError_t launch_linattn_backward(const LinattnCall& c);
+hipError_t launch_linattn_zero(float* dlog_w, int64_t H, hipStream_t stream);
+
+constexpr int64_t kLinattnBlock = 128;              // tokens a workgroup takes at a time
+constexpr int64_t kLinattnStateBytes = 64 * 64 * 4;  // one state
+
+// Pieces of every sequence: `pieces` of `piece_blocks` blocks (the last may have fewer), and the device memory
+// for the states at their starts.
+struct LinattnPieces {
+  int32_t pieces;
+  int64_t piece_blocks;
+  void* states;       // [units][pieces] states
+  float* decay;       // [units][pieces]
+  void* marks;        // may be null; [units][blocks] states
+  float* mark_decay;  // [units][blocks]
+};
+// states <- the state before each piece (reverse: its gradient behind each), and, if asked for, the sums of each
+// piece before each of its blocks but the first.
+hipError_t launch_linattn_states(const LinattnCall& c, const LinattnPieces& q, const void* keys, const void* values,
+                                 bool reverse);
 
 }  // namespace rwkv7

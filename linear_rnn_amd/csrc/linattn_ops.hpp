@@ -199,7 +199,9 @@ struct Decay {
   float col[2];      // exp(c) of token 16I + li
   float row[2][4];   // exp(c_31 - c) of token 16J + 4q + i: what is left of it at the end
   float inrow[2][4]; // exp(c) of token 16J + 4q + i
-  f32x4 d00, d01, d11;  // D of (token row, token column) tiles: rows 16J + 4q + i, columns 16I + li, 0 where row > column
+  float out[2];      // exp(c_31 - c) of token 16J + li
+  f32x4 d00, d01, d11;  // D with the tokens j as rows: tile (J, I) has rows j = 16J + 4q + i, columns i = 16I + li
+  f32x4 t00, t10, t11;  // D with the tokens i as rows: tile (I, J) has rows i = 16I + 4q + i, columns j = 16J + li
   float all;         // exp(c_31)
 };
 
@@ -248,6 +250,7 @@ __device__ __forceinline__ Decay make_decay(float log_w, double* sums, int lane)
 #pragma unroll
   for (int J = 0; J < 2; ++J) {
     d.col[J] = exp_diff(cc[J], 0.0);
+    d.out[J] = exp_diff(end, cc[J]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       d.row[J][i] = exp_diff(end, cr[J][i]);
@@ -255,20 +258,29 @@ __device__ __forceinline__ Decay make_decay(float log_w, double* sums, int lane)
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool low = 4 * q + i <= li;
-    d.d00[i] = low ? exp_diff(cc[0], cr[0][i]) : 0.f;
+  for (int i = 0; i < 4; ++i) {  // in the tiles on the diagonal also where D is 0 (masked() leaves that out)
+    d.d00[i] = exp_diff(cc[0], cr[0][i]);
     d.d01[i] = exp_diff(cc[1], cr[0][i]);
-    d.d11[i] = low ? exp_diff(cc[1], cr[1][i]) : 0.f;
+    d.d11[i] = exp_diff(cc[1], cr[1][i]);
+    d.t00[i] = exp_diff(cr[0][i], cc[0]);
+    d.t10[i] = exp_diff(cr[1][i], cc[0]);
+    d.t11[i] = exp_diff(cr[1][i], cc[1]);
   }
   d.all = exp_diff(end, 0.0);
   return d;
 }
-// p D, 0 where D leaves the pair out (whatever p is there).
-__device__ __forceinline__ f32x4 masked(f32x4 p, f32x4 d, int lane) {
+// p D in a tile on the diagonal, 0 for the pairs that D leaves out (whatever p and the factor are there):
+// rows j <= columns i, or rows i >= columns j.
+__device__ __forceinline__ f32x4 masked_j(f32x4 p, f32x4 d, int lane) {
   f32x4 o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = (4 * (lane >> 4) + i <= (lane & 15)) ? p[i] * d[i] : 0.f;
+  return o;
+}
+__device__ __forceinline__ f32x4 masked_i(f32x4 p, f32x4 d, int lane) {
+  f32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = (4 * (lane >> 4) + i >= (lane & 15)) ? p[i] * d[i] : 0.f;
   return o;
 }
 
@@ -299,6 +311,14 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t token_buffer(const void* base,
   // the last token's row ends 64 channels behind this head's start
   const uint32_t bytes = left ? ((uint32_t)(left - 1) * s.H * kN + kN) * ESZ : 0;
   return buffer(static_cast<const char*>(base) + ((b * s.T + t0) * s.H + h) * (int64_t)(kN * ESZ), bytes);
+}
+// Where the segments of a sequence start from: `pieces` of them, each `blocks` blocks of kBlk tokens, in
+// the wave layout [unit][piece][16 tiles][64 lanes].
+__device__ __forceinline__ f32x4* state_tile(void* states, int64_t index, int tu, int lane) {
+  return static_cast<f32x4*>(states) + (index * 16 + tu) * 64 + lane;
+}
+__device__ __forceinline__ const f32x4* state_tile(const void* states, int64_t index, int tu, int lane) {
+  return static_cast<const f32x4*>(states) + (index * 16 + tu) * 64 + lane;
 }
 // log w of the token t0 + lane % 32; 0 (decay 1) behind the sequence's end.
 __device__ __forceinline__ float load_log_w(const float* log_w, bool per_token, const Seq& s, int64_t b, int32_t h,

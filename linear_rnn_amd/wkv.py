@@ -39,7 +39,7 @@ EXPORTED = ("rwkv7_wkv_prefill", "rwkv7_wkv_step", "rwkv7_wkv_step_q", "rwkv7_wk
             "rwkv7_tmix_prefill", "rwkv7_tmix_prefill_ex", "rwkv7_tmix_step", "rwkv7_wkv_backward",
             "rwkv7_wkv_backward_ex",
             "rwkv7_stack_forward", "rwkv7_wkv_prefill_algo", "rwkv7_wkv_prefill_noalloc",
-            "rwkv7_linattn_prefill", "rwkv7_linattn_step",
+            "rwkv7_linattn_prefill", "rwkv7_linattn_step", "rwkv7_linattn_backward",
             "rwkv7_layernorm_forward", "rwkv7_layernorm_backward",
             "rwkv7_wkv_strerror")
 
@@ -87,6 +87,8 @@ def lib() -> ctypes.CDLL:
             L.rwkv7_linattn_prefill.argtypes = [vp] * 8 + [i64] * 4 + [ci, ci, vp]
             L.rwkv7_linattn_step.restype = ci
             L.rwkv7_linattn_step.argtypes = [vp] * 7 + [i64] * 4 + [ci, ci, vp]
+            L.rwkv7_linattn_backward.restype = ci
+            L.rwkv7_linattn_backward.argtypes = [vp] * 13 + [i64] * 4 + [ci, ci, vp]
             cf = ctypes.c_float
             L.rwkv7_layernorm_forward.restype = ci
             L.rwkv7_layernorm_forward.argtypes = [vp] * 6 + [i64] * 3 + [cf, ci, ci, vp]
@@ -449,6 +451,33 @@ def linattn_step(r, log_w, k, v, state_in=None, stream=None):
     s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
     rwkv7_linattn_step(r, log_w, k, v, state_in, y, s_out, stream=stream)
     return y, s_out
+
+
+def rwkv7_linattn_backward(r, log_w, k, v, state_in, lens, dy, dstate_out, dr, dlog_w, dk, dv, dstate_in, stream=None):
+    """Gradients of the linear attention: dr, dk, dv in r's dtype, dlog_w float32 in log_w's layout, dstate_in
+    float32 or None (may be dstate_out)."""
+    B, T, H, N, decay = _linattn_inputs(r, log_w, k, v, state_in, lens)
+    _expect(dy, "dy", r.shape, (r.dtype,), r)
+    _expect(dstate_out, "dstate_out", (B, H, N, N), _f32(), r, optional=True)
+    for name, t in (("dr", dr), ("dk", dk), ("dv", dv)):
+        _expect(t, name, r.shape, (r.dtype,), r)
+    _expect(dlog_w, "dlog_w", log_w.shape, _f32(), r)
+    _expect(dstate_in, "dstate_in", (B, H, N, N), _f32(), r, optional=True)
+    _on_gpu(r, stream)
+    args = [_ptr(x) for x in (r, log_w, k, v, state_in, lens, dy, dstate_out, dr, dlog_w, dk, dv, dstate_in)]
+    _launch(lib().rwkv7_linattn_backward, args + [B, T, H, N, _dtype_code(r), decay], r, stream)
+
+
+def linattn_backward(r, log_w, k, v, dy, state_in=None, lens=None, dstate_out=None, want_dstate=True, stream=None):
+    """Allocate the gradients, run the backward, return dict dr, dlog_w, dk, dv, dstate_in."""
+    import torch
+    B, T, H, N = r.shape
+    out = {n: torch.empty_like(r) for n in ("dr", "dk", "dv")}
+    out["dlog_w"] = torch.empty_like(log_w)
+    out["dstate_in"] = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device) if want_dstate else None
+    rwkv7_linattn_backward(r, log_w, k, v, state_in, lens, dy, dstate_out, out["dr"], out["dlog_w"], out["dk"],
+                           out["dv"], out["dstate_in"], stream=stream)
+    return out
 
 
 # ---- layer norm over groups of channels

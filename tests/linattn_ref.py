@@ -110,7 +110,12 @@ def backward(x):
 # under 2^-23: within the same count. What pieces leave out: 2^-24 (three pieces: 4 dropped
 # products, in the same count) or 2^-16 for each of the two factors of a product (two pieces, only
 # where the output is bfloat16). The output's own rounding: 2^-8 (bfloat16) of the value.
+#
+# Underflow: a decay factor under 2^-126, the smallest normal float32, may be 0, so it is off by at most
+# 2^-126, and so is a product of factors. It multiplies a sum of at most 2^13 terms (64 * 64 of a state
+# product and the tokens), each a product of at most four inputs under 8 in magnitude, 2^12: together 2^-101.
 U32 = 2.0 ** -24
+UNDERFLOW = 2.0 ** -101
 
 
 def roundings(T):
@@ -118,7 +123,7 @@ def roundings(T):
 
 
 def limit(ref, mag, T, bf16):
-    return (2.0 ** -8 * ref.abs() if bf16 else 0.0) + (2.0 ** -15 if bf16 else 0.0) * mag + roundings(T) * U32 * mag
+    return (2.0 ** -8 * ref.abs() if bf16 else 0.0) + (2.0 ** -15 if bf16 else 0.0) * mag + roundings(T) * U32 * mag + UNDERFLOW
 
 
 def check(name, got, ref, mag, T, bf16):
@@ -132,6 +137,7 @@ def check(name, got, ref, mag, T, bf16):
         return
     over = (got - ref).abs() - limit(ref, mag, T, bf16)
     assert over.max() <= 0, "%s: %g over its bound" % (name, float(over.max()))
-    unit = (2.0 ** -8 / 3 ** 0.5 * ref.norm() if bf16 else 0.0) + roundings(T) ** 0.5 * U32 * mag.norm()
+    unit = (2.0 ** -8 / 3 ** 0.5 * ref.norm() if bf16 else 0.0) + roundings(T) ** 0.5 * U32 * mag.norm() + \
+        UNDERFLOW * mag.numel() ** 0.5
     err = float((got - ref).norm())
     assert err <= float(unit), "%s: 2-norm of the error %g, bound %g" % (name, err, float(unit))

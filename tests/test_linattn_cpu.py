@@ -102,6 +102,32 @@ def test_overlaps(L, call, n, y, s):
             assert call(L, p) == E_ALIAS, (out, i)
 
 
+def backward(L, p=None, B=2, T=3, H=4, N=64, dtype=BF16, decay=TOKEN):
+    # r, log_w, k, v, state_in, lens, dy, dstate_out, dr, dlog_w, dk, dv, dstate_in
+    return L.rwkv7_linattn_backward(*(ptrs(13) if p is None else p), B, T, H, N, dtype, decay, None)
+
+
+def test_backward_refusals(L):
+    assert backward(L, dtype=2) == E_DTYPE and backward(L, decay=2) == E_DECAY and backward(L, N=128) == E_HEAD
+    for bad in (dict(B=-1), dict(T=-1), dict(H=-4), dict(B=1 << 22, H=4), dict(H=(1 << 18) + 1, B=1), dict(T=1 << 60)):
+        assert backward(L, **bad) == E_SHAPE, bad
+    for i in range(13):
+        p = ptrs(13)
+        p[i] += 4
+        assert backward(L, p) == E_ALIGN, i
+        if i not in (4, 5, 7, 12):
+            p = ptrs(13)
+            p[i] = None
+            assert backward(L, p) == E_NULL, i
+    for out in (8, 9, 10, 11, 12):
+        for i in range(13):
+            if i == out:
+                continue
+            p = ptrs(13)
+            p[out] = p[i] + (1024 if i == 7 and out == 12 else 0)  # dstate_in may be dstate_out, but not part of it
+            assert backward(L, p) == E_ALIAS, (out, i)
+
+
 def test_empty_work_needs_no_device(L):
     assert prefill(L, B=0) == OK and prefill(L, H=0) == OK and step(L, B=0) == OK
     p = ptrs(8)
@@ -110,6 +136,10 @@ def test_empty_work_needs_no_device(L):
     p[7] = p[4]  # no tokens, the state in place
     assert prefill(L, p, T=0) == OK
     assert prefill(L, [None] * 8, B=0) == OK
+    assert backward(L, B=0) == OK and backward(L, H=0) == OK
+    p = ptrs(13)
+    p[12] = p[7]
+    assert backward(L, p, T=0) == OK
 
 
 # ---- refusals of the binding
@@ -157,6 +187,23 @@ def test_binding_refuses(no_library, name, value, match):
         del a["lens"]
         with pytest.raises(ValueError, match=match):
             wkv.rwkv7_linattn_step(**a)
+
+
+@pytest.mark.parametrize("name,value,match", [b for b in BAD if b[0] not in ("y", "state_out")] + [
+    ("dy", None, "dy is required"), ("dy", torch.zeros((B, T, H, N)), "dy has dtype"),
+    ("dr", torch.zeros((B, T, H, N)), "dr has dtype"), ("dk", torch.zeros((B, T, H), dtype=torch.bfloat16), "dk has shape"),
+    ("dv", None, "dv is required"), ("dlog_w", torch.zeros((H,)), "dlog_w has shape"),
+    ("dlog_w", torch.zeros((B, T, H), dtype=torch.bfloat16), "dlog_w has dtype"),
+    ("dstate_out", torch.zeros((H, N, N)), "dstate_out has shape"), ("dstate_in", torch.zeros((H, N, N)), "dstate_in has")])
+def test_binding_refuses_backward(no_library, name, value, match):
+    a = good()
+    a = {n: a[n] for n in ("r", "log_w", "k", "v", "state_in", "lens")}
+    a.update({n: torch.zeros((B, T, H, N), dtype=torch.bfloat16) for n in ("dy", "dr", "dk", "dv")},
+             dlog_w=torch.zeros((B, T, H)), dstate_out=None, dstate_in=None)
+    with pytest.raises(ValueError, match="must be on a HIP device"):
+        wkv.rwkv7_linattn_backward(**a)
+    with pytest.raises(ValueError, match=match):
+        wkv.rwkv7_linattn_backward(**dict(a, **{name: value}))
 
 
 def test_binding_refuses_host_tensors(no_library):
