@@ -451,7 +451,7 @@ int rwkv7_wkv_prefill_algo(int64_t B, int64_t T, int64_t H, int64_t N, int dtype
  *              hold: y there is 0 and the state is that after token lens[b] - 1
  *   y          [B,T,H,N] output in `dtype`
  *   state_out  [B,H,N,N] float32 final state, or NULL; may equal state_in
- *   B, T, H    batch, tokens, heads (>= 0); B*H at most 2^23, H at most 2^18
+ *   B, T, H    batch, tokens, heads (>= 0); B*H at most 2^22, H at most 2^18
  *   N          head size; must be 64
  *
  * The state and every sum are float32 (sums of log_w float64). bfloat16 inputs

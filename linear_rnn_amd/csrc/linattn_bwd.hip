@@ -134,7 +134,7 @@ __global__ __launch_bounds__(256, 1) void linattn_grad_kernel(GradParams p) {
     load_raw<F32>(rd, at(p.dy, t0, len - t0), row_bytes, lane);
     load_raw<F32>(rk, at(p.k, t0, len - t0), row_bytes, lane);
     load_raw<F32>(rv, at(p.v, t0, len - t0), row_bytes, lane);
-    const Decay d = make_decay(load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane), sums[wave], lane);
+    const Decay d = make_decay(log_w_here(load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane), t0, len, lane), sums[wave], lane);
 
     auto turn = [&](const Raw<F32>& x, int t) { return turned_op(natural<F32>(x, 0, t >> 1), natural<F32>(x, 1, t >> 1), E, t); };
     // What the 32 tokens add to S and to G, for the other waves (wave 0's G for the next carry). A phase ends where
@@ -175,7 +175,7 @@ __global__ __launch_bounds__(256, 1) void linattn_grad_kernel(GradParams p) {
     // the gradient behind the wave's tokens, tile (t, u)
     auto grad_tile = [&](int tu) {
       f32x4 g = carry[tu][lane];
-      for (int w = kWaves - 1; w > wave; --w) g = g * all[w] + addG[w][tu][lane];
+      for (int w = kWaves - 1; w > wave; --w) g = fma4(g, all[w], addG[w][tu][lane]);
       return g;
     };
     float cross[2] = {0.f, 0.f};  // this lane's rows of the pairs that cross token 16J + li
@@ -280,8 +280,8 @@ __global__ __launch_bounds__(256, 1) void linattn_grad_kernel(GradParams p) {
               s[t] = *state_tile(p.states, unit * p.pieces + piece, tu, lane);
             else if (p.s_in)
               s[t] = *reinterpret_cast<const f32x4*>(p.s_in + unit * kN * kN + state_offset(t, u, lane));
-            if (marked) s[t] = s[t] * mark_decay + *state_tile(p.marks, unit * nblk + blk, tu, lane);
-            for (int w = 0; w < wave; ++w) s[t] = s[t] * all[w] + addS[w][tu][lane];
+            if (marked) s[t] = fma4(s[t], mark_decay, *state_tile(p.marks, unit * nblk + blk, tu, lane));
+            for (int w = 0; w < wave; ++w) s[t] = fma4(s[t], all[w], addS[w][tu][lane]);
             const f32x4 g = grad_tile(tu);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dot = fmaf(s[t][i], g[i], dot);
@@ -347,7 +347,7 @@ __global__ __launch_bounds__(256, 1) void linattn_grad_kernel(GradParams p) {
       const int tu = 4 * wave + m;
       f32x4 g = carry[tu][lane];
 #pragma unroll
-      for (int w = kWaves - 1; w >= 0; --w) g = g * all[w] + addG[w][tu][lane];
+      for (int w = kWaves - 1; w >= 0; --w) g = fma4(g, all[w], addG[w][tu][lane]);
       carry[tu][lane] = g;
     }
     __syncthreads();

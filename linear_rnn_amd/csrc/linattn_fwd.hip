@@ -1,8 +1,7 @@
 // Linear attention with a decay for each head: whole prompts and single tokens.
 // The chunk algebra and its number formats are in linattn_ops.hpp.
-#include "linattn_ops.hpp"
-#include "rwkv7_wkv.h"
 #include "linattn_internal.hpp"
+#include "linattn_ops.hpp"
 
 namespace rwkv7 {
 namespace {
@@ -14,30 +13,42 @@ struct OutParams {
   const float* log_w;
   const void* k;
   const void* v;
-  const float* first;  // [units][nseg] starts in the wave layout (nseg > 1), or the caller's state, or null
+  const f32x4* states;  // [units][nseg] states before the segments (nseg > 1)
+  const float* s_in;    // the caller's state (nseg == 1), may be null
   void* y;
-  float* s_out;        // may be null
+  float* s_out;  // may be null
   Seq seq;
   int32_t per_token;
   int32_t nseg;        // segments of a sequence
   int64_t seg_blocks;  // blocks of kBlk tokens in a segment
-  int32_t pieces;      // state pieces in a segment: its start is that of piece seg * pieces
-  int64_t piece_stride;  // pieces of a sequence in `first`
 };
 
-// One workgroup carries one segment of one head from its start state, kBlk = 128 tokens at a time:
-// each wave takes 32 of them, forms what they add to the state, leaves it in LDS, and takes the
-// state before its own tokens from the carried state and what the waves before it added.
+// A workgroup carries 32 of the state's 64 value rows (two tiles) over one segment of one head, 128 tokens at a
+// time: each wave takes 32 of them and leaves what they add to the state in LDS. Then each wave takes a quarter of
+// the state's tiles through the four waves' tokens (the carried part stays in its registers) and leaves the
+// states before each wave's tokens, as operands, for the others. The two workgroups of a
+// head follow each other on the same die, so r and k come from memory once. Loads run a block ahead.
+constexpr int kVt = 2;  // value tiles of a workgroup
+
 template <bool F32>
-__global__ __launch_bounds__(256) void linattn_out_kernel(OutParams p) {
+struct Inputs {
+  Raw<F32> r, k;
+  u32x4 v[2][F32 ? 2 : 1];  // [token tile], the workgroup's 32 values
+  float log_w;
+};
+
+template <bool F32>
+__global__ __launch_bounds__(256, F32 ? 1 : 2) void linattn_out_kernel(OutParams p) {
   constexpr int NI = kIn<F32>, NO = F32 ? 3 : 2;
-  __shared__ f32x4 added[kWaves - 1][16][64];
-  __shared__ f32x4 carry[16][64];
+  __shared__ f32x4 added[kWaves][4 * kVt][64];
+  __shared__ bf16x8 before[kWaves][kVt][2][NO][64];  // [wave][value tile][key half]: operands
   __shared__ double sums[kWaves][kSub];
   __shared__ float all[kWaves];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t unit = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
+  const uint32_t id = xcd_swizzle(blockIdx.x, gridDim.x);
+  const int half = id & 1;
+  const uint32_t unit = (id >> 1) / p.nseg, seg = (id >> 1) % p.nseg;
   const int64_t b = unit / p.seq.H;
   const int32_t h = unit % p.seq.H;
   const int64_t T = p.seq.T, len = seq_len(p.seq, b);
@@ -45,62 +56,78 @@ __global__ __launch_bounds__(256) void linattn_out_kernel(OutParams p) {
   const int64_t blk0 = seg * p.seg_blocks;
   const int64_t nblk = (T + kBlk - 1) / kBlk;
   const int64_t blk1 = blk0 + p.seg_blocks < nblk ? blk0 + p.seg_blocks : nblk;
+  // blocks with tokens in them; behind those the sequence has ended
+  const int64_t live = (len + kBlk - 1) / kBlk < blk1 ? (len + kBlk - 1) / kBlk : blk1;
+  const uint32_t off = (lane & 15) * row_bytes + ((lane >> 4) * 8 + half * 32) * kEsz<F32>;  // of v and y
 
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {  // the start state: tiles 4m .. of the wave m
-    const int tu = 4 * wave + m;
-    f32x4 s = zero4();
-    if (p.nseg > 1)
-      s = reinterpret_cast<const f32x4*>(p.first)[((unit * p.piece_stride + (int64_t)seg * p.pieces) * 16 + tu) * 64 + lane];
-    else if (p.first)
-      s = *reinterpret_cast<const f32x4*>(p.first + (int64_t)unit * kN * kN + state_offset(tu >> 2, tu & 3, lane));
-    carry[tu][lane] = s;
-  }
-  const Turn E = make_turn(lane);
-  for (int64_t blk = blk0; blk < blk1; ++blk) {
+  Inputs<F32> x;
+  auto load = [&](Inputs<F32>& x, int64_t blk) {
     const int64_t t0 = blk * kBlk + wave * kSub;
-    const __amdgpu_buffer_rsrc_t yb = token_buffer<kEsz<F32>>(p.y, p.seq, b, h, t0, T - t0, kSub);
-    const uint32_t yoff = (lane & 15) * row_bytes + (lane >> 4) * 8 * kEsz<F32>;
-    if (blk * kBlk >= len) {  // nothing but tokens behind the sequence's end: zeros
-#pragma unroll
-      for (int I = 0; I < 2; ++I)
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
-          store_pair<F32>(yb, yoff + I * 16 * row_bytes + hh * 32 * kEsz<F32>, zero4(), zero4());
-      continue;
-    }
-    Raw<F32> rr, rk, rv;
-    load_raw<F32>(rk, token_buffer<kEsz<F32>>(p.k, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
-    load_raw<F32>(rv, token_buffer<kEsz<F32>>(p.v, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
-    load_raw<F32>(rr, token_buffer<kEsz<F32>>(p.r, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
-    const Decay d = make_decay(load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane), sums[wave], lane);
-    Op<NI> K[2][2], R[2][2];
+    const __amdgpu_buffer_rsrc_t vb = token_buffer<kEsz<F32>>(p.v, p.seq, b, h, t0, len - t0, kSub);
+    load_raw<F32>(x.k, token_buffer<kEsz<F32>>(p.k, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
 #pragma unroll
     for (int J = 0; J < 2; ++J)
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) K[J][hh] = natural<F32>(rk, J, hh), R[J][hh] = natural<F32>(rr, J, hh);
-    // what the 32 tokens add to the state: tiles (t, u) of sum_j k_j (left_j v_j)^T
-    Op<NI> Vt[4];
-    f32x4 S[4][4];
-    {
-      Op<3> Vs[4];
+      for (int m = 0; m < (F32 ? 2 : 1); ++m) x.v[J][m] = load16(vb, off + J * 16 * row_bytes + 16 * m);
+    load_raw<F32>(x.r, token_buffer<kEsz<F32>>(p.r, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
+    x.log_w = load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane);
+  };
+  if (blk0 < live) load(x, blk0);
+  f32x4 carry[kVt];  // tiles (wave, 0), (wave, 1) of the half
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const Op<NI> v0 = natural<F32>(rv, 0, u >> 1), v1 = natural<F32>(rv, 1, u >> 1);
-        f32x4 a0 = turned(v0, E, u), a1 = turned(v1, E, u);
+  for (int m = 0; m < kVt; ++m) {
+    carry[m] = zero4();
+    if (p.nseg > 1)
+      carry[m] = *state_tile(p.states, (int64_t)unit * p.nseg + seg, 4 * wave + kVt * half + m, lane);
+    else if (p.s_in)
+      carry[m] = *reinterpret_cast<const f32x4*>(p.s_in + (int64_t)unit * kN * kN + state_offset(wave, kVt * half + m, lane));
+  }
+  const Turn E = make_turn(lane);
+  // the first loads end here: a value that might still be in flight from before the loop would make the
+  // compiler wait for the loads ahead too
+  __builtin_amdgcn_s_waitcnt(0x0f70);
+  for (int64_t blk = blk0; blk < live; ++blk) {
+    Inputs<F32> ahead;
+    load(ahead, blk + 1);  // behind the last block the descriptors are empty or what comes is not used
+    const int64_t t0 = blk * kBlk + wave * kSub;
+    const Decay d = make_decay(log_w_here(x.log_w, t0, len, lane), sums[wave], lane);
+    // what the 32 tokens add to the state: tiles (t, u) of sum_j k_j (left_j v_j)^T
+    Op<NI> Vt[kVt];
+    {
+      Op<3> Vs[kVt];
+#pragma unroll
+      for (int m = 0; m < kVt; ++m) {
+        const Op<NI> v0 = pieces<F32>(x.v[0]), v1 = pieces<F32>(x.v[1]);
+        f32x4 a0 = turned(v0, E, m), a1 = turned(v1, E, m);
         if constexpr (F32)
-          Vt[u] = turned_op(v0, v1, E, u);
+          Vt[m] = turned_op(v0, v1, E, m);
         else
-          Vt[u] = pack<NI>(a0, a1);
+          Vt[m] = pack<NI>(a0, a1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a0[i] *= d.row[0][i], a1[i] *= d.row[1][i];
-        Vs[u] = pack<3>(a0, a1);
+        Vs[m] = pack<3>(a0, a1);
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const Op<NI> Kt = turned_op(K[0][t >> 1], K[1][t >> 1], E, t);
+        const Op<NI> Kt = turned_op(natural<F32>(x.k, 0, t >> 1), natural<F32>(x.k, 1, t >> 1), E, t);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) S[t][u] = mma(Kt, Vs[u], zero4());
+        for (int m = 0; m < kVt; ++m) added[wave][kVt * t + m][lane] = mma(Kt, Vs[m], zero4());
+      }
+    }
+    if (lane == 0) all[wave] = d.all;
+    lds_barrier();
+    // the states before each wave's tokens: this wave's two tiles of them
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float a = all[w];
+#pragma unroll
+      for (int m = 0; m < kVt; ++m) {
+        Op<NO> o = pack<NO>(carry[m], zero4());
+#pragma unroll
+        for (int n = 0; n < NO; ++n)
+          reinterpret_cast<bf16x4*>(&before[w][m][wave >> 1][n][lane])[wave & 1] =
+              __builtin_shufflevector(o.p[n], o.p[n], 0, 1, 2, 3);
+        carry[m] = fma4(carry[m], a, added[w][kVt * wave + m][lane]);
       }
     }
     // the pairs inside the 32 tokens, as operands over the tokens j: column i
@@ -109,80 +136,249 @@ __global__ __launch_bounds__(256) void linattn_out_kernel(OutParams p) {
       f32x4 a00 = zero4(), a01 = zero4(), a11 = zero4();
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
+        const Op<NI> K0 = natural<F32>(x.k, 0, hh), K1 = natural<F32>(x.k, 1, hh);
+        const Op<NI> R0 = natural<F32>(x.r, 0, hh), R1 = natural<F32>(x.r, 1, hh);
+        a00 = mma(K0, R0, a00);
+        a01 = mma(K0, R1, a01);
+        a11 = mma(K1, R1, a11);
+      }
+      P[0] = pack<NO>(masked_j(a00, d.d00, lane), zero4());
+      P[1] = pack<NO>(a01 * d.d01, masked_j(a11, d.d11, lane));
+    }
+    lds_barrier();
+    f32x4 y[2][kVt];
+#pragma unroll
+    for (int m = 0; m < kVt; ++m) {
+      Op<NO> S0, S1;
+#pragma unroll
+      for (int n = 0; n < NO; ++n) S0.p[n] = before[wave][m][0][n][lane], S1.p[n] = before[wave][m][1][n][lane];
+#pragma unroll
+      for (int I = 0; I < 2; ++I) {
+        f32x4 o = mma(S0, natural<F32>(x.r, I, 0), zero4());
+        o = mma(S1, natural<F32>(x.r, I, 1), o);
+        y[I][m] = mma(Vt[m], P[I], o * d.col[I]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const __amdgpu_buffer_rsrc_t yb = token_buffer<kEsz<F32>>(p.y, p.seq, b, h, t0, T - t0, kSub);
+#pragma unroll
+    for (int I = 0; I < 2; ++I) store_pair<F32>(yb, off + I * 16 * row_bytes, y[I][0], y[I][1]);
+    x = ahead;
+  }
+  for (int64_t blk = live > blk0 ? live : blk0; blk < blk1; ++blk) {  // behind the sequence's end: zeros
+    const int64_t t0 = blk * kBlk + wave * kSub;
+    const __amdgpu_buffer_rsrc_t yb = token_buffer<kEsz<F32>>(p.y, p.seq, b, h, t0, T - t0, kSub);
+#pragma unroll
+    for (int I = 0; I < 2; ++I) store_pair<F32>(yb, off + I * 16 * row_bytes, zero4(), zero4());
+  }
+  if (p.s_out && blk1 == nblk) {
+#pragma unroll
+    for (int m = 0; m < kVt; ++m)
+      *reinterpret_cast<f32x4*>(p.s_out + (int64_t)unit * kN * kN + state_offset(wave, kVt * half + m, lane)) = carry[m];
+  }
+}
+
+// ---- bfloat16. Eight waves of one workgroup take a whole head: 128 tokens at a time, in quarters of 32, two waves
+// (32 value rows each) to a quarter. Memory bounds this kernel, and what it reaches hangs on whole 128-byte rows, each
+// asked for once: a stream of this layout (three tensors read, one written, a workgroup a head) measured 4.9 TB/s
+// in whole rows without temporal hint and consecutive workgroups on consecutive dies, 4.3 with an L2-friendly
+// numbering, and 3.2 where two workgroups a head loaded 64-byte pieces in operand order. So the rows go to LDS by
+// direct loads, up to two blocks ahead, their 16-byte pieces exchanged within a row so that the
+// operand reads of 16 rows fall into different banks.
+constexpr int kRow = kN * 2;              // bytes of a token's row
+constexpr int kTile = kSub * kRow;        // bytes of a quarter's rows of one tensor
+constexpr int kExchange = 0;              // [quarter][half][8 tiles][64 lanes] 16 bytes
+constexpr int kStageKV = 64 << 10;        // [parity][quarter][k, v] kTile
+constexpr int kStageR = kStageKV + 16 * kTile;      // [quarter] kTile
+constexpr int kStageW = kStageR + 4 * kTile;        // [parity][wave][64] float
+constexpr int kSums = kStageW + 2 * 8 * 256;        // [wave][32] double
+constexpr int kAll = kSums + 8 * kSub * 8;          // [quarter] float
+constexpr int kOutLds = kAll + 16;
+static_assert(kOutLds <= 160 * 1024, "LDS of a compute unit");
+
+__global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
+  extern __shared__ char lds[];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave >> 2, quarter = wave & 3;
+  const uint32_t unit = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
+  const int64_t b = unit / p.seq.H;
+  const int32_t h = unit % p.seq.H;
+  const int64_t T = p.seq.T, len = seq_len(p.seq, b);
+  const uint32_t row_bytes = p.seq.H * kRow;
+  const int64_t blk0 = seg * p.seg_blocks;
+  const int64_t nblk = (T + kBlk - 1) / kBlk;
+  const int64_t blk1 = blk0 + p.seg_blocks < nblk ? blk0 + p.seg_blocks : nblk;
+  const int64_t live = (len + kBlk - 1) / kBlk < blk1 ? (len + kBlk - 1) / kBlk : blk1;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+
+  // Rows to LDS: an instruction takes 8 rows, row r's piece c to place c ^ (r / 2 % 8). The two waves of a quarter
+  // take 16 rows each.
+  const int row = 16 * half + (lane >> 3);
+  const uint32_t src0 = row * row_bytes + 16 * ((lane & 7) ^ (row >> 1 & 7));
+  const uint32_t src1 = src0 + 8 * row_bytes + 16 * (((lane & 7) ^ ((row + 8) >> 1 & 7)) - ((lane & 7) ^ (row >> 1 & 7)));
+  auto stage = [&](const void* x, int64_t blk, uint32_t to) {
+    const int64_t t0 = blk * kBlk + quarter * kSub;
+    const Span span = token_span<2>(x, p.seq, b, h, t0, len - t0, kSub);
+    const u32x4 r = descriptor(span.base, span.bytes);
+    to_lds16(r, src0, lds0 + to + 16 * half * kRow);
+    to_lds16(r, src1, lds0 + to + (16 * half + 8) * kRow);
+  };
+  auto stage_kv = [&](int64_t blk) {
+    const int par = blk & 1;
+    stage(p.k, blk, kStageKV + ((par * 4 + quarter) * 2) * kTile);
+    stage(p.v, blk, kStageKV + ((par * 4 + quarter) * 2 + 1) * kTile);
+    const int64_t t0 = blk * kBlk + quarter * kSub;
+    const Span span = log_w_span(p.log_w, p.per_token, p.seq, b, h, t0, len);
+    to_lds4(descriptor(span.base, half ? 0 : span.bytes), (lane & 31) * (p.per_token ? p.seq.H * 4 : 0),
+            lds0 + kStageW + (par * 8 + wave) * 256);
+  };
+  auto stage_r = [&](int64_t blk) { stage(p.r, blk, kStageR + quarter * kTile); };
+  // operand of the rows 16J + li, channels 32hh + 8q ..
+  const int li = lane & 15, q = lane >> 4;
+  auto staged = [&](int from, int J, int hh) {
+    const int place = (4 * hh + q) ^ (li >> 1);
+    return Op<1>{{*reinterpret_cast<const bf16x8*>(lds + from + (16 * J + li) * kRow + 16 * place)}};
+  };
+
+  f32x4 carry[kVt];  // tiles (quarter, 0), (quarter, 1) of the half
+#pragma unroll
+  for (int m = 0; m < kVt; ++m) {
+    carry[m] = zero4();
+    if (p.nseg > 1)
+      carry[m] = *state_tile(p.states, (int64_t)unit * p.nseg + seg, 4 * quarter + kVt * half + m, lane);
+    else if (p.s_in)
+      carry[m] = *reinterpret_cast<const f32x4*>(p.s_in + (int64_t)unit * kN * kN + state_offset(quarter, kVt * half + m, lane));
+  }
+  const Turn E = make_turn(lane);
+  if (blk0 < live) stage_r(blk0), stage_kv(blk0), stage_kv(blk0 + 1);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  f32x4(*exch)[2][8][64] = reinterpret_cast<f32x4(*)[2][8][64]>(lds + kExchange);
+  float* all = reinterpret_cast<float*>(lds + kAll);
+  for (int64_t blk = blk0; blk < live; ++blk) {
+    const int par = blk & 1;
+    const int64_t t0 = blk * kBlk + quarter * kSub;
+    const int kv = kStageKV + ((par * 4 + quarter) * 2) * kTile;
+    Op<1> R[2][2];
+    Op<1> Vt[kVt];
+    Op<2> P[2];
+    float col[2];
+    {
+      const float lw = reinterpret_cast<const float*>(lds + kStageW + (par * 8 + quarter) * 256)[lane];
+      const Decay d = make_decay(log_w_here(lw, t0, len, lane), reinterpret_cast<double*>(lds + kSums) + wave * kSub, lane);
+      col[0] = d.col[0], col[1] = d.col[1];
+      Op<1> K[2][2];
+#pragma unroll
+      for (int J = 0; J < 2; ++J)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) K[J][hh] = staged(kv, J, hh), R[J][hh] = staged(kStageR + quarter * kTile, J, hh);
+      // what the 32 tokens add to the state: tiles (t, m) of sum_j k_j (left_j v_j)^T
+      const Op<1> v0 = staged(kv + kTile, 0, half), v1 = staged(kv + kTile, 1, half);
+      Op<3> Vs[kVt];
+#pragma unroll
+      for (int m = 0; m < kVt; ++m) {
+        f32x4 a0 = turned(v0, E, m), a1 = turned(v1, E, m);
+        Vt[m] = pack<1>(a0, a1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a0[i] *= d.row[0][i], a1[i] *= d.row[1][i];
+        Vs[m] = pack<3>(a0, a1);
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const Op<1> Kt = turned_op(K[0][t >> 1], K[1][t >> 1], E, t);
+#pragma unroll
+        for (int m = 0; m < kVt; ++m) exch[quarter][half][kVt * t + m][lane] = mma(Kt, Vs[m], zero4());
+      }
+      if (lane == 0 && half == 0) all[quarter] = d.all;
+      // the pairs inside the 32 tokens, as operands over the tokens j: column i
+      f32x4 a00 = zero4(), a01 = zero4(), a11 = zero4();
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
         a00 = mma(K[0][hh], R[0][hh], a00);
         a01 = mma(K[0][hh], R[1][hh], a01);
         a11 = mma(K[1][hh], R[1][hh], a11);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) a01[i] *= d.d01[i];
-      P[0] = pack<NO>(masked_j(a00, d.d00, lane), zero4());
-      P[1] = pack<NO>(a01, masked_j(a11, d.d11, lane));
+      P[0] = pack<2>(masked_j(a00, d.d00, lane), zero4());
+      P[1] = pack<2>(a01 * d.d01, masked_j(a11, d.d11, lane));
     }
-    if (wave < kWaves - 1) {
+    lds_barrier();
+    stage_r(blk + 1);  // what was staged for this block is in registers now
+    stage_kv(blk + 2);
+    // The states before each quarter's tokens: this wave takes its two tiles through them, and leaves each as two
+    // bfloat16 pieces where it found what the quarter adds (nobody else reads that).
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+    for (int w = 0; w < 4; ++w) {
+      const float a = all[w];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) added[wave][4 * t + u][lane] = S[t][u];
-    }
-    if (lane == 0) all[wave] = d.all;
-    __syncthreads();
-    f32x4 next[4][4];
-    const __amdgpu_buffer_rsrc_t* ybp = &yb;
+      for (int m = 0; m < kVt; ++m) {
+        f32x4* slot = exch[w][half][kVt * quarter + m];
+        const f32x4 add = slot[lane];
+        const Op<2> o = pack<2>(carry[m], zero4());
 #pragma unroll
-    for (int uu = 0; uu < 2; ++uu) {  // value tiles 2uu, 2uu + 1: eight values of a token at a time
-      f32x4 y[2][2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int u = 2 * uu + e;
-        f32x4 s[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          s[t] = carry[4 * t + u][lane];
-          for (int w = 0; w < wave; ++w) s[t] = s[t] * all[w] + added[w][4 * t + u][lane];
-          next[t][u] = s[t] * d.all + S[t][u];
-        }
-        const Op<NO> S0 = pack<NO>(s[0], s[1]), S1 = pack<NO>(s[2], s[3]);
-#pragma unroll
-        for (int I = 0; I < 2; ++I) {
-          f32x4 o = mma(S0, R[I][0], zero4());
-          o = mma(S1, R[I][1], o);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] *= d.col[I];
-          y[I][e] = mma(Vt[u], P[I], o);
-        }
+        for (int n = 0; n < 2; ++n)
+          reinterpret_cast<bf16x4*>(slot)[64 * n + lane] = __builtin_shufflevector(o.p[n], o.p[n], 0, 1, 2, 3);
+        carry[m] = fma4(carry[m], a, add);
       }
-#pragma unroll
-      for (int I = 0; I < 2; ++I)
-        store_pair<F32>(*ybp, yoff + I * 16 * row_bytes + uu * 32 * kEsz<F32>, y[I][0], y[I][1]);
     }
-    __syncthreads();  // every wave has read what was added and the carried state
-    if (wave == kWaves - 1) {
+    lds_barrier();
+    f32x4 y[2][kVt];
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+    for (int m = 0; m < kVt; ++m) {
+      Op<2> S[2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) carry[4 * t + u][lane] = next[t][u];
+      for (int kh = 0; kh < 2; ++kh)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const bf16x4 e0 = reinterpret_cast<const bf16x4*>(exch[quarter][half][kVt * (2 * kh) + m])[64 * n + lane];
+          const bf16x4 e1 = reinterpret_cast<const bf16x4*>(exch[quarter][half][kVt * (2 * kh + 1) + m])[64 * n + lane];
+          S[kh].p[n] = __builtin_shufflevector(e0, e1, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+#pragma unroll
+      for (int I = 0; I < 2; ++I) {
+        f32x4 o = mma(S[0], R[I][0], zero4());
+        o = mma(S[1], R[I][1], o);
+        y[I][m] = mma(Vt[m], P[I], o * col[I]);
+      }
     }
+    const __amdgpu_buffer_rsrc_t yb = token_buffer<2>(p.y, p.seq, b, h, t0, T - t0, kSub);
+#pragma unroll
+    for (int I = 0; I < 2; ++I)
+      store_pair<false>(yb, (16 * I + li) * row_bytes + 64 * half + 16 * q, y[I][0], y[I][1]);
+    // r of the next block, and k, v, log w of it (asked for a block ago), are there: behind them are five loads
+    // and two stores
+    asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
-  __syncthreads();
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to this workgroup's LDS when it ends
+  for (int64_t blk = live > blk0 ? live : blk0; blk < blk1; ++blk) {  // behind the sequence's end: zeros
+    const int64_t t0 = blk * kBlk + quarter * kSub;
+    const __amdgpu_buffer_rsrc_t yb = token_buffer<2>(p.y, p.seq, b, h, t0, T - t0, kSub);
+#pragma unroll
+    for (int I = 0; I < 2; ++I) store_pair<false>(yb, (16 * I + li) * row_bytes + 64 * half + 16 * q, zero4(), zero4());
+  }
   if (p.s_out && blk1 == nblk) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int tu = 4 * wave + m;
-      *reinterpret_cast<f32x4*>(p.s_out + (int64_t)unit * kN * kN + state_offset(tu >> 2, tu & 3, lane)) = carry[tu][lane];
-    }
+    for (int m = 0; m < kVt; ++m)
+      *reinterpret_cast<f32x4*>(p.s_out + (int64_t)unit * kN * kN + state_offset(quarter, kVt * half + m, lane)) = carry[m];
   }
 }
 
 template <bool F32>
 hipError_t launch_out(const LinattnCall& c) {
   OutParams p{};
-  p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.first = c.s_in, p.y = c.y, p.s_out = c.s_out;
+  p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.s_in = c.s_in, p.y = c.y, p.s_out = c.s_out;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
   p.nseg = 1;
   p.seg_blocks = (c.T + kBlk - 1) / kBlk;
   void* args[] = {&p};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out_kernel<F32>), dim3((uint32_t)(c.B * c.H)),
+  if constexpr (!F32) {
+    static const hipError_t a = hipFuncSetAttribute(reinterpret_cast<const void*>(&linattn_out16_kernel),
+                                                    hipFuncAttributeMaxDynamicSharedMemorySize, kOutLds);
+    if (a != hipSuccess) return a;
+    return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out16_kernel), dim3((uint32_t)(c.B * c.H)), dim3(512),
+                           args, kOutLds, c.stream);
+  }
+  return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out_kernel<F32>), dim3((uint32_t)(c.B * c.H * 2)),
                          dim3(64 * kWaves), args, 0, c.stream);
 }
 

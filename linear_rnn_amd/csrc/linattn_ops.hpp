@@ -39,6 +39,7 @@ namespace rwkv7 {
 namespace linattn {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -68,7 +69,17 @@ __device__ __forceinline__ f32x4 mma(const Op<NA>& a, const Op<NB>& b, f32x4 acc
   return acc;
 }
 
-// Elements i, i + 1 of an operand from two float32 values, in NP pieces.
+// a b + c with one rounding.
+__device__ __forceinline__ f32x4 fma4(f32x4 a, float b, f32x4 c) {
+  f32x4 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = fmaf(a[i], b, c[i]);
+  return o;
+}
+
+// Elements i, i + 1 of an operand from two float32 values, in NP pieces; the remainders are exact in float32.
+// (A remainder as one two-term dot product with (-1, 0), v_dot2c_f32_bf16, saves two of five instructions and
+// measured far slower: the prompt of B=4 T=16384 H=64 1160 us against 700.)
 template <int NP>
 __device__ __forceinline__ void put2(Op<NP>& o, int i, float x0, float x1) {
 #pragma unroll
@@ -106,6 +117,23 @@ __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t b, uint32_t off, 
   __builtin_amdgcn_raw_buffer_store_b128(x, b, off, 0, 0);
 }
 
+// The same descriptor as four scalar words, for the direct loads to LDS: 16 (or 4) bytes a lane, lane l's to
+// `lds` + 16 l (4 l), zeros from behind the end. vmcnt counts them and the caller waits for them.
+__device__ __forceinline__ u32x4 descriptor(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu)),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00027000u};
+}
+__device__ __forceinline__ void to_lds16(u32x4 b, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(off), "s"(b), "s"(lds)
+               : "memory");
+}
+__device__ __forceinline__ void to_lds4(u32x4 b, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(b), "s"(lds)
+               : "memory");
+}
+
 // One tensor's 32 tokens of one head, as loaded: [token tile][depth step].
 template <bool F32>
 struct Raw {
@@ -128,20 +156,24 @@ __device__ __forceinline__ void load_raw(Raw<F32>& o, __amdgpu_buffer_rsrc_t b, 
       for (int m = 0; m < (F32 ? 2 : 1); ++m)
         o.x[J][h][m] = load16(b, off + J * 16 * row_bytes + h * 32 * kEsz<F32> + 16 * m);
 }
+// The operand of a lane's eight channels as loaded.
 template <bool F32>
-__device__ __forceinline__ Op<kIn<F32>> natural(const Raw<F32>& r, int J, int h) {
+__device__ __forceinline__ Op<kIn<F32>> pieces(const u32x4 (&x)[F32 ? 2 : 1]) {
   Op<kIn<F32>> o;
   if constexpr (F32) {
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const u32x4 u = r.x[J][h][m];
-      put2(o, 4 * m, __uint_as_float(u[0]), __uint_as_float(u[1]));
-      put2(o, 4 * m + 2, __uint_as_float(u[2]), __uint_as_float(u[3]));
+      put2(o, 4 * m, __uint_as_float(x[m][0]), __uint_as_float(x[m][1]));
+      put2(o, 4 * m + 2, __uint_as_float(x[m][2]), __uint_as_float(x[m][3]));
     }
   } else {
-    o.p[0] = __builtin_bit_cast(bf16x8, r.x[J][h][0]);
+    o.p[0] = __builtin_bit_cast(bf16x8, x[0]);
   }
   return o;
+}
+template <bool F32>
+__device__ __forceinline__ Op<kIn<F32>> natural(const Raw<F32>& r, int J, int h) {
+  return pieces<F32>(r.x[J][h]);
 }
 // Element 4e + i of a lane's eight channels, as float32.
 template <bool F32>
@@ -303,14 +335,24 @@ __device__ __forceinline__ int64_t seq_len(const Seq& s, int64_t b) {
   const int64_t n = s.lens[b];
   return n < 0 ? 0 : n < s.T ? n : s.T;
 }
-// Descriptor of `n` tokens (at most kBlk) of a [B, T, H, 64] tensor from token t0 on, head h first.
+// `n` tokens (at most `most`) of a [B, T, H, 64] tensor from token t0 on, head h first: where they start, and the
+// bytes to the end of the last one's 64 channels.
+struct Span {
+  const char* base;
+  uint32_t bytes;
+};
+template <uint32_t ESZ>
+__device__ __forceinline__ Span token_span(const void* base, const Seq& s, int64_t b, int32_t h, int64_t t0, int64_t n,
+                                           int most) {
+  const int64_t left = n <= 0 ? 0 : n < most ? n : most;
+  return Span{static_cast<const char*>(base) + ((b * s.T + t0) * s.H + h) * (int64_t)(kN * ESZ),
+              left ? ((uint32_t)(left - 1) * s.H * kN + kN) * ESZ : 0};
+}
 template <uint32_t ESZ>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t token_buffer(const void* base, const Seq& s, int64_t b, int32_t h,
                                                                int64_t t0, int64_t n, int most) {
-  const int64_t left = n <= 0 ? 0 : n < most ? n : most;
-  // the last token's row ends 64 channels behind this head's start
-  const uint32_t bytes = left ? ((uint32_t)(left - 1) * s.H * kN + kN) * ESZ : 0;
-  return buffer(static_cast<const char*>(base) + ((b * s.T + t0) * s.H + h) * (int64_t)(kN * ESZ), bytes);
+  const Span x = token_span<ESZ>(base, s, b, h, t0, n, most);
+  return buffer(x.base, x.bytes);
 }
 // Where the segments of a sequence start from: `pieces` of them, each `blocks` blocks of kBlk tokens, in
 // the wave layout [unit][piece][16 tiles][64 lanes].
@@ -320,12 +362,23 @@ __device__ __forceinline__ f32x4* state_tile(void* states, int64_t index, int tu
 __device__ __forceinline__ const f32x4* state_tile(const void* states, int64_t index, int tu, int lane) {
   return static_cast<const f32x4*>(states) + (index * 16 + tu) * 64 + lane;
 }
-// log w of the token t0 + lane % 32; 0 (decay 1) behind the sequence's end.
+// log w of the tokens t0 + lane % 32: 0 (decay 1) behind the sequence's end for a decay of each token, by a
+// descriptor that ends with the sequence; a head's one decay is the same load with a stride of 0, so that there is
+// no branch around the load. log_w_here() takes out the tokens behind the end in both.
+__device__ __forceinline__ Span log_w_span(const float* log_w, bool per_token, const Seq& s, int64_t b, int32_t h,
+                                           int64_t t0, int64_t len) {
+  const int64_t left = len - t0 <= 0 ? 0 : len - t0 < kSub ? len - t0 : kSub;
+  return Span{reinterpret_cast<const char*>(log_w + (per_token ? (b * s.T + t0) * s.H + h : h)),
+              !left ? 0 : per_token ? ((uint32_t)(left - 1) * s.H + 1) * 4 : 4};
+}
 __device__ __forceinline__ float load_log_w(const float* log_w, bool per_token, const Seq& s, int64_t b, int32_t h,
                                             int64_t t0, int64_t len, int lane) {
-  const int64_t t = t0 + (lane & 31);
-  if (t >= len) return 0.f;
-  return per_token ? log_w[(b * s.T + t) * s.H + h] : log_w[h];
+  const Span x = log_w_span(log_w, per_token, s, b, h, t0, len);
+  return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer(x.base, x.bytes),
+                                                                        (lane & 31) * (per_token ? s.H * 4 : 0), 0, 0));
+}
+__device__ __forceinline__ float log_w_here(float loaded, int64_t t0, int64_t len, int lane) {
+  return t0 + (lane & 31) < len ? loaded : 0.f;
 }
 
 }  // namespace linattn

@@ -66,7 +66,7 @@ __global__ __launch_bounds__(256) void linattn_state_kernel(StateParams p) {
     Raw<F32> rk, rv;
     load_raw<F32>(rk, token_buffer<kEsz<F32>>(p.k, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
     load_raw<F32>(rv, token_buffer<kEsz<F32>>(p.v, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
-    const Decay d = make_decay(load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane), sums[wave], lane);
+    const Decay d = make_decay(log_w_here(load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane), t0, len, lane), sums[wave], lane);
     Op<3> Vs[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(256) void linattn_join_kernel(f32x4* total, const f
     f32x4* x = state_tile(total, at, tu, lane);
     const f32x4 add = *x;
     *x = s;
-    s = s * decay[at] + add;
+    s = fma4(s, decay[at], add);
   }
 }
 

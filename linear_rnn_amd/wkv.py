@@ -56,6 +56,8 @@ class Rwkv7Error(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load the HIP library (raises OSError if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -117,19 +119,36 @@ def _ptr(t):
     return None if t is None else (t.data_ptr() or None)
 
 
+# torch is imported at the first use (the library's own functions need none), and what every call asks of it is
+# kept here: a single-token step takes a few microseconds, and so would a handful of imports and lookups.
+class _Torch:
+    module = None
+
+    def __getattr__(self, name):
+        import torch
+        self.module = torch
+        self.Tensor = torch.Tensor
+        self.f32 = (torch.float32,)
+        self.inputs = (torch.bfloat16, torch.float32)
+        self.i32 = (torch.int32,)
+        self.codes = {torch.bfloat16: RWKV7_DTYPE_BF16, torch.float32: RWKV7_DTYPE_F32}
+        self.current_device = torch.cuda.current_device
+        # the current stream's handle of a device, without the stream object around it
+        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        return self.__dict__[name]
+
+
+_T = _Torch()
+
+
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return RWKV7_DTYPE_BF16
-    if t.dtype == torch.float32:
-        return RWKV7_DTYPE_F32
-    return -1
+    return _T.codes.get(t.dtype, -1)
 
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _T.raw_stream(_T.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -143,12 +162,15 @@ def _stream(stream):
 
 def _expect(t, name, shape, dtypes, like, optional=False):
     """Raise unless t is a contiguous, 16-byte aligned tensor of this shape and dtype on like's device."""
-    import torch
     if t is None:
         if optional:
             return
         raise ValueError("%s is required" % name)
-    if not isinstance(t, torch.Tensor):
+    if isinstance(t, _T.Tensor) and t.shape == shape and t.dtype in dtypes and t.is_contiguous() and \
+            not t.data_ptr() & 15 and t.device == like.device:
+        return
+    # something is wrong (or an empty tensor's address is odd, which does not matter): say what
+    if not isinstance(t, _T.Tensor):
         raise TypeError("%s must be a torch.Tensor, not %s" % (name, type(t).__name__))
     if tuple(t.shape) != tuple(shape):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
@@ -164,22 +186,19 @@ def _expect(t, name, shape, dtypes, like, optional=False):
 
 def _on_gpu(like, stream):
     """The tensors must be device memory of the device the kernels launch on."""
-    import torch
     if like.device.type != "cuda":
         raise ValueError("tensors must be on a HIP device (torch 'cuda'), got %s" % like.device)
-    if stream is None and like.device.index != torch.cuda.current_device():
+    if stream is None and like.device.index != _T.current_device():
         raise ValueError("tensors are on %s but the current device is cuda:%d; pass a stream of that device or "
-                         "select it" % (like.device, torch.cuda.current_device()))
+                         "select it" % (like.device, _T.current_device()))
 
 
 def _input_dtypes():
-    import torch
-    return (torch.bfloat16, torch.float32)
+    return _T.inputs
 
 
 def _f32():
-    import torch
-    return (torch.float32,)
+    return _T.f32
 
 
 def _args(r, w, k, v, a, b, state_in, y, state_out, stream=None, state_dtypes=None):
@@ -377,18 +396,16 @@ def rwkv7_stack_forward(w_in, w_out, vecs, x, states, stream=None):
 
 def _launch(fn, args, like, stream):
     """Call the library with `like`'s device current (a stream given by the caller may be another device's)."""
-    import torch
-    if like.device.index == torch.cuda.current_device():
+    if like.device.index == _T.current_device():
         _check(fn(*args, _stream(stream)))
     else:
-        with torch.cuda.device(like.device):
+        with _T.module.cuda.device(like.device):
             _check(fn(*args, _stream(stream)))
 
 
 def _decay_code(log_w, B, T, H) -> int:
     """Which of the two layouts log_w has."""
-    import torch
-    if not isinstance(log_w, torch.Tensor):
+    if not isinstance(log_w, _T.Tensor):
         raise TypeError("log_w must be a torch.Tensor, not %s" % type(log_w).__name__)
     if log_w.dim() not in (1, 3):
         raise ValueError("log_w has shape %s, expected (%d,) or (%d, %d, %d)" % (tuple(log_w.shape), H, B, T, H))
@@ -397,8 +414,7 @@ def _decay_code(log_w, B, T, H) -> int:
 
 def _linattn_inputs(r, log_w, k, v, state_in, lens):
     """Checks the inputs that the linear attention's calls share; returns (B, T, H, N, decay)."""
-    import torch
-    if not isinstance(r, torch.Tensor) or r.dim() != 4:
+    if not isinstance(r, _T.Tensor) or r.dim() != 4:
         raise ValueError("r must be a [B, T, H, N] tensor")
     B, T, H, N = r.shape
     _expect(r, "r", r.shape, _input_dtypes(), r)
@@ -407,7 +423,7 @@ def _linattn_inputs(r, log_w, k, v, state_in, lens):
     for name, t in (("k", k), ("v", v)):
         _expect(t, name, r.shape, (r.dtype,), r)
     _expect(state_in, "state_in", (B, H, N, N), _f32(), r, optional=True)
-    _expect(lens, "lens", (B,), (torch.int32,), r, optional=True)
+    _expect(lens, "lens", (B,), _T.i32, r, optional=True)
     return B, T, H, N, decay
 
 
@@ -484,8 +500,7 @@ def linattn_backward(r, log_w, k, v, dy, state_in=None, lens=None, dstate_out=No
 
 def _rows(x, groups):
     """x's rows and channels: the last dimension is normalised, in `groups` groups."""
-    import torch
-    if not isinstance(x, torch.Tensor) or x.dim() < 1:
+    if not isinstance(x, _T.Tensor) or x.dim() < 1:
         raise ValueError("x must be a tensor with the channels in its last dimension")
     _expect(x, "x", x.shape, _input_dtypes(), x)
     D, G = x.shape[-1], int(groups)
