@@ -43,9 +43,8 @@ struct GradParams {
   float* ds_in;  // may be null
   Seq seq;
   int32_t per_token;
-  int32_t nseg, pieces;
-  int64_t piece_blocks;
-  int32_t seg_pieces;
+  int32_t nseg;
+  int64_t pieces, seg_pieces;  // of a sequence, of a segment
 };
 
 // Sums over 32 lanes' values from each on (lane l and l + 32 alike), and of those before each.
@@ -95,10 +94,10 @@ __global__ __launch_bounds__(256, 1) void linattn_grad_kernel(GradParams p) {
   const int64_t T = p.seq.T, len = seq_len(p.seq, b);
   const uint32_t row_bytes = p.seq.H * kN * kEsz<F32>;
   const int64_t nblk = (T + kBlk - 1) / kBlk;
-  const int64_t blk0 = (int64_t)seg * p.seg_pieces * p.piece_blocks;
-  int64_t blk1 = blk0 + (int64_t)p.seg_pieces * p.piece_blocks;
+  const int64_t blk0 = seg * p.seg_pieces * kPieceBlocks;
+  int64_t blk1 = blk0 + p.seg_pieces * kPieceBlocks;
   if (blk1 > nblk) blk1 = nblk;
-  const int last_piece = (int)((blk1 - 1) / p.piece_blocks);
+  const int last_piece = (int)((blk1 - 1) / kPieceBlocks);
   const uint32_t off = li * row_bytes + q * 8 * kEsz<F32>;
   auto at = [&](const void* x, int64_t t0, int64_t n) { return token_buffer<kEsz<F32>>(x, p.seq, b, h, t0, n, kSub); };
 
@@ -259,8 +258,8 @@ __global__ __launch_bounds__(256, 1) void linattn_grad_kernel(GradParams p) {
     }
     __builtin_amdgcn_sched_barrier(0);
     {  // dr
-      const int64_t piece = blk / p.piece_blocks;
-      const bool marked = blk % p.piece_blocks != 0;
+      const int64_t piece = blk / kPieceBlocks;
+      const bool marked = blk % kPieceBlocks != 0;
       const float mark_decay = marked ? p.mark_decay[unit * nblk + blk] : 1.f;
       f32x4 dr[4][2];
 #pragma unroll
@@ -395,26 +394,21 @@ hipError_t launch_linattn_zero(float* dlog_w, int64_t H, hipStream_t stream) {
 }
 
 hipError_t launch_linattn_backward(const LinattnCall& c) {
-  const int64_t units = c.B * c.H, nblk = (c.T + kBlk - 1) / kBlk;
-  // Pieces: enough waves for the device (2048), of at least two blocks. Segments: a workgroup for each compute
-  // unit, of whole pieces.
-  int64_t pieces = (2048 + units - 1) / units;
-  if (pieces > nblk / 2) pieces = nblk / 2 > 0 ? nblk / 2 : 1;
-  const int64_t piece_blocks = (nblk + pieces - 1) / pieces;
-  pieces = (nblk + piece_blocks - 1) / piece_blocks;
-  int64_t nseg = 256 / units > 0 ? 256 / units : 1;
+  const int64_t units = c.B * c.H, nblk = linattn_blocks(c.T), pieces = linattn_pieces(c.T), cus = linattn_cus();
+  // Segments: a workgroup for each compute unit, of whole pieces.
+  int64_t nseg = cus / units > 0 ? cus / units : 1;
   if (nseg > pieces) nseg = pieces;
   const int64_t seg_pieces = (pieces + nseg - 1) / nseg;
   nseg = (pieces + seg_pieces - 1) / seg_pieces;
 
-  const bool states = pieces > 1, marks = piece_blocks > 1;
+  const bool marks = nblk > 1, states = marks;
   size_t need = 0;
   auto room = [&](size_t bytes) {
     const size_t at = need;
     need += (bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t o_states = room(states || marks ? units * pieces * kLinattnStateBytes : 0), o_decay = room(units * pieces * 4);
+  const size_t o_states = room(states ? units * pieces * kLinattnStateBytes : 0), o_decay = room(units * pieces * 4);
   const size_t o_marks = room(marks ? units * nblk * kLinattnStateBytes : 0), o_mdecay = room(marks ? units * nblk * 4 : 0);
   const size_t o_grads = room(nseg > 1 ? units * pieces * kLinattnStateBytes : 0);
   const size_t o_parts = room(c.per_token ? 0 : units * nseg * 4);
@@ -424,17 +418,17 @@ hipError_t launch_linattn_backward(const LinattnCall& c) {
   char* base = static_cast<char*>(ws);
 
   LinattnPieces q{};
-  q.pieces = (int32_t)pieces;
-  q.piece_blocks = piece_blocks;
+  q.pieces = pieces;
+  q.every = 1;
   q.decay = reinterpret_cast<float*>(base + o_decay);
   if (nseg > 1) {
     q.states = base + o_grads;
     e = launch_linattn_states(c, q, c.r, c.dy, true);
     if (e != hipSuccess) return e;
   }
-  if (states || marks) {
+  if (states) {
     q.states = base + o_states;
-    q.marks = marks ? base + o_marks : nullptr;
+    q.marks = base + o_marks;
     q.mark_decay = reinterpret_cast<float*>(base + o_mdecay);
     e = launch_linattn_states(c, q, c.k, c.v, false);
     if (e != hipSuccess) return e;
@@ -449,7 +443,7 @@ hipError_t launch_linattn_backward(const LinattnCall& c) {
   p.dr = c.dr, p.dlog_w = c.per_token ? c.dlog_w : parts, p.dk = c.dk, p.dv = c.dv, p.ds_in = c.ds_in;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
-  p.nseg = (int32_t)nseg, p.pieces = (int32_t)pieces, p.piece_blocks = piece_blocks, p.seg_pieces = (int32_t)seg_pieces;
+  p.nseg = (int32_t)nseg, p.pieces = pieces, p.seg_pieces = seg_pieces;
   const void* fn = c.f32 ? reinterpret_cast<const void*>(&linattn_grad_kernel<true>)
                          : reinterpret_cast<const void*>(&linattn_grad_kernel<false>);
   static const hipError_t a0 = hipFuncSetAttribute(reinterpret_cast<const void*>(&linattn_grad_kernel<true>),

@@ -1,7 +1,10 @@
 // Linear attention with a decay for each head: whole prompts and single tokens.
 // The chunk algebra and its number formats are in linattn_ops.hpp.
+#include <atomic>
+
 #include "linattn_internal.hpp"
 #include "linattn_ops.hpp"
+#include "wkv7_internal.hpp"
 
 namespace rwkv7 {
 namespace {
@@ -13,7 +16,7 @@ struct OutParams {
   const float* log_w;
   const void* k;
   const void* v;
-  const f32x4* states;  // [units][nseg] states before the segments (nseg > 1)
+  const f32x4* states;  // [units][pieces] states, the first nseg those before the segments (nseg > 1)
   const float* s_in;    // the caller's state (nseg == 1), may be null
   void* y;
   float* s_out;  // may be null
@@ -21,6 +24,7 @@ struct OutParams {
   int32_t per_token;
   int32_t nseg;        // segments of a sequence
   int64_t seg_blocks;  // blocks of kBlk tokens in a segment
+  int64_t pieces;
 };
 
 // A workgroup carries 32 of the state's 64 value rows (two tiles) over one segment of one head, 128 tokens at a
@@ -78,7 +82,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void linattn_out_kernel(OutParams
   for (int m = 0; m < kVt; ++m) {
     carry[m] = zero4();
     if (p.nseg > 1)
-      carry[m] = *state_tile(p.states, (int64_t)unit * p.nseg + seg, 4 * wave + kVt * half + m, lane);
+      carry[m] = *state_tile(p.states, (int64_t)unit * p.pieces + seg, 4 * wave + kVt * half + m, lane);
     else if (p.s_in)
       carry[m] = *reinterpret_cast<const f32x4*>(p.s_in + (int64_t)unit * kN * kN + state_offset(wave, kVt * half + m, lane));
   }
@@ -183,17 +187,24 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void linattn_out_kernel(OutParams
 // asked for once: a stream of this layout (three tensors read, one written, a workgroup a head) measured 4.9 TB/s
 // in whole rows without temporal hint and consecutive workgroups on consecutive dies, 4.3 with an L2-friendly
 // numbering, and 3.2 where two workgroups a head loaded 64-byte pieces in operand order. So the rows go to LDS by
-// direct loads, up to two blocks ahead, their 16-byte pieces exchanged within a row so that the
-// operand reads of 16 rows fall into different banks.
+// direct loads, a block ahead (into the same place, as soon as every wave has taken its operands into registers),
+// their 16-byte pieces exchanged within a row so that the operand reads of 16 rows fall into different banks.
+//
+// What is common to the two waves of a quarter, the decay factors of its tokens, one of them leaves in LDS during
+// the block before (once, if the head has one decay and the tokens are all there).
 constexpr int kRow = kN * 2;              // bytes of a token's row
 constexpr int kTile = kSub * kRow;        // bytes of a quarter's rows of one tensor
 constexpr int kExchange = 0;              // [quarter][half][8 tiles][64 lanes] 16 bytes
-constexpr int kStageKV = 64 << 10;        // [parity][quarter][k, v] kTile
-constexpr int kStageR = kStageKV + 16 * kTile;      // [quarter] kTile
-constexpr int kStageW = kStageR + 4 * kTile;        // [parity][wave][64] float
-constexpr int kSums = kStageW + 2 * 8 * 256;        // [wave][32] double
-constexpr int kAll = kSums + 8 * kSub * 8;          // [quarter] float
-constexpr int kOutLds = kAll + 16;
+constexpr int kStage = 64 << 10;          // [quarter][r, k, v] kTile
+constexpr int kStageW = kStage + 12 * kTile;       // [block % 4][quarter][32] float
+constexpr int kFactors = kStageW + 16 * kSub * 4;  // [quarter] Factors
+struct Factors {
+  f32x4 d[3][64];     // D tiles (0, 0), (0, 1), (1, 1) in the layout of Decay::d00
+  float left[kSub];   // exp(c_31 - c)
+  float in[kSub];     // exp(c)
+  float all, unused[3];
+};
+constexpr int kOutLds = kFactors + 4 * sizeof(Factors);
 static_assert(kOutLds <= 160 * 1024, "LDS of a compute unit");
 
 __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
@@ -217,23 +228,31 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
   const int row = 16 * half + (lane >> 3);
   const uint32_t src0 = row * row_bytes + 16 * ((lane & 7) ^ (row >> 1 & 7));
   const uint32_t src1 = src0 + 8 * row_bytes + 16 * (((lane & 7) ^ ((row + 8) >> 1 & 7)) - ((lane & 7) ^ (row >> 1 & 7)));
-  auto stage = [&](const void* x, int64_t blk, uint32_t to) {
-    const int64_t t0 = blk * kBlk + quarter * kSub;
-    const Span span = token_span<2>(x, p.seq, b, h, t0, len - t0, kSub);
-    const u32x4 r = descriptor(span.base, span.bytes);
-    to_lds16(r, src0, lds0 + to + 16 * half * kRow);
-    to_lds16(r, src1, lds0 + to + (16 * half + 8) * kRow);
+  const int64_t first = blk0 * kBlk + quarter * kSub, start = ((b * T + first) * p.seq.H + h) * kRow;
+  const char *next_r = static_cast<const char*>(p.r) + start, *next_k = static_cast<const char*>(p.k) + start,
+             *next_v = static_cast<const char*>(p.v) + start;
+  int64_t left = len - first;  // tokens from the next staged one on
+  const uint32_t to0 = lds0 + kStage + quarter * 3 * kTile + 16 * half * kRow;
+  auto stage_rkv = [&]() {
+    const uint32_t bytes = left <= 0 ? 0 : (uint32_t)((left < kSub ? left : kSub) - 1) * row_bytes + kRow;
+    const u32x4 k = descriptor(next_k, bytes), v = descriptor(next_v, bytes), r = descriptor(next_r, bytes);
+    to_lds16(k, src0, to0 + kTile);
+    to_lds16(k, src1, to0 + kTile + 8 * kRow);
+    to_lds16(v, src0, to0 + 2 * kTile);
+    to_lds16(v, src1, to0 + 2 * kTile + 8 * kRow);
+    to_lds16(r, src0, to0);
+    to_lds16(r, src1, to0 + 8 * kRow);
+    const int64_t step = (int64_t)kBlk * row_bytes;
+    next_r += step, next_k += step, next_v += step, left -= kBlk;
   };
-  auto stage_kv = [&](int64_t blk) {
-    const int par = blk & 1;
-    stage(p.k, blk, kStageKV + ((par * 4 + quarter) * 2) * kTile);
-    stage(p.v, blk, kStageKV + ((par * 4 + quarter) * 2 + 1) * kTile);
-    const int64_t t0 = blk * kBlk + quarter * kSub;
-    const Span span = log_w_span(p.log_w, p.per_token, p.seq, b, h, t0, len);
-    to_lds4(descriptor(span.base, half ? 0 : span.bytes), (lane & 31) * (p.per_token ? p.seq.H * 4 : 0),
-            lds0 + kStageW + (par * 8 + wave) * 256);
+  auto stage_w = [&](int64_t blk) {
+    if (half == 1 && lane < kSub) {
+      const Span span = log_w_span(p.log_w, p.per_token, p.seq, b, h, blk * kBlk + quarter * kSub, len);
+      to_lds4(descriptor(span.base, span.bytes), lane * (p.per_token ? p.seq.H * 4 : 0),
+              lds0 + kStageW + ((blk & 3) * 4 + quarter) * kSub * 4);
+    }
   };
-  auto stage_r = [&](int64_t blk) { stage(p.r, blk, kStageR + quarter * kTile); };
+  const int rows_r = kStage + quarter * 3 * kTile, rows_k = rows_r + kTile, rows_v = rows_k + kTile;
   // operand of the rows 16J + li, channels 32hh + 8q ..
   const int li = lane & 15, q = lane >> 4;
   auto staged = [&](int from, int J, int hh) {
@@ -246,42 +265,61 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
   for (int m = 0; m < kVt; ++m) {
     carry[m] = zero4();
     if (p.nseg > 1)
-      carry[m] = *state_tile(p.states, (int64_t)unit * p.nseg + seg, 4 * quarter + kVt * half + m, lane);
+      carry[m] = *state_tile(p.states, (int64_t)unit * p.pieces + seg, 4 * quarter + kVt * half + m, lane);
     else if (p.s_in)
       carry[m] = *reinterpret_cast<const f32x4*>(p.s_in + (int64_t)unit * kN * kN + state_offset(quarter, kVt * half + m, lane));
   }
   const Turn E = make_turn(lane);
-  if (blk0 < live) stage_r(blk0), stage_kv(blk0), stage_kv(blk0 + 1);
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   f32x4(*exch)[2][8][64] = reinterpret_cast<f32x4(*)[2][8][64]>(lds + kExchange);
-  float* all = reinterpret_cast<float*>(lds + kAll);
+  Factors* factors = reinterpret_cast<Factors*>(lds + kFactors);
+  // The factors of a block's quarter, by its second wave, which has its exchange slot to itself then.
+  auto fill = [&](int64_t blk) {
+    const float lw = reinterpret_cast<const float*>(lds + kStageW)[((blk & 3) * 4 + quarter) * kSub + (lane & 31)];
+    const Decay d = make_decay(log_w_here(lw, blk * kBlk + quarter * kSub, len, lane),
+                               reinterpret_cast<double*>(exch[quarter][1]), lane);
+    Factors& f = factors[quarter];
+    f.d[0][lane] = d.d00, f.d[1][lane] = d.d01, f.d[2][lane] = d.d11;
+    if ((lane & 15) == 0)
+#pragma unroll
+      for (int J = 0; J < 2; ++J)
+        *reinterpret_cast<f32x4*>(f.left + 16 * J + (lane >> 2)) = f32x4{d.row[J][0], d.row[J][1], d.row[J][2], d.row[J][3]};
+    if (lane < 16) f.in[lane] = d.col[0], f.in[16 + lane] = d.col[1];
+    if (lane == 0) f.all = d.all;
+  };
+  if (blk0 < live) {
+    stage_w(blk0), stage_w(blk0 + 1), stage_w(blk0 + 2);
+    stage_rkv();
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if (half == 1) fill(blk0);
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   for (int64_t blk = blk0; blk < live; ++blk) {
-    const int par = blk & 1;
     const int64_t t0 = blk * kBlk + quarter * kSub;
-    const int kv = kStageKV + ((par * 4 + quarter) * 2) * kTile;
+    const Factors& f = factors[quarter];
     Op<1> R[2][2];
-    Op<1> Vt[kVt];
-    Op<2> P[2];
-    float col[2];
+    f32x4 y[2][kVt];
+    float in[2];
     {
-      const float lw = reinterpret_cast<const float*>(lds + kStageW + (par * 8 + quarter) * 256)[lane];
-      const Decay d = make_decay(log_w_here(lw, t0, len, lane), reinterpret_cast<double*>(lds + kSums) + wave * kSub, lane);
-      col[0] = d.col[0], col[1] = d.col[1];
       Op<1> K[2][2];
 #pragma unroll
       for (int J = 0; J < 2; ++J)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) K[J][hh] = staged(kv, J, hh), R[J][hh] = staged(kStageR + quarter * kTile, J, hh);
+        for (int hh = 0; hh < 2; ++hh) K[J][hh] = staged(rows_k, J, hh), R[J][hh] = staged(rows_r, J, hh);
+      const Op<1> v0 = staged(rows_v, 0, half), v1 = staged(rows_v, 1, half);
+      lds_barrier();  // both waves of every quarter have their operands
+      stage_w(blk + 3);
+      stage_rkv();
+      const f32x4 left0 = *reinterpret_cast<const f32x4*>(f.left + 4 * q);
+      const f32x4 left1 = *reinterpret_cast<const f32x4*>(f.left + 16 + 4 * q);
+      in[0] = f.in[li], in[1] = f.in[16 + li];
       // what the 32 tokens add to the state: tiles (t, m) of sum_j k_j (left_j v_j)^T
-      const Op<1> v0 = staged(kv + kTile, 0, half), v1 = staged(kv + kTile, 1, half);
+      Op<1> Vt[kVt];
       Op<3> Vs[kVt];
 #pragma unroll
       for (int m = 0; m < kVt; ++m) {
-        f32x4 a0 = turned(v0, E, m), a1 = turned(v1, E, m);
+        const f32x4 a0 = turned(v0, E, m), a1 = turned(v1, E, m);
         Vt[m] = pack<1>(a0, a1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a0[i] *= d.row[0][i], a1[i] *= d.row[1][i];
-        Vs[m] = pack<3>(a0, a1);
+        Vs[m] = pack<3>(a0 * left0, a1 * left1);
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -289,8 +327,7 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
 #pragma unroll
         for (int m = 0; m < kVt; ++m) exch[quarter][half][kVt * t + m][lane] = mma(Kt, Vs[m], zero4());
       }
-      if (lane == 0 && half == 0) all[quarter] = d.all;
-      // the pairs inside the 32 tokens, as operands over the tokens j: column i
+      // the pairs inside the 32 tokens
       f32x4 a00 = zero4(), a01 = zero4(), a11 = zero4();
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -298,30 +335,34 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
         a01 = mma(K[0][hh], R[1][hh], a01);
         a11 = mma(K[1][hh], R[1][hh], a11);
       }
-      P[0] = pack<2>(masked_j(a00, d.d00, lane), zero4());
-      P[1] = pack<2>(a01 * d.d01, masked_j(a11, d.d11, lane));
+      const Op<2> P0 = pack<2>(masked_j(a00, f.d[0][lane], lane), zero4());
+      const Op<2> P1 = pack<2>(a01 * f.d[1][lane], masked_j(a11, f.d[2][lane], lane));
+#pragma unroll
+      for (int m = 0; m < kVt; ++m) y[0][m] = mma(Vt[m], P0, zero4()), y[1][m] = mma(Vt[m], P1, zero4());
     }
     lds_barrier();
-    stage_r(blk + 1);  // what was staged for this block is in registers now
-    stage_kv(blk + 2);
     // The states before each quarter's tokens: this wave takes its two tiles through them, and leaves each as two
     // bfloat16 pieces where it found what the quarter adds (nobody else reads that).
+    f32x4 add[4][kVt];
+    float all[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-      const float a = all[w];
+      all[w] = factors[w].all;
+#pragma unroll
+      for (int m = 0; m < kVt; ++m) add[w][m] = exch[w][half][kVt * quarter + m][lane];
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
 #pragma unroll
       for (int m = 0; m < kVt; ++m) {
-        f32x4* slot = exch[w][half][kVt * quarter + m];
-        const f32x4 add = slot[lane];
         const Op<2> o = pack<2>(carry[m], zero4());
 #pragma unroll
         for (int n = 0; n < 2; ++n)
-          reinterpret_cast<bf16x4*>(slot)[64 * n + lane] = __builtin_shufflevector(o.p[n], o.p[n], 0, 1, 2, 3);
-        carry[m] = fma4(carry[m], a, add);
+          reinterpret_cast<bf16x4*>(exch[w][half][kVt * quarter + m])[64 * n + lane] =
+              __builtin_shufflevector(o.p[n], o.p[n], 0, 1, 2, 3);
+        carry[m] = fma4(carry[m], all[w], add[w][m]);
       }
-    }
     lds_barrier();
-    f32x4 y[2][kVt];
 #pragma unroll
     for (int m = 0; m < kVt; ++m) {
       Op<2> S[2];
@@ -334,19 +375,15 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
           S[kh].p[n] = __builtin_shufflevector(e0, e1, 0, 1, 2, 3, 4, 5, 6, 7);
         }
 #pragma unroll
-      for (int I = 0; I < 2; ++I) {
-        f32x4 o = mma(S[0], R[I][0], zero4());
-        o = mma(S[1], R[I][1], o);
-        y[I][m] = mma(Vt[m], P[I], o * col[I]);
-      }
+      for (int I = 0; I < 2; ++I) y[I][m] = fma4(mma(S[1], R[I][1], mma(S[0], R[I][0], zero4())), in[I], y[I][m]);
     }
     const __amdgpu_buffer_rsrc_t yb = token_buffer<2>(p.y, p.seq, b, h, t0, T - t0, kSub);
 #pragma unroll
     for (int I = 0; I < 2; ++I)
       store_pair<false>(yb, (16 * I + li) * row_bytes + 64 * half + 16 * q, y[I][0], y[I][1]);
-    // r of the next block, and k, v, log w of it (asked for a block ago), are there: behind them are five loads
-    // and two stores
-    asm volatile("s_waitcnt vmcnt(7) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (half == 1 && blk + 1 < live && (p.per_token || t0 + kBlk + kSub > len)) fill(blk + 1);
+    // the next block's rows are there (and log w of three blocks): behind them are two stores
+    asm volatile("s_waitcnt vmcnt(2) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to this workgroup's LDS when it ends
   for (int64_t blk = live > blk0 ? live : blk0; blk < blk1; ++blk) {  // behind the sequence's end: zeros
@@ -362,23 +399,62 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
   }
 }
 
+// The segments of a sequence. A workgroup (float32: two) a head and segment, one at a time on a compute unit; a block
+// of 128 tokens takes it 3.5 us (float32: 5), so a call of few heads, or of a few more than a round of the
+// compute units takes, ends sooner in segments: each in its own workgroup, from the state that the pieces before
+// it add up to. Those cost another pass over k and v and two more launches: about 12 us, and 128 tokens of all heads
+// at 4 TB/s. `segments` weighs the two.
+int64_t segments(int64_t units, int64_t blocks, bool f32, int64_t* piece_count) {
+  const int64_t cus = linattn_cus(), pieces = (blocks + kPieceBlocks - 1) / kPieceBlocks;
+  const double block_us = f32 ? 5.0 : 3.5, groups = f32 ? 2.0 : 1.0;
+  int64_t best_every = pieces;
+  double best = 0;
+  for (int64_t every = pieces; every >= 1; every = every > 1 ? (every + 1) / 2 : 0) {
+    const int64_t nseg = (pieces + every - 1) / every;
+    const int64_t rounds = ((int64_t)(units * nseg * groups) + cus - 1) / cus;
+    const double length = (double)(every * kPieceBlocks < blocks ? every * kPieceBlocks : blocks);
+    double us = rounds * (length * block_us + 2.0);
+    if (nseg > 1) us += 12.0 + (double)units * blocks * kBlk * (f32 ? 512 : 256) / 4e6;
+    if (every == pieces || us < best) best = us, best_every = every;
+    if (every == 1) break;
+  }
+  *piece_count = pieces;
+  return best_every;
+}
+
 template <bool F32>
 hipError_t launch_out(const LinattnCall& c) {
+  const int64_t units = c.B * c.H, blocks = linattn_blocks(c.T);
   OutParams p{};
   p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.s_in = c.s_in, p.y = c.y, p.s_out = c.s_out;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
-  p.nseg = 1;
-  p.seg_blocks = (c.T + kBlk - 1) / kBlk;
+  const int64_t every = segments(units, blocks, F32, &p.pieces);
+  p.nseg = (int32_t)((p.pieces + every - 1) / every);
+  p.seg_blocks = p.nseg > 1 ? every * kPieceBlocks : blocks;
+  if (p.nseg > 1) {
+    const size_t states = (size_t)units * p.pieces * kLinattnStateBytes;
+    void* ws = nullptr;
+    hipError_t e = device_workspace(c.stream, states + units * p.pieces * 4, &ws, kWorkspaceOperators);
+    if (e != hipSuccess) return e;
+    LinattnPieces q{};
+    q.pieces = p.pieces;
+    q.every = (int32_t)every;
+    q.states = ws;
+    q.decay = reinterpret_cast<float*>(static_cast<char*>(ws) + states);
+    e = launch_linattn_states(c, q, c.k, c.v, false);
+    if (e != hipSuccess) return e;
+    p.states = static_cast<const f32x4*>(ws);
+  }
   void* args[] = {&p};
   if constexpr (!F32) {
     static const hipError_t a = hipFuncSetAttribute(reinterpret_cast<const void*>(&linattn_out16_kernel),
                                                     hipFuncAttributeMaxDynamicSharedMemorySize, kOutLds);
     if (a != hipSuccess) return a;
-    return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out16_kernel), dim3((uint32_t)(c.B * c.H)), dim3(512),
-                           args, kOutLds, c.stream);
+    return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out16_kernel), dim3((uint32_t)(units * p.nseg)),
+                           dim3(512), args, kOutLds, c.stream);
   }
-  return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out_kernel<F32>), dim3((uint32_t)(c.B * c.H * 2)),
+  return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out_kernel<F32>), dim3((uint32_t)(units * p.nseg * 2)),
                          dim3(64 * kWaves), args, 0, c.stream);
 }
 
@@ -449,6 +525,17 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(StepParams p) {
 }
 
 }  // namespace
+
+int64_t linattn_cus() {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> cached[kMaxDevices];
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) return 256;
+  cus = cached[dev].load(std::memory_order_relaxed);
+  if (cus == 0 && hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && cus > 0)
+    cached[dev].store(cus, std::memory_order_relaxed);
+  return cus > 0 ? cus : 256;
+}
 
 hipError_t launch_linattn(const LinattnCall& c) { return c.f32 ? launch_out<true>(c) : launch_out<false>(c); }
 

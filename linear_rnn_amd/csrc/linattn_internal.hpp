@@ -37,19 +37,23 @@ hipError_t launch_linattn_zero(float* dlog_w, int64_t H, hipStream_t stream);
 constexpr int64_t kLinattnBlock = 128;              // tokens a workgroup takes at a time
 constexpr int64_t kLinattnStateBytes = 64 * 64 * 4;  // one state
 
-// Pieces of every sequence: `pieces` of `piece_blocks` blocks (the last may have fewer), and the device memory
-// for the states at their starts.
+// Every sequence in pieces of kPieceBlocks blocks, and the device memory for the states at their starts.
+constexpr int64_t kPieceBlocks = 4;
+inline int64_t linattn_blocks(int64_t T) { return (T + kLinattnBlock - 1) / kLinattnBlock; }
+inline int64_t linattn_pieces(int64_t T) { return (linattn_blocks(T) + kPieceBlocks - 1) / kPieceBlocks; }
 struct LinattnPieces {
-  int32_t pieces;
-  int64_t piece_blocks;
-  void* states;       // [units][pieces] states
+  int64_t pieces;
+  int32_t every;      // keep the state before every every-th piece
+  void* states;       // [units][pieces] states; the kept ones come first in a sequence's
   float* decay;       // [units][pieces]
   void* marks;        // may be null; [units][blocks] states
   float* mark_decay;  // [units][blocks]
 };
-// states <- the state before each piece (reverse: its gradient behind each), and, if asked for, the sums of each
-// piece before each of its blocks but the first.
+// states <- the state before each every-th piece (reverse: its gradient behind each), and, if asked for, the sums of
+// each piece before each of its blocks but the first.
 hipError_t launch_linattn_states(const LinattnCall& c, const LinattnPieces& q, const void* keys, const void* values,
                                  bool reverse);
+// Compute units of the current device (256 if it cannot be asked).
+int64_t linattn_cus();
 
 }  // namespace rwkv7

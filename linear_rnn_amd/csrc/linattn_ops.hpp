@@ -126,11 +126,11 @@ __device__ __forceinline__ u32x4 descriptor(const void* base, uint32_t bytes) {
                (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00027000u};
 }
 __device__ __forceinline__ void to_lds16(u32x4 b, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(off), "s"(b), "s"(lds)
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
                : "memory");
 }
 __device__ __forceinline__ void to_lds4(u32x4 b, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(b), "s"(lds)
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
                : "memory");
 }
 

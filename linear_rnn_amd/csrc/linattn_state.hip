@@ -2,9 +2,11 @@
 // linear attention spreads one sequence over the device, and where its backward gets the states from.
 //
 // The state after a piece is (the piece's decay) (the state before) + (what the piece adds), so the pieces
-// are independent until a short scan over their sums. A wave takes a whole piece, 32 tokens at a time, with
-// the sum in registers; nothing is shared, no barriers. The gradient G = dL/dS of the reverse pass has the
-// same form with (r, dy) in place of (k, v), running backwards.
+// are independent until a short scan over their sums. A workgroup takes a piece of four blocks, each of its waves
+// one block of 128 tokens, 32 at a time from the last to the first: a token's factor is then the decay to
+// the block's end, known when the token is met, and the sum stays in the matrix products' accumulators. The
+// gradient G = dL/dS of the reverse pass has the same form with (r, dy) in place of (k, v), a token's factor being
+// the decay from the block's start.
 #include "linattn_internal.hpp"
 #include "linattn_ops.hpp"
 
@@ -23,29 +25,24 @@ struct StateParams {
   float* mark_decay;  // [units][blocks]: the decay since the piece's start
   Seq seq;
   int32_t per_token;
-  int32_t pieces;
-  int64_t piece_blocks;
-  int64_t units;
+  int64_t pieces;
 };
 
 template <bool F32, bool REV>
-__global__ __launch_bounds__(256) void linattn_state_kernel(StateParams p) {
+__global__ __launch_bounds__(256, 2) void linattn_state_kernel(StateParams p) {
   constexpr int NI = kIn<F32>;
-  __shared__ double sums[4][kSub];
+  __shared__ f32x4 sum[kWaves][16][64];
+  __shared__ double sums[kWaves][kSub];
+  __shared__ float all[kWaves];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t id = (int64_t)xcd_swizzle(blockIdx.x, gridDim.x) * 4 + wave;
-  const int64_t unit = id / p.pieces, piece = id % p.pieces;
-  if (unit >= p.units) return;
+  const int64_t unit = blockIdx.x / p.pieces, piece = blockIdx.x % p.pieces;
   const int64_t b = unit / p.seq.H;
   const int32_t h = unit % p.seq.H;
   const int64_t len = seq_len(p.seq, b);
   const uint32_t row_bytes = p.seq.H * kN * kEsz<F32>;
   const int64_t nblk = (p.seq.T + kBlk - 1) / kBlk;
-  const int64_t first = piece * p.piece_blocks * kBlk;
-  int64_t end = first + p.piece_blocks * kBlk;
-  if (end > len) end = len;
-  const int64_t subs = end > first ? (end - first + kSub - 1) / kSub : 0;
+  const int64_t blk = piece * kPieceBlocks + wave;
   const Turn E = make_turn(lane);
   f32x4 S[4][4];
 #pragma unroll
@@ -53,61 +50,92 @@ __global__ __launch_bounds__(256) void linattn_state_kernel(StateParams p) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) S[t][u] = zero4();
   float decay = 1.f;
-  for (int64_t n = 0; n < subs; ++n) {
-    const int64_t t0 = first + (REV ? subs - 1 - n : n) * kSub;
-    if (!REV && p.marks && n > 0 && n % kWaves == 0) {
-      const int64_t at = unit * nblk + t0 / kBlk;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int u = 0; u < 4; ++u) *state_tile(p.marks, at, 4 * t + u, lane) = S[t][u];
-      if (lane == 0) p.mark_decay[at] = decay;
-    }
+  const int64_t left = len - blk * kBlk;
+  const int subs = left <= 0 ? 0 : left >= kBlk ? kBlk / kSub : (int)((left + kSub - 1) / kSub);
+#pragma clang loop unroll(disable)
+  for (int n = 0; n < subs; ++n) {
+    const int64_t t0 = blk * kBlk + (REV ? n : subs - 1 - n) * kSub;
     Raw<F32> rk, rv;
-    load_raw<F32>(rk, token_buffer<kEsz<F32>>(p.k, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
     load_raw<F32>(rv, token_buffer<kEsz<F32>>(p.v, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
+    load_raw<F32>(rk, token_buffer<kEsz<F32>>(p.k, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
     const Decay d = make_decay(log_w_here(load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane), t0, len, lane), sums[wave], lane);
+    float f[2][4];
+#pragma unroll
+    for (int J = 0; J < 2; ++J)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[J][i] = (REV ? d.inrow[J][i] : d.row[J][i]) * decay;
     Op<3> Vs[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       f32x4 a0 = turned(natural<F32>(rv, 0, u >> 1), E, u), a1 = turned(natural<F32>(rv, 1, u >> 1), E, u);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a0[i] *= REV ? d.inrow[0][i] : d.row[0][i];
-        a1[i] *= REV ? d.inrow[1][i] : d.row[1][i];
-      }
+      for (int i = 0; i < 4; ++i) a0[i] *= f[0][i], a1[i] *= f[1][i];
       Vs[u] = pack<3>(a0, a1);
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const Op<NI> Kt = turned_op(natural<F32>(rk, 0, t >> 1), natural<F32>(rk, 1, t >> 1), E, t);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) S[t][u] = mma(Kt, Vs[u], S[t][u] * d.all);
+      for (int u = 0; u < 4; ++u) S[t][u] = mma(Kt, Vs[u], S[t][u]);
     }
     decay *= d.all;
   }
 #pragma unroll
   for (int t = 0; t < 4; ++t)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) *state_tile(p.total, unit * p.pieces + piece, 4 * t + u, lane) = S[t][u];
-  if (lane == 0) p.decay[unit * p.pieces + piece] = decay;
+    for (int u = 0; u < 4; ++u) sum[wave][4 * t + u][lane] = S[t][u];
+  if (lane == 0) all[wave] = decay;
+  __syncthreads();
+  // the four blocks one after the other: a quarter of the tiles each
+  f32x4 s[4];
+#pragma unroll
+  for (int m = 0; m < 4; ++m) s[m] = zero4();
+  float since = 1.f;
+#pragma unroll
+  for (int n = 0; n < kWaves; ++n) {
+    const int w = REV ? kWaves - 1 - n : n;
+    const int64_t at = unit * nblk + piece * kPieceBlocks + w;
+    if (!REV && p.marks && w > 0 && piece * kPieceBlocks + w < nblk) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) *state_tile(p.marks, at, 4 * wave + m, lane) = s[m];
+      if (threadIdx.x == 0) p.mark_decay[at] = since;
+    }
+    const float a = all[w];
+    since *= a;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) s[m] = fma4(s[m], a, sum[w][4 * wave + m][lane]);
+  }
+#pragma unroll
+  for (int m = 0; m < 4; ++m) *state_tile(p.total, unit * p.pieces + piece, 4 * wave + m, lane) = s[m];
+  if (threadIdx.x == 0) p.decay[unit * p.pieces + piece] = since;
 }
 
-// total[piece] <- the state before the piece (backwards: the gradient behind it), from `start` before the first
-// (behind the last). A thread four elements of one head's state.
+// states[piece / every] <- the state before every every-th piece (backwards: the gradient behind each piece, in place),
+// from `start` before the first (behind the last). A thread four elements of one head's state; eight loads at a time.
 template <bool REV>
 __global__ __launch_bounds__(256) void linattn_join_kernel(f32x4* total, const float* decay, const float* start,
-                                                           int32_t pieces) {
+                                                           int64_t pieces, int32_t every) {
+  constexpr int kAhead = 8;
   const int64_t unit = blockIdx.x / 4;
   const int tu = (blockIdx.x % 4) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   f32x4 s = start ? *reinterpret_cast<const f32x4*>(start + unit * kN * kN + state_offset(tu >> 2, tu & 3, lane)) : zero4();
-#pragma unroll 4
-  for (int n = 0; n < pieces; ++n) {
-    const int64_t at = unit * pieces + (REV ? pieces - 1 - n : n);
-    f32x4* x = state_tile(total, at, tu, lane);
-    const f32x4 add = *x;
-    *x = s;
-    s = fma4(s, decay[at], add);
+  for (int64_t n0 = 0; n0 < pieces; n0 += kAhead) {
+    f32x4 add[kAhead];
+    float a[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t n = n0 + i < pieces ? n0 + i : pieces - 1, at = unit * pieces + (REV ? pieces - 1 - n : n);
+      add[i] = *state_tile(total, at, tu, lane);
+      a[i] = decay[at];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int64_t n = n0 + i;
+      if (n < pieces) {
+        if (n % every == 0) *state_tile(total, unit * pieces + (REV ? pieces - 1 - n : n / every), tu, lane) = s;
+        s = fma4(s, a[i], add[i]);
+      }
+    }
   }
 }
 
@@ -122,22 +150,22 @@ hipError_t launch_linattn_states(const LinattnCall& c, const LinattnPieces& q, c
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
   p.pieces = q.pieces;
-  p.piece_blocks = q.piece_blocks;
-  p.units = c.B * c.H;
+  const int64_t units = c.B * c.H;
   const void* fn = c.f32 ? (reverse ? reinterpret_cast<const void*>(&linattn_state_kernel<true, true>)
                                     : reinterpret_cast<const void*>(&linattn_state_kernel<true, false>))
                          : (reverse ? reinterpret_cast<const void*>(&linattn_state_kernel<false, true>)
                                     : reinterpret_cast<const void*>(&linattn_state_kernel<false, false>));
   void* args[] = {&p};
-  hipError_t e = hipLaunchKernel(fn, dim3((uint32_t)((p.units * q.pieces + 3) / 4)), dim3(256), args, 0, c.stream);
+  hipError_t e = hipLaunchKernel(fn, dim3((uint32_t)(units * q.pieces)), dim3(256), args, 0, c.stream);
   if (e != hipSuccess) return e;
   f32x4* total = p.total;
   const float *decay = p.decay, *start = reverse ? c.ds_out : c.s_in;
-  int32_t pieces = q.pieces;
-  void* jargs[] = {&total, &decay, &start, &pieces};
+  int64_t pieces = q.pieces;
+  int32_t every = q.every;
+  void* jargs[] = {&total, &decay, &start, &pieces, &every};
   return hipLaunchKernel(reverse ? reinterpret_cast<const void*>(&linattn_join_kernel<true>)
                                  : reinterpret_cast<const void*>(&linattn_join_kernel<false>),
-                         dim3((uint32_t)(p.units * 4)), dim3(256), jargs, 0, c.stream);
+                         dim3((uint32_t)(units * 4)), dim3(256), jargs, 0, c.stream);
 }
 
 }  // namespace rwkv7
