@@ -32,10 +32,10 @@ struct GradParams {
   const void* dy;
   const float* s_in;       // the caller's state (pieces == 1), may be null
   const float* ds_out;     // the caller's (nseg == 1), may be null
-  const f32x4* states;     // [units][pieces] states before the pieces (pieces > 1)
-  const f32x4* marks;      // [units][blocks]
+  const float* states;     // [units][pieces] states before the pieces (pieces > 1)
+  const float* marks;      // [units][blocks]
   const float* mark_decay; // [units][blocks]
-  const f32x4* grads;      // [units][pieces] gradients behind the pieces (nseg > 1)
+  const float* grads;      // [units][pieces] gradients behind the pieces (nseg > 1)
   void* dr;
   float* dlog_w;  // per token, or [units][nseg] sums
   void* dk;
@@ -393,7 +393,14 @@ hipError_t launch_linattn_zero(float* dlog_w, int64_t H, hipStream_t stream) {
                          args, 0, stream);
 }
 
+hipError_t launch_linattn_head_sum(const float* parts, float* dlog_w, int64_t B, int64_t H, int64_t n, hipStream_t stream) {
+  int32_t heads = (int32_t)H, nseg = (int32_t)n;
+  void* args[] = {&parts, &dlog_w, &B, &heads, &nseg};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_head_sum_kernel), dim3((uint32_t)H), dim3(64), args, 0, stream);
+}
+
 hipError_t launch_linattn_backward(const LinattnCall& c) {
+  if (!c.f32) return launch_linattn_backward16(c);
   const int64_t units = c.B * c.H, nblk = linattn_blocks(c.T), pieces = linattn_pieces(c.T), cus = linattn_cus();
   // Segments: a workgroup for each compute unit, of whole pieces.
   int64_t nseg = cus / units > 0 ? cus / units : 1;
@@ -408,7 +415,7 @@ hipError_t launch_linattn_backward(const LinattnCall& c) {
     need += (bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t o_states = room(states ? units * pieces * kLinattnStateBytes : 0), o_decay = room(units * pieces * 4);
+  const size_t o_states = room(states ? units * pieces * kLinattnStateBytes : 0), o_decay = room(units * pieces * 4), o_gdecay = room(units * pieces * 4);
   const size_t o_marks = room(marks ? units * nblk * kLinattnStateBytes : 0), o_mdecay = room(marks ? units * nblk * 4 : 0);
   const size_t o_grads = room(nseg > 1 ? units * pieces * kLinattnStateBytes : 0);
   const size_t o_parts = room(c.per_token ? 0 : units * nseg * 4);
@@ -417,28 +424,21 @@ hipError_t launch_linattn_backward(const LinattnCall& c) {
   if (e != hipSuccess) return e;
   char* base = static_cast<char*>(ws);
 
-  LinattnPieces q{};
-  q.pieces = pieces;
-  q.every = 1;
-  q.decay = reinterpret_cast<float*>(base + o_decay);
-  if (nseg > 1) {
-    q.states = base + o_grads;
-    e = launch_linattn_states(c, q, c.r, c.dy, true);
-    if (e != hipSuccess) return e;
-  }
+  LinattnPieces f{}, g{};
+  f.every = g.every = 1;
+  f.states = reinterpret_cast<float*>(base + o_states), f.decay = reinterpret_cast<float*>(base + o_decay);
+  f.marks = reinterpret_cast<float*>(base + o_marks), f.mark_decay = reinterpret_cast<float*>(base + o_mdecay);
+  g.states = reinterpret_cast<float*>(base + o_grads), g.decay = reinterpret_cast<float*>(base + o_gdecay);
   if (states) {
-    q.states = base + o_states;
-    q.marks = base + o_marks;
-    q.mark_decay = reinterpret_cast<float*>(base + o_mdecay);
-    e = launch_linattn_states(c, q, c.k, c.v, false);
+    e = launch_linattn_states(c, &f, nseg > 1 ? &g : nullptr);
     if (e != hipSuccess) return e;
   }
   GradParams p{};
   p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.dy = c.dy, p.s_in = c.s_in, p.ds_out = c.ds_out;
-  p.states = reinterpret_cast<const f32x4*>(base + o_states);
-  p.marks = reinterpret_cast<const f32x4*>(base + o_marks);
+  p.states = reinterpret_cast<const float*>(base + o_states);
+  p.marks = reinterpret_cast<const float*>(base + o_marks);
   p.mark_decay = reinterpret_cast<const float*>(base + o_mdecay);
-  p.grads = reinterpret_cast<const f32x4*>(base + o_grads);
+  p.grads = reinterpret_cast<const float*>(base + o_grads);
   float* parts = reinterpret_cast<float*>(base + o_parts);
   p.dr = c.dr, p.dlog_w = c.per_token ? c.dlog_w : parts, p.dk = c.dk, p.dv = c.dv, p.ds_in = c.ds_in;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
@@ -455,13 +455,7 @@ hipError_t launch_linattn_backward(const LinattnCall& c) {
   void* args[] = {&p};
   e = hipLaunchKernel(fn, dim3((uint32_t)(units * nseg)), dim3(64 * kWaves), args, kGradLds, c.stream);
   if (e != hipSuccess || c.per_token) return e;
-  const float* src = parts;
-  float* dst = c.dlog_w;
-  int64_t B = c.B;
-  int32_t H = (int32_t)c.H, n = (int32_t)nseg;
-  void* hargs[] = {&src, &dst, &B, &H, &n};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_head_sum_kernel), dim3((uint32_t)c.H), dim3(64), hargs, 0,
-                         c.stream);
+  return launch_linattn_head_sum(parts, c.dlog_w, c.B, c.H, nseg, c.stream);
 }
 
 }  // namespace rwkv7

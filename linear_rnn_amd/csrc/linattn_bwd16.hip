@@ -1,0 +1,505 @@
+// Gradients of the linear attention for bfloat16 inputs (the formulas are in linattn_bwd.hip, number formats and
+// operand layouts in linattn_ops.hpp).
+//
+// With the state before and the gradient behind every block of 128 tokens at hand (linattn_state.hip), the blocks are
+// independent. A workgroup takes the blocks of a segment one after the other, each of its eight waves 16 tokens
+// (a tile): dr of its tokens i from the tiles J before, dk and dv of its tokens j from the tiles I behind, and each
+// from the block's border through S_0 and G. That is quadratic within a block, but neither S nor G has to be
+// carried through it, and what all waves need of them, their bfloat16 pieces, is formed once.
+//
+// Decays. With c the sum of log w since a tile's start, the factor between token j of tile J and i of a later tile I
+// is left_j (J's end to the tiles between) in_i: left_j = exp(c_end - c_j), in_i = exp(c_i), all at most 1. A wave's own
+// factor is common to all of its tokens' sums, so it is applied once, to the accumulators, and only the tile on the
+// diagonal needs a factor for each pair.
+//
+// dlog_w_t, t in tile w: the pairs of the tile that cross t, the sums over i >= t of r_i . dr_i from before the tile, over
+// j < t of k_j . dk_j to behind it, and the paths over the whole tile: <S_0, G> with the block's decay, what S_0 gives
+// to later tiles, what earlier tiles give to G, and the pairs of earlier with later tiles. All of them are sums of what
+// crosses t, so nothing cancels.
+//
+// Memory bounds it: rows come to LDS by direct loads a block ahead, and with two buffers and the pieces of one state the
+// LDS is full, so that dk and dv are done with G, then dr with S in the same place.
+#include "linattn_internal.hpp"
+#include "linattn_ops.hpp"
+#include "wkv7_internal.hpp"
+
+namespace rwkv7 {
+namespace {
+
+using namespace linattn;
+
+constexpr int kTiles = 8;                 // 16-token tiles of a block, one a wave
+constexpr int kRow = kN * 2;              // bytes of a row
+constexpr int kRows = (int)kBlk * kRow;   // one tensor's rows of a block
+constexpr int kIn0 = 0;                   // [parity][r, k, v, dy] kRows
+constexpr int kPieces = 8 * kRows;        // [piece][64 values] rows of 64 keys
+constexpr int kPiece = kN * kRow;
+constexpr int kSums = kPieces + 3 * kPiece;    // [128] double: c
+constexpr int kLeft = kSums + (int)kBlk * 8;   // [128] float
+constexpr int kInto = kLeft + (int)kBlk * 4;   // [128] float
+constexpr int kPerTile = kInto + (int)kBlk * 4;  // [4][8] float: exp(c_end), and the three sums below
+constexpr int kPairs = kPerTile + 4 * kTiles * 4;  // [J][I] float: sums over the pairs of two tiles
+constexpr int kLogW = kPairs + kTiles * kTiles * 4;  // [parity][128] float
+constexpr int kLds = kLogW + 2 * (int)kBlk * 4;
+static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
+
+struct Grad16Params {
+  const void* r;
+  const float* log_w;
+  const void* k;
+  const void* v;
+  const void* dy;
+  // the state before a block: of its piece (or the caller's), decayed since, and the piece's sum up to the block
+  const float* states;
+  const float* marks;
+  const float* mark_decay;
+  const float* grads;  // the gradient behind a block, alike
+  const float* grad_marks;
+  const float* grad_mark_decay;
+  int64_t state_stride, grad_stride;  // states of a sequence
+  void* dr;
+  float* dlog_w;  // per token, or [units][nseg] sums
+  void* dk;
+  void* dv;
+  Seq seq;
+  int32_t per_token;
+  int32_t nseg;
+  int64_t seg_blocks;
+};
+
+__device__ __forceinline__ int swizzled(int row, int piece) { return row * kRow + 16 * (piece ^ (row >> 1 & 7)); }
+
+// Sums over a row of 16 lanes up to each lane, and from each lane on.
+__device__ __forceinline__ float sums_to(float x) {
+  x += dpp_f32<0x111>(x);
+  x += dpp_f32<0x112>(x);
+  x += dpp_f32<0x114>(x);
+  x += dpp_f32<0x118>(x);
+  return x;
+}
+__device__ __forceinline__ float sums_from(float x) {
+  x += dpp_f32<0x101>(x);
+  x += dpp_f32<0x102>(x);
+  x += dpp_f32<0x104>(x);
+  x += dpp_f32<0x108>(x);
+  return x;
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor(x, 16, 64);
+  x += __shfl_xor(x, 32, 64);
+  return x;
+}
+__device__ __forceinline__ float wave_sum(float x) { return quad_sum(row16_sum(x)); }
+
+// Element 4e + i of an operand, as float32.
+__device__ __forceinline__ float value(const Op<1>& o, int e, int i) { return (float)o.p[0][4 * e + i]; }
+
+// Eight floats of a state: row `row`, columns from `col`; zeros where there is no state.
+struct Eight {
+  f32x4 x[2];
+};
+__device__ __forceinline__ Eight load_eight(const float* states, int64_t index, bool there, int row, int col) {
+  const __amdgpu_buffer_rsrc_t b = buffer(states + index * (kN * kN), there ? kN * kN * 4 : 0);
+  const uint32_t off = (row * kN + col) * 4;
+  return Eight{{__builtin_bit_cast(f32x4, load16(b, off)), __builtin_bit_cast(f32x4, load16(b, off + 16))}};
+}
+
+struct Borders {
+  Eight s, sm, g, gm;  // the piece's state and the mark; the same of the gradient
+  float sd, gd;        // the decays since
+};
+
+__global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) {
+  extern __shared__ char lds[];
+  const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // the wave's tile
+  const int64_t unit = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
+  const int64_t b = unit / p.seq.H;
+  const int32_t h = unit % p.seq.H;
+  const int64_t T = p.seq.T, len = seq_len(p.seq, b);
+  const uint32_t row_bytes = p.seq.H * kRow;
+  const int64_t nblk = (T + kBlk - 1) / kBlk;
+  const int64_t blk0 = seg * p.seg_blocks;
+  const int64_t blk1 = blk0 + p.seg_blocks < nblk ? blk0 + p.seg_blocks : nblk;
+  const int64_t live = (len + kBlk - 1) / kBlk < blk1 ? (len + kBlk - 1) / kBlk : blk1;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  auto f32s = [&](int at) { return reinterpret_cast<float*>(lds + at); };
+
+  // ---- loads
+  const uint32_t src0 = (lane >> 3) * row_bytes + 16 * ((lane & 7) ^ (lane >> 4));
+  const uint32_t src1 = ((lane >> 3) + 8) * row_bytes + 16 * ((lane & 7) ^ (4 + (lane >> 4)));
+  auto stage = [&](int64_t blk) {
+    const int64_t t0 = blk * kBlk + 16 * w;
+    const uint32_t to = lds0 + kIn0 + (blk & 1) * 4 * kRows + w * 16 * kRow;
+    const void* src[4] = {p.r, p.k, p.v, p.dy};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const Span s = token_span<2>(src[x], p.seq, b, h, t0, len - t0, 16);
+      const u32x4 d = descriptor(s.base, s.bytes);
+      to_lds16(d, src0, to + x * kRows);
+      to_lds16(d, src1, to + x * kRows + 8 * kRow);
+    }
+    if (w < 4 && lane < kSub) {
+      const int64_t t32 = blk * kBlk + w * kSub;
+      const Span s = log_w_span(p.log_w, p.per_token, p.seq, b, h, t32, len);
+      to_lds4(descriptor(s.base, s.bytes), lane * (p.per_token ? p.seq.H * 4 : 0),
+              lds0 + kLogW + (blk & 1) * (int)kBlk * 4 + w * kSub * 4);
+    }
+  };
+  const int own_row = 8 * w + (lane >> 3), own_col = 8 * (lane & 7);  // the wave's eighth of a state
+  auto load_borders = [&](int64_t blk) {
+    Borders x;
+    const bool there = blk < live;
+    const int64_t piece = blk / kPieceBlocks, at = unit * nblk + (there ? blk : blk0);
+    const bool sm = there && p.marks && blk % kPieceBlocks != 0;
+    const bool gm = there && p.grad_marks && blk % kPieceBlocks != kPieceBlocks - 1;
+    const bool s = there && p.states, g = there && p.grads;
+    x.s = load_eight(p.states, s ? unit * p.state_stride + (p.state_stride > 1 ? piece : 0) : 0, s, own_row, own_col);
+    x.sm = load_eight(p.marks, sm ? at : 0, sm, own_row, own_col);
+    x.g = load_eight(p.grads, g ? unit * p.grad_stride + (p.grad_stride > 1 ? piece : 0) : 0, g, own_row, own_col);
+    x.gm = load_eight(p.grad_marks, gm ? at : 0, gm, own_row, own_col);
+    x.sd = sm ? p.mark_decay[at] : 1.f;
+    x.gd = gm ? p.grad_mark_decay[at] : 1.f;
+    return x;
+  };
+  auto state_of = [&](const Eight& s, float d, const Eight& m, float (&o)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = fmaf(s.x[i >> 2][i & 3], d, m.x[i >> 2][i & 3]);
+  };
+  auto put_pieces = [&](const float (&x)[8]) {
+    Op<3> o;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) put2(o, i, x[i], x[i + 1]);
+#pragma unroll
+    for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(lds + kPieces + n * kPiece + swizzled(own_row, lane & 7)) = o.p[n];
+  };
+  // ---- operands
+  // rows row0 + li as they are
+  auto nat = [&](int from, int row0, int hh) {
+    return Op<1>{{*reinterpret_cast<const bf16x8*>(lds + from + swizzled(row0 + li, 4 * hh + q))}};
+  };
+  // turned: column li of tile t, of the four rows row0 + `step` q + i
+  auto turn4 = [&](int from, int row0, int step, int t) {
+    const int row = row0 + step * q + (li >> 2);
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    const char* at = lds + from + swizzled(row, 4 * (t >> 1) + (li & 3)) + 8 * (t & 1);
+    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                          (__attribute__((address_space(3))) s16x4*)const_cast<char*>(at)));
+  };
+  auto join = [](bf16x4 a, bf16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); };
+  // an operand over the tokens of tiles I0, I1 of a tensor, rows its channels of tile t
+  auto turned_tokens = [&](int from, int I0, int I1, int t) {
+    return Op<1>{{join(turn4(from, 16 * I0, 4, t), turn4(from, 16 * I1, 4, t))}};
+  };
+  // the pieces' operand over values 32 hv .., rows the keys of tile t
+  auto turned_values = [&](int t, int hv) {
+    Op<3> o;
+#pragma unroll
+    for (int n = 0; n < 3; ++n)
+      o.p[n] = join(turn4(kPieces + n * kPiece, 32 * hv, 8, t), turn4(kPieces + n * kPiece, 32 * hv + 4, 8, t));
+    return o;
+  };
+
+  float head_sum = 0.f;
+  Borders border;
+  if (blk0 < live) stage(blk0), border = load_borders(blk0);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  for (int64_t blk = blk0; blk < live; ++blk) {
+    const int64_t t0 = blk * kBlk + 16 * w;
+    const int rows_r = kIn0 + (blk & 1) * 4 * kRows, rows_k = rows_r + kRows, rows_v = rows_k + kRows, rows_d = rows_v + kRows;
+    float s8[8];
+    {
+      float g8[8];
+      state_of(border.s, border.sd, border.sm, s8);
+      state_of(border.g, border.gd, border.gm, g8);
+      stage(blk + 1);
+      put_pieces(g8);
+      float x = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x = fmaf(s8[i], g8[i], x);
+      x = wave_sum(x);
+      if (lane == 0) f32s(kPerTile)[kTiles + w] = x;
+    }
+    // decays of the tile's tokens, in all four rows of lanes
+    float left, into;
+    double c;
+    {
+      const float lw = f32s(kLogW + (blk & 1) * (int)kBlk * 4)[16 * w + li];
+      c = t0 + li < len ? (double)(lw < -1e4f ? -1e4f : lw) * 1.4426950408889634 : 0.0;
+      c += dpp_f64<0x111>(c);
+      c += dpp_f64<0x112>(c);
+      c += dpp_f64<0x114>(c);
+      c += dpp_f64<0x118>(c);
+      const double end = readlane_f64(c, 15);
+      left = exp_diff(end, c), into = exp_diff(c, 0.0);
+      if (lane < 16) {
+        reinterpret_cast<double*>(lds + kSums)[16 * w + li] = c;
+        f32s(kLeft)[16 * w + li] = left;
+        f32s(kInto)[16 * w + li] = into;
+      }
+      if (lane == 0) f32s(kPerTile)[w] = exp_diff(end, 0.0);
+    }
+    Op<1> R[2], K[2], V[2], D[2];
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh)
+      R[hh] = nat(rows_r, 16 * w, hh), K[hh] = nat(rows_k, 16 * w, hh), V[hh] = nat(rows_v, 16 * w, hh),
+      D[hh] = nat(rows_d, 16 * w, hh);
+    lds_barrier();
+
+    float before = 1.f, behind = 1.f, all = 1.f;  // decays of the tiles before and behind, of the block
+#pragma unroll
+    for (int x = 0; x < kTiles; ++x) {
+      const float e = f32s(kPerTile)[x];
+      before *= x < w ? e : 1.f;
+      behind *= x > w ? e : 1.f;
+      all *= e;
+    }
+    f32x4 dj, di;  // factors of the tile on the diagonal: rows j, rows i
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double r = reinterpret_cast<const double*>(lds + kSums)[16 * w + 4 * q + i];
+      dj[i] = exp_diff(c, r), di[i] = exp_diff(r, c);
+    }
+    float cross = 0.f, kdk, rdr;
+    {  // dk and dv
+      f32x4 ak[4], av[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int row = channel(u, li);
+        f32x4 o = zero4();
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          Op<2> G;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+            G.p[n] = *reinterpret_cast<const bf16x8*>(lds + kPieces + n * kPiece + swizzled(row, 4 * hh + q));
+          o = mma(G, K[hh], o);
+        }
+        av[u] = o * behind;
+      }
+      float kg = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        f32x4 o = mma(turned_values(t, 0), V[0], zero4());
+        o = mma(turned_values(t, 1), V[1], o);
+        ak[t] = o * behind;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kg = fmaf(ak[t][i], value(K[t >> 1], t & 1, i), kg);
+      }
+      kg = wave_sum(kg * left);
+      if (lane == 0) f32s(kPerTile)[2 * kTiles + w] = kg;
+      float between = 1.f;
+#pragma clang loop unroll(disable)
+      for (int I = w + 1; I < kTiles; I += 2) {
+        const int I1 = I + 1 < kTiles ? I + 1 : I;
+        f32x4 pq[2], pa[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int X = e ? I1 : I;
+          f32x4 x = zero4(), a = zero4();
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) x = mma(nat(rows_d, 16 * X, hh), V[hh], x), a = mma(nat(rows_r, 16 * X, hh), K[hh], a);
+          const bool on = e == 0 || I1 > I;
+          const f32x4 f = *reinterpret_cast<const f32x4*>(f32s(kInto) + 16 * X + 4 * q) * (on ? between : 0.f);
+          pq[e] = x * f, pa[e] = a * f;
+          if (on) {
+            const float s = wave_sum((a[0] * pq[e][0] + a[1] * pq[e][1] + a[2] * pq[e][2] + a[3] * pq[e][3]) * left);
+            if (lane == 0) f32s(kPairs)[w * kTiles + X] = s;
+            between *= f32s(kPerTile)[X];
+          }
+        }
+        const Op<2> Pq = pack<2>(pq[0], pq[1]), Pa = pack<2>(pa[0], pa[1]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          ak[t] = mma(turned_tokens(rows_r, I, I1, t), Pq, ak[t]);
+          av[t] = mma(turned_tokens(rows_d, I, I1, t), Pa, av[t]);
+        }
+      }
+      kdk = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        ak[t] = ak[t] * left, av[t] = av[t] * left;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kdk = fmaf(ak[t][i], value(K[t >> 1], t & 1, i), kdk);
+      }
+      kdk = quad_sum(kdk);
+      f32x4 x = mma(D[1], V[1], mma(D[0], V[0], zero4())), a = mma(R[1], K[1], mma(R[0], K[0], zero4()));
+      x = masked_i(x, di, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float to = sums_to(dpp_f32<0x111>(a[i] * x[i]));  // columns j before t of the row i
+        cross += 4 * q + i >= li ? to : 0.f;
+      }
+      cross = quad_sum(cross);
+      const Op<2> Pq = pack<2>(x, zero4()), Pa = pack<2>(masked_i(a, di, lane), zero4());
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        ak[t] = mma(turned_tokens(rows_r, w, w, t), Pq, ak[t]);
+        av[t] = mma(turned_tokens(rows_d, w, w, t), Pa, av[t]);
+      }
+      const __amdgpu_buffer_rsrc_t kb = token_buffer<2>(p.dk, p.seq, b, h, t0, T - t0, 16);
+      const __amdgpu_buffer_rsrc_t vb = token_buffer<2>(p.dv, p.seq, b, h, t0, T - t0, 16);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        store_pair<false>(kb, li * row_bytes + 64 * hh + 16 * q, ak[2 * hh], ak[2 * hh + 1]);
+        store_pair<false>(vb, li * row_bytes + 64 * hh + 16 * q, av[2 * hh], av[2 * hh + 1]);
+      }
+    }
+    lds_barrier();
+    put_pieces(s8);
+    border = load_borders(blk + 1);
+    lds_barrier();
+    {  // dr
+      f32x4 ar[4];
+      float rs = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        f32x4 o = mma(turned_values(t, 0), D[0], zero4());
+        o = mma(turned_values(t, 1), D[1], o);
+        ar[t] = o * before;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rs = fmaf(ar[t][i], value(R[t >> 1], t & 1, i), rs);
+      }
+      rs = wave_sum(rs * into);
+      if (lane == 0) f32s(kPerTile)[3 * kTiles + w] = rs;
+      float between = 1.f;
+#pragma clang loop unroll(disable)
+      for (int J = w - 1; J >= 0; J -= 2) {
+        const int J1 = J > 0 ? J - 1 : J;
+        f32x4 pp[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int X = e ? J1 : J;
+          const bool on = e == 0 || J1 < J;
+          f32x4 x = mma(nat(rows_v, 16 * X, 0), D[0], zero4());
+          x = mma(nat(rows_v, 16 * X, 1), D[1], x);
+          pp[e] = x * (*reinterpret_cast<const f32x4*>(f32s(kLeft) + 16 * X + 4 * q) * (on ? between : 0.f));
+          if (on) between *= f32s(kPerTile)[X];
+        }
+        const Op<2> P = pack<2>(pp[0], pp[1]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ar[t] = mma(turned_tokens(rows_k, J, J1, t), P, ar[t]);
+      }
+      rdr = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        ar[t] = ar[t] * into;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rdr = fmaf(ar[t][i], value(R[t >> 1], t & 1, i), rdr);
+      }
+      rdr = quad_sum(rdr);
+      const f32x4 x = masked_j(mma(V[1], D[1], mma(V[0], D[0], zero4())), dj, lane);
+      const Op<2> P = pack<2>(x, zero4());
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ar[t] = mma(turned_tokens(rows_k, w, w, t), P, ar[t]);
+      const __amdgpu_buffer_rsrc_t rb = token_buffer<2>(p.dr, p.seq, b, h, t0, T - t0, 16);
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh)
+        store_pair<false>(rb, li * row_bytes + 64 * hh + 16 * q, ar[2 * hh], ar[2 * hh + 1]);
+    }
+    lds_barrier();
+    {  // dlog_w: lane 8J + I the pairs of two tiles, lanes 0 .. 7 the borders
+      const int J = lane >> 3, I = lane & 7;
+      float x = J < w && I > w ? f32s(kPairs)[lane] : 0.f;
+      if (lane < kTiles)
+        x += all * f32s(kPerTile)[kTiles + lane] + (lane < w ? f32s(kPerTile)[2 * kTiles + lane] : 0.f) +
+             (lane > w ? f32s(kPerTile)[3 * kTiles + lane] : 0.f);
+      float dlw = cross + sums_from(rdr) + sums_to(dpp_f32<0x111>(kdk)) + wave_sum(x);
+      const int64_t t = t0 + li;
+      if (t >= len) dlw = 0.f;
+      if (p.per_token) {
+        if (lane < 16 && t < T) p.dlog_w[(b * T + t) * p.seq.H + h] = dlw;
+      } else {
+        head_sum += dlw;
+      }
+    }
+    // the next block's rows are there: behind them are at least six stores
+    asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to this workgroup's LDS when it ends
+  for (int64_t blk = live > blk0 ? live : blk0; blk < blk1; ++blk) {  // behind the sequence's end: no gradients
+    const int64_t t0 = blk * kBlk + 16 * w;
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const uint32_t off = li * row_bytes + 64 * hh + 16 * q;
+      store_pair<false>(token_buffer<2>(p.dr, p.seq, b, h, t0, T - t0, 16), off, zero4(), zero4());
+      store_pair<false>(token_buffer<2>(p.dk, p.seq, b, h, t0, T - t0, 16), off, zero4(), zero4());
+      store_pair<false>(token_buffer<2>(p.dv, p.seq, b, h, t0, T - t0, 16), off, zero4(), zero4());
+    }
+    if (p.per_token && lane < 16 && t0 + lane < T) p.dlog_w[(b * T + t0 + lane) * p.seq.H + h] = 0.f;
+  }
+  if (!p.per_token) {
+    const float s = row16_sum(head_sum);
+    if (lane == 0) f32s(kPerTile)[w] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float x = 0.f;
+      for (int i = 0; i < kTiles; ++i) x += f32s(kPerTile)[i];
+      p.dlog_w[unit * p.nseg + seg] = x;
+    }
+  }
+}
+
+}  // namespace
+
+hipError_t launch_linattn_backward16(const LinattnCall& c) {
+  const int64_t units = c.B * c.H, nblk = linattn_blocks(c.T), pieces = linattn_pieces(c.T), cus = linattn_cus();
+  // Segments: as many workgroups as fill the compute units in whole rounds best, each with its first loads to wait for.
+  int64_t nseg = 1;
+  double best = 0;
+  for (int64_t n = 1; n <= nblk && (n == 1 || units * n <= 4 * cus); ++n) {
+    const int64_t length = (nblk + n - 1) / n, rounds = (units * n + cus - 1) / cus;
+    const double us = rounds * (length * 5.0 + 3.0);
+    if (n == 1 || us < best) best = us, nseg = n;
+  }
+  const int64_t seg_blocks = (nblk + nseg - 1) / nseg;
+  nseg = (nblk + seg_blocks - 1) / seg_blocks;
+
+  const bool border = nblk > 1;  // blocks whose state is not the caller's
+  size_t need = 0;
+  auto room = [&](size_t bytes) {
+    const size_t at = need;
+    need += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t o_states = room(border ? units * pieces * kLinattnStateBytes : 0), o_decay = room(units * pieces * 4);
+  const size_t o_marks = room(border ? units * nblk * kLinattnStateBytes : 0), o_mdecay = room(units * nblk * 4);
+  const size_t o_grads = room(units * pieces * kLinattnStateBytes), o_gdecay = room(units * pieces * 4);
+  const size_t o_gmarks = room(border ? units * nblk * kLinattnStateBytes : 0), o_gmdecay = room(units * nblk * 4);
+  const size_t o_parts = room(c.per_token ? 0 : units * nseg * 4);
+  void* ws = nullptr;
+  hipError_t e = device_workspace(c.stream, need, &ws, kWorkspaceOperators);
+  if (e != hipSuccess) return e;
+  char* base = static_cast<char*>(ws);
+  auto at = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
+
+  LinattnPieces f{}, g{};
+  f.every = g.every = 1;
+  f.states = at(o_states), f.decay = at(o_decay), f.marks = border ? at(o_marks) : nullptr, f.mark_decay = at(o_mdecay);
+  g.states = at(o_grads), g.decay = at(o_gdecay), g.marks = border ? at(o_gmarks) : nullptr, g.mark_decay = at(o_gmdecay);
+  g.end = c.ds_in;
+  Grad16Params p{};
+  p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.dy = c.dy;
+  // one block: its state is the caller's, and so is its gradient; a copy where dstate_in is written over it
+  p.states = border ? f.states : c.s_in, p.marks = f.marks, p.mark_decay = f.mark_decay;
+  p.grads = border || c.ds_in ? g.states : c.ds_out, p.grad_marks = g.marks, p.grad_mark_decay = g.mark_decay;
+  p.state_stride = p.grad_stride = border ? pieces : 1;
+  if (border || c.ds_in) {
+    e = launch_linattn_states(c, border ? &f : nullptr, &g);
+    if (e != hipSuccess) return e;
+  }
+  p.dr = c.dr, p.dlog_w = c.per_token ? c.dlog_w : at(o_parts), p.dk = c.dk, p.dv = c.dv;
+  p.seq = Seq{c.T, (int32_t)c.H, c.lens};
+  p.per_token = c.per_token;
+  p.nseg = (int32_t)nseg, p.seg_blocks = seg_blocks;
+  static const hipError_t a = hipFuncSetAttribute(reinterpret_cast<const void*>(&linattn_grad16_kernel),
+                                                  hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (a != hipSuccess) return a;
+  void* args[] = {&p};
+  e = hipLaunchKernel(reinterpret_cast<const void*>(&linattn_grad16_kernel), dim3((uint32_t)(units * nseg)), dim3(512), args,
+                      kLds, c.stream);
+  if (e != hipSuccess || c.per_token) return e;
+  return launch_linattn_head_sum(at(o_parts), c.dlog_w, c.B, c.H, nseg, c.stream);
+}
+
+}  // namespace rwkv7

@@ -16,7 +16,7 @@ struct OutParams {
   const float* log_w;
   const void* k;
   const void* v;
-  const f32x4* states;  // [units][pieces] states, the first nseg those before the segments (nseg > 1)
+  const float* states;  // [units][pieces] states, the first nseg those before the segments (nseg > 1)
   const float* s_in;    // the caller's state (nseg == 1), may be null
   void* y;
   float* s_out;  // may be null
@@ -438,13 +438,12 @@ hipError_t launch_out(const LinattnCall& c) {
     hipError_t e = device_workspace(c.stream, states + units * p.pieces * 4, &ws, kWorkspaceOperators);
     if (e != hipSuccess) return e;
     LinattnPieces q{};
-    q.pieces = p.pieces;
     q.every = (int32_t)every;
-    q.states = ws;
+    q.states = static_cast<float*>(ws);
     q.decay = reinterpret_cast<float*>(static_cast<char*>(ws) + states);
-    e = launch_linattn_states(c, q, c.k, c.v, false);
+    e = launch_linattn_states(c, &q, nullptr);
     if (e != hipSuccess) return e;
-    p.states = static_cast<const f32x4*>(ws);
+    p.states = static_cast<const float*>(ws);
   }
   void* args[] = {&p};
   if constexpr (!F32) {

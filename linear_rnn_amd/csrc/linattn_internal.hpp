@@ -32,6 +32,9 @@ struct LinattnCall {
 hipError_t launch_linattn(const LinattnCall& c);
 hipError_t launch_linattn_step(const LinattnCall& c);
 hipError_t launch_linattn_backward(const LinattnCall& c);
+hipError_t launch_linattn_backward16(const LinattnCall& c);  // bfloat16, called by the one above
+// dlog_w[h] <- the sum of parts [B][H][n] over all but h, in order.
+hipError_t launch_linattn_head_sum(const float* parts, float* dlog_w, int64_t B, int64_t H, int64_t n, hipStream_t stream);
 hipError_t launch_linattn_zero(float* dlog_w, int64_t H, hipStream_t stream);
 
 constexpr int64_t kLinattnBlock = 128;              // tokens a workgroup takes at a time
@@ -42,17 +45,17 @@ constexpr int64_t kPieceBlocks = 4;
 inline int64_t linattn_blocks(int64_t T) { return (T + kLinattnBlock - 1) / kLinattnBlock; }
 inline int64_t linattn_pieces(int64_t T) { return (linattn_blocks(T) + kPieceBlocks - 1) / kPieceBlocks; }
 struct LinattnPieces {
-  int64_t pieces;
   int32_t every;      // keep the state before every every-th piece
-  void* states;       // [units][pieces] states; the kept ones come first in a sequence's
+  float* states;      // [units][pieces] states; the kept ones come first in a sequence's
   float* decay;       // [units][pieces]
-  void* marks;        // may be null; [units][blocks] states
+  float* marks;       // may be null; [units][blocks] states
   float* mark_decay;  // [units][blocks]
+  float* end;         // may be null; backward only: [units] the gradient before the first piece
 };
-// states <- the state before each every-th piece (reverse: its gradient behind each), and, if asked for, the sums of
-// each piece before each of its blocks but the first.
-hipError_t launch_linattn_states(const LinattnCall& c, const LinattnPieces& q, const void* keys, const void* values,
-                                 bool reverse);
+// Forward (from k, v): states <- the state before each every-th piece, and, if asked for, marks <- the sum of each
+// piece before each of its blocks but the first. Backward (from r, dy; every is 1): the gradient behind each piece,
+// and the sums behind each block but the last. Either may be null.
+hipError_t launch_linattn_states(const LinattnCall& c, const LinattnPieces* forward, const LinattnPieces* backward);
 // Compute units of the current device (256 if it cannot be asked).
 int64_t linattn_cus();
 

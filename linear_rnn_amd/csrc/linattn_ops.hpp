@@ -316,9 +316,9 @@ __device__ __forceinline__ f32x4 masked_i(f32x4 p, f32x4 d, int lane) {
   return o;
 }
 
-// ---- state tiles. A state [value][key] in the caller's memory; tile (t, u) of the wave's layout is D
-// with rows the keys of tile t and columns the values of tile u: a lane's four elements are four
-// consecutive keys of one value row. Between kernels and waves a state is 16 tiles [4t + u][lane].
+// ---- state tiles. A state is [value][key] in memory; tile (t, u) of the wave's layout is D with rows the keys of
+// tile t and columns the values of tile u: a lane's four elements are four consecutive keys of one value row.
+// Between waves a state is 16 tiles [4t + u][lane].
 __device__ __forceinline__ int channel(int t, int rho) { return 32 * (t >> 1) + 8 * (rho >> 2) + 4 * (t & 1) + (rho & 3); }
 __device__ __forceinline__ uint32_t state_offset(int t, int u, int lane) {  // in elements
   return channel(u, lane & 15) * kN + channel(t, 4 * (lane >> 4));
@@ -354,13 +354,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t token_buffer(const void* base,
   const Span x = token_span<ESZ>(base, s, b, h, t0, n, most);
   return buffer(x.base, x.bytes);
 }
-// Where the segments of a sequence start from: `pieces` of them, each `blocks` blocks of kBlk tokens, in
-// the wave layout [unit][piece][16 tiles][64 lanes].
-__device__ __forceinline__ f32x4* state_tile(void* states, int64_t index, int tu, int lane) {
-  return static_cast<f32x4*>(states) + (index * 16 + tu) * 64 + lane;
+// Tile tu = 4t + u of state number `index` of an array of states in the caller's layout.
+__device__ __forceinline__ f32x4* state_tile(float* states, int64_t index, int tu, int lane) {
+  return reinterpret_cast<f32x4*>(states + index * (kN * kN) + state_offset(tu >> 2, tu & 3, lane));
 }
-__device__ __forceinline__ const f32x4* state_tile(const void* states, int64_t index, int tu, int lane) {
-  return static_cast<const f32x4*>(states) + (index * 16 + tu) * 64 + lane;
+__device__ __forceinline__ const f32x4* state_tile(const float* states, int64_t index, int tu, int lane) {
+  return reinterpret_cast<const f32x4*>(states + index * (kN * kN) + state_offset(tu >> 2, tu & 3, lane));
 }
 // log w of the tokens t0 + lane % 32: 0 (decay 1) behind the sequence's end for a decay of each token, by a
 // descriptor that ends with the sequence; a head's one decay is the same load with a stride of 0, so that there is

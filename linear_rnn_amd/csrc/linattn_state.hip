@@ -15,21 +15,31 @@ namespace {
 
 using namespace linattn;
 
-struct StateParams {
+struct Side {
   const void* k;  // the key rows: k, or r backwards
   const void* v;  // the value rows: v, or dy backwards
-  const float* log_w;
-  f32x4* total;   // [units][pieces]: what each piece adds
+  float* total;   // [units][pieces]: what each piece adds
   float* decay;   // [units][pieces]
-  f32x4* marks;   // may be null; [units][blocks]: the sum from the piece's start before each block but the piece's first
-  float* mark_decay;  // [units][blocks]: the decay since the piece's start
+  float* marks;   // may be null; [units][blocks]: the sum from the piece's start before each block but the piece's first
+                  // (backwards: from its end behind each block but its last)
+  float* mark_decay;  // [units][blocks]: the decay since then
+  const float* start;  // the state before the first piece (backwards: the gradient behind the last), may be null
+  float* end;          // may be null: that behind the last (before the first)
+  int32_t rev;
+  int32_t every;
+};
+struct StateParams {
+  Side side[2];
+  const float* log_w;
   Seq seq;
   int32_t per_token;
   int64_t pieces;
 };
 
-template <bool F32, bool REV>
+template <bool F32>
 __global__ __launch_bounds__(256, 2) void linattn_state_kernel(StateParams p) {
+  const Side x = p.side[blockIdx.y];
+  const bool rev = x.rev;
   constexpr int NI = kIn<F32>;
   __shared__ f32x4 sum[kWaves][16][64];
   __shared__ double sums[kWaves][kSub];
@@ -54,16 +64,16 @@ __global__ __launch_bounds__(256, 2) void linattn_state_kernel(StateParams p) {
   const int subs = left <= 0 ? 0 : left >= kBlk ? kBlk / kSub : (int)((left + kSub - 1) / kSub);
 #pragma clang loop unroll(disable)
   for (int n = 0; n < subs; ++n) {
-    const int64_t t0 = blk * kBlk + (REV ? n : subs - 1 - n) * kSub;
+    const int64_t t0 = blk * kBlk + (rev ? n : subs - 1 - n) * kSub;
     Raw<F32> rk, rv;
-    load_raw<F32>(rv, token_buffer<kEsz<F32>>(p.v, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
-    load_raw<F32>(rk, token_buffer<kEsz<F32>>(p.k, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
+    load_raw<F32>(rv, token_buffer<kEsz<F32>>(x.v, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
+    load_raw<F32>(rk, token_buffer<kEsz<F32>>(x.k, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
     const Decay d = make_decay(log_w_here(load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane), t0, len, lane), sums[wave], lane);
     float f[2][4];
 #pragma unroll
     for (int J = 0; J < 2; ++J)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[J][i] = (REV ? d.inrow[J][i] : d.row[J][i]) * decay;
+      for (int i = 0; i < 4; ++i) f[J][i] = (rev ? d.inrow[J][i] : d.row[J][i]) * decay;
     Op<3> Vs[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -93,12 +103,12 @@ __global__ __launch_bounds__(256, 2) void linattn_state_kernel(StateParams p) {
   float since = 1.f;
 #pragma unroll
   for (int n = 0; n < kWaves; ++n) {
-    const int w = REV ? kWaves - 1 - n : n;
+    const int w = rev ? kWaves - 1 - n : n;
     const int64_t at = unit * nblk + piece * kPieceBlocks + w;
-    if (!REV && p.marks && w > 0 && piece * kPieceBlocks + w < nblk) {
+    if (x.marks && n > 0 && piece * kPieceBlocks + w < nblk) {
 #pragma unroll
-      for (int m = 0; m < 4; ++m) *state_tile(p.marks, at, 4 * wave + m, lane) = s[m];
-      if (threadIdx.x == 0) p.mark_decay[at] = since;
+      for (int m = 0; m < 4; ++m) *state_tile(x.marks, at, 4 * wave + m, lane) = s[m];
+      if (threadIdx.x == 0) x.mark_decay[at] = since;
     }
     const float a = all[w];
     since *= a;
@@ -106,66 +116,62 @@ __global__ __launch_bounds__(256, 2) void linattn_state_kernel(StateParams p) {
     for (int m = 0; m < 4; ++m) s[m] = fma4(s[m], a, sum[w][4 * wave + m][lane]);
   }
 #pragma unroll
-  for (int m = 0; m < 4; ++m) *state_tile(p.total, unit * p.pieces + piece, 4 * wave + m, lane) = s[m];
-  if (threadIdx.x == 0) p.decay[unit * p.pieces + piece] = since;
+  for (int m = 0; m < 4; ++m) *state_tile(x.total, unit * p.pieces + piece, 4 * wave + m, lane) = s[m];
+  if (threadIdx.x == 0) x.decay[unit * p.pieces + piece] = since;
 }
 
-// states[piece / every] <- the state before every every-th piece (backwards: the gradient behind each piece, in place),
-// from `start` before the first (behind the last). A thread four elements of one head's state; eight loads at a time.
-template <bool REV>
-__global__ __launch_bounds__(256) void linattn_join_kernel(f32x4* total, const float* decay, const float* start,
-                                                           int64_t pieces, int32_t every) {
+// total[piece / every] <- the state before every every-th piece (backwards: the gradient behind each piece, in place).
+// A thread four elements of one head's state; eight loads at a time.
+__global__ __launch_bounds__(256) void linattn_join_kernel(StateParams p) {
   constexpr int kAhead = 8;
+  const Side x = p.side[blockIdx.y];
   const int64_t unit = blockIdx.x / 4;
   const int tu = (blockIdx.x % 4) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  f32x4 s = start ? *reinterpret_cast<const f32x4*>(start + unit * kN * kN + state_offset(tu >> 2, tu & 3, lane)) : zero4();
-  for (int64_t n0 = 0; n0 < pieces; n0 += kAhead) {
+  f32x4 s = x.start ? *state_tile(x.start, unit, tu, lane) : zero4();
+  for (int64_t n0 = 0; n0 < p.pieces; n0 += kAhead) {
     f32x4 add[kAhead];
     float a[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int64_t n = n0 + i < pieces ? n0 + i : pieces - 1, at = unit * pieces + (REV ? pieces - 1 - n : n);
-      add[i] = *state_tile(total, at, tu, lane);
-      a[i] = decay[at];
+      const int64_t n = n0 + i < p.pieces ? n0 + i : p.pieces - 1, at = unit * p.pieces + (x.rev ? p.pieces - 1 - n : n);
+      add[i] = *state_tile(x.total, at, tu, lane);
+      a[i] = x.decay[at];
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int64_t n = n0 + i;
-      if (n < pieces) {
-        if (n % every == 0) *state_tile(total, unit * pieces + (REV ? pieces - 1 - n : n / every), tu, lane) = s;
+      if (n < p.pieces) {
+        if (n % x.every == 0) *state_tile(x.total, unit * p.pieces + (x.rev ? p.pieces - 1 - n : n / x.every), tu, lane) = s;
         s = fma4(s, a[i], add[i]);
       }
     }
   }
+  if (x.end) *state_tile(x.end, unit, tu, lane) = s;
 }
 
 }  // namespace
 
-hipError_t launch_linattn_states(const LinattnCall& c, const LinattnPieces& q, const void* keys, const void* values,
-                                 bool reverse) {
+hipError_t launch_linattn_states(const LinattnCall& c, const LinattnPieces* forward, const LinattnPieces* backward) {
   StateParams p{};
-  p.k = keys, p.v = values, p.log_w = c.log_w;
-  p.total = static_cast<f32x4*>(q.states), p.decay = q.decay;
-  p.marks = static_cast<f32x4*>(q.marks), p.mark_decay = q.mark_decay;
+  int sides = 0;
+  if (forward)
+    p.side[sides++] = Side{c.k, c.v, forward->states, forward->decay, forward->marks, forward->mark_decay, c.s_in, nullptr, 0,
+                           forward->every};
+  if (backward)
+    p.side[sides++] = Side{c.r, c.dy, backward->states, backward->decay, backward->marks, backward->mark_decay, c.ds_out,
+                           backward->end, 1, backward->every};
+  p.log_w = c.log_w;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
-  p.pieces = q.pieces;
+  p.pieces = linattn_pieces(c.T);
   const int64_t units = c.B * c.H;
-  const void* fn = c.f32 ? (reverse ? reinterpret_cast<const void*>(&linattn_state_kernel<true, true>)
-                                    : reinterpret_cast<const void*>(&linattn_state_kernel<true, false>))
-                         : (reverse ? reinterpret_cast<const void*>(&linattn_state_kernel<false, true>)
-                                    : reinterpret_cast<const void*>(&linattn_state_kernel<false, false>));
+  const void* fn = c.f32 ? reinterpret_cast<const void*>(&linattn_state_kernel<true>)
+                         : reinterpret_cast<const void*>(&linattn_state_kernel<false>);
   void* args[] = {&p};
-  hipError_t e = hipLaunchKernel(fn, dim3((uint32_t)(units * q.pieces)), dim3(256), args, 0, c.stream);
+  const hipError_t e = hipLaunchKernel(fn, dim3((uint32_t)(units * p.pieces), sides), dim3(256), args, 0, c.stream);
   if (e != hipSuccess) return e;
-  f32x4* total = p.total;
-  const float *decay = p.decay, *start = reverse ? c.ds_out : c.s_in;
-  int64_t pieces = q.pieces;
-  int32_t every = q.every;
-  void* jargs[] = {&total, &decay, &start, &pieces, &every};
-  return hipLaunchKernel(reverse ? reinterpret_cast<const void*>(&linattn_join_kernel<true>)
-                                 : reinterpret_cast<const void*>(&linattn_join_kernel<false>),
-                         dim3((uint32_t)(units * 4)), dim3(256), jargs, 0, c.stream);
+  return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_join_kernel), dim3((uint32_t)(units * 4), sides), dim3(256),
+                         args, 0, c.stream);
 }
 
 }  // namespace rwkv7
