@@ -37,21 +37,54 @@ struct NormParams {
   float eps;
 };
 
+// VEC channels as loaded, and as float32.
 template <bool F32, int VEC>
-__device__ __forceinline__ void load_vec(const void* base, int64_t at, float (&o)[VEC]) {
+struct Raw;
+template <>
+struct Raw<true, 8> {
+  float4 a, b;
+};
+template <>
+struct Raw<false, 8> {
+  uint4 a;
+};
+template <>
+struct Raw<true, 1> {
+  float a;
+};
+template <>
+struct Raw<false, 1> {
+  uint16_t a;
+};
+template <bool F32, int VEC>
+__device__ __forceinline__ Raw<F32, VEC> load_raw(const void* base, int64_t at) {
   if constexpr (VEC == 8 && F32) {
     const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-    const float4 a = p[0], b = p[1];
-    o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+    return {p[0], p[1]};
   } else if constexpr (VEC == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
-    o[0] = bf16_lo(u.x), o[1] = bf16_hi(u.x), o[2] = bf16_lo(u.y), o[3] = bf16_hi(u.y);
-    o[4] = bf16_lo(u.z), o[5] = bf16_hi(u.z), o[6] = bf16_lo(u.w), o[7] = bf16_hi(u.w);
+    return {*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at)};
   } else if constexpr (F32) {
-    o[0] = static_cast<const float*>(base)[at];
+    return {static_cast<const float*>(base)[at]};
   } else {
-    o[0] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[at] << 16);
+    return {static_cast<const uint16_t*>(base)[at]};
   }
+}
+template <bool F32, int VEC>
+__device__ __forceinline__ void widen(const Raw<F32, VEC>& r, float (&o)[VEC]) {
+  if constexpr (VEC == 8 && F32) {
+    o[0] = r.a.x, o[1] = r.a.y, o[2] = r.a.z, o[3] = r.a.w, o[4] = r.b.x, o[5] = r.b.y, o[6] = r.b.z, o[7] = r.b.w;
+  } else if constexpr (VEC == 8) {
+    o[0] = bf16_lo(r.a.x), o[1] = bf16_hi(r.a.x), o[2] = bf16_lo(r.a.y), o[3] = bf16_hi(r.a.y);
+    o[4] = bf16_lo(r.a.z), o[5] = bf16_hi(r.a.z), o[6] = bf16_lo(r.a.w), o[7] = bf16_hi(r.a.w);
+  } else if constexpr (F32) {
+    o[0] = r.a;
+  } else {
+    o[0] = __uint_as_float((uint32_t)r.a << 16);
+  }
+}
+template <bool F32, int VEC>
+__device__ __forceinline__ void load_vec(const void* base, int64_t at, float (&o)[VEC]) {
+  widen<F32, VEC>(load_raw<F32, VEC>(base, at), o);
 }
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {  // round to nearest even
   return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)lo) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)hi) << 16);
@@ -72,8 +105,9 @@ __device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&
   }
 }
 
-// Sums over the L threads of a group, the same bits in each of them. L over 64: through LDS (`red`, two
-// floats for each wave), with a barrier before and one after, so every thread of the workgroup calls it.
+// Sums over the L threads of a group, the same bits in each of them. L over 64: through LDS with a barrier, so
+// every thread of the workgroup calls it; consecutive calls take the halves of `red` (two floats for each wave and
+// half) in turn, so that one barrier is enough.
 template <int L>
 __device__ __forceinline__ float wave_sum(float x) {
 #pragma unroll
@@ -81,25 +115,25 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 template <int L>
-__device__ __forceinline__ void group_sum2(float& a, float& b, float2* red) {
+__device__ __forceinline__ void group_sum2(float& a, float& b, float2 (*red)[16], int& turn) {
   a = wave_sum<L>(a);
   b = wave_sum<L>(b);
   if constexpr (L > 64) {
     constexpr int W = L / 64;
     const int wave = threadIdx.x >> 6;
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[wave] = make_float2(a, b);
-    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[turn][wave] = make_float2(a, b);
+    lds_barrier();
     const int w0 = wave / W * W;
     a = b = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) a += red[w0 + w].x, b += red[w0 + w].y;
+    for (int w = 0; w < W; ++w) a += red[turn][w0 + w].x, b += red[turn][w0 + w].y;
+    turn ^= 1;
   }
 }
 template <int L>
-__device__ __forceinline__ float group_sum(float a, float2* red) {
+__device__ __forceinline__ float group_sum(float a, float2 (*red)[16], int& turn) {
   float b = 0.f;
-  group_sum2<L>(a, b, red);
+  group_sum2<L>(a, b, red, turn);
   return a;
 }
 
@@ -127,7 +161,8 @@ struct Place {
 
 template <bool XF, bool YF, int VEC, int L, int NV>
 __global__ __launch_bounds__(kBlock<L>) void layernorm_forward_kernel(NormParams p) {
-  __shared__ float2 red[kBlock<L> / 64];
+  __shared__ float2 red[2][16];
+  int turn = 0;
   const Place<L> at(p);
   float w[NV][VEC], b[NV][VEC];
 #pragma unroll
@@ -141,24 +176,32 @@ __global__ __launch_bounds__(kBlock<L>) void layernorm_forward_kernel(NormParams
     }
   }
   const float inv = 1.f / (float)p.n;
+  // The next row's loads are in flight while this one is summed. A thread without a row or channels of its own
+  // loads what the first has, and its values count as 0.
+  Raw<XF, VEC> x0[NV];
+  auto load = [&](int64_t m) {
+    const int64_t base = (at.on && m < p.M ? m : 0) * p.D + (int64_t)at.group * p.n;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * L + at.lane) * VEC;
+      x0[v] = load_raw<XF, VEC>(p.x, base + (c < p.n ? c : 0));
+    }
+  };
+  load(at.row);
   // every thread of the workgroup takes the same number of turns (the sums may hold barriers)
   for (int64_t m0 = (int64_t)at.chunk * p.R; m0 < p.M; m0 += at.stride) {
     const int64_t m = at.row + (m0 - (int64_t)at.chunk * p.R);
     const bool on = at.on && m < p.M;
-    const int64_t base = on ? m * p.D + (int64_t)at.group * p.n : 0;
     float x[NV][VEC], sum = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * L + at.lane) * VEC;
+      widen<XF, VEC>(x0[v], x[v]);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) x[v][i] = 0.f;
-      if (on && c < p.n) load_vec<XF, VEC>(p.x, base + c, x[v]);
+      for (int i = 0; i < VEC; ++i) sum += c < p.n ? x[v][i] : 0.f;
     }
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) sum += x[v][i];
-    const float mean = group_sum<L>(sum, red) * inv;
+    load(m + at.stride);
+    const float mean = group_sum<L>(sum, red, turn) * inv;
     float sq = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -169,12 +212,13 @@ __global__ __launch_bounds__(kBlock<L>) void layernorm_forward_kernel(NormParams
         sq += c < p.n ? x[v][i] * x[v][i] : 0.f;
       }
     }
-    const float rstd = 1.f / sqrtf(group_sum<L>(sq, red) * inv + p.eps);
+    const float rstd = 1.f / sqrtf(group_sum<L>(sq, red, turn) * inv + p.eps);
     if (!on) continue;
     if (at.lane == 0) {
       if (p.mean) p.mean[m * p.G + at.group] = mean;
       if (p.rstd) p.rstd[m * p.G + at.group] = rstd;
     }
+    const int64_t base = m * p.D + (int64_t)at.group * p.n;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * L + at.lane) * VEC;
@@ -190,8 +234,9 @@ __global__ __launch_bounds__(kBlock<L>) void layernorm_forward_kernel(NormParams
 template <bool XF, bool YF, int VEC, int L, int NV>
 __global__ __launch_bounds__(kBlock<L>) void layernorm_backward_kernel(NormParams p) {
   constexpr int kThreads = kBlock<L>;
-  __shared__ float2 red[kThreads / 64];
+  __shared__ float2 red[2][16];
   __shared__ float rows[NV * VEC][kThreads];
+  int turn = 0;
   const Place<L> at(p);
   float w[NV][VEC], dw[NV][VEC], db[NV][VEC];
 #pragma unroll
@@ -202,22 +247,36 @@ __global__ __launch_bounds__(kBlock<L>) void layernorm_backward_kernel(NormParam
     if (c < p.n && p.weight) load_vec<true, VEC>(p.weight, (int64_t)at.group * p.n + c, w[v]);
   }
   const float inv = 1.f / (float)p.n;
+  Raw<XF, VEC> x0[NV];  // the next row, as in the forward
+  Raw<YF, VEC> g0[NV];
+  float mean0, rstd0;
+  auto load = [&](int64_t m) {
+    m = at.on && m < p.M ? m : 0;
+    const int64_t base = m * p.D + (int64_t)at.group * p.n;
+    mean0 = p.mean[m * p.G + at.group], rstd0 = p.rstd[m * p.G + at.group];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * L + at.lane) * VEC;
+      x0[v] = load_raw<XF, VEC>(p.x, base + (c < p.n ? c : 0));
+      g0[v] = load_raw<YF, VEC>(p.dy, base + (c < p.n ? c : 0));
+    }
+  };
+  load(at.row);
   for (int64_t m0 = (int64_t)at.chunk * p.R; m0 < p.M; m0 += at.stride) {
     const int64_t m = at.row + (m0 - (int64_t)at.chunk * p.R);
     const bool on = at.on && m < p.M;
-    const int64_t base = on ? m * p.D + (int64_t)at.group * p.n : 0;
-    const float mean = on ? p.mean[m * p.G + at.group] : 0.f, rstd = on ? p.rstd[m * p.G + at.group] : 0.f;
+    const float mean = mean0, rstd = rstd0;
     float x[NV][VEC], g[NV][VEC], s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * L + at.lane) * VEC;
+      widen<XF, VEC>(x0[v], x[v]);
+      widen<YF, VEC>(g0[v], g[v]);
+      const bool counts = on && c < p.n;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) x[v][i] = mean, g[v][i] = 0.f;
-      if (on && c < p.n) {
-        load_vec<XF, VEC>(p.x, base + c, x[v]);
-        load_vec<YF, VEC>(p.dy, base + c, g[v]);
-      }
+      for (int i = 0; i < VEC; ++i) x[v][i] = counts ? x[v][i] : mean, g[v][i] = counts ? g[v][i] : 0.f;
     }
+    load(m + at.stride);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
@@ -229,10 +288,11 @@ __global__ __launch_bounds__(kBlock<L>) void layernorm_backward_kernel(NormParam
         s1 += g[v][i];
         s2 = fmaf(g[v][i], x[v][i], s2);
       }
-    group_sum2<L>(s1, s2, red);
+    group_sum2<L>(s1, s2, red, turn);
     s1 *= inv;
     s2 *= inv;
     if (!on) continue;
+    const int64_t base = m * p.D + (int64_t)at.group * p.n;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = (v * L + at.lane) * VEC;
@@ -272,17 +332,18 @@ __global__ __launch_bounds__(kBlock<L>) void layernorm_backward_kernel(NormParam
 // Groups too long for registers: a workgroup reads its group once for each pass (from the caches mostly).
 template <bool XF, bool YF>
 __global__ __launch_bounds__(1024) void layernorm_forward_long_kernel(NormParams p) {
-  __shared__ float2 red[16];
+  __shared__ float2 red[2][16];
+  int turn = 0;
   const float inv = 1.f / (float)p.n;
   const int64_t units = p.M * p.G;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
     const int64_t base = u * p.n, wb = u % p.G * p.n;
     float sum = 0.f, v[1];
     for (int c = threadIdx.x; c < p.n; c += 1024) load_vec<XF, 1>(p.x, base + c, v), sum += v[0];
-    const float mean = group_sum<1024>(sum, red) * inv;
+    const float mean = group_sum<1024>(sum, red, turn) * inv;
     float sq = 0.f;
     for (int c = threadIdx.x; c < p.n; c += 1024) load_vec<XF, 1>(p.x, base + c, v), sq += (v[0] - mean) * (v[0] - mean);
-    const float rstd = 1.f / sqrtf(group_sum<1024>(sq, red) * inv + p.eps);
+    const float rstd = 1.f / sqrtf(group_sum<1024>(sq, red, turn) * inv + p.eps);
     if (threadIdx.x == 0) {
       if (p.mean) p.mean[u] = mean;
       if (p.rstd) p.rstd[u] = rstd;
@@ -297,7 +358,8 @@ __global__ __launch_bounds__(1024) void layernorm_forward_long_kernel(NormParams
 }
 template <bool XF, bool YF>
 __global__ __launch_bounds__(1024) void layernorm_backward_long_kernel(NormParams p) {
-  __shared__ float2 red[16];
+  __shared__ float2 red[2][16];
+  int turn = 0;
   const float inv = 1.f / (float)p.n;
   const int64_t units = p.M * p.G;
   for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -311,7 +373,7 @@ __global__ __launch_bounds__(1024) void layernorm_backward_long_kernel(NormParam
       s1 += g;
       s2 = fmaf(g, (x[0] - mean) * rstd, s2);
     }
-    group_sum2<1024>(s1, s2, red);
+    group_sum2<1024>(s1, s2, red, turn);
     s1 *= inv;
     s2 *= inv;
     for (int c = threadIdx.x; c < p.n; c += 1024) {
@@ -342,10 +404,10 @@ __global__ __launch_bounds__(256) void layernorm_columns_kernel(NormParams p) {
   p.partial[((int64_t)p.nb + chunk) * p.D + c] = db;
 }
 
-// dweight and dbias from the partial rows: 64 channels a workgroup, 4 of its threads a channel.
-__global__ __launch_bounds__(256) void layernorm_join_kernel(const float* partial, float* dweight, float* dbias, int32_t nb,
-                                                             int32_t D) {
-  __shared__ float part[4][64];
+// dweight and dbias from the partial rows: 64 channels a workgroup, 16 of its threads a channel.
+__global__ __launch_bounds__(1024) void layernorm_join_kernel(const float* partial, float* dweight, float* dbias, int32_t nb,
+                                                              int32_t D) {
+  __shared__ float part[16][64];
   float* out = blockIdx.y ? dbias : dweight;
   if (!out) return;
   const int64_t c = (int64_t)blockIdx.x * 64 + (threadIdx.x & 63);
@@ -353,12 +415,16 @@ __global__ __launch_bounds__(256) void layernorm_join_kernel(const float* partia
   float s = 0.f;
   if (c < D) {
     const float* src = partial + (int64_t)blockIdx.y * nb * D + c;
-#pragma unroll 8
-    for (int i = k; i < nb; i += 4) s += src[(int64_t)i * D];
+#pragma unroll 16
+    for (int i = k; i < nb; i += 16) s += src[(int64_t)i * D];
   }
   part[k][threadIdx.x & 63] = s;
   __syncthreads();
-  if (k == 0 && c < D) out[c] = ((part[0][threadIdx.x] + part[1][threadIdx.x]) + part[2][threadIdx.x]) + part[3][threadIdx.x];
+  if (k == 0 && c < D) {
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s += part[i][threadIdx.x];
+    out[c] = s;
+  }
 }
 
 struct Config {
@@ -468,7 +534,7 @@ hipError_t backward(const NormCall& c) {
   float *dweight = c.dweight, *dbias = c.dbias;
   void* args[] = {&partial, &dweight, &dbias, &p.nb, &p.D};
   return hipLaunchKernel(reinterpret_cast<const void*>(&layernorm_join_kernel), dim3((uint32_t)((p.D + 63) / 64), 2),
-                         dim3(256), args, 0, c.stream);
+                         dim3(1024), args, 0, c.stream);
 }
 
 __global__ __launch_bounds__(256) void layernorm_zero_kernel(float* a, float* b, int32_t D) {

@@ -121,32 +121,34 @@ __global__ __launch_bounds__(256, 2) void linattn_state_kernel(StateParams p) {
 }
 
 // total[piece / every] <- the state before every every-th piece (backwards: the gradient behind each piece, in place).
-// A thread four elements of one head's state; eight loads at a time.
+// A thread four elements of one head's state, which lie one after the other; eight loads at a time.
 __global__ __launch_bounds__(256) void linattn_join_kernel(StateParams p) {
-  constexpr int kAhead = 8;
+  constexpr int kAhead = 8, kFours = kN * kN / 4;
   const Side x = p.side[blockIdx.y];
   const int64_t unit = blockIdx.x / 4;
-  const int tu = (blockIdx.x % 4) * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  f32x4 s = x.start ? *state_tile(x.start, unit, tu, lane) : zero4();
+  const int e = (blockIdx.x % 4) * 256 + threadIdx.x;
+  const f32x4* start = reinterpret_cast<const f32x4*>(x.start);
+  f32x4* total = reinterpret_cast<f32x4*>(x.total);
+  f32x4 s = start ? start[unit * kFours + e] : zero4();
   for (int64_t n0 = 0; n0 < p.pieces; n0 += kAhead) {
     f32x4 add[kAhead];
     float a[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int64_t n = n0 + i < p.pieces ? n0 + i : p.pieces - 1, at = unit * p.pieces + (x.rev ? p.pieces - 1 - n : n);
-      add[i] = *state_tile(x.total, at, tu, lane);
+      add[i] = total[at * kFours + e];
       a[i] = x.decay[at];
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       const int64_t n = n0 + i;
       if (n < p.pieces) {
-        if (n % x.every == 0) *state_tile(x.total, unit * p.pieces + (x.rev ? p.pieces - 1 - n : n / x.every), tu, lane) = s;
+        if (n % x.every == 0) total[(unit * p.pieces + (x.rev ? p.pieces - 1 - n : n / x.every)) * kFours + e] = s;
         s = fma4(s, a[i], add[i]);
       }
     }
   }
-  if (x.end) *state_tile(x.end, unit, tu, lane) = s;
+  if (x.end) reinterpret_cast<f32x4*>(x.end)[unit * kFours + e] = s;
 }
 
 }  // namespace
