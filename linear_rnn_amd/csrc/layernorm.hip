@@ -109,9 +109,14 @@ __device__ __forceinline__ void store_vec(void* base, int64_t at, const float (&
 // every thread of the workgroup calls it; consecutive calls take the halves of `red` (two floats for each wave and
 // half) in turn, so that one barrier is enough.
 template <int L>
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-  for (int m = 1; m < (L < 64 ? L : 64); m *= 2) x += __shfl_xor(x, m, 64);
+__device__ __forceinline__ float wave_sum(float x) {  // butterflies of the vector unit, no LDS
+  static_assert(L >= 8, "");
+  if constexpr (L >= 16) x = x + dpp_f32<0x128>(x);  // row_ror:8
+  x = x + dpp_f32<0x141>(x);                         // row_half_mirror
+  x = x + dpp_f32<0x4E>(x);                          // quad_perm [2,3,0,1]
+  x = x + dpp_f32<0xB1>(x);                          // quad_perm [1,0,3,2]
+  if constexpr (L >= 32) x = pair_rows_sum(x);
+  if constexpr (L >= 64) x = halves_sum(x);
   return x;
 }
 template <int L>

@@ -68,13 +68,6 @@ __device__ __forceinline__ float sum_before(float x, int lane) {
   const float s = row_sums_to(dpp_f32<0x111>(x));
   return (lane & 16) ? s + first : s;
 }
-// Sum over the four lanes with the same li, the same bits in each.
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor(x, 16, 64);
-  x += __shfl_xor(x, 32, 64);
-  return x;
-}
-
 template <bool F32>
 __global__ __launch_bounds__(256, 1) void linattn_grad_kernel(GradParams p) {
   constexpr int NI = kIn<F32>, NO = F32 ? 3 : 2;
@@ -327,11 +320,11 @@ __global__ __launch_bounds__(256, 1) void linattn_grad_kernel(GradParams p) {
     __builtin_amdgcn_sched_barrier(0);
     // dlog_w: lane l has token l % 32
 #pragma unroll
-    for (int J = 0; J < 2; ++J) cross[J] = quad_sum(cross[J]), rdr[J] = quad_sum(rdr[J]), kdk[J] = quad_sum(kdk[J]);
+    for (int J = 0; J < 2; ++J) cross[J] = rows_sum(cross[J]), rdr[J] = rows_sum(rdr[J]), kdk[J] = rows_sum(kdk[J]);
     const bool second = lane & 16;
     const float pairs = second ? cross[1] : cross[0];
     const float here = second ? rdr[1] : rdr[0], before = second ? kdk[1] : kdk[0];
-    dot = quad_sum(row16_sum(dot));
+    dot = rows_sum(row16_sum(dot));
     const int64_t t = t0 + (lane & 31);
     float dlw = pairs + sum_from(here, lane) + sum_before(before, lane) + dot * d.all;
     if (t >= len) dlw = 0.f;

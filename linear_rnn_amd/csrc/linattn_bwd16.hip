@@ -67,7 +67,14 @@ struct Grad16Params {
   int64_t seg_blocks;
 };
 
-__device__ __forceinline__ int swizzled(int row, int piece) { return row * kRow + 16 * (piece ^ (row >> 1 & 7)); }
+// Where 16-byte piece `piece` of a row is: exchanged within the row so that reads of one piece of 16 rows, and turned
+// reads of four pieces of 8 rows, meet as many banks as there are; rows that follow each other in a block's inputs,
+// rows as channel() numbers them in a state's pieces.
+__device__ __forceinline__ int row_key(int row) { return (row >> 1 & 1) | (row >> 2 & 2) | (row & 4); }
+__device__ __forceinline__ int swizzled(int row, int piece) { return row * kRow + 16 * (piece ^ row_key(row)); }
+__device__ __forceinline__ int in_pieces(int row, int piece) {
+  return row * kRow + 16 * (piece ^ ((row >> 1 & 1) | (row >> 3 & 2) | (row >> 1 & 4)));
+}
 
 // Sums over a row of 16 lanes up to each lane, and from each lane on.
 __device__ __forceinline__ float sums_to(float x) {
@@ -84,12 +91,7 @@ __device__ __forceinline__ float sums_from(float x) {
   x += dpp_f32<0x108>(x);
   return x;
 }
-__device__ __forceinline__ float quad_sum(float x) {
-  x += __shfl_xor(x, 16, 64);
-  x += __shfl_xor(x, 32, 64);
-  return x;
-}
-__device__ __forceinline__ float wave_sum(float x) { return quad_sum(row16_sum(x)); }
+__device__ __forceinline__ float wave_sum(float x) { return rows_sum(row16_sum(x)); }
 
 // Element 4e + i of an operand, as float32.
 __device__ __forceinline__ float value(const Op<1>& o, int e, int i) { return (float)o.p[0][4 * e + i]; }
@@ -112,7 +114,9 @@ struct Borders {
 __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) {
   extern __shared__ char lds[];
   const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // the wave's tile
+  // The wave's tile. Tile w has w tiles before it (one product of pairs each) and 7 - w behind it (two), and the waves
+  // i and i + 4 share a SIMD: tiles w and 7 - w together have the same work on every one.
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave < 4 ? wave : 11 - wave;
   const int64_t unit = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
   const int64_t b = unit / p.seq.H;
   const int32_t h = unit % p.seq.H;
@@ -126,24 +130,27 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
   auto f32s = [&](int at) { return reinterpret_cast<float*>(lds + at); };
 
   // ---- loads
-  const uint32_t src0 = (lane >> 3) * row_bytes + 16 * ((lane & 7) ^ (lane >> 4));
-  const uint32_t src1 = ((lane >> 3) + 8) * row_bytes + 16 * ((lane & 7) ^ (4 + (lane >> 4)));
+  const uint32_t src0 = (lane >> 3) * row_bytes + 16 * ((lane & 7) ^ row_key(lane >> 3));
+  const uint32_t src1 = ((lane >> 3) + 8) * row_bytes + 16 * ((lane & 7) ^ row_key(8 + (lane >> 3)));
+  // where the wave's 16 rows of a block start in every tensor, and the bytes to the end of the last of n of them
+  auto rows_at = [&](int64_t blk) { return ((b * T + blk * kBlk + 16 * w) * p.seq.H + h) * (int64_t)kRow; };
+  auto rows_bytes = [&](int64_t n) { return n <= 0 ? 0 : (uint32_t)((n < 16 ? n : 16) - 1) * row_bytes + kRow; };
   auto stage = [&](int64_t blk) {
-    const int64_t t0 = blk * kBlk + 16 * w;
+    const int64_t from = rows_at(blk);
+    const uint32_t bytes = rows_bytes(len - blk * kBlk - 16 * w);
     const uint32_t to = lds0 + kIn0 + (blk & 1) * 4 * kRows + w * 16 * kRow;
     const void* src[4] = {p.r, p.k, p.v, p.dy};
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const Span s = token_span<2>(src[x], p.seq, b, h, t0, len - t0, 16);
-      const u32x4 d = descriptor(s.base, s.bytes);
+      const u32x4 d = descriptor(static_cast<const char*>(src[x]) + from, bytes);
       to_lds16(d, src0, to + x * kRows);
       to_lds16(d, src1, to + x * kRows + 8 * kRow);
     }
-    if (w < 4 && lane < kSub) {
-      const int64_t t32 = blk * kBlk + w * kSub;
+    if (wave < 4 && lane < kSub) {
+      const int64_t t32 = blk * kBlk + wave * kSub;
       const Span s = log_w_span(p.log_w, p.per_token, p.seq, b, h, t32, len);
       to_lds4(descriptor(s.base, s.bytes), lane * (p.per_token ? p.seq.H * 4 : 0),
-              lds0 + kLogW + (blk & 1) * (int)kBlk * 4 + w * kSub * 4);
+              lds0 + kLogW + (blk & 1) * (int)kBlk * 4 + wave * kSub * 4);
     }
   };
   const int own_row = 8 * w + (lane >> 3), own_col = 8 * (lane & 7);  // the wave's eighth of a state
@@ -171,32 +178,34 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
 #pragma unroll
     for (int i = 0; i < 8; i += 2) put2(o, i, x[i], x[i + 1]);
 #pragma unroll
-    for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(lds + kPieces + n * kPiece + swizzled(own_row, lane & 7)) = o.p[n];
+    for (int n = 0; n < 3; ++n) *reinterpret_cast<bf16x8*>(lds + kPieces + n * kPiece + in_pieces(own_row, lane & 7)) = o.p[n];
   };
-  // ---- operands
-  // rows row0 + li as they are
+  // ---- operands. Piece 4m + x of a row is 64 m bytes, by exclusive or, from piece x, in both numberings, so a lane's
+  // place in a tile is one of two and everything else in an address a constant or the tile's.
+  const int nat0 = swizzled(li, q), turn0 = swizzled(4 * q + (li >> 2), li & 3);
+  const int pnat0 = in_pieces(8 * (li >> 2) + (li & 3), q), pturn0 = in_pieces(8 * q + (li >> 2), li & 3);
+  // rows row0 + li as they are (row0 a multiple of 16)
   auto nat = [&](int from, int row0, int hh) {
-    return Op<1>{{*reinterpret_cast<const bf16x8*>(lds + from + swizzled(row0 + li, 4 * hh + q))}};
+    return Op<1>{{*reinterpret_cast<const bf16x8*>(lds + (from + row0 * kRow) + (nat0 ^ 64 * hh))}};
   };
-  // turned: column li of tile t, of the four rows row0 + `step` q + i
-  auto turn4 = [&](int from, int row0, int step, int t) {
-    const int row = row0 + step * q + (li >> 2);
+  // turned: column li of tile t, of four rows
+  auto turn4 = [&](int at) {
     typedef short s16x4 __attribute__((ext_vector_type(4)));
-    const char* at = lds + from + swizzled(row, 4 * (t >> 1) + (li & 3)) + 8 * (t & 1);
-    return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                          (__attribute__((address_space(3))) s16x4*)const_cast<char*>(at)));
+    return __builtin_bit_cast(
+        bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds + at)));
   };
   auto join = [](bf16x4 a, bf16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); };
   // an operand over the tokens of tiles I0, I1 of a tensor, rows its channels of tile t
   auto turned_tokens = [&](int from, int I0, int I1, int t) {
-    return Op<1>{{join(turn4(from, 16 * I0, 4, t), turn4(from, 16 * I1, 4, t))}};
+    const int in_tile = (turn0 ^ 64 * (t >> 1)) + 8 * (t & 1);
+    return Op<1>{{join(turn4(from + I0 * 16 * kRow + in_tile), turn4(from + I1 * 16 * kRow + in_tile))}};
   };
   // the pieces' operand over values 32 hv .., rows the keys of tile t
   auto turned_values = [&](int t, int hv) {
     Op<3> o;
+    const int at = kPieces + (pturn0 ^ 64 * (t >> 1)) + 8 * (t & 1) + 32 * hv * kRow;
 #pragma unroll
-    for (int n = 0; n < 3; ++n)
-      o.p[n] = join(turn4(kPieces + n * kPiece, 32 * hv, 8, t), turn4(kPieces + n * kPiece, 32 * hv + 4, 8, t));
+    for (int n = 0; n < 3; ++n) o.p[n] = join(turn4(at + n * kPiece), turn4(at + n * kPiece + 4 * kRow));
     return o;
   };
 
@@ -260,69 +269,90 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
       const double r = reinterpret_cast<const double*>(lds + kSums)[16 * w + 4 * q + i];
       dj[i] = exp_diff(c, r), di[i] = exp_diff(r, c);
     }
-    float cross = 0.f, kdk, rdr;
-    {  // dk and dv
-      f32x4 ak[4], av[4];
+    // the pairs with the tiles behind (for dk, dv) and before (for dr)
+    f32x4 ak[4], av[4], ar[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) ak[t] = av[t] = ar[t] = zero4();
+    float between = 1.f;
+#pragma clang loop unroll(disable)
+    for (int I = w + 1; I < kTiles; I += 2) {
+      const int I1 = I + 1 < kTiles ? I + 1 : I;
+      f32x4 pq[2], pa[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int X = e ? I1 : I;
+        f32x4 x = zero4(), a = zero4();
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) x = mma(nat(rows_d, 16 * X, hh), V[hh], x), a = mma(nat(rows_r, 16 * X, hh), K[hh], a);
+        const bool on = e == 0 || I1 > I;
+        const f32x4 f = *reinterpret_cast<const f32x4*>(f32s(kInto) + 16 * X + 4 * q) * (on ? between : 0.f);
+        pq[e] = x * f, pa[e] = a * f;
+        if (on) {
+          const float s = wave_sum((a[0] * pq[e][0] + a[1] * pq[e][1] + a[2] * pq[e][2] + a[3] * pq[e][3]) * left);
+          if (lane == 0) f32s(kPairs)[w * kTiles + X] = s;
+          between *= f32s(kPerTile)[X];
+        }
+      }
+      const Op<2> Pq = pack<2>(pq[0], pq[1]), Pa = pack<2>(pa[0], pa[1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        ak[t] = mma(turned_tokens(rows_r, I, I1, t), Pq, ak[t]);
+        av[t] = mma(turned_tokens(rows_d, I, I1, t), Pa, av[t]);
+      }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    between = 1.f;
+#pragma clang loop unroll(disable)
+    for (int J = w - 1; J >= 0; J -= 2) {
+      const int J1 = J > 0 ? J - 1 : J;
+      f32x4 pp[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int X = e ? J1 : J;
+        const bool on = e == 0 || J1 < J;
+        f32x4 x = mma(nat(rows_v, 16 * X, 0), D[0], zero4());
+        x = mma(nat(rows_v, 16 * X, 1), D[1], x);
+        pp[e] = x * (*reinterpret_cast<const f32x4*>(f32s(kLeft) + 16 * X + 4 * q) * (on ? between : 0.f));
+        if (on) between *= f32s(kPerTile)[X];
+      }
+      const Op<2> P = pack<2>(pp[0], pp[1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ar[t] = mma(turned_tokens(rows_k, J, J1, t), P, ar[t]);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // phases whose registers would not fit together
+    float cross = 0.f, kdk = 0.f, rdr = 0.f;
+    {  // dk and dv: the gradient behind the block, the factor of the tokens, the tile's own pairs
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int row = channel(u, li);
+        const int rows = (32 * (u >> 1) + 4 * (u & 1)) * kRow;  // value channel(u, li)
         f32x4 o = zero4();
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           Op<2> G;
 #pragma unroll
           for (int n = 0; n < 2; ++n)
-            G.p[n] = *reinterpret_cast<const bf16x8*>(lds + kPieces + n * kPiece + swizzled(row, 4 * hh + q));
+            G.p[n] = *reinterpret_cast<const bf16x8*>(lds + kPieces + (pnat0 ^ 64 * hh) + rows + n * kPiece);
           o = mma(G, K[hh], o);
         }
-        av[u] = o * behind;
+        av[u] = fma4(o, behind, av[u]) * left;
       }
+      __builtin_amdgcn_sched_barrier(0);
       float kg = 0.f;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         f32x4 o = mma(turned_values(t, 0), V[0], zero4());
-        o = mma(turned_values(t, 1), V[1], o);
-        ak[t] = o * behind;
+        o = mma(turned_values(t, 1), V[1], o) * (behind * left);
+        ak[t] = fma4(ak[t], left, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kg = fmaf(ak[t][i], value(K[t >> 1], t & 1, i), kg);
+        for (int i = 0; i < 4; ++i) {
+          const float k = value(K[t >> 1], t & 1, i);
+          kg = fmaf(o[i], k, kg), kdk = fmaf(ak[t][i], k, kdk);
+        }
       }
-      kg = wave_sum(kg * left);
+      kg = wave_sum(kg);
       if (lane == 0) f32s(kPerTile)[2 * kTiles + w] = kg;
-      float between = 1.f;
-#pragma clang loop unroll(disable)
-      for (int I = w + 1; I < kTiles; I += 2) {
-        const int I1 = I + 1 < kTiles ? I + 1 : I;
-        f32x4 pq[2], pa[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int X = e ? I1 : I;
-          f32x4 x = zero4(), a = zero4();
-#pragma unroll
-          for (int hh = 0; hh < 2; ++hh) x = mma(nat(rows_d, 16 * X, hh), V[hh], x), a = mma(nat(rows_r, 16 * X, hh), K[hh], a);
-          const bool on = e == 0 || I1 > I;
-          const f32x4 f = *reinterpret_cast<const f32x4*>(f32s(kInto) + 16 * X + 4 * q) * (on ? between : 0.f);
-          pq[e] = x * f, pa[e] = a * f;
-          if (on) {
-            const float s = wave_sum((a[0] * pq[e][0] + a[1] * pq[e][1] + a[2] * pq[e][2] + a[3] * pq[e][3]) * left);
-            if (lane == 0) f32s(kPairs)[w * kTiles + X] = s;
-            between *= f32s(kPerTile)[X];
-          }
-        }
-        const Op<2> Pq = pack<2>(pq[0], pq[1]), Pa = pack<2>(pa[0], pa[1]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          ak[t] = mma(turned_tokens(rows_r, I, I1, t), Pq, ak[t]);
-          av[t] = mma(turned_tokens(rows_d, I, I1, t), Pa, av[t]);
-        }
-      }
-      kdk = 0.f;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        ak[t] = ak[t] * left, av[t] = av[t] * left;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) kdk = fmaf(ak[t][i], value(K[t >> 1], t & 1, i), kdk);
-      }
-      kdk = quad_sum(kdk);
+      kdk = rows_sum(kdk);
+      __builtin_amdgcn_sched_barrier(0);
       f32x4 x = mma(D[1], V[1], mma(D[0], V[0], zero4())), a = mma(R[1], K[1], mma(R[0], K[0], zero4()));
       x = masked_i(x, di, lane);
 #pragma unroll
@@ -330,15 +360,15 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
         const float to = sums_to(dpp_f32<0x111>(a[i] * x[i]));  // columns j before t of the row i
         cross += 4 * q + i >= li ? to : 0.f;
       }
-      cross = quad_sum(cross);
+      cross = rows_sum(cross);
       const Op<2> Pq = pack<2>(x, zero4()), Pa = pack<2>(masked_i(a, di, lane), zero4());
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         ak[t] = mma(turned_tokens(rows_r, w, w, t), Pq, ak[t]);
         av[t] = mma(turned_tokens(rows_d, w, w, t), Pa, av[t]);
       }
-      const __amdgpu_buffer_rsrc_t kb = token_buffer<2>(p.dk, p.seq, b, h, t0, T - t0, 16);
-      const __amdgpu_buffer_rsrc_t vb = token_buffer<2>(p.dv, p.seq, b, h, t0, T - t0, 16);
+      const __amdgpu_buffer_rsrc_t kb = buffer(static_cast<char*>(p.dk) + rows_at(blk), rows_bytes(T - t0));
+      const __amdgpu_buffer_rsrc_t vb = buffer(static_cast<char*>(p.dv) + rows_at(blk), rows_bytes(T - t0));
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         store_pair<false>(kb, li * row_bytes + 64 * hh + 16 * q, ak[2 * hh], ak[2 * hh + 1]);
@@ -349,50 +379,27 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
     put_pieces(s8);
     border = load_borders(blk + 1);
     lds_barrier();
-    {  // dr
-      f32x4 ar[4];
+    {  // dr, alike with the state before the block
       float rs = 0.f;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         f32x4 o = mma(turned_values(t, 0), D[0], zero4());
-        o = mma(turned_values(t, 1), D[1], o);
-        ar[t] = o * before;
+        o = mma(turned_values(t, 1), D[1], o) * (before * into);
+        ar[t] = fma4(ar[t], into, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) rs = fmaf(ar[t][i], value(R[t >> 1], t & 1, i), rs);
-      }
-      rs = wave_sum(rs * into);
-      if (lane == 0) f32s(kPerTile)[3 * kTiles + w] = rs;
-      float between = 1.f;
-#pragma clang loop unroll(disable)
-      for (int J = w - 1; J >= 0; J -= 2) {
-        const int J1 = J > 0 ? J - 1 : J;
-        f32x4 pp[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int X = e ? J1 : J;
-          const bool on = e == 0 || J1 < J;
-          f32x4 x = mma(nat(rows_v, 16 * X, 0), D[0], zero4());
-          x = mma(nat(rows_v, 16 * X, 1), D[1], x);
-          pp[e] = x * (*reinterpret_cast<const f32x4*>(f32s(kLeft) + 16 * X + 4 * q) * (on ? between : 0.f));
-          if (on) between *= f32s(kPerTile)[X];
+        for (int i = 0; i < 4; ++i) {
+          const float r = value(R[t >> 1], t & 1, i);
+          rs = fmaf(o[i], r, rs), rdr = fmaf(ar[t][i], r, rdr);
         }
-        const Op<2> P = pack<2>(pp[0], pp[1]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) ar[t] = mma(turned_tokens(rows_k, J, J1, t), P, ar[t]);
       }
-      rdr = 0.f;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        ar[t] = ar[t] * into;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) rdr = fmaf(ar[t][i], value(R[t >> 1], t & 1, i), rdr);
-      }
-      rdr = quad_sum(rdr);
+      rs = wave_sum(rs);
+      if (lane == 0) f32s(kPerTile)[3 * kTiles + w] = rs;
+      rdr = rows_sum(rdr);
       const f32x4 x = masked_j(mma(V[1], D[1], mma(V[0], D[0], zero4())), dj, lane);
       const Op<2> P = pack<2>(x, zero4());
 #pragma unroll
       for (int t = 0; t < 4; ++t) ar[t] = mma(turned_tokens(rows_k, w, w, t), P, ar[t]);
-      const __amdgpu_buffer_rsrc_t rb = token_buffer<2>(p.dr, p.seq, b, h, t0, T - t0, 16);
+      const __amdgpu_buffer_rsrc_t rb = buffer(static_cast<char*>(p.dr) + rows_at(blk), rows_bytes(T - t0));
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
         store_pair<false>(rb, li * row_bytes + 64 * hh + 16 * q, ar[2 * hh], ar[2 * hh + 1]);
@@ -422,9 +429,10 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       const uint32_t off = li * row_bytes + 64 * hh + 16 * q;
-      store_pair<false>(token_buffer<2>(p.dr, p.seq, b, h, t0, T - t0, 16), off, zero4(), zero4());
-      store_pair<false>(token_buffer<2>(p.dk, p.seq, b, h, t0, T - t0, 16), off, zero4(), zero4());
-      store_pair<false>(token_buffer<2>(p.dv, p.seq, b, h, t0, T - t0, 16), off, zero4(), zero4());
+      void* const out[3] = {p.dr, p.dk, p.dv};
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        store_pair<false>(buffer(static_cast<char*>(out[x]) + rows_at(blk), rows_bytes(T - t0)), off, zero4(), zero4());
     }
     if (p.per_token && lane < 16 && t0 + lane < T) p.dlog_w[(b * T + t0 + lane) * p.seq.H + h] = 0.f;
   }
