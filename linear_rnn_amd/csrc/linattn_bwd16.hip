@@ -106,9 +106,9 @@ __device__ __forceinline__ Eight load_eight(const float* states, int64_t index, 
   return Eight{{__builtin_bit_cast(f32x4, load16(b, off)), __builtin_bit_cast(f32x4, load16(b, off + 16))}};
 }
 
-struct Borders {
-  Eight s, sm, g, gm;  // the piece's state and the mark; the same of the gradient
-  float sd, gd;        // the decays since
+struct Border {
+  Eight piece, mark;  // the piece's state or gradient, and what the piece adds to it
+  float decay;        // since the piece's border
 };
 
 __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) {
@@ -153,25 +153,23 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
               lds0 + kLogW + (blk & 1) * (int)kBlk * 4 + wave * kSub * 4);
     }
   };
-  const int own_row = 8 * w + (lane >> 3), own_col = 8 * (lane & 7);  // the wave's eighth of a state
-  auto load_borders = [&](int64_t blk) {
-    Borders x;
-    const bool there = blk < live;
-    const int64_t piece = blk / kPieceBlocks, at = unit * nblk + (there ? blk : blk0);
-    const bool sm = there && p.marks && blk % kPieceBlocks != 0;
-    const bool gm = there && p.grad_marks && blk % kPieceBlocks != kPieceBlocks - 1;
-    const bool s = there && p.states, g = there && p.grads;
-    x.s = load_eight(p.states, s ? unit * p.state_stride + (p.state_stride > 1 ? piece : 0) : 0, s, own_row, own_col);
-    x.sm = load_eight(p.marks, sm ? at : 0, sm, own_row, own_col);
-    x.g = load_eight(p.grads, g ? unit * p.grad_stride + (p.grad_stride > 1 ? piece : 0) : 0, g, own_row, own_col);
-    x.gm = load_eight(p.grad_marks, gm ? at : 0, gm, own_row, own_col);
-    x.sd = sm ? p.mark_decay[at] : 1.f;
-    x.gd = gm ? p.grad_mark_decay[at] : 1.f;
+  const int own_row = 8 * wave + (lane >> 3), own_col = 8 * (lane & 7);  // the wave's eighth of a state
+  auto load_border = [&](const float* states, const float* marks, const float* decays, int64_t stride, int unmarked,
+                         int64_t blk) {
+    Border x;
+    const bool there = blk < live && states, marked = there && marks && blk % kPieceBlocks != unmarked;
+    const int64_t at = unit * nblk + (marked ? blk : 0);
+    x.piece = load_eight(states, there ? unit * stride + (stride > 1 ? blk / kPieceBlocks : 0) : 0, there, own_row, own_col);
+    x.mark = load_eight(marks, marked ? at : 0, marked, own_row, own_col);
+    x.decay = marked ? decays[at] : 1.f;
     return x;
   };
-  auto state_of = [&](const Eight& s, float d, const Eight& m, float (&o)[8]) {
+  auto load_grad = [&](int64_t blk) {
+    return load_border(p.grads, p.grad_marks, p.grad_mark_decay, p.grad_stride, kPieceBlocks - 1, blk);
+  };
+  auto state_of = [&](const Border& x, float (&o)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = fmaf(s.x[i >> 2][i & 3], d, m.x[i >> 2][i & 3]);
+    for (int i = 0; i < 8; ++i) o[i] = fmaf(x.piece.x[i >> 2][i & 3], x.decay, x.mark.x[i >> 2][i & 3]);
   };
   auto put_pieces = [&](const float (&x)[8]) {
     Op<3> o;
@@ -210,25 +208,17 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
   };
 
   float head_sum = 0.f;
-  Borders border;
-  if (blk0 < live) stage(blk0), border = load_borders(blk0);
+  Border grad;
+  if (blk0 < live) stage(blk0), grad = load_grad(blk0);
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   for (int64_t blk = blk0; blk < live; ++blk) {
     const int64_t t0 = blk * kBlk + 16 * w;
     const int rows_r = kIn0 + (blk & 1) * 4 * kRows, rows_k = rows_r + kRows, rows_v = rows_k + kRows, rows_d = rows_v + kRows;
-    float s8[8];
-    {
-      float g8[8];
-      state_of(border.s, border.sd, border.sm, s8);
-      state_of(border.g, border.gd, border.gm, g8);
-      stage(blk + 1);
-      put_pieces(g8);
-      float x = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x = fmaf(s8[i], g8[i], x);
-      x = wave_sum(x);
-      if (lane == 0) f32s(kPerTile)[kTiles + w] = x;
-    }
+    float g8[8];
+    state_of(grad, g8);
+    stage(blk + 1);
+    put_pieces(g8);
+    const Border state = load_border(p.states, p.marks, p.mark_decay, p.state_stride, 0, blk);
     // decays of the tile's tokens, in all four rows of lanes
     float left, into;
     double c;
@@ -375,9 +365,17 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
         store_pair<false>(vb, li * row_bytes + 64 * hh + 16 * q, av[2 * hh], av[2 * hh + 1]);
       }
     }
+    grad = load_grad(blk + 1);
     lds_barrier();
-    put_pieces(s8);
-    border = load_borders(blk + 1);
+    {
+      float s8[8], x = 0.f;
+      state_of(state, s8);
+      put_pieces(s8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x = fmaf(s8[i], g8[i], x);
+      x = wave_sum(x);
+      if (lane == 0) f32s(kPerTile)[kTiles + wave] = x;
+    }
     lds_barrier();
     {  // dr, alike with the state before the block
       float rs = 0.f;
