@@ -135,17 +135,13 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
   // where the wave's 16 rows of a block start in every tensor, and the bytes to the end of the last of n of them
   auto rows_at = [&](int64_t blk) { return ((b * T + blk * kBlk + 16 * w) * p.seq.H + h) * (int64_t)kRow; };
   auto rows_bytes = [&](int64_t n) { return n <= 0 ? 0 : (uint32_t)((n < 16 ? n : 16) - 1) * row_bytes + kRow; };
-  auto stage = [&](int64_t blk) {
-    const int64_t from = rows_at(blk);
-    const uint32_t bytes = rows_bytes(len - blk * kBlk - 16 * w);
-    const uint32_t to = lds0 + kIn0 + (blk & 1) * 4 * kRows + w * 16 * kRow;
-    const void* src[4] = {p.r, p.k, p.v, p.dy};
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const u32x4 d = descriptor(static_cast<const char*>(src[x]) + from, bytes);
-      to_lds16(d, src0, to + x * kRows);
-      to_lds16(d, src1, to + x * kRows + 8 * kRow);
-    }
+  auto stage = [&](const void* x, int number, int64_t blk) {
+    const u32x4 d = descriptor(static_cast<const char*>(x) + rows_at(blk), rows_bytes(len - blk * kBlk - 16 * w));
+    const uint32_t to = lds0 + kIn0 + ((blk & 1) * 4 + number) * kRows + w * 16 * kRow;
+    to_lds16(d, src0, to);
+    to_lds16(d, src1, to + 8 * kRow);
+  };
+  auto stage_w = [&](int64_t blk) {
     if (wave < 4 && lane < kSub) {
       const int64_t t32 = blk * kBlk + wave * kSub;
       const Span s = log_w_span(p.log_w, p.per_token, p.seq, b, h, t32, len);
@@ -209,14 +205,20 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
 
   float head_sum = 0.f;
   Border grad;
-  if (blk0 < live) stage(blk0), grad = load_grad(blk0);
+  if (blk0 < live) {
+    stage(p.r, 0, blk0), stage(p.k, 1, blk0), stage(p.v, 2, blk0), stage(p.dy, 3, blk0), stage_w(blk0);
+    grad = load_grad(blk0);
+  }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   for (int64_t blk = blk0; blk < live; ++blk) {
     const int64_t t0 = blk * kBlk + 16 * w;
     const int rows_r = kIn0 + (blk & 1) * 4 * kRows, rows_k = rows_r + kRows, rows_v = rows_k + kRows, rows_d = rows_v + kRows;
     float g8[8];
     state_of(grad, g8);
-    stage(blk + 1);
+    // the next block's rows, a tensor at a time through the block: all at once they fill the queue of loads and hold the
+    // waves up where they are asked for
+    stage_w(blk + 1);
+    stage(p.r, 0, blk + 1);
     put_pieces(g8);
     const Border state = load_border(p.states, p.marks, p.mark_decay, p.state_stride, 0, blk);
     // decays of the tile's tokens, in all four rows of lanes
@@ -259,6 +261,7 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
       const double r = reinterpret_cast<const double*>(lds + kSums)[16 * w + 4 * q + i];
       dj[i] = exp_diff(c, r), di[i] = exp_diff(r, c);
     }
+    stage(p.k, 1, blk + 1);
     // the pairs with the tiles behind (for dk, dv) and before (for dr)
     f32x4 ak[4], av[4], ar[4];
 #pragma unroll
@@ -291,6 +294,7 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
       }
     }
     __builtin_amdgcn_sched_barrier(0);
+    stage(p.v, 2, blk + 1);
     between = 1.f;
 #pragma clang loop unroll(disable)
     for (int J = w - 1; J >= 0; J -= 2) {
@@ -310,6 +314,7 @@ __global__ __launch_bounds__(512, 2) void linattn_grad16_kernel(Grad16Params p) 
       for (int t = 0; t < 4; ++t) ar[t] = mma(turned_tokens(rows_k, J, J1, t), P, ar[t]);
     }
     __builtin_amdgcn_sched_barrier(0);  // phases whose registers would not fit together
+    stage(p.dy, 3, blk + 1);
     float cross = 0.f, kdk = 0.f, rdr = 0.f;
     {  // dk and dv: the gradient behind the block, the factor of the tokens, the tile's own pairs
 #pragma unroll

@@ -233,17 +233,11 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
              *next_v = static_cast<const char*>(p.v) + start;
   int64_t left = len - first;  // tokens from the next staged one on
   const uint32_t to0 = lds0 + kStage + quarter * 3 * kTile + 16 * half * kRow;
-  auto stage_rkv = [&]() {
-    const uint32_t bytes = left <= 0 ? 0 : (uint32_t)((left < kSub ? left : kSub) - 1) * row_bytes + kRow;
-    const u32x4 k = descriptor(next_k, bytes), v = descriptor(next_v, bytes), r = descriptor(next_r, bytes);
-    to_lds16(k, src0, to0 + kTile);
-    to_lds16(k, src1, to0 + kTile + 8 * kRow);
-    to_lds16(v, src0, to0 + 2 * kTile);
-    to_lds16(v, src1, to0 + 2 * kTile + 8 * kRow);
-    to_lds16(r, src0, to0);
-    to_lds16(r, src1, to0 + 8 * kRow);
-    const int64_t step = (int64_t)kBlk * row_bytes;
-    next_r += step, next_k += step, next_v += step, left -= kBlk;
+  auto stage = [&](const char*& x, int number) {
+    const u32x4 d = descriptor(x, left <= 0 ? 0 : (uint32_t)((left < kSub ? left : kSub) - 1) * row_bytes + kRow);
+    to_lds16(d, src0, to0 + number * kTile);
+    to_lds16(d, src1, to0 + number * kTile + 8 * kRow);
+    x += (int64_t)kBlk * row_bytes;
   };
   auto stage_w = [&](int64_t blk) {
     if (half == 1 && lane < kSub) {
@@ -288,7 +282,8 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
   };
   if (blk0 < live) {
     stage_w(blk0), stage_w(blk0 + 1), stage_w(blk0 + 2);
-    stage_rkv();
+    stage(next_k, 1), stage(next_v, 2), stage(next_r, 0);
+    left -= kBlk;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     if (half == 1) fill(blk0);
   }
@@ -307,8 +302,9 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
         for (int hh = 0; hh < 2; ++hh) K[J][hh] = staged(rows_k, J, hh), R[J][hh] = staged(rows_r, J, hh);
       const Op<1> v0 = staged(rows_v, 0, half), v1 = staged(rows_v, 1, half);
       lds_barrier();  // both waves of every quarter have their operands
+      // the next block's rows, a tensor at a time: all at once they fill the queue of loads and hold the waves up
       stage_w(blk + 3);
-      stage_rkv();
+      stage(next_k, 1);
       const f32x4 left0 = *reinterpret_cast<const f32x4*>(f.left + 4 * q);
       const f32x4 left1 = *reinterpret_cast<const f32x4*>(f.left + 16 + 4 * q);
       in[0] = f.in[li], in[1] = f.in[16 + li];
@@ -327,6 +323,7 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
 #pragma unroll
         for (int m = 0; m < kVt; ++m) exch[quarter][half][kVt * t + m][lane] = mma(Kt, Vs[m], zero4());
       }
+      stage(next_v, 2);
       // the pairs inside the 32 tokens
       f32x4 a00 = zero4(), a01 = zero4(), a11 = zero4();
 #pragma unroll
@@ -340,6 +337,8 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
 #pragma unroll
       for (int m = 0; m < kVt; ++m) y[0][m] = mma(Vt[m], P0, zero4()), y[1][m] = mma(Vt[m], P1, zero4());
     }
+    stage(next_r, 0);
+    left -= kBlk;
     lds_barrier();
     // The states before each quarter's tokens: this wave takes its two tiles through them, and leaves each as two
     // bfloat16 pieces where it found what the quarter adds (nobody else reads that).
