@@ -128,6 +128,7 @@ class _Torch:
         import torch
         self.module = torch
         self.Tensor = torch.Tensor
+        self.empty_like = torch.empty_like
         self.f32 = (torch.float32,)
         self.inputs = (torch.bfloat16, torch.float32)
         self.i32 = (torch.int32,)
@@ -182,6 +183,17 @@ def _expect(t, name, shape, dtypes, like, optional=False):
         raise ValueError("%s must be 16-byte aligned" % name)
     if t.device != like.device:
         raise ValueError("%s is on %s, the other tensors on %s" % (name, t.device, like.device))
+
+
+def _at(t, name, shape, dtypes, like, optional=False):
+    """The address of a tensor that is as _expect() wants it (None for an empty or a left out one)."""
+    if t.__class__ is _T.Tensor and t.shape == shape and t.dtype in dtypes and t.is_contiguous() and \
+            t.get_device() == like.get_device():
+        p = t.data_ptr()
+        if not p & 15:
+            return p or None
+    _expect(t, name, shape, dtypes, like, optional)
+    return _ptr(t)
 
 
 def _on_gpu(like, stream):
@@ -394,174 +406,170 @@ def rwkv7_stack_forward(w_in, w_out, vecs, x, states, stream=None):
 
 # ---- linear attention with a decay for each head
 
-def _launch(fn, args, like, stream):
+def _launch(name, args, like, stream):
     """Call the library with `like`'s device current (a stream given by the caller may be another device's)."""
-    if like.device.index == _T.current_device():
-        _check(fn(*args, _stream(stream)))
+    index = like.get_device()
+    if index < 0 or (stream is None and index != _T.current_device()):
+        _on_gpu(like, stream)  # says what is wrong
+    fn = getattr(lib(), name)
+    if index == _T.current_device():
+        _check(fn(*args, _T.raw_stream(index) if stream is None else _stream(stream)))
     else:
-        with _T.module.cuda.device(like.device):
+        with _T.module.cuda.device(index):
             _check(fn(*args, _stream(stream)))
 
 
-def _decay_code(log_w, B, T, H) -> int:
-    """Which of the two layouts log_w has."""
-    if not isinstance(log_w, _T.Tensor):
-        raise TypeError("log_w must be a torch.Tensor, not %s" % type(log_w).__name__)
-    if log_w.dim() not in (1, 3):
-        raise ValueError("log_w has shape %s, expected (%d,) or (%d, %d, %d)" % (tuple(log_w.shape), H, B, T, H))
-    return RWKV7_DECAY_HEAD if log_w.dim() == 1 else RWKV7_DECAY_TOKEN
-
-
-def _linattn_inputs(r, log_w, k, v, state_in, lens):
-    """Checks the inputs that the linear attention's calls share; returns (B, T, H, N, decay)."""
+def _linattn_inputs(r, log_w, k, v, state_in):
+    """The addresses of the inputs that the linear attention's calls share, the sizes and log_w's layout."""
     if not isinstance(r, _T.Tensor) or r.dim() != 4:
         raise ValueError("r must be a [B, T, H, N] tensor")
-    B, T, H, N = r.shape
-    _expect(r, "r", r.shape, _input_dtypes(), r)
-    decay = _decay_code(log_w, B, T, H)
-    _expect(log_w, "log_w", (H,) if decay == RWKV7_DECAY_HEAD else (B, T, H), _f32(), r)
-    for name, t in (("k", k), ("v", v)):
-        _expect(t, name, r.shape, (r.dtype,), r)
-    _expect(state_in, "state_in", (B, H, N, N), _f32(), r, optional=True)
-    _expect(lens, "lens", (B,), _T.i32, r, optional=True)
-    return B, T, H, N, decay
+    shape = r.shape
+    B, T, H, N = shape
+    at = [_at(r, "r", shape, _T.inputs, r)]
+    if not isinstance(log_w, _T.Tensor):
+        raise TypeError("log_w must be a torch.Tensor, not %s" % type(log_w).__name__)
+    decay = RWKV7_DECAY_HEAD if log_w.dim() == 1 else RWKV7_DECAY_TOKEN
+    at.append(_at(log_w, "log_w", (H,) if decay == RWKV7_DECAY_HEAD else (B, T, H), _T.f32, r))
+    same = (r.dtype,)
+    at.append(_at(k, "k", shape, same, r))
+    at.append(_at(v, "v", shape, same, r))
+    at.append(None if state_in is None else _at(state_in, "state_in", (B, H, N, N), _T.f32, r))
+    return at, shape, same, decay
 
 
 def rwkv7_linattn_prefill(r, log_w, k, v, state_in, lens, y, state_out, stream=None):
     """Linear attention over a prompt. r, k, v, y [B,T,H,64] in one dtype; log_w float32 [H] or [B,T,H];
     lens int32 [B] or None; states float32 [B,H,64,64] or None."""
-    B, T, H, N, decay = _linattn_inputs(r, log_w, k, v, state_in, lens)
-    _expect(y, "y", (B, T, H, N), (r.dtype,), r)
-    _expect(state_out, "state_out", (B, H, N, N), _f32(), r, optional=True)
-    _on_gpu(r, stream)
-    args = [_ptr(x) for x in (r, log_w, k, v, state_in, lens, y, state_out)] + [B, T, H, N, _dtype_code(r), decay]
-    _launch(lib().rwkv7_linattn_prefill, args, r, stream)
+    at, shape, same, decay = _linattn_inputs(r, log_w, k, v, state_in)
+    B, T, H, N = shape
+    at.append(None if lens is None else _at(lens, "lens", (B,), _T.i32, r))
+    at.append(_at(y, "y", shape, same, r))
+    at.append(None if state_out is None else _at(state_out, "state_out", (B, H, N, N), _T.f32, r))
+    at += (B, T, H, N, _dtype_code(r), decay)
+    _launch("rwkv7_linattn_prefill", at, r, stream)
 
 
 def rwkv7_linattn_step(r, log_w, k, v, state_in, y, state_out, stream=None):
     """Single-token step (T == 1) of the linear attention; state_out may be state_in."""
-    B, T, H, N, decay = _linattn_inputs(r, log_w, k, v, state_in, None)
-    _expect(y, "y", (B, T, H, N), (r.dtype,), r)
-    _expect(state_out, "state_out", (B, H, N, N), _f32(), r, optional=True)
-    _on_gpu(r, stream)
-    args = [_ptr(x) for x in (r, log_w, k, v, state_in, y, state_out)] + [B, T, H, N, _dtype_code(r), decay]
-    _launch(lib().rwkv7_linattn_step, args, r, stream)
+    at, shape, same, decay = _linattn_inputs(r, log_w, k, v, state_in)
+    B, T, H, N = shape
+    at.append(_at(y, "y", shape, same, r))
+    at.append(None if state_out is None else _at(state_out, "state_out", (B, H, N, N), _T.f32, r))
+    at += (B, T, H, N, _dtype_code(r), decay)
+    _launch("rwkv7_linattn_step", at, r, stream)
 
 
 def linattn(r, log_w, k, v, state_in=None, lens=None, want_state=True, stream=None):
     """Allocate y ([B,T,H,64] in r's dtype) and the final state, run the prompt, return (y, state_out)."""
-    import torch
     B, T, H, N = r.shape
-    y = torch.empty_like(r)
-    s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device) if want_state else None
-    rwkv7_linattn_prefill(r, log_w, k, v, state_in, lens, y, s_out, stream=stream)
+    y = _T.empty_like(r)
+    s_out = r.new_empty((B, H, N, N), dtype=_T.f32[0]) if want_state else None
+    rwkv7_linattn_prefill(r, log_w, k, v, state_in, lens, y, s_out, stream)
     return y, s_out
 
 
 def linattn_step(r, log_w, k, v, state_in=None, stream=None):
     """Allocate y ([B,1,H,64] in r's dtype) and the new state, run one token, return (y, state_out).
     rwkv7_linattn_step updates a state in place."""
-    import torch
     B, T, H, N = r.shape
-    y = torch.empty_like(r)
-    s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device)
-    rwkv7_linattn_step(r, log_w, k, v, state_in, y, s_out, stream=stream)
+    y = _T.empty_like(r)
+    s_out = r.new_empty((B, H, N, N), dtype=_T.f32[0])
+    rwkv7_linattn_step(r, log_w, k, v, state_in, y, s_out, stream)
     return y, s_out
 
 
 def rwkv7_linattn_backward(r, log_w, k, v, state_in, lens, dy, dstate_out, dr, dlog_w, dk, dv, dstate_in, stream=None):
     """Gradients of the linear attention: dr, dk, dv in r's dtype, dlog_w float32 in log_w's layout, dstate_in
     float32 or None (may be dstate_out)."""
-    B, T, H, N, decay = _linattn_inputs(r, log_w, k, v, state_in, lens)
-    _expect(dy, "dy", r.shape, (r.dtype,), r)
-    _expect(dstate_out, "dstate_out", (B, H, N, N), _f32(), r, optional=True)
-    for name, t in (("dr", dr), ("dk", dk), ("dv", dv)):
-        _expect(t, name, r.shape, (r.dtype,), r)
-    _expect(dlog_w, "dlog_w", log_w.shape, _f32(), r)
-    _expect(dstate_in, "dstate_in", (B, H, N, N), _f32(), r, optional=True)
-    _on_gpu(r, stream)
-    args = [_ptr(x) for x in (r, log_w, k, v, state_in, lens, dy, dstate_out, dr, dlog_w, dk, dv, dstate_in)]
-    _launch(lib().rwkv7_linattn_backward, args + [B, T, H, N, _dtype_code(r), decay], r, stream)
+    at, shape, same, decay = _linattn_inputs(r, log_w, k, v, state_in)
+    B, T, H, N = shape
+    states = (B, H, N, N)
+    at.append(None if lens is None else _at(lens, "lens", (B,), _T.i32, r))
+    at.append(_at(dy, "dy", shape, same, r))
+    at.append(None if dstate_out is None else _at(dstate_out, "dstate_out", states, _T.f32, r))
+    at.append(_at(dr, "dr", shape, same, r))
+    at.append(_at(dlog_w, "dlog_w", log_w.shape, _T.f32, r))
+    at.append(_at(dk, "dk", shape, same, r))
+    at.append(_at(dv, "dv", shape, same, r))
+    at.append(None if dstate_in is None else _at(dstate_in, "dstate_in", states, _T.f32, r))
+    at += (B, T, H, N, _dtype_code(r), decay)
+    _launch("rwkv7_linattn_backward", at, r, stream)
 
 
 def linattn_backward(r, log_w, k, v, dy, state_in=None, lens=None, dstate_out=None, want_dstate=True, stream=None):
     """Allocate the gradients, run the backward, return dict dr, dlog_w, dk, dv, dstate_in."""
-    import torch
     B, T, H, N = r.shape
-    out = {n: torch.empty_like(r) for n in ("dr", "dk", "dv")}
-    out["dlog_w"] = torch.empty_like(log_w)
-    out["dstate_in"] = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device) if want_dstate else None
+    out = {n: _T.empty_like(r) for n in ("dr", "dk", "dv")}
+    out["dlog_w"] = _T.empty_like(log_w)
+    out["dstate_in"] = r.new_empty((B, H, N, N), dtype=_T.f32[0]) if want_dstate else None
     rwkv7_linattn_backward(r, log_w, k, v, state_in, lens, dy, dstate_out, out["dr"], out["dlog_w"], out["dk"],
-                           out["dv"], out["dstate_in"], stream=stream)
+                           out["dv"], out["dstate_in"], stream)
     return out
 
 
 # ---- layer norm over groups of channels
 
 def _rows(x, groups):
-    """x's rows and channels: the last dimension is normalised, in `groups` groups."""
+    """x's address, rows and channels: the last dimension is normalised, in `groups` groups."""
     if not isinstance(x, _T.Tensor) or x.dim() < 1:
         raise ValueError("x must be a tensor with the channels in its last dimension")
-    _expect(x, "x", x.shape, _input_dtypes(), x)
-    D, G = x.shape[-1], int(groups)
+    shape = x.shape
+    at = _at(x, "x", shape, _T.inputs, x)
+    D, G = shape[-1], int(groups)
     if G < 1 or D % G:
         raise ValueError("groups is %d, expected a divisor of the %d channels" % (G, D))
-    M = 1
-    for n in x.shape[:-1]:
-        M *= n
-    return M, D, G
+    M = shape[0] if len(shape) == 2 else shape[:-1].numel()
+    return at, shape, M, D, G
 
 
 def rwkv7_layernorm_forward(x, weight, bias, y, mean, rstd, groups=1, eps=1e-5, stream=None):
     """Layer norm of x's last dimension in `groups` groups. x and y [..., D] in float32 or bfloat16 (each its
     own), weight and bias [D] float32 or None, mean and rstd [..., groups] float32 or None."""
-    M, D, G = _rows(x, groups)
-    _expect(weight, "weight", (D,), _f32(), x, optional=True)
-    _expect(bias, "bias", (D,), _f32(), x, optional=True)
-    _expect(y, "y", x.shape, _input_dtypes(), x)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _expect(t, name, x.shape[:-1] + (G,), _f32(), x, optional=True)
-    _on_gpu(x, stream)
-    args = [_ptr(t) for t in (x, weight, bias, y, mean, rstd)] + [M, D, G, float(eps), _dtype_code(x), _dtype_code(y)]
-    _launch(lib().rwkv7_layernorm_forward, args, x, stream)
+    at_x, shape, M, D, G = _rows(x, groups)
+    stats = shape[:-1] + (G,)
+    args = [at_x,
+            None if weight is None else _at(weight, "weight", (D,), _T.f32, x),
+            None if bias is None else _at(bias, "bias", (D,), _T.f32, x),
+            _at(y, "y", shape, _T.inputs, x),
+            None if mean is None else _at(mean, "mean", stats, _T.f32, x),
+            None if rstd is None else _at(rstd, "rstd", stats, _T.f32, x),
+            M, D, G, eps, _dtype_code(x), _dtype_code(y)]
+    _launch("rwkv7_layernorm_forward", args, x, stream)
 
 
 def rwkv7_layernorm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, groups=1, stream=None):
     """Gradients of the layer norm from its x, weight, mean and rstd; dweight and dbias [D] float32 or None."""
-    M, D, G = _rows(x, groups)
-    _expect(weight, "weight", (D,), _f32(), x, optional=True)
-    for name, t in (("mean", mean), ("rstd", rstd)):
-        _expect(t, name, x.shape[:-1] + (G,), _f32(), x)
-    _expect(dy, "dy", x.shape, _input_dtypes(), x)
-    _expect(dx, "dx", x.shape, (x.dtype,), x)
-    _expect(dweight, "dweight", (D,), _f32(), x, optional=True)
-    _expect(dbias, "dbias", (D,), _f32(), x, optional=True)
-    _on_gpu(x, stream)
-    args = [_ptr(t) for t in (x, weight, mean, rstd, dy, dx, dweight, dbias)] + \
-        [M, D, G, _dtype_code(x), _dtype_code(dy)]
-    _launch(lib().rwkv7_layernorm_backward, args, x, stream)
+    at_x, shape, M, D, G = _rows(x, groups)
+    stats = shape[:-1] + (G,)
+    args = [at_x,
+            None if weight is None else _at(weight, "weight", (D,), _T.f32, x),
+            _at(mean, "mean", stats, _T.f32, x),
+            _at(rstd, "rstd", stats, _T.f32, x),
+            _at(dy, "dy", shape, _T.inputs, x),
+            _at(dx, "dx", shape, (x.dtype,), x),
+            None if dweight is None else _at(dweight, "dweight", (D,), _T.f32, x),
+            None if dbias is None else _at(dbias, "dbias", (D,), _T.f32, x),
+            M, D, G, _dtype_code(x), _dtype_code(dy)]
+    _launch("rwkv7_layernorm_backward", args, x, stream)
 
 
 def layernorm(x, weight=None, bias=None, groups=1, eps=1e-5, out_dtype=None, want_stats=True, stream=None):
     """Allocate y (in out_dtype, or x's) and the statistics, run the forward, return (y, mean, rstd)."""
-    import torch
-    y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    y = _T.empty_like(x, dtype=out_dtype)
     mean = rstd = None
     if want_stats:
-        mean = torch.empty(x.shape[:-1] + (groups,), dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
-    rwkv7_layernorm_forward(x, weight, bias, y, mean, rstd, groups=groups, eps=eps, stream=stream)
+        mean = x.new_empty(x.shape[:-1] + (groups,), dtype=_T.f32[0])
+        rstd = _T.empty_like(mean)
+    rwkv7_layernorm_forward(x, weight, bias, y, mean, rstd, groups, eps, stream)
     return y, mean, rstd
 
 
 def layernorm_backward(x, weight, mean, rstd, dy, groups=1, want_dweight=True, stream=None):
     """Allocate the gradients, run the backward, return dict dx, dweight, dbias (the last two None unless
     want_dweight)."""
-    import torch
-    out = {"dx": torch.empty(x.shape, dtype=x.dtype, device=x.device), "dweight": None, "dbias": None}
+    out = {"dx": _T.empty_like(x), "dweight": None, "dbias": None}
     if want_dweight:
-        out["dweight"] = torch.empty(x.shape[-1:], dtype=torch.float32, device=x.device)
-        out["dbias"] = torch.empty_like(out["dweight"])
-    rwkv7_layernorm_backward(x, weight, mean, rstd, dy, out["dx"], out["dweight"], out["dbias"], groups=groups,
-                             stream=stream)
+        out["dweight"] = x.new_empty(x.shape[-1:], dtype=_T.f32[0])
+        out["dbias"] = _T.empty_like(out["dweight"])
+    rwkv7_layernorm_backward(x, weight, mean, rstd, dy, out["dx"], out["dweight"], out["dbias"], groups, stream)
     return out
