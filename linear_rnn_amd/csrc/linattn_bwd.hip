@@ -1,20 +1,30 @@
-// Gradients of the linear attention with a decay for each head. The chunk algebra, number formats and
-// layouts are those of linattn_ops.hpp.
+// Gradients of the linear attention with a decay for each head (number formats and operand layouts in
+// linattn_ops.hpp).
 //
-// With G_t = dL/dS_t from the tokens behind t, for the 32 tokens of a wave (S_0 the state before them, G_32 the
-// gradient behind them, A_ij = r_i . k_j, P_ij = D_ij dy_i . v_j):
+// With G_t = dL/dS_t from the tokens behind t; for a block, S_0 the state before it, G the gradient behind it, c the sum of
+// log w from its start, D_ij = exp(c_i - c_j) for i >= j, P_ij = D_ij dy_i . v_j:
 //   dr_i = sum_{j<=i} P_ij k_j + exp(c_i) S_0^T dy_i
-//   dk_j = sum_{i>=j} P_ij r_i + exp(c_31 - c_j) G_32^T v_j
-//   dv_j = sum_{i>=j} D_ij A_ij dy_i + exp(c_31 - c_j) G_32 k_j
-//   G_0  = exp(c_31) G_32 + sum_i exp(c_i) dy_i r_i^T
-// A token's log decay scales every path that crosses it, from tokens j before it to tokens i from it on:
-//   dlog_w_t = sum_{j<t<=i} A_ij P_ij + sum_{i>=t} r_i . exp(c_i) S_0^T dy_i
-//            + sum_{j<t} k_j . exp(c_31 - c_j) G_32^T v_j + exp(c_31) <S_0, G_32>
-// each of them a sum of prefix and suffix sums, so that nothing cancels but what cancels in the value itself.
+//   dk_j = sum_{i>=j} P_ij r_i + exp(c_end - c_j) G^T v_j
+//   dv_j = sum_{i>=j} D_ij (r_i . k_j) dy_i + exp(c_end - c_j) G k_j
+// With S_0 and G of every block at hand (linattn_state.hip), the blocks are independent. A workgroup takes the blocks of
+// a segment one after the other, each of its waves 16 tokens (a tile): dr of its tokens i from the tiles J before,
+// dk and dv of its tokens j from the tiles I behind, and each from the block's border through S_0 and G. That is
+// quadratic within a block, but neither S nor G has to be carried through it, and what all waves need of them, their
+// bfloat16 pieces, is formed once.
 //
-// Kernels: the states before the blocks of 128 tokens (linattn_state.hip: the sums of pieces, a scan), then a
-// workgroup for each head and segment walks its blocks from the last to the first with G carried in LDS; its
-// four waves take 32 tokens each and exchange what they add to S (forwards) and to G (backwards).
+// Decays. With c now the sum since a tile's start, the factor between token j of tile J and i of a later tile I is
+// left_j (J's end to the tiles between) in_i: left_j = exp(c_end - c_j), in_i = exp(c_i), all at most 1. A wave's own
+// factor is common to all of its tokens' sums, so it is applied once, to the accumulators, and only the tile on the
+// diagonal needs a factor for each pair.
+//
+// dlog_w_t, t in tile w: the pairs of the tile that cross t, the sums over i >= t of r_i . dr_i from before the tile, over
+// j < t of k_j . dk_j to behind it, and the paths over the whole tile: <S_0, G> with the block's decay, what S_0 gives
+// to later tiles, what earlier tiles give to G, and the pairs of earlier with later tiles. All of them are sums of what
+// crosses t, so nothing cancels.
+//
+// bfloat16: blocks of 128 tokens, eight waves; rows come to LDS by direct loads a block ahead, and with two buffers and
+// the pieces of one state the LDS is full, so that dk and dv are done with G, then dr with S in the same place.
+// float32: the rows are kept as three bfloat16 pieces each, so blocks of 64 tokens, four waves, one buffer.
 #include "linattn_internal.hpp"
 #include "linattn_ops.hpp"
 #include "wkv7_internal.hpp"
@@ -24,339 +34,501 @@ namespace {
 
 using namespace linattn;
 
+constexpr int kRow = kN * 2;  // bytes of a row of one piece
+constexpr int kPiece = kN * kRow;  // of one piece of a state
+// Sizes and the LDS of one element type.
+template <bool F32>
+struct Cfg {
+  static constexpr int kTiles = F32 ? 4 : 8;      // 16-token tiles of a block, one a wave
+  static constexpr int kTokens = 16 * kTiles;
+  static constexpr int kRows = kTokens * kRow;    // one piece of one tensor's rows of a block
+  static constexpr int kIn = 0;                   // bfloat16: [parity][r, k, v, dy] kRows; float32: [r, k, v, dy][piece]
+  static constexpr int kPieces = (F32 ? 12 : 8) * kRows;  // [piece][64 values] rows of 64 keys
+  static constexpr int kSums = kPieces + 3 * kPiece;      // [kTokens] double: c
+  static constexpr int kLeft = kSums + kTokens * 8;       // [kTokens] float
+  static constexpr int kInto = kLeft + kTokens * 4;       // [kTokens] float
+  static constexpr int kPerTile = kInto + kTokens * 4;    // [4][kTiles] float: exp(c_end), and the three sums below
+  static constexpr int kPairs = kPerTile + 4 * kTiles * 4;     // [J][I] float: sums over the pairs of two tiles
+  static constexpr int kLogW = kPairs + kTiles * kTiles * 4;   // bfloat16: [parity][kTokens] float
+  static constexpr int kLds = kLogW + (F32 ? 0 : 2 * kTokens * 4);
+  static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
+};
+
 struct GradParams {
   const void* r;
   const float* log_w;
   const void* k;
   const void* v;
   const void* dy;
-  const float* s_in;       // the caller's state (pieces == 1), may be null
-  const float* ds_out;     // the caller's (nseg == 1), may be null
-  const float* states;     // [units][pieces] states before the pieces (pieces > 1)
-  const float* marks;      // [units][blocks]
-  const float* mark_decay; // [units][blocks]
-  const float* grads;      // [units][pieces] gradients behind the pieces (nseg > 1)
+  // the state before a block: of its piece (or the caller's), decayed since, and the piece's sum up to the block
+  const float* states;
+  const float* marks;
+  const float* mark_decay;
+  const float* grads;  // the gradient behind a block, alike
+  const float* grad_marks;
+  const float* grad_mark_decay;
+  int64_t state_stride, grad_stride;  // states of a sequence
   void* dr;
   float* dlog_w;  // per token, or [units][nseg] sums
   void* dk;
   void* dv;
-  float* ds_in;  // may be null
   Seq seq;
   int32_t per_token;
   int32_t nseg;
-  int64_t pieces, seg_pieces;  // of a sequence, of a segment
+  int64_t seg_blocks;
 };
 
-// Sums over 32 lanes' values from each on (lane l and l + 32 alike), and of those before each.
-__device__ __forceinline__ float sum_from(float x, int lane) {
-  x += dpp_f32<0x101>(x);  // row_shl:1, 2, 4, 8 (zeros come in)
-  x += dpp_f32<0x102>(x);
-  x += dpp_f32<0x104>(x);
-  x += dpp_f32<0x108>(x);
-  const float second = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 16));
-  return (lane & 16) ? x : x + second;
+// Where 16-byte piece `piece` of a row is: exchanged within the row so that reads of one piece of 16 rows, and turned
+// reads of four pieces of 8 rows, meet as many banks as there are; rows that follow each other in a block's inputs,
+// rows as channel() numbers them in a state's pieces.
+__device__ __forceinline__ int row_key(int row) { return (row >> 1 & 1) | (row >> 2 & 2) | (row & 4); }
+__device__ __forceinline__ int swizzled(int row, int piece) { return row * kRow + 16 * (piece ^ row_key(row)); }
+__device__ __forceinline__ int in_pieces(int row, int piece) {
+  return row * kRow + 16 * (piece ^ ((row >> 1 & 1) | (row >> 3 & 2) | (row >> 1 & 4)));
 }
-__device__ __forceinline__ float row_sums_to(float x) {  // of a row's 16 lanes up to each
-  x += dpp_f32<0x111>(x);  // row_shr
+
+// Sums over a row of 16 lanes up to each lane, and from each lane on.
+__device__ __forceinline__ float sums_to(float x) {
+  x += dpp_f32<0x111>(x);
   x += dpp_f32<0x112>(x);
   x += dpp_f32<0x114>(x);
   x += dpp_f32<0x118>(x);
   return x;
 }
-__device__ __forceinline__ float sum_before(float x, int lane) {
-  const float first = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, row_sums_to(x)), 15));
-  const float s = row_sums_to(dpp_f32<0x111>(x));
-  return (lane & 16) ? s + first : s;
+__device__ __forceinline__ float sums_from(float x) {
+  x += dpp_f32<0x101>(x);
+  x += dpp_f32<0x102>(x);
+  x += dpp_f32<0x104>(x);
+  x += dpp_f32<0x108>(x);
+  return x;
 }
+__device__ __forceinline__ float wave_sum(float x) { return rows_sum(row16_sum(x)); }
+
+// Element 4e + i of an operand, as float32.
+template <int NP>
+__device__ __forceinline__ float value(const Op<NP>& o, int e, int i) {
+  float x = (float)o.p[NP - 1][4 * e + i];
+#pragma unroll
+  for (int n = NP - 2; n >= 0; --n) x += (float)o.p[n][4 * e + i];
+  return x;
+}
+
+// Eight floats of a state: row `row`, columns from `col`; zeros where there is no state.
+struct Eight {
+  f32x4 x[2];
+};
+__device__ __forceinline__ Eight load_eight(const float* states, int64_t index, bool there, int row, int col) {
+  const __amdgpu_buffer_rsrc_t b = buffer(states + index * (kN * kN), there ? kN * kN * 4 : 0);
+  const uint32_t off = (row * kN + col) * 4;
+  return Eight{{__builtin_bit_cast(f32x4, load16(b, off)), __builtin_bit_cast(f32x4, load16(b, off + 16))}};
+}
+
+template <int M>
+struct Border {
+  Eight piece[M], mark[M];  // the piece's state or gradient, and what the piece adds to it
+  float decay;              // since the piece's border
+};
+
 template <bool F32>
-__global__ __launch_bounds__(256, 1) void linattn_grad_kernel(GradParams p) {
+__global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_grad_kernel(GradParams p) {
+  using C = Cfg<F32>;
+  constexpr int kTiles = C::kTiles, kTokens = C::kTokens, kRows = C::kRows, kPieces = C::kPieces;
   constexpr int NI = kIn<F32>, NO = F32 ? 3 : 2;
-  extern __shared__ f32x4 shared[];
-  f32x4(*addS)[16][64] = reinterpret_cast<f32x4(*)[16][64]>(shared);              // of waves 0 .. 2
-  f32x4(*addG)[16][64] = reinterpret_cast<f32x4(*)[16][64]>(shared + 3 * 1024);   // of waves 0 .. 3
-  f32x4(*carry)[64] = reinterpret_cast<f32x4(*)[64]>(shared + 7 * 1024);          // G behind the block
-  double(*sums)[kSub] = reinterpret_cast<double(*)[kSub]>(shared + 8 * 1024);     // [kWaves]
-  float* all = reinterpret_cast<float*>(shared + 8 * 1024 + kWaves * kSub / 2);
+  extern __shared__ char lds[];
   const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t id = xcd_swizzle(blockIdx.x, gridDim.x);
-  const int64_t unit = id / p.nseg;
-  const int32_t seg = id % p.nseg;
+  // The wave's tile. Tile w has w tiles before it (one product of pairs each) and 7 - w behind it (two), and the waves
+  // i and i + 4 share a SIMD: tiles w and 7 - w together have the same work on every one. (float32: tile w is wave w's.)
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave < 4 ? wave : 11 - wave;
+  const int64_t unit = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
   const int64_t b = unit / p.seq.H;
   const int32_t h = unit % p.seq.H;
   const int64_t T = p.seq.T, len = seq_len(p.seq, b);
-  const uint32_t row_bytes = p.seq.H * kN * kEsz<F32>;
-  const int64_t nblk = (T + kBlk - 1) / kBlk;
-  const int64_t blk0 = seg * p.seg_pieces * kPieceBlocks;
-  int64_t blk1 = blk0 + p.seg_pieces * kPieceBlocks;
-  if (blk1 > nblk) blk1 = nblk;
-  const int last_piece = (int)((blk1 - 1) / kPieceBlocks);
-  const uint32_t off = li * row_bytes + q * 8 * kEsz<F32>;
-  auto at = [&](const void* x, int64_t t0, int64_t n) { return token_buffer<kEsz<F32>>(x, p.seq, b, h, t0, n, kSub); };
+  constexpr int kRowBytes = kN * kEsz<F32>;  // a token's, in memory
+  const uint32_t row_bytes = p.seq.H * kRowBytes;
+  const int64_t nblk = (T + kTokens - 1) / kTokens;
+  const int64_t blk0 = seg * p.seg_blocks;
+  const int64_t blk1 = blk0 + p.seg_blocks < nblk ? blk0 + p.seg_blocks : nblk;
+  const int64_t live = (len + kTokens - 1) / kTokens < blk1 ? (len + kTokens - 1) / kTokens : blk1;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
+  auto f32s = [&](int at) { return reinterpret_cast<float*>(lds + at); };
 
+  // ---- loads
+  const uint32_t src0 = (lane >> 3) * row_bytes + 16 * ((lane & 7) ^ row_key(lane >> 3));
+  const uint32_t src1 = ((lane >> 3) + 8) * row_bytes + 16 * ((lane & 7) ^ row_key(8 + (lane >> 3)));
+  // where the wave's 16 rows of a block start in every tensor, and the bytes to the end of the last of n of them
+  auto rows_at = [&](int64_t blk) { return ((b * T + blk * kTokens + 16 * w) * p.seq.H + h) * (int64_t)kRowBytes; };
+  auto rows_bytes = [&](int64_t n) { return n <= 0 ? 0 : (uint32_t)((n < 16 ? n : 16) - 1) * row_bytes + kRowBytes; };
+  auto stage = [&](const void* x, int number, int64_t blk) {
+    const u32x4 d = descriptor(static_cast<const char*>(x) + rows_at(blk), rows_bytes(len - blk * kTokens - 16 * w));
+    const uint32_t to = lds0 + C::kIn + ((blk & 1) * 4 + number) * kRows + w * 16 * kRow;
+    to_lds16(d, src0, to);
+    to_lds16(d, src1, to + 8 * kRow);
+  };
+  auto stage_w = [&](int64_t blk) {
+    if (wave < 4 && lane < kSub) {
+      const int64_t t32 = blk * kTokens + wave * kSub;
+      const Span s = log_w_span(p.log_w, p.per_token, p.seq, b, h, t32, len);
+      to_lds4(descriptor(s.base, s.bytes), lane * (p.per_token ? p.seq.H * 4 : 0),
+              lds0 + C::kLogW + (blk & 1) * kTokens * 4 + wave * kSub * 4);
+    }
+  };
+  // float32: the wave's rows from memory to LDS by way of registers, in pieces
+  struct Rows {
+    u32x4 x[4][2][F32 ? 2 : 1];
+  };
+  auto load_rows = [&](int64_t blk) {
+    Rows o;
+    const void* src[4] = {p.r, p.k, p.v, p.dy};
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const int tu = 4 * wave + m;
-    f32x4 g = zero4();
-    if (p.nseg > 1)
-      g = *state_tile(p.grads, unit * p.pieces + last_piece, tu, lane);
-    else if (p.ds_out)
-      g = *reinterpret_cast<const f32x4*>(p.ds_out + unit * kN * kN + state_offset(tu >> 2, tu & 3, lane));
-    carry[tu][lane] = g;
+    for (int x = 0; x < 4; ++x) {
+      const __amdgpu_buffer_rsrc_t from = buffer(static_cast<const char*>(src[x]) + rows_at(blk),
+                                                 rows_bytes(len - blk * kTokens - 16 * w));
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+        for (int m = 0; m < (F32 ? 2 : 1); ++m)
+          o.x[x][hh][m] = load16(from, li * row_bytes + 32 * q + 128 * hh + 16 * m);
+    }
+    return o;
+  };
+  // Eighths of a state, of 8 value rows each: the wave's
+  constexpr int kEighths = 8 / kTiles;
+  const int own_col = 8 * (lane & 7);
+  auto own_row = [&](int m) { return 8 * (wave + m * kTiles) + (lane >> 3); };
+  auto load_border = [&](const float* states, const float* marks, const float* decays, int64_t stride, int unmarked,
+                         int64_t blk) {
+    Border<kEighths> x;
+    const bool there = blk < live && states, marked = there && marks && blk % kPieceBlocks != unmarked;
+    const int64_t at = unit * nblk + (marked ? blk : 0);
+#pragma unroll
+    for (int m = 0; m < kEighths; ++m) {
+      x.piece[m] = load_eight(states, there ? unit * stride + (stride > 1 ? blk / kPieceBlocks : 0) : 0, there, own_row(m), own_col);
+      x.mark[m] = load_eight(marks, marked ? at : 0, marked, own_row(m), own_col);
+    }
+    x.decay = marked ? decays[at] : 1.f;
+    return x;
+  };
+  auto load_grad = [&](int64_t blk) {
+    return load_border(p.grads, p.grad_marks, p.grad_mark_decay, p.grad_stride, kPieceBlocks - 1, blk);
+  };
+  auto state_of = [&](const Border<kEighths>& x, float (&o)[kEighths][8]) {
+#pragma unroll
+    for (int m = 0; m < kEighths; ++m)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[m][i] = fmaf(x.piece[m].x[i >> 2][i & 3], x.decay, x.mark[m].x[i >> 2][i & 3]);
+  };
+  auto put_pieces = [&](const float (&x)[kEighths][8]) {
+#pragma unroll
+    for (int m = 0; m < kEighths; ++m) {
+      Op<3> o;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) put2(o, i, x[m][i], x[m][i + 1]);
+#pragma unroll
+      for (int n = 0; n < 3; ++n)
+        *reinterpret_cast<bf16x8*>(lds + kPieces + n * kPiece + in_pieces(own_row(m), lane & 7)) = o.p[n];
+    }
+  };
+  // ---- operands. Piece 4m + x of a row is 64 m bytes, by exclusive or, from piece x, in both numberings, so a lane's
+  // place in a tile is one of two and everything else in an address a constant or the tile's.
+  const int nat0 = swizzled(li, q), turn0 = swizzled(4 * q + (li >> 2), li & 3);
+  const int pnat0 = in_pieces(8 * (li >> 2) + (li & 3), q), pturn0 = in_pieces(8 * q + (li >> 2), li & 3);
+  // rows row0 + li as they are (row0 a multiple of 16)
+  auto nat = [&](int from, int row0, int hh) {
+    Op<NI> o;
+#pragma unroll
+    for (int n = 0; n < NI; ++n)
+      o.p[n] = *reinterpret_cast<const bf16x8*>(lds + (from + row0 * kRow) + (nat0 ^ 64 * hh) + n * kRows);
+    return o;
+  };
+  // turned: column li of tile t, of four rows
+  auto turn4 = [&](int at) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(
+        bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds + at)));
+  };
+  auto join = [](bf16x4 a, bf16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); };
+  // an operand over the tokens of tiles I0, I1 of a tensor, rows its channels of tile t
+  auto turned_tokens = [&](int from, int I0, int I1, int t) {
+    const int in_tile = (turn0 ^ 64 * (t >> 1)) + 8 * (t & 1);
+    Op<NI> o;
+#pragma unroll
+    for (int n = 0; n < NI; ++n)
+      o.p[n] = join(turn4(from + I0 * 16 * kRow + in_tile + n * kRows), turn4(from + I1 * 16 * kRow + in_tile + n * kRows));
+    return o;
+  };
+  // the pieces' operand over values 32 hv .., rows the keys of tile t
+  auto turned_values = [&](int t, int hv) {
+    Op<3> o;
+    const int at = kPieces + (pturn0 ^ 64 * (t >> 1)) + 8 * (t & 1) + 32 * hv * kRow;
+#pragma unroll
+    for (int n = 0; n < 3; ++n) o.p[n] = join(turn4(at + n * kPiece), turn4(at + n * kPiece + 4 * kRow));
+    return o;
+  };
+
+  float head_sum = 0.f;
+  Border<kEighths> grad;
+  if (blk0 < live) {
+    if constexpr (!F32) stage(p.r, 0, blk0), stage(p.k, 1, blk0), stage(p.v, 2, blk0), stage(p.dy, 3, blk0), stage_w(blk0);
+    grad = load_grad(blk0);
   }
-  const Turn E = make_turn(lane);
-  float head_sum = 0.f;  // one decay per head: its gradient's terms of this lane's tokens
-  for (int64_t blk = blk1 - 1; blk >= blk0; --blk) {
-    const int64_t t0 = blk * kBlk + wave * kSub;
-    if (blk * kBlk >= len) {  // behind the sequence's end: no gradients
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  for (int64_t blk = blk0; blk < live; ++blk) {
+    const int64_t t0 = blk * kTokens + 16 * w;
+    const int rows_r = C::kIn + (F32 ? 0 : (blk & 1) * 4 * kRows), rows_k = rows_r + NI * kRows,
+              rows_v = rows_k + NI * kRows, rows_d = rows_v + NI * kRows;
+    float lw;
+    if constexpr (F32) {
+      const Rows x = load_rows(blk);
+      const Span s = log_w_span(p.log_w, p.per_token, p.seq, b, h, t0, len);
+      lw = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer(s.base, s.bytes),
+                                                                          li * (p.per_token ? p.seq.H * 4 : 0), 0, 0));
 #pragma unroll
-      for (int J = 0; J < 2; ++J)
+      for (int n = 0; n < 4; ++n)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const uint32_t o = off + J * 16 * row_bytes + hh * 32 * kEsz<F32>;
-          store_pair<F32>(at(p.dr, t0, T - t0), o, zero4(), zero4());
-          store_pair<F32>(at(p.dk, t0, T - t0), o, zero4(), zero4());
-          store_pair<F32>(at(p.dv, t0, T - t0), o, zero4(), zero4());
+          const Op<NI> o = pieces<F32>(x.x[n][hh]);
+#pragma unroll
+          for (int m = 0; m < NI; ++m)
+            *reinterpret_cast<bf16x8*>(lds + C::kIn + (n * NI + m) * kRows + 16 * w * kRow + (nat0 ^ 64 * hh)) = o.p[m];
         }
-      if (p.per_token && lane < kSub && t0 + lane < T) p.dlog_w[(b * T + t0 + lane) * p.seq.H + h] = 0.f;
-      continue;
+    } else {
+      lw = f32s(C::kLogW + (blk & 1) * kTokens * 4)[16 * w + li];
     }
-    Raw<F32> rr, rk, rv, rd;
-    load_raw<F32>(rr, at(p.r, t0, len - t0), row_bytes, lane);
-    load_raw<F32>(rd, at(p.dy, t0, len - t0), row_bytes, lane);
-    load_raw<F32>(rk, at(p.k, t0, len - t0), row_bytes, lane);
-    load_raw<F32>(rv, at(p.v, t0, len - t0), row_bytes, lane);
-    const Decay d = make_decay(log_w_here(load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane), t0, len, lane), sums[wave], lane);
-
-    auto turn = [&](const Raw<F32>& x, int t) { return turned_op(natural<F32>(x, 0, t >> 1), natural<F32>(x, 1, t >> 1), E, t); };
-    // What the 32 tokens add to S and to G, for the other waves (wave 0's G for the next carry). A phase ends where
-    // its registers do: the compiler is kept from mixing the phases, whose operands together would not fit.
-    if (wave < kWaves - 1) {
-      Op<NI> Kt[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) Kt[t] = turn(rk, t);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        f32x4 a0 = turned(natural<F32>(rv, 0, u >> 1), E, u), a1 = turned(natural<F32>(rv, 1, u >> 1), E, u);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) a0[i] *= d.row[0][i], a1[i] *= d.row[1][i];
-        const Op<3> Vs = pack<3>(a0, a1);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) addS[wave][4 * t + u][lane] = mma(Kt[t], Vs, zero4());
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
+    float g8[kEighths][8];
+    state_of(grad, g8);
+    // the next block's rows, a tensor at a time through the block: all at once they fill the queue of loads and hold the
+    // waves up where they are asked for
+    if constexpr (!F32) stage_w(blk + 1), stage(p.r, 0, blk + 1);
+    put_pieces(g8);
+    const Border<kEighths> state = load_border(p.states, p.marks, p.mark_decay, p.state_stride, 0, blk);
+    // decays of the tile's tokens, in all four rows of lanes
+    float left, into;
+    double c;
     {
-      Op<NI> Rt[4];
+      c = t0 + li < len ? (double)(lw < -1e4f ? -1e4f : lw) * 1.4426950408889634 : 0.0;
+      c += dpp_f64<0x111>(c);
+      c += dpp_f64<0x112>(c);
+      c += dpp_f64<0x114>(c);
+      c += dpp_f64<0x118>(c);
+      const double end = readlane_f64(c, 15);
+      left = exp_diff(end, c), into = exp_diff(c, 0.0);
+      if (lane < 16) {
+        reinterpret_cast<double*>(lds + C::kSums)[16 * w + li] = c;
+        f32s(C::kLeft)[16 * w + li] = left;
+        f32s(C::kInto)[16 * w + li] = into;
+      }
+      if (lane == 0) f32s(C::kPerTile)[w] = exp_diff(end, 0.0);
+    }
+    Op<NI> R[2], K[2], V[2], D[2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) Rt[t] = turn(rr, t);
+    for (int hh = 0; hh < 2; ++hh)
+      R[hh] = nat(rows_r, 16 * w, hh), K[hh] = nat(rows_k, 16 * w, hh), V[hh] = nat(rows_v, 16 * w, hh),
+      D[hh] = nat(rows_d, 16 * w, hh);
+    lds_barrier();
+
+    float before = 1.f, behind = 1.f, all = 1.f;  // decays of the tiles before and behind, of the block
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        f32x4 a0 = turned(natural<F32>(rd, 0, u >> 1), E, u), a1 = turned(natural<F32>(rd, 1, u >> 1), E, u);
+    for (int x = 0; x < kTiles; ++x) {
+      const float e = f32s(C::kPerTile)[x];
+      before *= x < w ? e : 1.f;
+      behind *= x > w ? e : 1.f;
+      all *= e;
+    }
+    f32x4 dj, di;  // factors of the tile on the diagonal: rows j, rows i
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a0[i] *= d.inrow[0][i], a1[i] *= d.inrow[1][i];
-        const Op<3> Ds = pack<3>(a0, a1);
+    for (int i = 0; i < 4; ++i) {
+      const double r = reinterpret_cast<const double*>(lds + C::kSums)[16 * w + 4 * q + i];
+      dj[i] = exp_diff(c, r), di[i] = exp_diff(r, c);
+    }
+    if constexpr (!F32) stage(p.k, 1, blk + 1);
+    // the pairs with the tiles behind (for dk, dv) and before (for dr)
+    f32x4 ak[4], av[4], ar[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) addG[wave][4 * t + u][lane] = mma(Rt[t], Ds, zero4());
+    for (int t = 0; t < 4; ++t) ak[t] = av[t] = ar[t] = zero4();
+    float between = 1.f;
+#pragma clang loop unroll(disable)
+    for (int I = w + 1; I < kTiles; I += 2) {
+      const int I1 = I + 1 < kTiles ? I + 1 : I;
+      f32x4 pq[2], pa[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int X = e ? I1 : I;
+        f32x4 x = zero4(), a = zero4();
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) x = mma(nat(rows_d, 16 * X, hh), V[hh], x), a = mma(nat(rows_r, 16 * X, hh), K[hh], a);
+        const bool on = e == 0 || I1 > I;
+        const f32x4 f = *reinterpret_cast<const f32x4*>(f32s(C::kInto) + 16 * X + 4 * q) * (on ? between : 0.f);
+        pq[e] = x * f, pa[e] = a * f;
+        if (on) {
+          const float s = wave_sum((a[0] * pq[e][0] + a[1] * pq[e][1] + a[2] * pq[e][2] + a[3] * pq[e][3]) * left);
+          if (lane == 0) f32s(C::kPairs)[w * kTiles + X] = s;
+          between *= f32s(C::kPerTile)[X];
+        }
+      }
+      const Op<NO> Pq = pack<NO>(pq[0], pq[1]), Pa = pack<NO>(pa[0], pa[1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        ak[t] = mma(turned_tokens(rows_r, I, I1, t), Pq, ak[t]);
+        av[t] = mma(turned_tokens(rows_d, I, I1, t), Pa, av[t]);
       }
     }
-    if (lane == 0) all[wave] = d.all;
-    __syncthreads();
     __builtin_amdgcn_sched_barrier(0);
-
-    // the gradient behind the wave's tokens, tile (t, u)
-    auto grad_tile = [&](int tu) {
-      f32x4 g = carry[tu][lane];
-      for (int w = kWaves - 1; w > wave; --w) g = fma4(g, all[w], addG[w][tu][lane]);
-      return g;
-    };
-    float cross[2] = {0.f, 0.f};  // this lane's rows of the pairs that cross token 16J + li
-    float kdk[2] = {0.f, 0.f}, rdr[2] = {0.f, 0.f}, dot = 0.f;
-    {  // dv and dk
-      Op<NO> Pi[2], Ai[2];  // P and D A with rows i
-      {
-        f32x4 q00 = zero4(), q10 = zero4(), q11 = zero4(), a00 = zero4(), a10 = zero4(), a11 = zero4();
+    if constexpr (!F32) stage(p.v, 2, blk + 1);
+    between = 1.f;
+#pragma clang loop unroll(disable)
+    for (int J = w - 1; J >= 0; J -= 2) {
+      const int J1 = J > 0 ? J - 1 : J;
+      f32x4 pp[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int X = e ? J1 : J;
+        const bool on = e == 0 || J1 < J;
+        f32x4 x = mma(nat(rows_v, 16 * X, 0), D[0], zero4());
+        x = mma(nat(rows_v, 16 * X, 1), D[1], x);
+        pp[e] = x * (*reinterpret_cast<const f32x4*>(f32s(C::kLeft) + 16 * X + 4 * q) * (on ? between : 0.f));
+        if (on) between *= f32s(C::kPerTile)[X];
+      }
+      const Op<NO> P = pack<NO>(pp[0], pp[1]);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ar[t] = mma(turned_tokens(rows_k, J, J1, t), P, ar[t]);
+    }
+    __builtin_amdgcn_sched_barrier(0);  // phases whose registers would not fit together
+    if constexpr (!F32) stage(p.dy, 3, blk + 1);
+    float cross = 0.f, kdk = 0.f, rdr = 0.f;
+    {  // dk and dv: the gradient behind the block, the factor of the tokens, the tile's own pairs
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int rows = (32 * (u >> 1) + 4 * (u & 1)) * kRow;  // value channel(u, li)
+        f32x4 o = zero4();
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const Op<NI> D0 = natural<F32>(rd, 0, hh), D1 = natural<F32>(rd, 1, hh);
-          const Op<NI> V0 = natural<F32>(rv, 0, hh), V1 = natural<F32>(rv, 1, hh);
-          q00 = mma(D0, V0, q00), q10 = mma(D1, V0, q10), q11 = mma(D1, V1, q11);
-          const Op<NI> R0 = natural<F32>(rr, 0, hh), R1 = natural<F32>(rr, 1, hh);
-          const Op<NI> K0 = natural<F32>(rk, 0, hh), K1 = natural<F32>(rk, 1, hh);
-          a00 = mma(R0, K0, a00), a10 = mma(R1, K0, a10), a11 = mma(R1, K1, a11);
-        }
-        q00 = masked_i(q00, d.t00, lane), q10 = q10 * d.t10, q11 = masked_i(q11, d.t11, lane);
-        Pi[0] = pack<NO>(q00, q10);
-        Pi[1] = pack<NO>(zero4(), q11);
-        Ai[0] = pack<NO>(masked_i(a00, d.t00, lane), a10 * d.t10);
-        Ai[1] = pack<NO>(zero4(), masked_i(a11, d.t11, lane));
-        // pairs i >= t > j: what each row has in the columns before t, from the rows from t on
+          Op<NO> G;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float w00 = a00[i] * q00[i], w10 = a10[i] * q10[i], w11 = a11[i] * q11[i];
-          const float before00 = row_sums_to(dpp_f32<0x111>(w00)), before10 = row_sums_to(dpp_f32<0x111>(w10));
-          const float before11 = row_sums_to(dpp_f32<0x111>(w11)) + row16_sum(w10);
-          const bool from = 4 * q + i >= li;
-          cross[0] += (from ? before00 : 0.f) + before10;
-          cross[1] += from ? before11 : 0.f;
+          for (int n = 0; n < NO; ++n)
+            G.p[n] = *reinterpret_cast<const bf16x8*>(lds + kPieces + (pnat0 ^ 64 * hh) + rows + n * kPiece);
+          o = mma(G, K[hh], o);
         }
+        av[u] = fma4(o, behind, av[u]) * left;
       }
       __builtin_amdgcn_sched_barrier(0);
-      f32x4 dk[4][2];
+      float kg = 0.f;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) dk[t][0] = dk[t][1] = zero4();
+      for (int t = 0; t < 4; ++t) {
+        f32x4 o = mma(turned_values(t, 0), V[0], zero4());
+        o = mma(turned_values(t, 1), V[1], o) * (behind * left);
+        ak[t] = fma4(ak[t], left, o);
 #pragma unroll
-      for (int hv = 0; hv < 2; ++hv) {  // half of the values at a time
-        f32x4 dv[2][2];
-        Op<3> Go[2][2];  // [value tile 2hv + e][key half]: rows are values
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int u = 2 * hv + e;
-#pragma unroll
-          for (int m = 0; m < 2; ++m) Go[e][m] = pack<3>(grad_tile(8 * m + u), grad_tile(8 * m + 4 + u));
-          const Op<NI> Dt = turn(rd, u);
-#pragma unroll
-          for (int J = 0; J < 2; ++J) {
-            f32x4 o = mma(Go[e][0], natural<F32>(rk, J, 0), zero4());
-            o = mma(Go[e][1], natural<F32>(rk, J, 1), o);
-            dv[e][J] = mma(Dt, Ai[J], o * d.out[J]);
-          }
+        for (int i = 0; i < 4; ++i) {
+          const float k = value(K[t >> 1], t & 1, i);
+          kg = fmaf(o[i], k, kg), kdk = fmaf(ak[t][i], k, kdk);
         }
-#pragma unroll
-        for (int J = 0; J < 2; ++J)
-          store_pair<F32>(at(p.dv, t0, T - t0), off + J * 16 * row_bytes + hv * 32 * kEsz<F32>, dv[0][J], dv[1][J]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const Op<3> Gt = turned_op(Go[0][t >> 1], Go[1][t >> 1], E, t);
-#pragma unroll
-          for (int J = 0; J < 2; ++J) dk[t][J] = mma(Gt, natural<F32>(rv, J, hv), dk[t][J]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
       }
+      kg = wave_sum(kg);
+      if (lane == 0) f32s(C::kPerTile)[2 * kTiles + w] = kg;
+      kdk = rows_sum(kdk);
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4 x = mma(D[1], V[1], mma(D[0], V[0], zero4())), a = mma(R[1], K[1], mma(R[0], K[0], zero4()));
+      x = masked_i(x, di, lane);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float to = sums_to(dpp_f32<0x111>(a[i] * x[i]));  // columns j before t of the row i
+        cross += 4 * q + i >= li ? to : 0.f;
+      }
+      cross = rows_sum(cross);
+      const Op<NO> Pq = pack<NO>(x, zero4()), Pa = pack<NO>(masked_i(a, di, lane), zero4());
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        ak[t] = mma(turned_tokens(rows_r, w, w, t), Pq, ak[t]);
+        av[t] = mma(turned_tokens(rows_d, w, w, t), Pa, av[t]);
+      }
+      const __amdgpu_buffer_rsrc_t kb = buffer(static_cast<char*>(p.dk) + rows_at(blk), rows_bytes(T - t0));
+      const __amdgpu_buffer_rsrc_t vb = buffer(static_cast<char*>(p.dv) + rows_at(blk), rows_bytes(T - t0));
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        store_pair<F32>(kb, li * row_bytes + (32 * hh + 8 * q) * kEsz<F32>, ak[2 * hh], ak[2 * hh + 1]);
+        store_pair<F32>(vb, li * row_bytes + (32 * hh + 8 * q) * kEsz<F32>, av[2 * hh], av[2 * hh + 1]);
+      }
+    }
+    grad = load_grad(blk + 1);
+    lds_barrier();
+    {
+      float s8[kEighths][8], x = 0.f;
+      state_of(state, s8);
+      put_pieces(s8);
+#pragma unroll
+      for (int m = 0; m < kEighths; ++m)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x = fmaf(s8[m][i], g8[m][i], x);
+      x = wave_sum(x);
+      if (lane == 0) f32s(C::kPerTile)[kTiles + wave] = x;
+    }
+    lds_barrier();
+    {  // dr, alike with the state before the block
+      float rs = 0.f;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        f32x4 o = mma(turned_values(t, 0), D[0], zero4());
+        o = mma(turned_values(t, 1), D[1], o) * (before * into);
+        ar[t] = fma4(ar[t], into, o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float r = value(R[t >> 1], t & 1, i);
+          rs = fmaf(o[i], r, rs), rdr = fmaf(ar[t][i], r, rdr);
+        }
+      }
+      rs = wave_sum(rs);
+      if (lane == 0) f32s(C::kPerTile)[3 * kTiles + w] = rs;
+      rdr = rows_sum(rdr);
+      const f32x4 x = masked_j(mma(V[1], D[1], mma(V[0], D[0], zero4())), dj, lane);
+      const Op<NO> P = pack<NO>(x, zero4());
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ar[t] = mma(turned_tokens(rows_k, w, w, t), P, ar[t]);
+      const __amdgpu_buffer_rsrc_t rb = buffer(static_cast<char*>(p.dr) + rows_at(blk), rows_bytes(T - t0));
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-        for (int J = 0; J < 2; ++J) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int t = 2 * hh + e;
-            dk[t][J] = dk[t][J] * d.out[J];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) kdk[J] = fmaf(dk[t][J][i], element<F32>(rk, J, hh, e, i), kdk[J]);
-            dk[t][J] = mma(turn(rr, t), Pi[J], dk[t][J]);
-          }
-          store_pair<F32>(at(p.dk, t0, T - t0), off + J * 16 * row_bytes + hh * 32 * kEsz<F32>, dk[2 * hh][J],
-                          dk[2 * hh + 1][J]);
-        }
+        store_pair<F32>(rb, li * row_bytes + (32 * hh + 8 * q) * kEsz<F32>, ar[2 * hh], ar[2 * hh + 1]);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    {  // dr
-      const int64_t piece = blk / kPieceBlocks;
-      const bool marked = blk % kPieceBlocks != 0;
-      const float mark_decay = marked ? p.mark_decay[unit * nblk + blk] : 1.f;
-      f32x4 dr[4][2];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) dr[t][0] = dr[t][1] = zero4();
-#pragma unroll
-      for (int hv = 0; hv < 2; ++hv) {
-        Op<3> So[2][2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int u = 2 * hv + e;
-          f32x4 s[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int tu = 4 * t + u;
-            s[t] = zero4();
-            if (p.pieces > 1)
-              s[t] = *state_tile(p.states, unit * p.pieces + piece, tu, lane);
-            else if (p.s_in)
-              s[t] = *reinterpret_cast<const f32x4*>(p.s_in + unit * kN * kN + state_offset(t, u, lane));
-            if (marked) s[t] = fma4(s[t], mark_decay, *state_tile(p.marks, unit * nblk + blk, tu, lane));
-            for (int w = 0; w < wave; ++w) s[t] = fma4(s[t], all[w], addS[w][tu][lane]);
-            const f32x4 g = grad_tile(tu);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dot = fmaf(s[t][i], g[i], dot);
-          }
-#pragma unroll
-          for (int m = 0; m < 2; ++m) So[e][m] = pack<3>(s[2 * m], s[2 * m + 1]);
-        }
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const Op<3> St = turned_op(So[0][t >> 1], So[1][t >> 1], E, t);
-#pragma unroll
-          for (int J = 0; J < 2; ++J) dr[t][J] = mma(St, natural<F32>(rd, J, hv), dr[t][J]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+    lds_barrier();
+    {  // dlog_w: lane kTiles J + I the pairs of two tiles, lanes 0 .. kTiles - 1 the borders
+      const int J = lane / kTiles, I = lane % kTiles;
+      float x = J < w && I > w ? f32s(C::kPairs)[lane] : 0.f;
+      if (lane < kTiles)
+        x += all * f32s(C::kPerTile)[kTiles + lane] + (lane < w ? f32s(C::kPerTile)[2 * kTiles + lane] : 0.f) +
+             (lane > w ? f32s(C::kPerTile)[3 * kTiles + lane] : 0.f);
+      float dlw = cross + sums_from(rdr) + sums_to(dpp_f32<0x111>(kdk)) + wave_sum(x);
+      const int64_t t = t0 + li;
+      if (t >= len) dlw = 0.f;
+      if (p.per_token) {
+        if (lane < 16 && t < T) p.dlog_w[(b * T + t) * p.seq.H + h] = dlw;
+      } else {
+        head_sum += dlw;
       }
-      Op<NO> Pj[2];  // P with rows j
-      {
-        f32x4 p00 = zero4(), p01 = zero4(), p11 = zero4();
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const Op<NI> D0 = natural<F32>(rd, 0, hh), D1 = natural<F32>(rd, 1, hh);
-          const Op<NI> V0 = natural<F32>(rv, 0, hh), V1 = natural<F32>(rv, 1, hh);
-          p00 = mma(V0, D0, p00), p01 = mma(V0, D1, p01), p11 = mma(V1, D1, p11);
-        }
-        Pj[0] = pack<NO>(masked_j(p00, d.d00, lane), zero4());
-        Pj[1] = pack<NO>(p01 * d.d01, masked_j(p11, d.d11, lane));
-      }
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-        for (int J = 0; J < 2; ++J) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int t = 2 * hh + e;
-            dr[t][J] = dr[t][J] * d.col[J];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) rdr[J] = fmaf(dr[t][J][i], element<F32>(rr, J, hh, e, i), rdr[J]);
-            dr[t][J] = mma(turn(rk, t), Pj[J], dr[t][J]);
-          }
-          store_pair<F32>(at(p.dr, t0, T - t0), off + J * 16 * row_bytes + hh * 32 * kEsz<F32>, dr[2 * hh][J],
-                          dr[2 * hh + 1][J]);
-        }
     }
-    __builtin_amdgcn_sched_barrier(0);
-    // dlog_w: lane l has token l % 32
-#pragma unroll
-    for (int J = 0; J < 2; ++J) cross[J] = rows_sum(cross[J]), rdr[J] = rows_sum(rdr[J]), kdk[J] = rows_sum(kdk[J]);
-    const bool second = lane & 16;
-    const float pairs = second ? cross[1] : cross[0];
-    const float here = second ? rdr[1] : rdr[0], before = second ? kdk[1] : kdk[0];
-    dot = rows_sum(row16_sum(dot));
-    const int64_t t = t0 + (lane & 31);
-    float dlw = pairs + sum_from(here, lane) + sum_before(before, lane) + dot * d.all;
-    if (t >= len) dlw = 0.f;
-    if (p.per_token) {
-      if (lane < kSub && t < T) p.dlog_w[(b * T + t) * p.seq.H + h] = dlw;
-    } else {
-      head_sum += dlw;
-    }
-    __syncthreads();  // every wave has read what was added and the carried gradient
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {  // the gradient behind the next block, before this one
-      const int tu = 4 * wave + m;
-      f32x4 g = carry[tu][lane];
-#pragma unroll
-      for (int w = kWaves - 1; w >= 0; --w) g = fma4(g, all[w], addG[w][tu][lane]);
-      carry[tu][lane] = g;
-    }
-    __syncthreads();
+    // the next block's rows are there: behind them are at least six stores
+    asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
-  if (p.ds_in && seg == 0) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to this workgroup's LDS when it ends
+  for (int64_t blk = live > blk0 ? live : blk0; blk < blk1; ++blk) {  // behind the sequence's end: no gradients
+    const int64_t t0 = blk * kTokens + 16 * w;
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int tu = 4 * wave + m;
-      *reinterpret_cast<f32x4*>(p.ds_in + unit * kN * kN + state_offset(tu >> 2, tu & 3, lane)) = carry[tu][lane];
+    for (int hh = 0; hh < 2; ++hh) {
+      const uint32_t off = li * row_bytes + (32 * hh + 8 * q) * kEsz<F32>;
+      void* const out[3] = {p.dr, p.dk, p.dv};
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+        store_pair<F32>(buffer(static_cast<char*>(out[x]) + rows_at(blk), rows_bytes(T - t0)), off, zero4(), zero4());
     }
+    if (p.per_token && lane < 16 && t0 + lane < T) p.dlog_w[(b * T + t0 + lane) * p.seq.H + h] = 0.f;
   }
-  if (!p.per_token) {  // both halves of the wave hold the same 32 tokens
-    float s = row16_sum(head_sum);
-    s += __shfl_xor(s, 16, 64);
-    if (lane == 0) all[wave] = s;
+  if (!p.per_token) {
+    const float s = row16_sum(head_sum);
+    if (lane == 0) f32s(C::kPerTile)[w] = s;
     __syncthreads();
-    if (threadIdx.x == 0) p.dlog_w[unit * p.nseg + seg] = (all[0] + all[1]) + (all[2] + all[3]);
+    if (threadIdx.x == 0) {
+      float x = 0.f;
+      for (int i = 0; i < kTiles; ++i) x += f32s(C::kPerTile)[i];
+      p.dlog_w[unit * p.nseg + seg] = x;
+    }
   }
 }
 
@@ -376,7 +548,72 @@ __global__ __launch_bounds__(256) void linattn_zero_kernel(float* x, int64_t n) 
   if (i < n) x[i] = 0.f;
 }
 
-constexpr int kGradLds = 8 * 16384 + kWaves * kSub * 8 + 64;
+template <bool F32>
+hipError_t launch(const LinattnCall& c) {
+  constexpr int64_t kTokens = Cfg<F32>::kTokens;
+  const int64_t units = c.B * c.H, nblk = (c.T + kTokens - 1) / kTokens,
+                pieces = (nblk + kPieceBlocks - 1) / kPieceBlocks, cus = linattn_cus();
+  // Segments: as many workgroups as fill the compute units in whole rounds best, each with its first loads to wait for.
+  int64_t nseg = 1;
+  double best = 0;
+  for (int64_t n = 1; n <= nblk && (n == 1 || units * n <= 4 * cus); ++n) {
+    const int64_t length = (nblk + n - 1) / n, rounds = (units * n + cus - 1) / cus;
+    const double us = rounds * (length * (F32 ? 10.0 : 5.0) + 3.0);
+    if (n == 1 || us < best) best = us, nseg = n;
+  }
+  const int64_t seg_blocks = (nblk + nseg - 1) / nseg;
+  nseg = (nblk + seg_blocks - 1) / seg_blocks;
+
+  const bool border = nblk > 1;  // blocks whose state is not the caller's
+  size_t need = 0;
+  auto room = [&](size_t bytes) {
+    const size_t at = need;
+    need += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  const size_t o_states = room(border ? units * pieces * kLinattnStateBytes : 0), o_decay = room(units * pieces * 4);
+  const size_t o_marks = room(border ? units * nblk * kLinattnStateBytes : 0), o_mdecay = room(units * nblk * 4);
+  const size_t o_grads = room(units * pieces * kLinattnStateBytes), o_gdecay = room(units * pieces * 4);
+  const size_t o_gmarks = room(border ? units * nblk * kLinattnStateBytes : 0), o_gmdecay = room(units * nblk * 4);
+  const size_t o_parts = room(c.per_token ? 0 : units * nseg * 4);
+  void* ws = nullptr;
+  hipError_t e = device_workspace(c.stream, need, &ws, kWorkspaceOperators);
+  if (e != hipSuccess) return e;
+  char* base = static_cast<char*>(ws);
+  auto at = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
+
+  LinattnPieces f{}, g{};
+  f.every = g.every = 1;
+  f.states = at(o_states), f.decay = at(o_decay), f.marks = border ? at(o_marks) : nullptr, f.mark_decay = at(o_mdecay);
+  g.states = at(o_grads), g.decay = at(o_gdecay), g.marks = border ? at(o_gmarks) : nullptr, g.mark_decay = at(o_gmdecay);
+  g.end = c.ds_in;
+  GradParams p{};
+  p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.dy = c.dy;
+  // one block: its state is the caller's, and so is its gradient; a copy where dstate_in is written over it
+  p.states = border ? f.states : c.s_in, p.marks = f.marks, p.mark_decay = f.mark_decay;
+  p.grads = border || c.ds_in ? g.states : c.ds_out, p.grad_marks = g.marks, p.grad_mark_decay = g.mark_decay;
+  p.state_stride = p.grad_stride = border ? pieces : 1;
+  if (border || c.ds_in) {
+    e = launch_linattn_states(c, kTokens, border ? &f : nullptr, &g);
+    if (e != hipSuccess) return e;
+  }
+  p.dr = c.dr, p.dlog_w = c.per_token ? c.dlog_w : at(o_parts), p.dk = c.dk, p.dv = c.dv;
+  p.seq = Seq{c.T, (int32_t)c.H, c.lens};
+  p.per_token = c.per_token;
+  p.nseg = (int32_t)nseg, p.seg_blocks = seg_blocks;
+  const void* fn = reinterpret_cast<const void*>(&linattn_grad_kernel<F32>);
+  static const hipError_t a = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, Cfg<F32>::kLds);
+  if (a != hipSuccess) return a;
+  void* args[] = {&p};
+  e = hipLaunchKernel(fn, dim3((uint32_t)(units * nseg)), dim3(64 * Cfg<F32>::kTiles), args, Cfg<F32>::kLds, c.stream);
+  if (e != hipSuccess || c.per_token) return e;
+  const float* parts = at(o_parts);
+  float* dlog_w = c.dlog_w;
+  int64_t B = c.B;
+  int32_t H = (int32_t)c.H, n = (int32_t)nseg;
+  void* hargs[] = {&parts, &dlog_w, &B, &H, &n};
+  return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_head_sum_kernel), dim3((uint32_t)H), dim3(64), hargs, 0, c.stream);
+}
 
 }  // namespace
 
@@ -386,69 +623,6 @@ hipError_t launch_linattn_zero(float* dlog_w, int64_t H, hipStream_t stream) {
                          args, 0, stream);
 }
 
-hipError_t launch_linattn_head_sum(const float* parts, float* dlog_w, int64_t B, int64_t H, int64_t n, hipStream_t stream) {
-  int32_t heads = (int32_t)H, nseg = (int32_t)n;
-  void* args[] = {&parts, &dlog_w, &B, &heads, &nseg};
-  return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_head_sum_kernel), dim3((uint32_t)H), dim3(64), args, 0, stream);
-}
-
-hipError_t launch_linattn_backward(const LinattnCall& c) {
-  if (!c.f32) return launch_linattn_backward16(c);
-  const int64_t units = c.B * c.H, nblk = linattn_blocks(c.T), pieces = linattn_pieces(c.T), cus = linattn_cus();
-  // Segments: a workgroup for each compute unit, of whole pieces.
-  int64_t nseg = cus / units > 0 ? cus / units : 1;
-  if (nseg > pieces) nseg = pieces;
-  const int64_t seg_pieces = (pieces + nseg - 1) / nseg;
-  nseg = (pieces + seg_pieces - 1) / seg_pieces;
-
-  const bool marks = nblk > 1, states = marks;
-  size_t need = 0;
-  auto room = [&](size_t bytes) {
-    const size_t at = need;
-    need += (bytes + 255) / 256 * 256;
-    return at;
-  };
-  const size_t o_states = room(states ? units * pieces * kLinattnStateBytes : 0), o_decay = room(units * pieces * 4), o_gdecay = room(units * pieces * 4);
-  const size_t o_marks = room(marks ? units * nblk * kLinattnStateBytes : 0), o_mdecay = room(marks ? units * nblk * 4 : 0);
-  const size_t o_grads = room(nseg > 1 ? units * pieces * kLinattnStateBytes : 0);
-  const size_t o_parts = room(c.per_token ? 0 : units * nseg * 4);
-  void* ws = nullptr;
-  hipError_t e = device_workspace(c.stream, need, &ws, kWorkspaceOperators);
-  if (e != hipSuccess) return e;
-  char* base = static_cast<char*>(ws);
-
-  LinattnPieces f{}, g{};
-  f.every = g.every = 1;
-  f.states = reinterpret_cast<float*>(base + o_states), f.decay = reinterpret_cast<float*>(base + o_decay);
-  f.marks = reinterpret_cast<float*>(base + o_marks), f.mark_decay = reinterpret_cast<float*>(base + o_mdecay);
-  g.states = reinterpret_cast<float*>(base + o_grads), g.decay = reinterpret_cast<float*>(base + o_gdecay);
-  if (states) {
-    e = launch_linattn_states(c, &f, nseg > 1 ? &g : nullptr);
-    if (e != hipSuccess) return e;
-  }
-  GradParams p{};
-  p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.dy = c.dy, p.s_in = c.s_in, p.ds_out = c.ds_out;
-  p.states = reinterpret_cast<const float*>(base + o_states);
-  p.marks = reinterpret_cast<const float*>(base + o_marks);
-  p.mark_decay = reinterpret_cast<const float*>(base + o_mdecay);
-  p.grads = reinterpret_cast<const float*>(base + o_grads);
-  float* parts = reinterpret_cast<float*>(base + o_parts);
-  p.dr = c.dr, p.dlog_w = c.per_token ? c.dlog_w : parts, p.dk = c.dk, p.dv = c.dv, p.ds_in = c.ds_in;
-  p.seq = Seq{c.T, (int32_t)c.H, c.lens};
-  p.per_token = c.per_token;
-  p.nseg = (int32_t)nseg, p.pieces = pieces, p.seg_pieces = seg_pieces;
-  const void* fn = c.f32 ? reinterpret_cast<const void*>(&linattn_grad_kernel<true>)
-                         : reinterpret_cast<const void*>(&linattn_grad_kernel<false>);
-  static const hipError_t a0 = hipFuncSetAttribute(reinterpret_cast<const void*>(&linattn_grad_kernel<true>),
-                                                   hipFuncAttributeMaxDynamicSharedMemorySize, kGradLds);
-  static const hipError_t a1 = hipFuncSetAttribute(reinterpret_cast<const void*>(&linattn_grad_kernel<false>),
-                                                   hipFuncAttributeMaxDynamicSharedMemorySize, kGradLds);
-  if (a0 != hipSuccess) return a0;
-  if (a1 != hipSuccess) return a1;
-  void* args[] = {&p};
-  e = hipLaunchKernel(fn, dim3((uint32_t)(units * nseg)), dim3(64 * kWaves), args, kGradLds, c.stream);
-  if (e != hipSuccess || c.per_token) return e;
-  return launch_linattn_head_sum(parts, c.dlog_w, c.B, c.H, nseg, c.stream);
-}
+hipError_t launch_linattn_backward(const LinattnCall& c) { return c.f32 ? launch<true>(c) : launch<false>(c); }
 
 }  // namespace rwkv7

@@ -34,16 +34,15 @@ struct OutParams {
 // head follow each other on the same die, so r and k come from memory once. Loads run a block ahead.
 constexpr int kVt = 2;  // value tiles of a workgroup
 
-template <bool F32>
 struct Inputs {
-  Raw<F32> r, k;
-  u32x4 v[2][F32 ? 2 : 1];  // [token tile], the workgroup's 32 values
+  Raw<true> r, k;
+  u32x4 v[2][2];  // [token tile], the workgroup's 32 values
   float log_w;
 };
 
-template <bool F32>
-__global__ __launch_bounds__(256, F32 ? 1 : 2) void linattn_out_kernel(OutParams p) {
-  constexpr int NI = kIn<F32>, NO = F32 ? 3 : 2;
+__global__ __launch_bounds__(256, 1) void linattn_out32_kernel(OutParams p) {
+  constexpr bool F32 = true;
+  constexpr int NI = 3, NO = 3;
   __shared__ f32x4 added[kWaves][4 * kVt][64];
   __shared__ bf16x8 before[kWaves][kVt][2][NO][64];  // [wave][value tile][key half]: operands
   __shared__ double sums[kWaves][kSub];
@@ -64,15 +63,15 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void linattn_out_kernel(OutParams
   const int64_t live = (len + kBlk - 1) / kBlk < blk1 ? (len + kBlk - 1) / kBlk : blk1;
   const uint32_t off = (lane & 15) * row_bytes + ((lane >> 4) * 8 + half * 32) * kEsz<F32>;  // of v and y
 
-  Inputs<F32> x;
-  auto load = [&](Inputs<F32>& x, int64_t blk) {
+  Inputs x;
+  auto load = [&](Inputs& x, int64_t blk) {
     const int64_t t0 = blk * kBlk + wave * kSub;
     const __amdgpu_buffer_rsrc_t vb = token_buffer<kEsz<F32>>(p.v, p.seq, b, h, t0, len - t0, kSub);
     load_raw<F32>(x.k, token_buffer<kEsz<F32>>(p.k, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
 #pragma unroll
     for (int J = 0; J < 2; ++J)
 #pragma unroll
-      for (int m = 0; m < (F32 ? 2 : 1); ++m) x.v[J][m] = load16(vb, off + J * 16 * row_bytes + 16 * m);
+      for (int m = 0; m < 2; ++m) x.v[J][m] = load16(vb, off + J * 16 * row_bytes + 16 * m);
     load_raw<F32>(x.r, token_buffer<kEsz<F32>>(p.r, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
     x.log_w = load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane);
   };
@@ -91,7 +90,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void linattn_out_kernel(OutParams
   // compiler wait for the loads ahead too
   __builtin_amdgcn_s_waitcnt(0x0f70);
   for (int64_t blk = blk0; blk < live; ++blk) {
-    Inputs<F32> ahead;
+    Inputs ahead;
     load(ahead, blk + 1);  // behind the last block the descriptors are empty or what comes is not used
     const int64_t t0 = blk * kBlk + wave * kSub;
     const Decay d = make_decay(log_w_here(x.log_w, t0, len, lane), sums[wave], lane);
@@ -103,10 +102,7 @@ __global__ __launch_bounds__(256, F32 ? 1 : 2) void linattn_out_kernel(OutParams
       for (int m = 0; m < kVt; ++m) {
         const Op<NI> v0 = pieces<F32>(x.v[0]), v1 = pieces<F32>(x.v[1]);
         f32x4 a0 = turned(v0, E, m), a1 = turned(v1, E, m);
-        if constexpr (F32)
-          Vt[m] = turned_op(v0, v1, E, m);
-        else
-          Vt[m] = pack<NI>(a0, a1);
+        Vt[m] = turned_op(v0, v1, E, m);
 #pragma unroll
         for (int i = 0; i < 4; ++i) a0[i] *= d.row[0][i], a1[i] *= d.row[1][i];
         Vs[m] = pack<3>(a0, a1);
@@ -423,7 +419,7 @@ int64_t segments(int64_t units, int64_t blocks, bool f32, int64_t* piece_count) 
 
 template <bool F32>
 hipError_t launch_out(const LinattnCall& c) {
-  const int64_t units = c.B * c.H, blocks = linattn_blocks(c.T);
+  const int64_t units = c.B * c.H, blocks = linattn_blocks(c.T, kBlk);
   OutParams p{};
   p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.s_in = c.s_in, p.y = c.y, p.s_out = c.s_out;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
@@ -440,7 +436,7 @@ hipError_t launch_out(const LinattnCall& c) {
     q.every = (int32_t)every;
     q.states = static_cast<float*>(ws);
     q.decay = reinterpret_cast<float*>(static_cast<char*>(ws) + states);
-    e = launch_linattn_states(c, &q, nullptr);
+    e = launch_linattn_states(c, kBlk, &q, nullptr);
     if (e != hipSuccess) return e;
     p.states = static_cast<const float*>(ws);
   }
@@ -451,9 +447,10 @@ hipError_t launch_out(const LinattnCall& c) {
     if (a != hipSuccess) return a;
     return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out16_kernel), dim3((uint32_t)(units * p.nseg)),
                            dim3(512), args, kOutLds, c.stream);
+  } else {
+    return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out32_kernel), dim3((uint32_t)(units * p.nseg * 2)),
+                           dim3(64 * kWaves), args, 0, c.stream);
   }
-  return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out_kernel<F32>), dim3((uint32_t)(units * p.nseg * 2)),
-                         dim3(64 * kWaves), args, 0, c.stream);
 }
 
 // ---- single tokens. S is read and written once (32 KiB of a head's 32.5): 16 lanes hold a value

@@ -32,18 +32,15 @@ struct LinattnCall {
 hipError_t launch_linattn(const LinattnCall& c);
 hipError_t launch_linattn_step(const LinattnCall& c);
 hipError_t launch_linattn_backward(const LinattnCall& c);
-hipError_t launch_linattn_backward16(const LinattnCall& c);  // bfloat16, called by the one above
-// dlog_w[h] <- the sum of parts [B][H][n] over all but h, in order.
-hipError_t launch_linattn_head_sum(const float* parts, float* dlog_w, int64_t B, int64_t H, int64_t n, hipStream_t stream);
 hipError_t launch_linattn_zero(float* dlog_w, int64_t H, hipStream_t stream);
 
-constexpr int64_t kLinattnBlock = 128;              // tokens a workgroup takes at a time
+constexpr int64_t kLinattnBlock = 128;  // tokens a workgroup takes at a time (the float32 backward: 64)
 constexpr int64_t kLinattnStateBytes = 64 * 64 * 4;  // one state
 
 // Every sequence in pieces of kPieceBlocks blocks, and the device memory for the states at their starts.
 constexpr int64_t kPieceBlocks = 4;
-inline int64_t linattn_blocks(int64_t T) { return (T + kLinattnBlock - 1) / kLinattnBlock; }
-inline int64_t linattn_pieces(int64_t T) { return (linattn_blocks(T) + kPieceBlocks - 1) / kPieceBlocks; }
+inline int64_t linattn_blocks(int64_t T, int64_t block) { return (T + block - 1) / block; }
+inline int64_t linattn_pieces(int64_t T, int64_t block) { return (linattn_blocks(T, block) + kPieceBlocks - 1) / kPieceBlocks; }
 struct LinattnPieces {
   int32_t every;      // keep the state before every every-th piece
   float* states;      // [units][pieces] states; the kept ones come first in a sequence's
@@ -54,8 +51,8 @@ struct LinattnPieces {
 };
 // Forward (from k, v): states <- the state before each every-th piece, and, if asked for, marks <- the sum of each
 // piece before each of its blocks but the first. Backward (from r, dy; every is 1): the gradient behind each piece,
-// and the sums behind each block but the last. Either may be null.
-hipError_t launch_linattn_states(const LinattnCall& c, const LinattnPieces* forward, const LinattnPieces* backward);
+// and the sums behind each block but the last. Either may be null. `block`: tokens of a block, a multiple of 32.
+hipError_t launch_linattn_states(const LinattnCall& c, int64_t block, const LinattnPieces* forward, const LinattnPieces* backward);
 // Compute units of the current device (256 if it cannot be asked).
 int64_t linattn_cus();
 

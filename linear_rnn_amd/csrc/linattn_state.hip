@@ -3,7 +3,7 @@
 //
 // The state after a piece is (the piece's decay) (the state before) + (what the piece adds), so the pieces
 // are independent until a short scan over their sums. A workgroup takes a piece of four blocks, each of its waves
-// one block of 128 tokens, 32 at a time from the last to the first: a token's factor is then the decay to
+// one block (128 tokens, or 64), 32 at a time from the last to the first: a token's factor is then the decay to
 // the block's end, known when the token is met, and the sum stays in the matrix products' accumulators. The
 // gradient G = dL/dS of the reverse pass has the same form with (r, dy) in place of (k, v), a token's factor being
 // the decay from the block's start.
@@ -33,6 +33,7 @@ struct StateParams {
   const float* log_w;
   Seq seq;
   int32_t per_token;
+  int32_t block;  // tokens
   int64_t pieces;
 };
 
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(256, 2) void linattn_state_kernel(StateParams p) {
   const int32_t h = unit % p.seq.H;
   const int64_t len = seq_len(p.seq, b);
   const uint32_t row_bytes = p.seq.H * kN * kEsz<F32>;
-  const int64_t nblk = (p.seq.T + kBlk - 1) / kBlk;
+  const int64_t nblk = (p.seq.T + p.block - 1) / p.block;
   const int64_t blk = piece * kPieceBlocks + wave;
   const Turn E = make_turn(lane);
   f32x4 S[4][4];
@@ -60,11 +61,11 @@ __global__ __launch_bounds__(256, 2) void linattn_state_kernel(StateParams p) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) S[t][u] = zero4();
   float decay = 1.f;
-  const int64_t left = len - blk * kBlk;
-  const int subs = left <= 0 ? 0 : left >= kBlk ? kBlk / kSub : (int)((left + kSub - 1) / kSub);
+  const int64_t left = len - blk * p.block;
+  const int subs = left <= 0 ? 0 : left >= p.block ? p.block / kSub : (int)((left + kSub - 1) / kSub);
 #pragma clang loop unroll(disable)
   for (int n = 0; n < subs; ++n) {
-    const int64_t t0 = blk * kBlk + (rev ? n : subs - 1 - n) * kSub;
+    const int64_t t0 = blk * p.block + (rev ? n : subs - 1 - n) * kSub;
     Raw<F32> rk, rv;
     load_raw<F32>(rv, token_buffer<kEsz<F32>>(x.v, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
     load_raw<F32>(rk, token_buffer<kEsz<F32>>(x.k, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(256) void linattn_join_kernel(StateParams p) {
 
 }  // namespace
 
-hipError_t launch_linattn_states(const LinattnCall& c, const LinattnPieces* forward, const LinattnPieces* backward) {
+hipError_t launch_linattn_states(const LinattnCall& c, int64_t block, const LinattnPieces* forward, const LinattnPieces* backward) {
   StateParams p{};
   int sides = 0;
   if (forward)
@@ -165,7 +166,8 @@ hipError_t launch_linattn_states(const LinattnCall& c, const LinattnPieces* forw
   p.log_w = c.log_w;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
-  p.pieces = linattn_pieces(c.T);
+  p.block = (int32_t)block;
+  p.pieces = linattn_pieces(c.T, block);
   const int64_t units = c.B * c.H;
   const void* fn = c.f32 ? reinterpret_cast<const void*>(&linattn_state_kernel<true>)
                          : reinterpret_cast<const void*>(&linattn_state_kernel<false>);
