@@ -451,7 +451,7 @@ int rwkv7_wkv_prefill_algo(int64_t B, int64_t T, int64_t H, int64_t N, int dtype
  *              hold: y there is 0 and the state is that after token lens[b] - 1
  *   y          [B,T,H,N] output in `dtype`
  *   state_out  [B,H,N,N] float32 final state, or NULL; may equal state_in
- *   B, T, H    batch, tokens, heads (>= 0); B*H at most 2^22, H at most 2^18
+ *   B, T, H    batch, tokens, heads (>= 0); B*H at most 2^21, H at most 2^18
  *   N          head size; must be 64
  *
  * The state and every sum are float32 (sums of log_w float64). bfloat16 inputs
@@ -464,7 +464,13 @@ int rwkv7_wkv_prefill_algo(int64_t B, int64_t T, int64_t H, int64_t N, int dtype
  *
  * Ownership, alignment (every pointer 16 bytes), aliasing, empty work, streams
  * and error codes are as for rwkv7_wkv_prefill; a `decay` not one of
- * RWKV7_DECAY_* is RWKV7_ERR_DECAY.
+ * RWKV7_DECAY_* is RWKV7_ERR_DECAY. Where there are few heads for the device a
+ * prompt is taken in segments; the states at their starts (16 KiB for each head and
+ * 512 tokens) live in the per-(device, stream) workspace described for
+ * rwkv7_wkv_prefill_ex, and what is said there about growth and graph capture holds.
+ * Calls on one stream share that workspace: from two threads they are issued one
+ * after the other, and graphs captured on one stream are not replayed at the same
+ * time on two.
  */
 #define RWKV7_DECAY_HEAD 0  /* log_w [H] */
 #define RWKV7_DECAY_TOKEN 1 /* log_w [B, T, H] */
@@ -501,9 +507,9 @@ int rwkv7_linattn_step(const void *r, const float *log_w, const void *k, const v
  *
  * dr, dk, dv and dlog_w are required. With no tokens (B == 0 or T == 0) dlog_w of
  * RWKV7_DECAY_HEAD is zeros and dstate_in is dstate_out. The states are formed
- * again from the inputs: those before each 128 tokens (16 KiB each) live in the
- * per-(device, stream) workspace described for rwkv7_wkv_prefill_ex, and what is
- * said there about growth and graph capture holds.
+ * again from the inputs: those before each 128 tokens (float32: 64) and their
+ * gradients, 40 KiB in all for each head, live in the workspace as those of
+ * rwkv7_linattn_prefill.
  */
 int rwkv7_linattn_backward(const void *r, const float *log_w, const void *k, const void *v, const float *state_in,
                            const int32_t *lens, const void *dy, const float *dstate_out, void *dr, float *dlog_w,
@@ -548,9 +554,8 @@ int rwkv7_layernorm_forward(const void *x, const float *weight, const float *bia
  *
  * The sums over rows are float32, in an order that the sizes alone decide (the
  * same call gives the same bits). With dweight or dbias the partial sums live in
- * the per-(device, stream) workspace described for rwkv7_wkv_prefill_ex (at most
- * 64 MiB, or 8 bytes a channel where that is more), and what is said there about
- * growth and graph capture holds.
+ * the workspace as the states of rwkv7_linattn_prefill do (at most 64 MiB, or 8
+ * bytes a channel where that is more).
  */
 int rwkv7_layernorm_backward(const void *x, const float *weight, const float *mean, const float *rstd, const void *dy,
                              void *dx, float *dweight, float *dbias, int64_t M, int64_t D, int64_t G, int x_dtype,

@@ -23,10 +23,10 @@ int check_sizes(int64_t B, int64_t T, int64_t H, int64_t N, int dtype, int decay
   if (decay != RWKV7_DECAY_HEAD && decay != RWKV7_DECAY_TOKEN) return RWKV7_ERR_DECAY;
   if (B < 0 || T < 0 || H < 0) return RWKV7_ERR_SHAPE;
   if (N != RWKV7_HEAD_SIZE) return RWKV7_ERR_HEAD_SIZE;
-  // two workgroups of 256 threads for each head (and segment) within the grid's limit of 2^32 threads, and
-  // 32-bit offsets inside 32 tokens
+  // four workgroups of 256 threads for each head within the grid's limit of 2^32 threads, and 32-bit offsets inside
+  // 32 tokens
   int64_t units = 0, tok_heads = 0;
-  if (H > (int64_t(1) << 18) || __builtin_mul_overflow(B, H, &units) || units > (int64_t(1) << 22))
+  if (H > (int64_t(1) << 18) || __builtin_mul_overflow(B, H, &units) || units > (int64_t(1) << 21))
     return RWKV7_ERR_SHAPE;
   if (__builtin_mul_overflow(units, T, &tok_heads) || tok_heads > (int64_t(1) << 50)) return RWKV7_ERR_SHAPE;
   out->tokens = tok_heads * 64 * (dtype == RWKV7_DTYPE_BF16 ? 2 : 4);

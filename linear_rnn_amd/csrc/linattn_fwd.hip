@@ -27,11 +27,12 @@ struct OutParams {
   int64_t pieces;
 };
 
-// A workgroup carries 32 of the state's 64 value rows (two tiles) over one segment of one head, 128 tokens at a
-// time: each wave takes 32 of them and leaves what they add to the state in LDS. Then each wave takes a quarter of
-// the state's tiles through the four waves' tokens (the carried part stays in its registers) and leaves the
-// states before each wave's tokens, as operands, for the others. The two workgroups of a
-// head follow each other on the same die, so r and k come from memory once. Loads run a block ahead.
+// ---- float32. A workgroup carries 32 of the state's 64 value rows (two tiles) over one segment of one head, 128 tokens
+// at a time: each wave takes 32 of them and leaves what they add to the state in LDS. Then each wave takes a quarter of
+// the state's tiles through the four waves' tokens (the carried part stays in its registers) and leaves the states
+// before each wave's tokens for the others. The two workgroups of a head follow each other on the same die, so
+// r and k come from memory once. What the pieces of three operands take in registers leaves no room for loads ahead;
+// two workgroups on a compute unit cover for each other.
 constexpr int kVt = 2;  // value tiles of a workgroup
 
 struct Inputs {
@@ -40,11 +41,10 @@ struct Inputs {
   float log_w;
 };
 
-__global__ __launch_bounds__(256, 1) void linattn_out32_kernel(OutParams p) {
+__global__ __launch_bounds__(256, 2) void linattn_out32_kernel(OutParams p) {
   constexpr bool F32 = true;
   constexpr int NI = 3, NO = 3;
   __shared__ f32x4 added[kWaves][4 * kVt][64];
-  __shared__ bf16x8 before[kWaves][kVt][2][NO][64];  // [wave][value tile][key half]: operands
   __shared__ double sums[kWaves][kSub];
   __shared__ float all[kWaves];
   const int lane = threadIdx.x & 63;
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256, 1) void linattn_out32_kernel(OutParams p) {
   const uint32_t off = (lane & 15) * row_bytes + ((lane >> 4) * 8 + half * 32) * kEsz<F32>;  // of v and y
 
   Inputs x;
-  auto load = [&](Inputs& x, int64_t blk) {
+  auto load = [&](int64_t blk) {
     const int64_t t0 = blk * kBlk + wave * kSub;
     const __amdgpu_buffer_rsrc_t vb = token_buffer<kEsz<F32>>(p.v, p.seq, b, h, t0, len - t0, kSub);
     load_raw<F32>(x.k, token_buffer<kEsz<F32>>(p.k, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
@@ -75,7 +75,6 @@ __global__ __launch_bounds__(256, 1) void linattn_out32_kernel(OutParams p) {
     load_raw<F32>(x.r, token_buffer<kEsz<F32>>(p.r, p.seq, b, h, t0, len - t0, kSub), row_bytes, lane);
     x.log_w = load_log_w(p.log_w, p.per_token, p.seq, b, h, t0, len, lane);
   };
-  if (blk0 < live) load(x, blk0);
   f32x4 carry[kVt];  // tiles (wave, 0), (wave, 1) of the half
 #pragma unroll
   for (int m = 0; m < kVt; ++m) {
@@ -86,12 +85,8 @@ __global__ __launch_bounds__(256, 1) void linattn_out32_kernel(OutParams p) {
       carry[m] = *reinterpret_cast<const f32x4*>(p.s_in + (int64_t)unit * kN * kN + state_offset(wave, kVt * half + m, lane));
   }
   const Turn E = make_turn(lane);
-  // the first loads end here: a value that might still be in flight from before the loop would make the
-  // compiler wait for the loads ahead too
-  __builtin_amdgcn_s_waitcnt(0x0f70);
   for (int64_t blk = blk0; blk < live; ++blk) {
-    Inputs ahead;
-    load(ahead, blk + 1);  // behind the last block the descriptors are empty or what comes is not used
+    load(blk);
     const int64_t t0 = blk * kBlk + wave * kSub;
     const Decay d = make_decay(log_w_here(x.log_w, t0, len, lane), sums[wave], lane);
     // what the 32 tokens add to the state: tiles (t, u) of sum_j k_j (left_j v_j)^T
@@ -116,18 +111,19 @@ __global__ __launch_bounds__(256, 1) void linattn_out32_kernel(OutParams p) {
     }
     if (lane == 0) all[wave] = d.all;
     lds_barrier();
-    // the states before each wave's tokens: this wave's two tiles of them
+    // the states before each wave's tokens: this wave's two tiles of them, in the place of what the wave adds
+    f32x4 add[kWaves][kVt];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+      for (int m = 0; m < kVt; ++m) add[w][m] = added[w][kVt * wave + m][lane];
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) {
       const float a = all[w];
 #pragma unroll
       for (int m = 0; m < kVt; ++m) {
-        Op<NO> o = pack<NO>(carry[m], zero4());
-#pragma unroll
-        for (int n = 0; n < NO; ++n)
-          reinterpret_cast<bf16x4*>(&before[w][m][wave >> 1][n][lane])[wave & 1] =
-              __builtin_shufflevector(o.p[n], o.p[n], 0, 1, 2, 3);
-        carry[m] = fma4(carry[m], a, added[w][kVt * wave + m][lane]);
+        added[w][kVt * wave + m][lane] = carry[m];
+        carry[m] = fma4(carry[m], a, add[w][m]);
       }
     }
     // the pairs inside the 32 tokens, as operands over the tokens j: column i
@@ -149,9 +145,8 @@ __global__ __launch_bounds__(256, 1) void linattn_out32_kernel(OutParams p) {
     f32x4 y[2][kVt];
 #pragma unroll
     for (int m = 0; m < kVt; ++m) {
-      Op<NO> S0, S1;
-#pragma unroll
-      for (int n = 0; n < NO; ++n) S0.p[n] = before[wave][m][0][n][lane], S1.p[n] = before[wave][m][1][n][lane];
+      const Op<NO> S0 = pack<NO>(added[wave][m][lane], added[wave][kVt + m][lane]);
+      const Op<NO> S1 = pack<NO>(added[wave][2 * kVt + m][lane], added[wave][3 * kVt + m][lane]);
 #pragma unroll
       for (int I = 0; I < 2; ++I) {
         f32x4 o = mma(S0, natural<F32>(x.r, I, 0), zero4());
@@ -163,7 +158,6 @@ __global__ __launch_bounds__(256, 1) void linattn_out32_kernel(OutParams p) {
     const __amdgpu_buffer_rsrc_t yb = token_buffer<kEsz<F32>>(p.y, p.seq, b, h, t0, T - t0, kSub);
 #pragma unroll
     for (int I = 0; I < 2; ++I) store_pair<F32>(yb, off + I * 16 * row_bytes, y[I][0], y[I][1]);
-    x = ahead;
   }
   for (int64_t blk = live > blk0 ? live : blk0; blk < blk1; ++blk) {  // behind the sequence's end: zeros
     const int64_t t0 = blk * kBlk + wave * kSub;
@@ -394,14 +388,14 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
   }
 }
 
-// The segments of a sequence. A workgroup (float32: two) a head and segment, one at a time on a compute unit; a block
-// of 128 tokens takes it 3.5 us (float32: 5), so a call of few heads, or of a few more than a round of the
+// Pieces of a segment of a sequence. A workgroup (float32: two) a head and segment, a block of 128 tokens takes it 3.5 us
+// (float32: 5.5 of the compute unit, which two share), so a call of few heads, or of a few more than a round of the
 // compute units takes, ends sooner in segments: each in its own workgroup, from the state that the pieces before
 // it add up to. Those cost another pass over k and v and two more launches: about 12 us, and 128 tokens of all heads
-// at 4 TB/s. `segments` weighs the two.
-int64_t segments(int64_t units, int64_t blocks, bool f32, int64_t* piece_count) {
-  const int64_t cus = linattn_cus(), pieces = (blocks + kPieceBlocks - 1) / kPieceBlocks;
-  const double block_us = f32 ? 5.0 : 3.5, groups = f32 ? 2.0 : 1.0;
+// at 4 TB/s. One bfloat16 sequence of 16384 tokens and 12 heads: 61 us in segments, 469 without.
+int64_t segment_pieces(int64_t units, int64_t blocks, int64_t pieces, bool f32) {
+  const int64_t cus = linattn_cus();
+  const double block_us = f32 ? 5.5 : 3.5, groups = f32 ? 2.0 : 1.0;
   int64_t best_every = pieces;
   double best = 0;
   for (int64_t every = pieces; every >= 1; every = every > 1 ? (every + 1) / 2 : 0) {
@@ -411,9 +405,7 @@ int64_t segments(int64_t units, int64_t blocks, bool f32, int64_t* piece_count) 
     double us = rounds * (length * block_us + 2.0);
     if (nseg > 1) us += 12.0 + (double)units * blocks * kBlk * (f32 ? 512 : 256) / 4e6;
     if (every == pieces || us < best) best = us, best_every = every;
-    if (every == 1) break;
   }
-  *piece_count = pieces;
   return best_every;
 }
 
@@ -424,7 +416,8 @@ hipError_t launch_out(const LinattnCall& c) {
   p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.s_in = c.s_in, p.y = c.y, p.s_out = c.s_out;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
-  const int64_t every = segments(units, blocks, F32, &p.pieces);
+  p.pieces = linattn_pieces(c.T, kBlk);
+  const int64_t every = segment_pieces(units, blocks, p.pieces, F32);
   p.nseg = (int32_t)((p.pieces + every - 1) / every);
   p.seg_blocks = p.nseg > 1 ? every * kPieceBlocks : blocks;
   if (p.nseg > 1) {
@@ -473,7 +466,7 @@ __device__ __forceinline__ float4 widen4(const void* base, int64_t at, bool f32)
   return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
 }
 
-template <bool F32, bool NT>
+template <bool F32>
 __global__ __launch_bounds__(256) void linattn_step_kernel(StepParams p) {
   const int lane = threadIdx.x & 63, c = lane & 15, ri = lane >> 4;
   const int64_t unit = blockIdx.x;
@@ -482,8 +475,7 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(StepParams p) {
   f32x4 S[4];
 #pragma unroll
   for (int m = 0; m < 4; ++m) {
-    const f32x4* s = reinterpret_cast<const f32x4*>(p.s_in + sbase + (row0 + 4 * m + ri) * kN + 4 * c);
-    S[m] = !p.s_in ? zero4() : NT ? __builtin_nontemporal_load(s) : *s;
+    S[m] = p.s_in ? *reinterpret_cast<const f32x4*>(p.s_in + sbase + (row0 + 4 * m + ri) * kN + 4 * c) : zero4();
   }
   const float4 r4 = widen4(p.r, unit * kN + 4 * c, F32), k4 = widen4(p.k, unit * kN + 4 * c, F32);
   const float lw = p.log_w[p.per_token ? unit : unit % p.H];
@@ -502,13 +494,7 @@ __global__ __launch_bounds__(256) void linattn_step_kernel(StepParams p) {
     S[m][3] = fmaf(S[m][3], w, vm[m] * k4.w);
     const float y = row16_sum(fmaf(S[m][3], r4.w, fmaf(S[m][2], r4.z, fmaf(S[m][1], r4.y, S[m][0] * r4.x))));
     yo = c == m ? y : yo;
-    if (p.s_out) {
-      f32x4* s = reinterpret_cast<f32x4*>(p.s_out + sbase + (row0 + 4 * m + ri) * kN + 4 * c);
-      if (NT)
-        __builtin_nontemporal_store(S[m], s);
-      else
-        *s = S[m];
-    }
+    if (p.s_out) *reinterpret_cast<f32x4*>(p.s_out + sbase + (row0 + 4 * m + ri) * kN + 4 * c) = S[m];
   }
   if (c < 4) {
     const int64_t at = unit * kN + row0 + 4 * c + ri;
@@ -537,8 +523,8 @@ hipError_t launch_linattn(const LinattnCall& c) { return c.f32 ? launch_out<true
 hipError_t launch_linattn_step(const LinattnCall& c) {
   StepParams p{c.r, c.log_w, c.k, c.v, c.s_in, c.y, c.s_out, (int32_t)c.H, c.per_token};
   void* args[] = {&p};
-  const void* fn = c.f32 ? reinterpret_cast<const void*>(&linattn_step_kernel<true, false>)
-                         : reinterpret_cast<const void*>(&linattn_step_kernel<false, false>);
+  const void* fn = c.f32 ? reinterpret_cast<const void*>(&linattn_step_kernel<true>)
+                         : reinterpret_cast<const void*>(&linattn_step_kernel<false>);
   return hipLaunchKernel(fn, dim3((uint32_t)(c.B * c.H)), dim3(256), args, 0, c.stream);
 }
 

@@ -34,7 +34,6 @@ hipError_t launch_linattn_step(const LinattnCall& c);
 hipError_t launch_linattn_backward(const LinattnCall& c);
 hipError_t launch_linattn_zero(float* dlog_w, int64_t H, hipStream_t stream);
 
-constexpr int64_t kLinattnBlock = 128;  // tokens a workgroup takes at a time (the float32 backward: 64)
 constexpr int64_t kLinattnStateBytes = 64 * 64 * 4;  // one state
 
 // Every sequence in pieces of kPieceBlocks blocks, and the device memory for the states at their starts.

@@ -175,13 +175,6 @@ template <bool F32>
 __device__ __forceinline__ Op<kIn<F32>> natural(const Raw<F32>& r, int J, int h) {
   return pieces<F32>(r.x[J][h]);
 }
-// Element 4e + i of a lane's eight channels, as float32.
-template <bool F32>
-__device__ __forceinline__ float element(const Raw<F32>& r, int J, int h, int e, int i) {
-  if constexpr (F32) return __uint_as_float(r.x[J][h][e][i]);
-  const uint32_t u = r.x[J][h][0][2 * e + (i >> 1)];
-  return (i & 1) ? bf16_hi(u) : bf16_lo(u);
-}
 // Two D tiles (channels of a token column) as eight consecutive channels of a [token][channel] tensor.
 template <bool F32>
 __device__ __forceinline__ void store_pair(__amdgpu_buffer_rsrc_t b, uint32_t off, f32x4 d0, f32x4 d1) {
@@ -231,9 +224,7 @@ struct Decay {
   float col[2];      // exp(c) of token 16I + li
   float row[2][4];   // exp(c_31 - c) of token 16J + 4q + i: what is left of it at the end
   float inrow[2][4]; // exp(c) of token 16J + 4q + i
-  float out[2];      // exp(c_31 - c) of token 16J + li
   f32x4 d00, d01, d11;  // D with the tokens j as rows: tile (J, I) has rows j = 16J + 4q + i, columns i = 16I + li
-  f32x4 t00, t10, t11;  // D with the tokens i as rows: tile (I, J) has rows i = 16I + 4q + i, columns j = 16J + li
   float all;         // exp(c_31)
 };
 
@@ -282,7 +273,6 @@ __device__ __forceinline__ Decay make_decay(float log_w, double* sums, int lane)
 #pragma unroll
   for (int J = 0; J < 2; ++J) {
     d.col[J] = exp_diff(cc[J], 0.0);
-    d.out[J] = exp_diff(end, cc[J]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       d.row[J][i] = exp_diff(end, cr[J][i]);
@@ -294,9 +284,6 @@ __device__ __forceinline__ Decay make_decay(float log_w, double* sums, int lane)
     d.d00[i] = exp_diff(cc[0], cr[0][i]);
     d.d01[i] = exp_diff(cc[1], cr[0][i]);
     d.d11[i] = exp_diff(cc[1], cr[1][i]);
-    d.t00[i] = exp_diff(cr[0][i], cc[0]);
-    d.t10[i] = exp_diff(cr[1][i], cc[0]);
-    d.t11[i] = exp_diff(cr[1][i], cc[1]);
   }
   d.all = exp_diff(end, 0.0);
   return d;

@@ -77,6 +77,13 @@ def test_bad_kinds_and_sizes(L, call):
     assert step(L, T=2) == E_SHAPE and step(L, T=0) == E_SHAPE
 
 
+def test_most_heads(L):
+    p = ptrs(8)
+    p[4] = p[7] = None  # no state, so that a call without tokens has nothing to do
+    assert prefill(L, p, B=1 << 21, T=0, H=1) == 0
+    assert prefill(L, p, B=(1 << 21) + 1, T=0, H=1) == E_SHAPE
+
+
 @pytest.mark.parametrize("call,n,optional", [(prefill, 8, (4, 5, 7)), (step, 7, (4, 6))])
 def test_null_and_misaligned_pointers(L, call, n, optional):
     for i in range(n):
