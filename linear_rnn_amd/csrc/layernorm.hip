@@ -142,8 +142,10 @@ __device__ __forceinline__ float group_sum(float a, float2 (*red)[16], int& turn
   return a;
 }
 
-template <int L>
-constexpr int kBlock = L > 256 ? L : 256;
+// Threads of a workgroup whose threads hold NV vectors each. Groups of eight waves go two to a workgroup where the
+// registers allow it: half as many rows of partial sums.
+template <int L, int NV>
+constexpr int kBlock = L > 256 ? (NV == 1 ? 1024 : L) : 256;
 
 // A thread's place: its group of the row, its first row, its channels.
 template <int L>
@@ -165,7 +167,7 @@ struct Place {
 };
 
 template <bool XF, bool YF, int VEC, int L, int NV>
-__global__ __launch_bounds__(kBlock<L>) void layernorm_forward_kernel(NormParams p) {
+__global__ __launch_bounds__((kBlock<L, NV>)) void layernorm_forward_kernel(NormParams p) {
   __shared__ float2 red[2][16];
   int turn = 0;
   const Place<L> at(p);
@@ -237,8 +239,8 @@ __global__ __launch_bounds__(kBlock<L>) void layernorm_forward_kernel(NormParams
 }
 
 template <bool XF, bool YF, int VEC, int L, int NV>
-__global__ __launch_bounds__(kBlock<L>) void layernorm_backward_kernel(NormParams p) {
-  constexpr int kThreads = kBlock<L>;
+__global__ __launch_bounds__((kBlock<L, NV>)) void layernorm_backward_kernel(NormParams p) {
+  constexpr int kThreads = kBlock<L, NV>;
   __shared__ float2 red[2][16];
   __shared__ float rows[NV * VEC][kThreads];
   int turn = 0;
@@ -433,17 +435,17 @@ __global__ __launch_bounds__(1024) void layernorm_join_kernel(const float* parti
 
 struct Config {
   const void* fn;
-  int L;
+  int L, threads;
 };
 template <bool BWD, bool XF, bool YF, int VEC, int L, int NV>
 Config config() {
-  if constexpr (BWD) return {reinterpret_cast<const void*>(&layernorm_backward_kernel<XF, YF, VEC, L, NV>), L};
-  else return {reinterpret_cast<const void*>(&layernorm_forward_kernel<XF, YF, VEC, L, NV>), L};
+  if constexpr (BWD) return {reinterpret_cast<const void*>(&layernorm_backward_kernel<XF, YF, VEC, L, NV>), L, kBlock<L, NV>};
+  else return {reinterpret_cast<const void*>(&layernorm_forward_kernel<XF, YF, VEC, L, NV>), L, kBlock<L, NV>};
 }
-// The threads of a group: as few as hold it in 16 registers each (so that a wave takes several short
+// The threads of a group: as few as hold it in 16 registers each, or 8 where two rows share a workgroup (so that a wave takes several short
 // groups and a row of weights is spread over few threads), in vectors of 8 channels where every group
 // starts on 16 bytes. 1024 threads have 128 registers each, which the gradients of a long group pass by a little:
-// M=4096 n=16384 bfloat16 still 164 us, 234 by the long kernels, but channel by channel n=16380 403 against 234.
+// M=4096 n=16384 bfloat16 still 135 us, 234 by the long kernels, but channel by channel n=16380 403 against 234.
 template <bool BWD, bool XF, bool YF>
 Config pick(int n) {
   if (n % 8 == 0) {
@@ -453,8 +455,8 @@ Config pick(int n) {
     if (n <= 512) return config<BWD, XF, YF, 8, 64, 1>();
     if (n <= 1024) return config<BWD, XF, YF, 8, 64, 2>();
     if (n <= 2048) return config<BWD, XF, YF, 8, 128, 2>();
-    if (n <= 4096) return config<BWD, XF, YF, 8, 256, 2>();
-    if (n <= 8192) return config<BWD, XF, YF, 8, 512, 2>();
+    if (n <= 4096) return config<BWD, XF, YF, 8, 512, 1>();
+    if (n <= 8192) return config<BWD, XF, YF, 8, 1024, 1>();
     if (n <= 16384) return config<BWD, XF, YF, 8, 1024, 2>();
   } else {
     if (n <= 16) return config<BWD, XF, YF, 1, 16, 1>();
@@ -467,7 +469,7 @@ Config pick(int n) {
     if constexpr (!BWD)
       if (n <= 16384) return config<BWD, XF, YF, 1, 1024, 16>();
   }
-  return {nullptr, 0};
+  return {nullptr, 0, 0};
 }
 
 hipError_t start(const void* fn, int64_t blocks, int threads, NormParams& p, hipStream_t stream) {
@@ -481,13 +483,13 @@ NormParams params(const NormCall& c) {
   p.M = c.M, p.D = (int32_t)c.D, p.G = (int32_t)c.G, p.n = (int32_t)(c.D / c.G), p.eps = c.eps;
   return p;
 }
-// Workgroups: `most` over the whole device, no more than there are rows for.
-void spread(NormParams& p, int L, int64_t most) {
-  const int slots = L > 256 ? 1 : 256 / L;
+// Workgroups: of `most` threads together, no more than there are rows for.
+void spread(NormParams& p, const Config& f, int64_t most) {
+  const int slots = f.threads / f.L;
   p.S = p.G < slots ? p.G : slots;
   p.R = slots / p.S;
   p.slabs = (p.G + p.S - 1) / p.S;
-  int64_t nb = most / p.slabs;
+  int64_t nb = most / f.threads / p.slabs;
   const int64_t rows = (p.M + p.R - 1) / p.R;
   if (nb > rows) nb = rows;
   p.nb = (int32_t)(nb < 1 ? 1 : nb);
@@ -502,8 +504,8 @@ hipError_t forward(const NormCall& c) {
     return start(reinterpret_cast<const void*>(&layernorm_forward_long_kernel<XF, YF>), units < 2048 ? units : 2048, 1024,
                  p, c.stream);
   }
-  spread(p, f.L, f.L > 256 ? 1024 : 2048);
-  return start(f.fn, (int64_t)p.nb * p.slabs, f.L > 256 ? f.L : 256, p, c.stream);
+  spread(p, f, 1 << 19);
+  return start(f.fn, (int64_t)p.nb * p.slabs, f.threads, p, c.stream);
 }
 
 template <bool XF, bool YF>
@@ -512,7 +514,9 @@ hipError_t backward(const NormCall& c) {
   const bool sums = c.dweight || c.dbias;
   const Config f = pick<true, XF, YF>(p.n);
   if (f.fn) {
-    spread(p, f.L, f.L > 256 ? 512 : 1024);
+    // each workgroup adds a row of partial sums: M=16384 D=4096 bfloat16 97 us with four times as many, 79 so
+    // (M=32768 D=768 41 us with twice as many, 35 so)
+    spread(p, f, f.threads > 256 ? 1 << 18 : 1 << 17);
   } else {
     int64_t nb = (int64_t(1) << 23) / p.D;  // partial sums of at most 64 MiB, as those of shorter groups
     nb = nb < 1 ? 1 : nb < 64 ? nb : 64;
@@ -526,7 +530,7 @@ hipError_t backward(const NormCall& c) {
   }
   hipError_t e;
   if (f.fn) {
-    e = start(f.fn, (int64_t)p.nb * p.slabs, f.L > 256 ? f.L : 256, p, c.stream);
+    e = start(f.fn, (int64_t)p.nb * p.slabs, f.threads, p, c.stream);
   } else {
     const int64_t units = p.M * p.G;
     e = start(reinterpret_cast<const void*>(&layernorm_backward_long_kernel<XF, YF>), units < 2048 ? units : 2048, 1024, p,

@@ -64,7 +64,8 @@ def test_groups(torch, M, G, n, xk, yk):
 
 
 @pytest.mark.parametrize("xk", KINDS)
-@pytest.mark.parametrize("M,D,G", [(5000, 64, 1), (4099, 128, 2), (2500, 771, 1), (3001, 1024, 16)])
+@pytest.mark.parametrize("M,D,G", [(5000, 64, 1), (4099, 128, 2), (2500, 771, 1), (3001, 1024, 16), (1301, 4096, 1), (701, 8192, 2),
+                                   (523, 8192, 1)])
 def test_many_rows(torch, M, D, G, xk):
     """Every workgroup takes several rows, and the sums over rows meet from all of them."""
     both(torch, M, D, G, xk, xk, seed=M)
