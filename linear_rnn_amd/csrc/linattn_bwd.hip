@@ -34,7 +34,6 @@ namespace {
 
 using namespace linattn;
 
-constexpr int kRow = kN * 2;  // bytes of a row of one piece
 constexpr int kPiece = kN * kRow;  // of one piece of a state
 // Sizes and the LDS of one element type.
 template <bool F32>
@@ -78,11 +77,7 @@ struct GradParams {
   int64_t seg_blocks;
 };
 
-// Where 16-byte piece `piece` of a row is: exchanged within the row so that reads of one piece of 16 rows, and turned
-// reads of four pieces of 8 rows, meet as many banks as there are; rows that follow each other in a block's inputs,
-// rows as channel() numbers them in a state's pieces.
-__device__ __forceinline__ int row_key(int row) { return (row >> 1 & 1) | (row >> 2 & 2) | (row & 4); }
-__device__ __forceinline__ int swizzled(int row, int piece) { return row * kRow + 16 * (piece ^ row_key(row)); }
+// The same for a state's pieces, whose rows follow each other as channel() numbers them.
 __device__ __forceinline__ int in_pieces(int row, int piece) {
   return row * kRow + 16 * (piece ^ ((row >> 1 & 1) | (row >> 3 & 2) | (row >> 1 & 4)));
 }
@@ -161,8 +156,8 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
   auto stage = [&](const void* x, int number, int64_t blk) {
     const u32x4 d = descriptor(static_cast<const char*>(x) + rows_at(blk), rows_bytes(len - blk * kTokens - 16 * w));
     const uint32_t to = lds0 + C::kIn + ((blk & 1) * 4 + number) * kRows + w * 16 * kRow;
-    to_lds16(d, src0, to);
-    to_lds16(d, src1, to + 8 * kRow);
+    to_lds16_last(d, src0, to);
+    to_lds16_last(d, src1, to + 8 * kRow);
   };
   auto stage_w = [&](int64_t blk) {
     if (wave < 4 && lane < kSub) {
@@ -240,13 +235,7 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
       o.p[n] = *reinterpret_cast<const bf16x8*>(lds + (from + row0 * kRow) + (nat0 ^ 64 * hh) + n * kRows);
     return o;
   };
-  // turned: column li of tile t, of four rows
-  auto turn4 = [&](int at) {
-    typedef short s16x4 __attribute__((ext_vector_type(4)));
-    return __builtin_bit_cast(
-        bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(lds + at)));
-  };
-  auto join = [](bf16x4 a, bf16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); };
+  auto turn4 = [&](int at) { return turned4(lds + at); };
   // an operand over the tokens of tiles I0, I1 of a tensor, rows its channels of tile t
   auto turned_tokens = [&](int from, int I0, int I1, int t) {
     const int in_tile = (turn0 ^ 64 * (t >> 1)) + 8 * (t & 1);

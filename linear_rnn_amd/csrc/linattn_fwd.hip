@@ -182,7 +182,6 @@ __global__ __launch_bounds__(256, 2) void linattn_out32_kernel(OutParams p) {
 //
 // What is common to the two waves of a quarter, the decay factors of its tokens, one of them leaves in LDS during
 // the block before (once, if the head has one decay and the tokens are all there).
-constexpr int kRow = kN * 2;              // bytes of a token's row
 constexpr int kTile = kSub * kRow;        // bytes of a quarter's rows of one tensor
 constexpr int kExchange = 0;              // [quarter][half][8 tiles][64 lanes] 16 bytes
 constexpr int kStage = 64 << 10;          // [quarter][r, k, v] kTile
@@ -225,8 +224,8 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
   const uint32_t to0 = lds0 + kStage + quarter * 3 * kTile + 16 * half * kRow;
   auto stage = [&](const char*& x, int number) {
     const u32x4 d = descriptor(x, left <= 0 ? 0 : (uint32_t)((left < kSub ? left : kSub) - 1) * row_bytes + kRow);
-    to_lds16(d, src0, to0 + number * kTile);
-    to_lds16(d, src1, to0 + number * kTile + 8 * kRow);
+    to_lds16_last(d, src0, to0 + number * kTile);
+    to_lds16_last(d, src1, to0 + number * kTile + 8 * kRow);
     x += (int64_t)kBlk * row_bytes;
   };
   auto stage_w = [&](int64_t blk) {

@@ -126,6 +126,11 @@ __device__ __forceinline__ u32x4 descriptor(const void* base, uint32_t bytes) {
                (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00027000u};
 }
 __device__ __forceinline__ void to_lds16(u32x4 b, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
+               : "memory");
+}
+// Without temporal hint, for what no later kernel of the call reads.
+__device__ __forceinline__ void to_lds16_last(u32x4 b, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
                : "memory");
 }
@@ -133,6 +138,20 @@ __device__ __forceinline__ void to_lds4(u32x4 b, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
                : "memory");
 }
+
+// Rows of 64 bfloat16 in LDS. Where 16-byte piece `piece` of row `row` is: exchanged within the row so that reads of one
+// piece of 16 rows, and turned reads of four pieces of 8 rows, meet as many banks as there are.
+constexpr int kRow = kN * 2;  // bytes
+__device__ __forceinline__ int row_key(int row) { return (row >> 1 & 1) | (row >> 2 & 2) | (row & 4); }
+__device__ __forceinline__ int swizzled(int row, int piece) { return row * kRow + 16 * (piece ^ row_key(row)); }
+// Turned: of each 16 lanes, lanes 4r .. 4r + 3 give the places of 16 consecutive elements of a row r, lane c gets
+// element c of the four rows.
+__device__ __forceinline__ bf16x4 turned4(const char* at) {
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(
+      bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at));
+}
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7); }
 
 // One tensor's 32 tokens of one head, as loaded: [token tile][depth step].
 template <bool F32>
