@@ -212,11 +212,10 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
   const int64_t live = (len + kBlk - 1) / kBlk < blk1 ? (len + kBlk - 1) / kBlk : blk1;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)lds;
 
-  // Rows to LDS: an instruction takes 8 rows, row r's piece c to place c ^ (r / 2 % 8). The two waves of a quarter
-  // take 16 rows each.
+  // Rows to LDS: an instruction takes 8 rows. The two waves of a quarter take 16 rows each.
   const int row = 16 * half + (lane >> 3);
-  const uint32_t src0 = row * row_bytes + 16 * ((lane & 7) ^ (row >> 1 & 7));
-  const uint32_t src1 = src0 + 8 * row_bytes + 16 * (((lane & 7) ^ ((row + 8) >> 1 & 7)) - ((lane & 7) ^ (row >> 1 & 7)));
+  const uint32_t src0 = row * row_bytes + 16 * ((lane & 7) ^ row_key(row));
+  const uint32_t src1 = (row + 8) * row_bytes + 16 * ((lane & 7) ^ row_key(row + 8));
   const int64_t first = blk0 * kBlk + quarter * kSub, start = ((b * T + first) * p.seq.H + h) * kRow;
   const char *next_r = static_cast<const char*>(p.r) + start, *next_k = static_cast<const char*>(p.k) + start,
              *next_v = static_cast<const char*>(p.v) + start;
@@ -236,11 +235,16 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
     }
   };
   const int rows_r = kStage + quarter * 3 * kTile, rows_k = rows_r + kTile, rows_v = rows_k + kTile;
-  // operand of the rows 16J + li, channels 32hh + 8q ..
   const int li = lane & 15, q = lane >> 4;
+  const int nat0 = swizzled(li, q), turn0 = swizzled(4 * q + (li >> 2), li & 3);
+  // operand of the rows 16J + li, channels 32hh + 8q ..
   auto staged = [&](int from, int J, int hh) {
-    const int place = (4 * hh + q) ^ (li >> 1);
-    return Op<1>{{*reinterpret_cast<const bf16x8*>(lds + from + (16 * J + li) * kRow + 16 * place)}};
+    return Op<1>{{*reinterpret_cast<const bf16x8*>(lds + from + 16 * J * kRow + (nat0 ^ 64 * hh))}};
+  };
+  // operand over the 32 tokens, rows the channels of tile t
+  auto staged_turned = [&](int from, int t) {
+    const char* const at = lds + from + (turn0 ^ 64 * (t >> 1)) + 8 * (t & 1);
+    return Op<1>{{join(turned4(at), turned4(at + 16 * kRow))}};
   };
 
   f32x4 carry[kVt];  // tiles (quarter, 0), (quarter, 1) of the half
@@ -252,7 +256,6 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
     else if (p.s_in)
       carry[m] = *reinterpret_cast<const f32x4*>(p.s_in + (int64_t)unit * kN * kN + state_offset(quarter, kVt * half + m, lane));
   }
-  const Turn E = make_turn(lane);
   f32x4(*exch)[2][8][64] = reinterpret_cast<f32x4(*)[2][8][64]>(lds + kExchange);
   Factors* factors = reinterpret_cast<Factors*>(lds + kFactors);
   // The factors of a block's quarter, by its second wave, which has its exchange slot to itself then.
@@ -289,7 +292,11 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
       for (int J = 0; J < 2; ++J)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) K[J][hh] = staged(rows_k, J, hh), R[J][hh] = staged(rows_r, J, hh);
-      const Op<1> v0 = staged(rows_v, 0, half), v1 = staged(rows_v, 1, half);
+      Op<1> Kt[4], Vt[kVt];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) Kt[x] = staged_turned(rows_k, x);
+#pragma unroll
+      for (int m = 0; m < kVt; ++m) Vt[m] = staged_turned(rows_v, kVt * half + m);
       lds_barrier();  // both waves of every quarter have their operands
       // the next block's rows, a tensor at a time: all at once they fill the queue of loads and hold the waves up
       stage_w(blk + 3);
@@ -298,20 +305,18 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
       const f32x4 left1 = *reinterpret_cast<const f32x4*>(f.left + 16 + 4 * q);
       in[0] = f.in[li], in[1] = f.in[16 + li];
       // what the 32 tokens add to the state: tiles (t, m) of sum_j k_j (left_j v_j)^T
-      Op<1> Vt[kVt];
       Op<3> Vs[kVt];
 #pragma unroll
       for (int m = 0; m < kVt; ++m) {
-        const f32x4 a0 = turned(v0, E, m), a1 = turned(v1, E, m);
-        Vt[m] = pack<1>(a0, a1);
+        f32x4 a0, a1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a0[i] = (float)Vt[m].p[0][i], a1[i] = (float)Vt[m].p[0][4 + i];
         Vs[m] = pack<3>(a0 * left0, a1 * left1);
       }
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const Op<1> Kt = turned_op(K[0][t >> 1], K[1][t >> 1], E, t);
+      for (int x = 0; x < 4; ++x)
 #pragma unroll
-        for (int m = 0; m < kVt; ++m) exch[quarter][half][kVt * t + m][lane] = mma(Kt, Vs[m], zero4());
-      }
+        for (int m = 0; m < kVt; ++m) exch[quarter][half][kVt * x + m][lane] = mma(Kt[x], Vs[m], zero4());
       stage(next_v, 2);
       // the pairs inside the 32 tokens
       f32x4 a00 = zero4(), a01 = zero4(), a11 = zero4();
