@@ -77,7 +77,7 @@ struct GradParams {
   int64_t seg_blocks;
 };
 
-// The same for a state's pieces, whose rows follow each other as channel() numbers them.
+// swizzled() for a state's pieces, whose rows follow each other as channel() numbers them.
 __device__ __forceinline__ int in_pieces(int row, int piece) {
   return row * kRow + 16 * (piece ^ ((row >> 1 & 1) | (row >> 3 & 2) | (row >> 1 & 4)));
 }
@@ -330,7 +330,9 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
       dj[i] = exp_diff(c, r), di[i] = exp_diff(r, c);
     }
     if constexpr (!F32) stage(p.k, 1, blk + 1);
-    // the pairs with the tiles behind (for dk, dv) and before (for dr)
+    // The pairs with the tiles behind (for dk, dv) and before (for dr). Their part of k_j . dk_j and r_i . dr_i is summed
+    // here, in float32: the products with the pairs' pieces are only as good as dk and dr need them.
+    float kdk = 0.f, rdr = 0.f;
     f32x4 ak[4], av[4], ar[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) ak[t] = av[t] = ar[t] = zero4();
@@ -349,7 +351,9 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
         const f32x4 f = *reinterpret_cast<const f32x4*>(f32s(C::kInto) + 16 * X + 4 * q) * (on ? between : 0.f);
         pq[e] = x * f, pa[e] = a * f;
         if (on) {
-          const float s = wave_sum((a[0] * pq[e][0] + a[1] * pq[e][1] + a[2] * pq[e][2] + a[3] * pq[e][3]) * left);
+          const float own = (a[0] * pq[e][0] + a[1] * pq[e][1] + a[2] * pq[e][2] + a[3] * pq[e][3]) * left;
+          kdk += own;
+          const float s = wave_sum(own);
           if (lane == 0) f32s(C::kPairs)[w * kTiles + X] = s;
           between *= f32s(C::kPerTile)[X];
         }
@@ -374,8 +378,12 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
         const bool on = e == 0 || J1 < J;
         f32x4 x = mma(nat(rows_v, 16 * X, 0), D[0], zero4());
         x = mma(nat(rows_v, 16 * X, 1), D[1], x);
+        const f32x4 a = mma(nat(rows_k, 16 * X, 1), R[1], mma(nat(rows_k, 16 * X, 0), R[0], zero4()));
         pp[e] = x * (*reinterpret_cast<const f32x4*>(f32s(C::kLeft) + 16 * X + 4 * q) * (on ? between : 0.f));
-        if (on) between *= f32s(C::kPerTile)[X];
+        if (on) {
+          rdr += a[0] * pp[e][0] + a[1] * pp[e][1] + a[2] * pp[e][2] + a[3] * pp[e][3];
+          between *= f32s(C::kPerTile)[X];
+        }
       }
       const Op<NO> P = pack<NO>(pp[0], pp[1]);
 #pragma unroll
@@ -383,7 +391,8 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
     }
     __builtin_amdgcn_sched_barrier(0);  // phases whose registers would not fit together
     if constexpr (!F32) stage(p.dy, 3, blk + 1);
-    float cross = 0.f, kdk = 0.f, rdr = 0.f;
+    rdr *= into;
+    float cross = 0.f;
     {  // dk and dv: the gradient behind the block, the factor of the tokens, the tile's own pairs
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -409,12 +418,12 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float k = value(K[t >> 1], t & 1, i);
-          kg = fmaf(o[i], k, kg), kdk = fmaf(ak[t][i], k, kdk);
+          kg = fmaf(o[i], k, kg);
         }
       }
+      kdk = rows_sum(kdk + kg);
       kg = wave_sum(kg);
       if (lane == 0) f32s(C::kPerTile)[2 * kTiles + w] = kg;
-      kdk = rows_sum(kdk);
       __builtin_amdgcn_sched_barrier(0);
       f32x4 x = mma(D[1], V[1], mma(D[0], V[0], zero4())), a = mma(R[1], K[1], mma(R[0], K[0], zero4()));
       x = masked_i(x, di, lane);
@@ -462,12 +471,12 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float r = value(R[t >> 1], t & 1, i);
-          rs = fmaf(o[i], r, rs), rdr = fmaf(ar[t][i], r, rdr);
+          rs = fmaf(o[i], r, rs);
         }
       }
+      rdr = rows_sum(rdr + rs);
       rs = wave_sum(rs);
       if (lane == 0) f32s(C::kPerTile)[3 * kTiles + w] = rs;
-      rdr = rows_sum(rdr);
       const f32x4 x = masked_j(mma(V[1], D[1], mma(V[0], D[0], zero4())), dj, lane);
       const Op<NO> P = pack<NO>(x, zero4());
 #pragma unroll

@@ -29,8 +29,9 @@
 //    channels, and a token's 8 channels of tiles 2h, 2h + 1 are one 16-byte store;
 //  - token 16J + 4q + i is slot (q, e = J, i): the two token tiles of a D column are an operand of
 //    a product over the 32 tokens.
-// The only layout change left is to turn a token-row operand into a channel-row one: a product
-// with a 0/1 matrix (exact), so that no data goes through LDS but the state between waves.
+// The only layout change left is to turn a token-row operand into a channel-row one: bfloat16 rows
+// are read from LDS turned, float32 rows, which have no room there, go through products with a 0/1
+// matrix (exact).
 #pragma once
 
 #include "wkv7_device.hpp"

@@ -66,6 +66,22 @@ def test_one_head(torch, T, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [128, 515, 1300])
+def test_float32_outputs_are_as_good_as_float32(torch, T, dtype):
+    """dlog_w and dstate_in are float32 whatever the type of the others. Of inputs with random signs nothing cancels
+    but by chance, so the 2-norm of the error is that of the roundings on the way to the value: about 1000 of at most
+    2^-24 each (count in linattn_ref), on average 0.4 of that and of a sum that has half its size: 32 * 0.4 * 0.7 * 2^-24,
+    under 2^-20 of the value's norm. Products with two bfloat16 pieces (2^-17) would leave more."""
+    x = ref.make(2, T, 4, getattr(torch, DT[dtype]), "token", seed=60 + T, state=True)
+    say("linattn backward float32 outputs", T, dtype)
+    got = run(dev(x))
+    want, _ = ref.backward(x)
+    for n in ("dlog_w", "dstate_in"):
+        err = float((got[n].cpu().to(ref.F64) - want[n]).norm() / want[n].norm())
+        assert err <= 2.0 ** -20, (n, err)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,T,H", [(20, 150, 40), (9, 700, 32), (1, 129, 300), (2, 900, 64)])
 def test_many_heads(torch, B, T, H, dtype):
     x = ref.make(B, T, H, getattr(torch, DT[dtype]), "head", seed=50)
