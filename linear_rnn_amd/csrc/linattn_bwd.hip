@@ -25,6 +25,10 @@
 // bfloat16: blocks of 128 tokens, eight waves; rows come to LDS by direct loads a block ahead, and with two buffers and
 // the pieces of one state the LDS is full, so that dk and dv are done with G, then dr with S in the same place.
 // float32: the rows are kept as three bfloat16 pieces each, so blocks of 64 tokens, four waves, one buffer.
+//
+// B=8 T=4096 H=12 bfloat16 151 us (520 MB): vector instructions issue for 45% of it, matrix products for 20%, with two waves
+// on a SIMD; a wave's chain from block to block instead (the states carried, no borders in memory) took 432. B=3 T=515
+// H=16 float32 29 us, carried 156.
 #include "linattn_internal.hpp"
 #include "linattn_ops.hpp"
 #include "wkv7_internal.hpp"
