@@ -1,7 +1,10 @@
 // Argument checks shared by the C ABI sources: byte ranges and their overlap.
 #pragma once
 
+#include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include "rwkv7_wkv.h"
 
 namespace rwkv7 {
 
@@ -31,6 +34,16 @@ inline bool outputs_overlap(const Range* out, int nout, const Range* in, int nin
       if (overlap(out[o], out[e])) return true;
   }
   return false;
+}
+
+// A launch's status. It may allocate on the host or take a lock; nothing that these throw leaves a C entry point.
+template <class Launch>
+int status_of(Launch launch) {
+  try {
+    return launch() == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
+  } catch (...) {
+    return RWKV7_ERR_HIP;
+  }
 }
 
 }  // namespace rwkv7

@@ -14,6 +14,7 @@
 // All statistics and sums are float32; bfloat16 outputs are rounded once.
 // [32768, 768] float32 to bfloat16 27.8 us (5.4 TB/s); gradients of [16384, 4096] bfloat16 78 us (5.2), of [8191, 1024]
 // float32 in 16 groups 23.3 us (4.3).
+#include "lane_sums.hpp"
 #include "layernorm_internal.hpp"
 #include "wkv7_device.hpp"
 #include "wkv7_internal.hpp"

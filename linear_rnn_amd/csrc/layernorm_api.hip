@@ -52,7 +52,7 @@ int rwkv7_layernorm_forward(const void* x, const float* weight, const float* bia
   c.x = x, c.weight = weight, c.bias = bias, c.y = y, c.mean = mean, c.rstd = rstd, c.M = M, c.D = D, c.G = G, c.eps = eps;
   c.x_f32 = x_dtype == RWKV7_DTYPE_F32, c.y_f32 = y_dtype == RWKV7_DTYPE_F32;
   c.stream = static_cast<hipStream_t>(stream);
-  return rwkv7::launch_layernorm_forward(c) == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
+  return rwkv7::status_of([&] { return rwkv7::launch_layernorm_forward(c); });
 }
 
 int rwkv7_layernorm_backward(const void* x, const float* weight, const float* mean, const float* rstd, const void* dy,
@@ -75,7 +75,7 @@ int rwkv7_layernorm_backward(const void* x, const float* weight, const float* me
   c.dweight = dweight, c.dbias = dbias, c.M = M, c.D = D, c.G = G;
   c.x_f32 = x_dtype == RWKV7_DTYPE_F32, c.y_f32 = y_dtype == RWKV7_DTYPE_F32;
   c.stream = static_cast<hipStream_t>(stream);
-  return rwkv7::launch_layernorm_backward(c) == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
+  return rwkv7::status_of([&] { return rwkv7::launch_layernorm_backward(c); });
 }
 
 }  // extern "C"

@@ -61,8 +61,7 @@ int run_linattn(const void* r, const float* log_w, const void* k, const void* v,
   LinattnCall c{};
   c.r = r, c.log_w = log_w, c.k = k, c.v = v, c.s_in = state_in, c.lens = lens, c.y = y, c.s_out = state_out;
   c.B = B, c.T = T, c.H = H, c.f32 = dtype == RWKV7_DTYPE_F32, c.per_token = decay == RWKV7_DECAY_TOKEN, c.stream = s;
-  e = step ? rwkv7::launch_linattn_step(c) : rwkv7::launch_linattn(c);
-  return e == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
+  return rwkv7::status_of([&] { return step ? rwkv7::launch_linattn_step(c) : rwkv7::launch_linattn(c); });
 }
 
 int run_backward(const LinattnCall& c, int64_t N, int dtype, int decay) {
@@ -88,8 +87,7 @@ int run_backward(const LinattnCall& c, int64_t N, int dtype, int decay) {
     if (e == hipSuccess && !c.per_token && c.dlog_w) e = rwkv7::launch_linattn_zero(c.dlog_w, c.H, c.stream);
     return e == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
   }
-  e = rwkv7::launch_linattn_backward(c);
-  return e == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
+  return rwkv7::status_of([&] { return rwkv7::launch_linattn_backward(c); });
 }
 
 }  // namespace

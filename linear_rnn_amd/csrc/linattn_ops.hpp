@@ -34,6 +34,7 @@
 // matrix (exact).
 #pragma once
 
+#include "lane_sums.hpp"
 #include "wkv7_device.hpp"
 
 namespace rwkv7 {

@@ -406,7 +406,7 @@ size_t slab_budget_bytes() {
 
 }  // namespace
 
-hipError_t device_workspace(hipStream_t stream, size_t bytes, void** out, int slot) try {
+hipError_t device_workspace(hipStream_t stream, size_t bytes, void** out, int slot) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
@@ -420,7 +420,6 @@ hipError_t device_workspace(hipStream_t stream, size_t bytes, void** out, int sl
     if (e != hipSuccess) return e;
     if (cap != hipStreamCaptureStatusNone) return hipErrorStreamCaptureUnsupported;
     const size_t grow = ws.bytes > bytes / 2 ? 2 * ws.bytes : bytes;
-    if (ws.ptr) g_ws_retired.reserve(g_ws_retired.size() + 1);  // may throw: before there is a buffer to lose
     void* p = nullptr;
     e = hipMalloc(&p, grow);
     if (e != hipSuccess) return e;
@@ -430,9 +429,8 @@ hipError_t device_workspace(hipStream_t stream, size_t bytes, void** out, int sl
   }
   *out = ws.ptr;
   return hipSuccess;
-} catch (...) {  // of the containers or the lock: nothing may leave a C entry point
-  return hipErrorOutOfMemory;
 }
+
 
 namespace {
 
