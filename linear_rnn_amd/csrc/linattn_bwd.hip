@@ -26,8 +26,8 @@
 // the pieces of one state the LDS is full, so that dk and dv are done with G, then dr with S in the same place.
 // float32: the rows are kept as three bfloat16 pieces each, so blocks of 64 tokens, four waves, one buffer.
 //
-// B=8 T=4096 H=12 bfloat16 151 us (520 MB): vector instructions issue for 45% of it, matrix products for 20%, with two waves
-// on a SIMD; a wave's chain from block to block instead (the states carried, no borders in memory) took 432. B=3 T=515
+// B=8 T=4096 H=12 bfloat16 145 us (520 MB, but the same without waiting for memory): vector instructions issue for 45% of
+// it, matrix products for 20%, with two waves on a SIMD; a wave's chain from block to block instead (the states carried, no borders in memory) took 432. B=3 T=515
 // H=16 float32 29 us, carried 156.
 #include "linattn_internal.hpp"
 #include "linattn_ops.hpp"
@@ -101,6 +101,17 @@ __device__ __forceinline__ float sums_from(float x) {
   x += dpp_f32<0x108>(x);
   return x;
 }
+__device__ __forceinline__ float dot4(f32x4 a, f32x4 b, float c) {
+  return fmaf(a[3], b[3], fmaf(a[2], b[2], fmaf(a[1], b[1], fmaf(a[0], b[0], c))));
+}
+// Times the lane that many places up or down the row of 16, 1 behind its ends.
+template <int CTRL>
+__device__ __forceinline__ float times_dpp(float x) {
+  return x * __uint_as_float(__builtin_amdgcn_update_dpp(0x3f800000, (int)__float_as_uint(x), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float readlane_f32(float x, int l) {
+  return __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(x), l));
+}
 __device__ __forceinline__ float wave_sum(float x) { return rows_sum(row16_sum(x)); }
 
 // Element 4e + i of an operand, as float32.
@@ -154,34 +165,58 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
   // ---- loads
   const uint32_t src0 = (lane >> 3) * row_bytes + 16 * ((lane & 7) ^ row_key(lane >> 3));
   const uint32_t src1 = ((lane >> 3) + 8) * row_bytes + 16 * ((lane & 7) ^ row_key(8 + (lane >> 3)));
-  // where the wave's 16 rows of a block start in every tensor, and the bytes to the end of the last of n of them
-  auto rows_at = [&](int64_t blk) { return ((b * T + blk * kTokens + 16 * w) * p.seq.H + h) * (int64_t)kRowBytes; };
-  auto rows_bytes = [&](int64_t n) { return n <= 0 ? 0 : (uint32_t)((n < 16 ? n : 16) - 1) * row_bytes + kRowBytes; };
-  auto stage = [&](const void* x, int number, int64_t blk) {
-    const u32x4 d = descriptor(static_cast<const char*>(x) + rows_at(blk), rows_bytes(len - blk * kTokens - 16 * w));
-    const uint32_t to = lds0 + C::kIn + ((blk & 1) * 4 + number) * kRows + w * 16 * kRow;
+  // A block: the row of its first token in every tensor (and element of log w); of its tokens, how many count and how many the
+  // tensors hold; where the wave's 16 rows start, and the bytes to the end of the last of them that counts.
+  struct Block {
+    int64_t row;
+    int live, rows, parity;
+    int64_t start;
+    uint32_t bytes;
+  };
+  const uint32_t own = 16 * w * p.seq.H;  // the wave's first row, from the block's
+  auto rows_bytes = [&](int n) {
+    n -= 16 * w;
+    n = n < 16 ? n : 16;
+    return n > 0 ? (uint32_t)(n - 1) * row_bytes + kRowBytes : 0;
+  };
+  auto tokens = [&](int64_t n) { return n < 0 ? 0 : n < kTokens ? (int)n : kTokens; };
+  auto block = [&](int64_t blk) {
+    const int64_t t = blk * kTokens;
+    Block x{(b * T + t) * p.seq.H + h, tokens(len - t), tokens(T - t), (int)(blk & 1), 0, 0};
+    x.start = (x.row + own) * (int64_t)kRowBytes;
+    x.bytes = rows_bytes(x.live);
+    return x;
+  };
+  auto stage = [&](const void* x, int number, const Block& at) {
+    const u32x4 d = descriptor(static_cast<const char*>(x) + at.start, at.bytes);
+    const uint32_t to = lds0 + C::kIn + (at.parity * 4 + number) * kRows + w * 16 * kRow;
     to_lds16_last(d, src0, to);
     to_lds16_last(d, src1, to + 8 * kRow);
   };
-  auto stage_w = [&](int64_t blk) {
+  // log w of `most` tokens from the block's token `first` on, as log_w_span() has it
+  auto log_w_at = [&](const Block& at, int first, int most) {
+    int n = at.live - first;
+    n = n < most ? n : most;
+    return Span{reinterpret_cast<const char*>(p.log_w + (p.per_token ? at.row + (uint32_t)first * p.seq.H : h)),
+                n <= 0 ? 0 : p.per_token ? ((uint32_t)(n - 1) * p.seq.H + 1) * 4 : 4};
+  };
+  auto stage_w = [&](const Block& at) {
     if (wave < 4 && lane < kSub) {
-      const int64_t t32 = blk * kTokens + wave * kSub;
-      const Span s = log_w_span(p.log_w, p.per_token, p.seq, b, h, t32, len);
+      const Span s = log_w_at(at, wave * kSub, kSub);
       to_lds4(descriptor(s.base, s.bytes), lane * (p.per_token ? p.seq.H * 4 : 0),
-              lds0 + C::kLogW + (blk & 1) * kTokens * 4 + wave * kSub * 4);
+              lds0 + C::kLogW + at.parity * kTokens * 4 + wave * kSub * 4);
     }
   };
   // float32: the wave's rows from memory to LDS by way of registers, in pieces
   struct Rows {
     u32x4 x[4][2][F32 ? 2 : 1];
   };
-  auto load_rows = [&](int64_t blk) {
+  auto load_rows = [&](const Block& at) {
     Rows o;
     const void* src[4] = {p.r, p.k, p.v, p.dy};
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
-      const __amdgpu_buffer_rsrc_t from = buffer(static_cast<const char*>(src[x]) + rows_at(blk),
-                                                 rows_bytes(len - blk * kTokens - 16 * w));
+      const __amdgpu_buffer_rsrc_t from = buffer(static_cast<const char*>(src[x]) + at.start, at.bytes);
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
@@ -260,19 +295,20 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
 
   float head_sum = 0.f;
   Border<kEighths> grad;
+  Block now = block(blk0);
   if (blk0 < live) {
-    if constexpr (!F32) stage(p.r, 0, blk0), stage(p.k, 1, blk0), stage(p.v, 2, blk0), stage(p.dy, 3, blk0), stage_w(blk0);
+    if constexpr (!F32) stage(p.r, 0, now), stage(p.k, 1, now), stage(p.v, 2, now), stage(p.dy, 3, now), stage_w(now);
     grad = load_grad(blk0);
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   for (int64_t blk = blk0; blk < live; ++blk) {
-    const int64_t t0 = blk * kTokens + 16 * w;
-    const int rows_r = C::kIn + (F32 ? 0 : (blk & 1) * 4 * kRows), rows_k = rows_r + NI * kRows,
+    const Block next = block(blk + 1);
+    const int rows_r = C::kIn + (F32 ? 0 : now.parity * 4 * kRows), rows_k = rows_r + NI * kRows,
               rows_v = rows_k + NI * kRows, rows_d = rows_v + NI * kRows;
     float lw;
     if constexpr (F32) {
-      const Rows x = load_rows(blk);
-      const Span s = log_w_span(p.log_w, p.per_token, p.seq, b, h, t0, len);
+      const Rows x = load_rows(now);
+      const Span s = log_w_at(now, 16 * w, 16);
       lw = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(buffer(s.base, s.bytes),
                                                                           li * (p.per_token ? p.seq.H * 4 : 0), 0, 0));
 #pragma unroll
@@ -285,20 +321,20 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
             *reinterpret_cast<bf16x8*>(lds + C::kIn + (n * NI + m) * kRows + 16 * w * kRow + (nat0 ^ 64 * hh)) = o.p[m];
         }
     } else {
-      lw = f32s(C::kLogW + (blk & 1) * kTokens * 4)[16 * w + li];
+      lw = f32s(C::kLogW + now.parity * kTokens * 4)[16 * w + li];
     }
     float g8[kEighths][8];
     state_of(grad, g8);
     // the next block's rows, a tensor at a time through the block: all at once they fill the queue of loads and hold the
     // waves up where they are asked for
-    if constexpr (!F32) stage_w(blk + 1), stage(p.r, 0, blk + 1);
+    if constexpr (!F32) stage_w(next), stage(p.r, 0, next);
     put_pieces(g8);
     const Border<kEighths> state = load_border(p.states, p.marks, p.mark_decay, p.state_stride, 0, blk);
     // decays of the tile's tokens, in all four rows of lanes
     float left, into;
     double c;
     {
-      c = t0 + li < len ? (double)(lw < -1e4f ? -1e4f : lw) * 1.4426950408889634 : 0.0;
+      c = 16 * w + li < now.live ? (double)(lw < -1e4f ? -1e4f : lw) * 1.4426950408889634 : 0.0;
       c += dpp_f64<0x111>(c);
       c += dpp_f64<0x112>(c);
       c += dpp_f64<0x114>(c);
@@ -319,21 +355,26 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
       D[hh] = nat(rows_d, 16 * w, hh);
     lds_barrier();
 
-    float before = 1.f, behind = 1.f, all = 1.f;  // decays of the tiles before and behind, of the block
-#pragma unroll
-    for (int x = 0; x < kTiles; ++x) {
-      const float e = f32s(C::kPerTile)[x];
-      before *= x < w ? e : 1.f;
-      behind *= x > w ? e : 1.f;
-      all *= e;
+    // decays of the tiles before and behind, of the block: products over the lanes that hold the tiles'
+    float before, behind, all;
+    {
+      const float e = li < kTiles ? f32s(C::kPerTile)[li] : 1.f;
+      float to = times_dpp<0x111>(e), from = times_dpp<0x101>(e);
+      to = times_dpp<0x112>(to), from = times_dpp<0x102>(from);
+      if constexpr (kTiles == 8) to = times_dpp<0x114>(to), from = times_dpp<0x104>(from);
+      before = w > 0 ? readlane_f32(to, w - 1) : 1.f;
+      behind = readlane_f32(from, w + 1);
+      all = readlane_f32(to, kTiles - 1);
     }
+    int place = lane;  // in here, so that the masks made of it are not kept in scalar registers, of which there are too few
+    asm volatile("" : "+v"(place));
     f32x4 dj, di;  // factors of the tile on the diagonal: rows j, rows i
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const double r = reinterpret_cast<const double*>(lds + C::kSums)[16 * w + 4 * q + i];
       dj[i] = exp_diff(c, r), di[i] = exp_diff(r, c);
     }
-    if constexpr (!F32) stage(p.k, 1, blk + 1);
+    if constexpr (!F32) stage(p.k, 1, next);
     // The pairs with the tiles behind (for dk, dv) and before (for dr). Their part of k_j . dk_j and r_i . dr_i is summed
     // here, in float32: the products with the pairs' pieces are only as good as dk and dr need them.
     float kdk = 0.f, rdr = 0.f;
@@ -355,9 +396,9 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
         const f32x4 f = *reinterpret_cast<const f32x4*>(f32s(C::kInto) + 16 * X + 4 * q) * (on ? between : 0.f);
         pq[e] = x * f, pa[e] = a * f;
         if (on) {
-          const float own = (a[0] * pq[e][0] + a[1] * pq[e][1] + a[2] * pq[e][2] + a[3] * pq[e][3]) * left;
-          kdk += own;
-          const float s = wave_sum(own);
+          const float mine = dot4(a, pq[e], 0.f) * left;
+          kdk += mine;
+          const float s = wave_sum(mine);
           if (lane == 0) f32s(C::kPairs)[w * kTiles + X] = s;
           between *= f32s(C::kPerTile)[X];
         }
@@ -370,7 +411,7 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
       }
     }
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (!F32) stage(p.v, 2, blk + 1);
+    if constexpr (!F32) stage(p.v, 2, next);
     between = 1.f;
 #pragma clang loop unroll(disable)
     for (int J = w - 1; J >= 0; J -= 2) {
@@ -385,7 +426,7 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
         const f32x4 a = mma(nat(rows_k, 16 * X, 1), R[1], mma(nat(rows_k, 16 * X, 0), R[0], zero4()));
         pp[e] = x * (*reinterpret_cast<const f32x4*>(f32s(C::kLeft) + 16 * X + 4 * q) * (on ? between : 0.f));
         if (on) {
-          rdr += a[0] * pp[e][0] + a[1] * pp[e][1] + a[2] * pp[e][2] + a[3] * pp[e][3];
+          rdr = dot4(a, pp[e], rdr);
           between *= f32s(C::kPerTile)[X];
         }
       }
@@ -394,7 +435,7 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
       for (int t = 0; t < 4; ++t) ar[t] = mma(turned_tokens(rows_k, J, J1, t), P, ar[t]);
     }
     __builtin_amdgcn_sched_barrier(0);  // phases whose registers would not fit together
-    if constexpr (!F32) stage(p.dy, 3, blk + 1);
+    if constexpr (!F32) stage(p.dy, 3, next);
     rdr *= into;
     float cross = 0.f;
     {  // dk and dv: the gradient behind the block, the factor of the tokens, the tile's own pairs
@@ -430,21 +471,21 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
       if (lane == 0) f32s(C::kPerTile)[2 * kTiles + w] = kg;
       __builtin_amdgcn_sched_barrier(0);
       f32x4 x = mma(D[1], V[1], mma(D[0], V[0], zero4())), a = mma(R[1], K[1], mma(R[0], K[0], zero4()));
-      x = masked_i(x, di, lane);
+      x = masked_i(x, di, place);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float to = sums_to(dpp_f32<0x111>(a[i] * x[i]));  // columns j before t of the row i
-        cross += 4 * q + i >= li ? to : 0.f;
+        cross += 4 * (place >> 4) + i >= (place & 15) ? to : 0.f;
       }
       cross = rows_sum(cross);
-      const Op<NO> Pq = pack<NO>(x, zero4()), Pa = pack<NO>(masked_i(a, di, lane), zero4());
+      const Op<NO> Pq = pack<NO>(x, zero4()), Pa = pack<NO>(masked_i(a, di, place), zero4());
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         ak[t] = mma(turned_tokens(rows_r, w, w, t), Pq, ak[t]);
         av[t] = mma(turned_tokens(rows_d, w, w, t), Pa, av[t]);
       }
-      const __amdgpu_buffer_rsrc_t kb = buffer(static_cast<char*>(p.dk) + rows_at(blk), rows_bytes(T - t0));
-      const __amdgpu_buffer_rsrc_t vb = buffer(static_cast<char*>(p.dv) + rows_at(blk), rows_bytes(T - t0));
+      const __amdgpu_buffer_rsrc_t kb = buffer(static_cast<char*>(p.dk) + now.start, rows_bytes(now.rows));
+      const __amdgpu_buffer_rsrc_t vb = buffer(static_cast<char*>(p.dv) + now.start, rows_bytes(now.rows));
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         store_pair<F32>(kb, li * row_bytes + (32 * hh + 8 * q) * kEsz<F32>, ak[2 * hh], ak[2 * hh + 1]);
@@ -481,46 +522,46 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
       rdr = rows_sum(rdr + rs);
       rs = wave_sum(rs);
       if (lane == 0) f32s(C::kPerTile)[3 * kTiles + w] = rs;
-      const f32x4 x = masked_j(mma(V[1], D[1], mma(V[0], D[0], zero4())), dj, lane);
+      const f32x4 x = masked_j(mma(V[1], D[1], mma(V[0], D[0], zero4())), dj, place);
       const Op<NO> P = pack<NO>(x, zero4());
 #pragma unroll
       for (int t = 0; t < 4; ++t) ar[t] = mma(turned_tokens(rows_k, w, w, t), P, ar[t]);
-      const __amdgpu_buffer_rsrc_t rb = buffer(static_cast<char*>(p.dr) + rows_at(blk), rows_bytes(T - t0));
+      const __amdgpu_buffer_rsrc_t rb = buffer(static_cast<char*>(p.dr) + now.start, rows_bytes(now.rows));
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
         store_pair<F32>(rb, li * row_bytes + (32 * hh + 8 * q) * kEsz<F32>, ar[2 * hh], ar[2 * hh + 1]);
     }
     lds_barrier();
     {  // dlog_w: lane kTiles J + I the pairs of two tiles, lanes 0 .. kTiles - 1 the borders
-      const int J = lane / kTiles, I = lane % kTiles;
-      float x = J < w && I > w ? f32s(C::kPairs)[lane] : 0.f;
-      if (lane < kTiles)
-        x += all * f32s(C::kPerTile)[kTiles + lane] + (lane < w ? f32s(C::kPerTile)[2 * kTiles + lane] : 0.f) +
-             (lane > w ? f32s(C::kPerTile)[3 * kTiles + lane] : 0.f);
+      const int J = place / kTiles, I = place % kTiles;
+      float x = J < w && I > w ? f32s(C::kPairs)[place] : 0.f;
+      if (place < kTiles)
+        x += all * f32s(C::kPerTile)[kTiles + place] + (place < w ? f32s(C::kPerTile)[2 * kTiles + place] : 0.f) +
+             (place > w ? f32s(C::kPerTile)[3 * kTiles + place] : 0.f);
       float dlw = cross + sums_from(rdr) + sums_to(dpp_f32<0x111>(kdk)) + wave_sum(x);
-      const int64_t t = t0 + li;
-      if (t >= len) dlw = 0.f;
+      if (16 * w + li >= now.live) dlw = 0.f;
       if (p.per_token) {
-        if (lane < 16 && t < T) p.dlog_w[(b * T + t) * p.seq.H + h] = dlw;
+        if (lane < 16 && 16 * w + li < now.rows) p.dlog_w[now.row + own + (uint32_t)li * p.seq.H] = dlw;
       } else {
         head_sum += dlw;
       }
     }
     // the next block's rows are there: behind them are at least six stores
     asm volatile("s_waitcnt vmcnt(6) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    now = next;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing is on its way to this workgroup's LDS when it ends
   for (int64_t blk = live > blk0 ? live : blk0; blk < blk1; ++blk) {  // behind the sequence's end: no gradients
-    const int64_t t0 = blk * kTokens + 16 * w;
+    const Block at = block(blk);
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh) {
       const uint32_t off = li * row_bytes + (32 * hh + 8 * q) * kEsz<F32>;
       void* const out[3] = {p.dr, p.dk, p.dv};
 #pragma unroll
       for (int x = 0; x < 3; ++x)
-        store_pair<F32>(buffer(static_cast<char*>(out[x]) + rows_at(blk), rows_bytes(T - t0)), off, zero4(), zero4());
+        store_pair<F32>(buffer(static_cast<char*>(out[x]) + at.start, rows_bytes(at.rows)), off, zero4(), zero4());
     }
-    if (p.per_token && lane < 16 && t0 + lane < T) p.dlog_w[(b * T + t0 + lane) * p.seq.H + h] = 0.f;
+    if (p.per_token && lane < 16 && 16 * w + lane < at.rows) p.dlog_w[at.row + own + (uint32_t)lane * p.seq.H] = 0.f;
   }
   if (!p.per_token) {
     const float s = row16_sum(head_sum);
