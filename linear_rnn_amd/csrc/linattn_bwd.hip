@@ -626,10 +626,11 @@ hipError_t launch(const LinattnCall& c) {
   auto at = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
 
   LinattnPieces f{}, g{};
+  f.pieces = g.pieces = f.stride = g.stride = pieces;
   f.every = g.every = 1;
   f.states = at(o_states), f.decay = at(o_decay), f.marks = border ? at(o_marks) : nullptr, f.mark_decay = at(o_mdecay);
   g.states = at(o_grads), g.decay = at(o_gdecay), g.marks = border ? at(o_gmarks) : nullptr, g.mark_decay = at(o_gmdecay);
-  g.end = c.ds_in;
+  g.end = c.ds_in, g.end_stride = 1;
   GradParams p{};
   p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.dy = c.dy;
   // one block: its state is the caller's, and so is its gradient; a copy where dstate_in is written over it

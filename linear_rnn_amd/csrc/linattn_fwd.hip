@@ -16,7 +16,7 @@ struct OutParams {
   const float* log_w;
   const void* k;
   const void* v;
-  const float* states;  // [units][pieces] states, the first nseg those before the segments (nseg > 1)
+  const float* states;  // [units][stride] states, the first nseg those before the segments (nseg > 1)
   const float* s_in;    // the caller's state (nseg == 1), may be null
   void* y;
   float* s_out;  // may be null
@@ -24,7 +24,7 @@ struct OutParams {
   int32_t per_token;
   int32_t nseg;        // segments of a sequence
   int64_t seg_blocks;  // blocks of kBlk tokens in a segment
-  int64_t pieces;
+  int64_t stride;
 };
 
 // ---- float32. A workgroup carries 32 of the state's 64 value rows (two tiles) over one segment of one head, 128 tokens
@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256, 2) void linattn_out32_kernel(OutParams p) {
   for (int m = 0; m < kVt; ++m) {
     carry[m] = zero4();
     if (p.nseg > 1)
-      carry[m] = *state_tile(p.states, (int64_t)unit * p.pieces + seg, 4 * wave + kVt * half + m, lane);
+      carry[m] = *state_tile(p.states, (int64_t)unit * p.stride + seg, 4 * wave + kVt * half + m, lane);
     else if (p.s_in)
       carry[m] = *reinterpret_cast<const f32x4*>(p.s_in + (int64_t)unit * kN * kN + state_offset(wave, kVt * half + m, lane));
   }
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
   for (int m = 0; m < kVt; ++m) {
     carry[m] = zero4();
     if (p.nseg > 1)
-      carry[m] = *state_tile(p.states, (int64_t)unit * p.pieces + seg, 4 * quarter + kVt * half + m, lane);
+      carry[m] = *state_tile(p.states, (int64_t)unit * p.stride + seg, 4 * quarter + kVt * half + m, lane);
     else if (p.s_in)
       carry[m] = *reinterpret_cast<const f32x4*>(p.s_in + (int64_t)unit * kN * kN + state_offset(quarter, kVt * half + m, lane));
   }
@@ -398,8 +398,8 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
 // Pieces of a segment of a sequence. A workgroup (float32: two) a head and segment, a block of 128 tokens takes it 3.5 us
 // (float32: 5.5 of the compute unit, which two share), so a call of few heads, or of a few more than a round of the
 // compute units takes, ends sooner in segments: each in its own workgroup, from the state that the pieces before
-// it add up to. Those cost another pass over k and v and two more launches: about 12 us, and 128 tokens of all heads
-// at 4 TB/s. One bfloat16 sequence of 8191 tokens and 32 heads: 63 us in segments, 222 without.
+// it add up to. Those cost another pass over k and v and two more launches: about 12 us, and the segments but the
+// last at 4 TB/s. One bfloat16 sequence of 8191 tokens and 32 heads: 63 us in segments, 222 without.
 int64_t segment_pieces(int64_t units, int64_t blocks, int64_t pieces, bool f32) {
   const int64_t cus = linattn_cus();
   const double block_us = f32 ? 5.5 : 3.5, groups = f32 ? 2.0 : 1.0;
@@ -410,7 +410,7 @@ int64_t segment_pieces(int64_t units, int64_t blocks, int64_t pieces, bool f32) 
     const int64_t rounds = ((int64_t)(units * nseg * groups) + cus - 1) / cus;
     const double length = (double)(every * kPieceBlocks < blocks ? every * kPieceBlocks : blocks);
     double us = rounds * (length * block_us + 2.0);
-    if (nseg > 1) us += 12.0 + (double)units * blocks * kBlk * (f32 ? 512 : 256) / 4e6;
+    if (nseg > 1) us += 12.0 + (double)units * (nseg - 1) * length * kBlk * (f32 ? 512 : 256) / 4e6;
     if (every == pieces || us < best) best = us, best_every = every;
   }
   return best_every;
@@ -423,18 +423,20 @@ hipError_t launch_out(const LinattnCall& c) {
   p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.s_in = c.s_in, p.y = c.y, p.s_out = c.s_out;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
-  p.pieces = linattn_pieces(c.T, kBlk);
-  const int64_t every = segment_pieces(units, blocks, p.pieces, F32);
-  p.nseg = (int32_t)((p.pieces + every - 1) / every);
+  const int64_t pieces = linattn_pieces(c.T, kBlk), every = segment_pieces(units, blocks, pieces, F32);
+  p.nseg = (int32_t)((pieces + every - 1) / every);
   p.seg_blocks = p.nseg > 1 ? every * kPieceBlocks : blocks;
   if (p.nseg > 1) {
-    const size_t states = (size_t)units * p.pieces * kLinattnStateBytes;
-    void* ws = nullptr;
-    hipError_t e = device_workspace(c.stream, states + units * p.pieces * 4, &ws, kWorkspaceOperators);
-    if (e != hipSuccess) return e;
+    // what the last segment adds nobody asks for here
     LinattnPieces q{};
-    q.every = (int32_t)every;
+    q.pieces = (p.nseg - 1) * every, q.every = (int32_t)every;
+    p.stride = q.stride = q.end_stride = q.pieces + 1;
+    const size_t states = (size_t)units * q.stride * kLinattnStateBytes;
+    void* ws = nullptr;
+    hipError_t e = device_workspace(c.stream, states + units * q.stride * 4, &ws, kWorkspaceOperators);
+    if (e != hipSuccess) return e;
     q.states = static_cast<float*>(ws);
+    q.end = q.states + (p.nseg - 1) * (kLinattnStateBytes / 4);
     q.decay = reinterpret_cast<float*>(static_cast<char*>(ws) + states);
     e = launch_linattn_states(c, kBlk, &q, nullptr);
     if (e != hipSuccess) return e;

@@ -41,12 +41,15 @@ constexpr int64_t kPieceBlocks = 4;
 inline int64_t linattn_blocks(int64_t T, int64_t block) { return (T + block - 1) / block; }
 inline int64_t linattn_pieces(int64_t T, int64_t block) { return (linattn_blocks(T, block) + kPieceBlocks - 1) / kPieceBlocks; }
 struct LinattnPieces {
+  int64_t pieces;     // of a sequence, from its start on (backward: all of them)
   int32_t every;      // keep the state before every every-th piece
-  float* states;      // [units][pieces] states; the kept ones come first in a sequence's
-  float* decay;       // [units][pieces]
+  float* states;      // [units][stride] states, stride at least pieces; the kept ones come first in a sequence's
+  int64_t stride;
+  float* decay;       // [units][stride]
   float* marks;       // may be null; [units][blocks] states
   float* mark_decay;  // [units][blocks]
-  float* end;         // may be null; backward only: [units] the gradient before the first piece
+  float* end;         // may be null; the state behind the last piece (backward: the gradient before the first), [units] with
+  int64_t end_stride; // that many states from one to the next
 };
 // Forward (from k, v): states <- the state before each every-th piece, and, if asked for, marks <- the sum of each
 // piece before each of its blocks but the first. Backward (from r, dy; every is 1): the gradient behind each piece,

@@ -24,13 +24,14 @@ using namespace linattn;
 struct Side {
   const void* k;  // the key rows: k, or r backwards
   const void* v;  // the value rows: v, or dy backwards
-  float* total;   // [units][pieces]: what each piece adds
-  float* decay;   // [units][pieces]
+  float* total;   // [units][stride]: what each piece adds
+  float* decay;   // [units][stride]
   float* marks;   // may be null; [units][blocks]: the sum from the piece's start before each block but the piece's first
                   // (backwards: from its end behind each block but its last)
   float* mark_decay;  // [units][blocks]: the decay since then
   const float* start;  // the state before the first piece (backwards: the gradient behind the last), may be null
-  float* end;          // may be null: that behind the last (before the first)
+  float* end;          // may be null: that behind the last (before the first), `end_stride` states from one to the next
+  int64_t end_stride;
   int32_t rev;
   int32_t every;
 };
@@ -40,7 +41,7 @@ struct StateParams {
   Seq seq;
   int32_t per_token;
   int32_t block;  // tokens
-  int64_t pieces;
+  int64_t pieces, stride;
 };
 
 // Factors of a lane's tokens 16J + 4q + i of the 32, from their log w: what is left of them behind the 32 tokens (backwards:
@@ -208,8 +209,8 @@ __global__ __launch_bounds__(256, 2) void linattn_state_kernel(StateParams p) {
     for (int m = 0; m < 4; ++m) s[m] = fma4(s[m], a, sum[w][4 * wave + m][lane]);
   }
 #pragma unroll
-  for (int m = 0; m < 4; ++m) *state_tile(x.total, unit * p.pieces + piece, 4 * wave + m, lane) = s[m];
-  if (threadIdx.x == 0) x.decay[unit * p.pieces + piece] = since;
+  for (int m = 0; m < 4; ++m) *state_tile(x.total, unit * p.stride + piece, 4 * wave + m, lane) = s[m];
+  if (threadIdx.x == 0) x.decay[unit * p.stride + piece] = since;
 }
 
 // total[piece / every] <- the state before every every-th piece (backwards: the gradient behind each piece, in place).
@@ -227,7 +228,7 @@ __global__ __launch_bounds__(256) void linattn_join_kernel(StateParams p) {
     float a[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int64_t n = n0 + i < p.pieces ? n0 + i : p.pieces - 1, at = unit * p.pieces + (x.rev ? p.pieces - 1 - n : n);
+      const int64_t n = n0 + i < p.pieces ? n0 + i : p.pieces - 1, at = unit * p.stride + (x.rev ? p.pieces - 1 - n : n);
       add[i] = total[at * kFours + e];
       a[i] = x.decay[at];
     }
@@ -235,12 +236,12 @@ __global__ __launch_bounds__(256) void linattn_join_kernel(StateParams p) {
     for (int i = 0; i < kAhead; ++i) {
       const int64_t n = n0 + i;
       if (n < p.pieces) {
-        if (n % x.every == 0) total[(unit * p.pieces + (x.rev ? p.pieces - 1 - n : n / x.every)) * kFours + e] = s;
+        if (n % x.every == 0) total[(unit * p.stride + (x.rev ? p.pieces - 1 - n : n / x.every)) * kFours + e] = s;
         s = fma4(s, a[i], add[i]);
       }
     }
   }
-  if (x.end) reinterpret_cast<f32x4*>(x.end)[unit * kFours + e] = s;
+  if (x.end) reinterpret_cast<f32x4*>(x.end)[unit * x.end_stride * kFours + e] = s;
 }
 
 }  // namespace
@@ -249,16 +250,17 @@ hipError_t launch_linattn_states(const LinattnCall& c, int64_t block, const Lina
   StateParams p{};
   int sides = 0;
   if (forward)
-    p.side[sides++] = Side{c.k, c.v, forward->states, forward->decay, forward->marks, forward->mark_decay, c.s_in, nullptr, 0,
-                           forward->every};
+    p.side[sides++] = Side{c.k, c.v, forward->states, forward->decay, forward->marks, forward->mark_decay, c.s_in, forward->end,
+                           forward->end_stride, 0, forward->every};
   if (backward)
     p.side[sides++] = Side{c.r, c.dy, backward->states, backward->decay, backward->marks, backward->mark_decay, c.ds_out,
-                           backward->end, 1, backward->every};
+                           backward->end, backward->end_stride, 1, backward->every};
   p.log_w = c.log_w;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
   p.block = (int32_t)block;
-  p.pieces = linattn_pieces(c.T, block);
+  const LinattnPieces& any = forward ? *forward : *backward;
+  p.pieces = any.pieces, p.stride = any.stride;
   const int64_t units = c.B * c.H;
   const void* fn = c.f32 ? reinterpret_cast<const void*>(&linattn_state_kernel<true>)
                          : reinterpret_cast<const void*>(&linattn_state_kernel<false>);
