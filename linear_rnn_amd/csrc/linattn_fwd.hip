@@ -395,21 +395,22 @@ __global__ __launch_bounds__(512, 2) void linattn_out16_kernel(OutParams p) {
   }
 }
 
-// Pieces of a segment of a sequence. A workgroup (float32: two) a head and segment, a block of 128 tokens takes it 3.5 us
-// (float32: 5.5 of the compute unit, which two share), so a call of few heads, or of a few more than a round of the
-// compute units takes, ends sooner in segments: each in its own workgroup, from the state that the pieces before
-// it add up to. Those cost another pass over k and v and two more launches: about 12 us, and the segments but the
-// last at 4 TB/s. One bfloat16 sequence of 8191 tokens and 32 heads: 63 us in segments, 222 without.
+// Pieces of a segment of a sequence. A workgroup a head and segment, alone on a compute unit, takes 3.5 us for a block of 128
+// tokens; float32: two workgroups, two to a compute unit, 7 us alone and 10 side by side. So a call of few heads, or of a few
+// more than a round of the compute units takes, ends sooner in segments: each in its own workgroup, from the state that the
+// pieces before it add up to. Those cost another pass over k and v and two more launches: about 12 us, and the segments but
+// the last at 4 TB/s. B=1 T=16384 H=32 bfloat16 113 us in segments of 4 pieces, 133 of one, 162 of 8, 474 in one segment
+// (float32 H=64: 420 in segments of 8, 458 of one, 527 of 16, 831 in one); B=4 T=2048 H=64 71 in one segment, 104 in two
+// (float32 165 and 214).
 int64_t segment_pieces(int64_t units, int64_t blocks, int64_t pieces, bool f32) {
-  const int64_t cus = linattn_cus();
-  const double block_us = f32 ? 5.5 : 3.5, groups = f32 ? 2.0 : 1.0;
+  const int64_t cus = linattn_cus(), slots = f32 ? 2 : 1;  // workgroups of a head and segment, and of a compute unit
   int64_t best_every = pieces;
   double best = 0;
   for (int64_t every = pieces; every >= 1; every = every > 1 ? (every + 1) / 2 : 0) {
-    const int64_t nseg = (pieces + every - 1) / every;
-    const int64_t rounds = ((int64_t)(units * nseg * groups) + cus - 1) / cus;
+    const int64_t nseg = (pieces + every - 1) / every, groups = units * nseg * slots;
+    const int64_t rounds = (groups + slots * cus - 1) / (slots * cus);
     const double length = (double)(every * kPieceBlocks < blocks ? every * kPieceBlocks : blocks);
-    double us = rounds * (length * block_us + 2.0);
+    double us = rounds * (length * (!f32 ? 3.5 : groups <= cus ? 7.0 : 10.0) + 2.0);
     if (nseg > 1) us += 12.0 + (double)units * (nseg - 1) * length * kBlk * (f32 ? 512 : 256) / 4e6;
     if (every == pieces || us < best) best = us, best_every = every;
   }
