@@ -32,8 +32,8 @@ struct OutParams {
 // the state's tiles through the four waves' tokens (the carried part stays in its registers) and leaves the states
 // before each wave's tokens for the others. The two workgroups of a head follow each other on the same die, so
 // r and k come from memory once. What the pieces of three operands take in registers leaves no room for loads ahead;
-// two workgroups on a compute unit cover for each other. Issue bounds it: 6 us a block for a workgroup alone, 5.3 for each of
-// two; B=8 T=2048 H=32 170 us (3.1 TB/s), 236 with one on a compute unit and loads ahead.
+// two workgroups on a compute unit cover for each other. Issue bounds it: 6 to 7 us a block for a workgroup alone, 10 for two side
+// by side; B=8 T=2048 H=32 170 us (3.1 TB/s), 236 with one on a compute unit and loads ahead.
 constexpr int kVt = 2;  // value tiles of a workgroup
 
 struct Inputs {
@@ -181,7 +181,7 @@ __global__ __launch_bounds__(256, 2) void linattn_out32_kernel(OutParams p) {
 // direct loads, a block ahead (into the same place, as soon as every wave has taken its operands into registers),
 // their 16-byte pieces exchanged within a row so that the operand reads of 16 rows fall into different banks.
 //
-// B=4 T=16384 H=64 518 us (4.2 TB/s); the loads and stores alone take 482, the arithmetic alone 436.
+// B=4 T=16384 H=64 513 to 518 us (4.2 TB/s); the loads and stores alone take 482, the arithmetic alone 436.
 //
 // What is common to the two waves of a quarter, the decay factors of its tokens, one of them leaves in LDS during
 // the block before (once, if the head has one decay and the tokens are all there).
