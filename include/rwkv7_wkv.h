@@ -468,9 +468,8 @@ int rwkv7_wkv_prefill_algo(int64_t B, int64_t T, int64_t H, int64_t N, int dtype
  * prompt is taken in segments; the states at their starts (16 KiB for each head and
  * 512 tokens) live in the per-(device, stream) workspace described for
  * rwkv7_wkv_prefill_ex, and what is said there about growth and graph capture holds.
- * Calls on one stream share that workspace: from two threads they are issued one
- * after the other, and graphs captured on one stream are not replayed at the same
- * time on two.
+ * Calls on one stream share that workspace, also from two threads at once; graphs
+ * captured on one stream may not be replayed at the same time on two.
  */
 #define RWKV7_DECAY_HEAD 0  /* log_w [H] */
 #define RWKV7_DECAY_TOKEN 1 /* log_w [B, T, H] */

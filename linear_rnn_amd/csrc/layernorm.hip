@@ -16,6 +16,7 @@
 // float32 in 16 groups 23.3 us (4.3).
 #include "lane_sums.hpp"
 #include "layernorm_internal.hpp"
+#include "operators_lock.hpp"
 #include "wkv7_device.hpp"
 #include "wkv7_internal.hpp"
 
@@ -525,7 +526,9 @@ hipError_t backward(const NormCall& c) {
     nb = nb < 1 ? 1 : nb < 64 ? nb : 64;
     p.nb = (int32_t)(p.M < nb ? p.M : nb);
   }
+  std::unique_lock<std::mutex> lock(operators_mutex(), std::defer_lock);
   if (sums) {
+    lock.lock();
     void* ws = nullptr;
     const hipError_t e = device_workspace(c.stream, (size_t)2 * p.nb * p.D * 4, &ws, kWorkspaceOperators);
     if (e != hipSuccess) return e;

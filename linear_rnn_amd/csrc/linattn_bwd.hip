@@ -31,6 +31,7 @@
 // H=16 float32 29 us, carried 156.
 #include "linattn_internal.hpp"
 #include "linattn_ops.hpp"
+#include "operators_lock.hpp"
 #include "wkv7_internal.hpp"
 
 namespace rwkv7 {
@@ -620,6 +621,7 @@ hipError_t launch(const LinattnCall& c) {
   const size_t o_grads = room(units * pieces * kLinattnStateBytes), o_gdecay = room(units * pieces * 4);
   const size_t o_gmarks = room(border ? units * nblk * kLinattnStateBytes : 0), o_gmdecay = room(units * nblk * 4);
   const size_t o_parts = room(c.per_token ? 0 : units * nseg * 4);
+  std::lock_guard<std::mutex> lock(operators_mutex());
   void* ws = nullptr;
   hipError_t e = device_workspace(c.stream, need, &ws, kWorkspaceOperators);
   if (e != hipSuccess) return e;

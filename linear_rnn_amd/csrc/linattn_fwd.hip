@@ -4,6 +4,7 @@
 
 #include "linattn_internal.hpp"
 #include "linattn_ops.hpp"
+#include "operators_lock.hpp"
 #include "wkv7_internal.hpp"
 
 namespace rwkv7 {
@@ -427,7 +428,9 @@ hipError_t launch_out(const LinattnCall& c) {
   const int64_t pieces = linattn_pieces(c.T, kBlk), every = segment_pieces(units, blocks, pieces, F32);
   p.nseg = (int32_t)((pieces + every - 1) / every);
   p.seg_blocks = p.nseg > 1 ? every * kPieceBlocks : blocks;
+  std::unique_lock<std::mutex> lock(operators_mutex(), std::defer_lock);
   if (p.nseg > 1) {
+    lock.lock();
     // what the last segment adds nobody asks for here
     LinattnPieces q{};
     q.pieces = (p.nseg - 1) * every, q.every = (int32_t)every;

@@ -1,5 +1,7 @@
 """The linear attention and the layer norm at the ends of what their header allows: offsets past 32 bits, two
 streams at once, graphs that share a stream's workspace, and a workspace that would have to grow during capture."""
+import threading
+
 import pytest
 
 from linear_rnn_amd import wkv
@@ -116,6 +118,34 @@ def test_two_streams_at_once(torch):
     torch.cuda.synchronize()
     for (d, out), w in zip(cases, want):
         assert all(torch.equal(out[n], w[n]) for n in w)
+
+
+def test_two_threads_on_one_stream(torch):
+    """Their calls' kernels use one workspace and do not fall between each other."""
+    say("two threads on one stream")
+    cases = [case(torch, 1, 3000, 2, 75), case(torch, 2, 2100, 3, 76)]
+    st = torch.cuda.Stream()
+    want = []
+    for d, out in cases:
+        chain(torch, d, out, st)
+        st.synchronize()
+        want.append(clones(out))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(n):
+        d, out = cases[n]
+        for _ in range(20):
+            chain(torch, d, out, st)
+        st.synchronize()
+        bad.extend((n, name) for name in want[n] if not torch.equal(out[name], want[n][name]))
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
 
 
 def test_two_graphs_of_one_stream(torch):
