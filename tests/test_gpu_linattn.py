@@ -99,6 +99,21 @@ def test_prefill_lens(torch, decay, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_prefill_lens_in_segments(torch, dtype):
+    """Few heads, so that a sequence is taken in segments, which begin before, at and behind its end."""
+    T, lens = 2100, [0, 1, 511, 512, 513, 1024, 1500, 2099, 2100]
+    x = ref.make(len(lens), T, 2, getattr(torch, DT[dtype]), "token", seed=72, resets=0.002)
+    x["lens"] = torch.tensor(lens, dtype=torch.int32)
+    for b, n in enumerate(lens):
+        for name in ("r", "k", "v", "log_w"):
+            x[name][b, n:] = (float("nan"), float("inf"), -float("inf"))[b % 3]
+    y, s = compare(torch, x, ("lens in segments", dtype))
+    for b, n in enumerate(lens):
+        assert not y[b, n:].any()
+    assert torch.equal(s[0].cpu(), x["state_in"][0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_prefill_resumes_in_place(torch, dtype):
     """Parts of a prompt one after the other, the state updated in place."""
     x = ref.make(2, 333, 3, getattr(torch, DT[dtype]), "token", seed=80)
