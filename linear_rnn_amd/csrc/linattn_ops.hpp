@@ -244,7 +244,6 @@ __device__ __forceinline__ Op<NP> turned_op(const Op<NP>& x0, const Op<NP>& x1, 
 struct Decay {
   float col[2];      // exp(c) of token 16I + li
   float row[2][4];   // exp(c_31 - c) of token 16J + 4q + i: what is left of it at the end
-  float inrow[2][4]; // exp(c) of token 16J + 4q + i
   f32x4 d00, d01, d11;  // D with the tokens j as rows: tile (J, I) has rows j = 16J + 4q + i, columns i = 16I + li
   float all;         // exp(c_31)
 };
@@ -295,13 +294,10 @@ __device__ __forceinline__ Decay make_decay(float log_w, double* sums, int lane)
   for (int J = 0; J < 2; ++J) {
     d.col[J] = exp_diff(cc[J], 0.0);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      d.row[J][i] = exp_diff(end, cr[J][i]);
-      d.inrow[J][i] = exp_diff(cr[J][i], 0.0);
-    }
+    for (int i = 0; i < 4; ++i) d.row[J][i] = exp_diff(end, cr[J][i]);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {  // in the tiles on the diagonal also where D is 0 (masked() leaves that out)
+  for (int i = 0; i < 4; ++i) {  // in the tiles on the diagonal also where D is 0 (masked_j() leaves that out)
     d.d00[i] = exp_diff(cc[0], cr[0][i]);
     d.d01[i] = exp_diff(cc[1], cr[0][i]);
     d.d11[i] = exp_diff(cc[1], cr[1][i]);
