@@ -120,7 +120,9 @@ __device__ __forceinline__ void store16(__amdgpu_buffer_rsrc_t b, uint32_t off, 
 }
 
 // The same descriptor as four scalar words, for the direct loads to LDS: 16 (or 4) bytes a lane, lane l's to
-// `lds` + 16 l (4 l), zeros from behind the end. vmcnt counts them and the caller waits for them.
+// `lds` + 16 l (4 l), zeros from behind the end. vmcnt counts them and the caller waits for them. A memory instruction
+// may read a scalar register five wait states after the vector unit (a readfirstlane, as the descriptor's) wrote it and
+// M0 one after it was set. The compiler keeps no such distances into assembly, so the idle states are in here.
 __device__ __forceinline__ u32x4 descriptor(const void* base, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
   return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
@@ -128,16 +130,16 @@ __device__ __forceinline__ u32x4 descriptor(const void* base, uint32_t bytes) {
                (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes), 0x00027000u};
 }
 __device__ __forceinline__ void to_lds16(u32x4 b, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
-               : "memory");
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
+               : "memory", "m0");
 }
 // Without temporal hint, for what no later kernel of the call reads.
 __device__ __forceinline__ void to_lds16_last(u32x4 b, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen nt lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
                : "memory");
 }
 __device__ __forceinline__ void to_lds4(u32x4 b, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dword %0, %1, 0 offen lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
                : "memory");
 }
 
