@@ -160,15 +160,16 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 // Global-to-LDS load: lane l's BYTES land at LDS address lds + BYTES * l (lds
-// wave-uniform, in M0). Written as assembly so that the compiler, which cannot
+// wave-uniform, in M0, which is read one wait state after it is set: the idle
+// state between them). Written as assembly so that the compiler, which cannot
 // tell which later LDS reads these loads feed, inserts no wait of its own; every
 // wait on them is an explicit vm_wait.
 template <int BYTES>
 __device__ __forceinline__ void to_lds(const void* g, uint32_t lds) {
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %1\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(g), "s"(lds) : "memory", "m0");
 }
 // Waits until at most N of this wave's vector-memory operations are outstanding
 // (they complete in issue order), and orders every later memory access after it.

@@ -58,7 +58,7 @@ def test_lint_follows_branches():
     assert isa_waits.close_pairs(_parse(loop.replace("65529", "0"))) == []
 
 
-KERNELS = ("linattn_state_kernel", "linattn_out16_kernel", "linattn_grad_kernel")
+KERNELS = ("linattn_state_kernel", "linattn_out16_kernel", "linattn_grad_kernel", "wkv7_scan_kernel")
 
 
 @pytest.fixture(scope="module")
@@ -75,3 +75,7 @@ def test_built_kernels_with_direct_loads(built, kernel):
     mine = {n: i for n, i in built.items() if kernel in n}
     assert any(isa_waits._to_lds(mn, ops) for i in mine.values() for _, mn, ops in i)  # not vacuous
     assert [(n, f) for n, i in mine.items() for f in isa_waits.close_pairs(i)] == []
+
+
+def test_every_built_kernel(built):
+    assert [(n, f) for n, i in built.items() for f in isa_waits.close_pairs(i)] == []
