@@ -189,7 +189,8 @@ int rwkv7_wkv_step_q(const void *r, const void *w, const void *k, const void *v,
  * bfloat16 inputs with few heads): the chunk records that pass from its first
  * kernel to its second live in a device buffer that the library allocates on
  * the first call that needs it and keeps for later calls, one buffer per
- * (device, stream), grown when a call needs more (at most about 256 MiB plus
+ * (device, stream; hipStreamPerThread counts as a stream for each thread that
+ * passes it), grown when a call needs more (at most about 256 MiB plus
  * one state copy: a longer sequence is processed in slabs of chunks that fit;
  * the environment variable RWKV7_SPLIT_SLAB_MB overrides the budget). A buffer
  * that growth replaces stays allocated until the process ends, because a HIP

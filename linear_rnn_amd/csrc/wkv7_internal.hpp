@@ -123,7 +123,8 @@ struct StackCall {
 hipError_t launch_stack(const StackCall& c);
 
 // Device memory cached per (device, stream), shared by the launchers that need
-// scratch: calls on one stream run in order, so they can share it. Grown on
+// scratch: calls on one stream run in order, so they can share it (hipStreamPerThread
+// is another stream, with buffers of its own, in every thread). Grown on
 // demand (at least doubling); a replaced buffer stays allocated until the process
 // ends, since a HIP graph captured earlier may still use it. Growing while the
 // stream is being captured returns hipErrorStreamCaptureUnsupported.

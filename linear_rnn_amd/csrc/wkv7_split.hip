@@ -61,11 +61,11 @@
 #include <cstdlib>
 #include <map>
 #include <mutex>
-#include <tuple>
 #include <type_traits>
 #include <utility>
 #include <vector>
 
+#include "stream_key.hpp"
 #include "wkv7_chunk_ops.hpp"
 #include "wkv7_internal.hpp"
 
@@ -378,7 +378,7 @@ __global__ __launch_bounds__(64 * (WAVES + 1)) void wkv7_scan_kernel(ScanParams 
 // Device workspace (records of the chunked split prefill, checkpoints of the
 // backward, the layer stack's intermediates) cached per (device, stream): calls on
 // one stream run in order, so they can share it; calls on different streams get
-// different buffers. A buffer that a larger call replaces is retired, not freed: a
+// different buffers (hipStreamPerThread is another stream in every thread). A buffer that a larger call replaces is retired, not freed: a
 // HIP graph captured earlier on that stream may still hold its address, so it stays
 // allocated until the process ends. Growth is at least geometric (x2), so retired
 // buffers add at most the size of the live one.
@@ -387,7 +387,7 @@ struct Workspace {
   size_t bytes = 0;
 };
 std::mutex g_ws_mu;
-std::map<std::tuple<int, uintptr_t, int>, Workspace> g_ws;
+std::map<std::pair<StreamKey, int>, Workspace> g_ws;
 std::vector<void*> g_ws_retired;  // never freed (see above)
 
 
@@ -412,7 +412,7 @@ hipError_t device_workspace(hipStream_t stream, size_t bytes, void** out, int sl
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
   std::lock_guard<std::mutex> lk(g_ws_mu);
-  Workspace& ws = g_ws[std::make_tuple(dev, reinterpret_cast<uintptr_t>(stream), slot)];
+  Workspace& ws = g_ws[std::make_pair(stream_key(dev, stream, hipStreamPerThread), slot)];
   if (ws.bytes < bytes) {
     // growing allocates, which a stream under graph capture cannot record: such a call
     // must be preceded by an eager call of at least its size on the same stream

@@ -32,6 +32,7 @@
 
 #include "wkv7_device.hpp"
 #include "rwkv7_wkv.h"
+#include "stream_key.hpp"
 #include "wkv7_internal.hpp"
 
 namespace rwkv7 {
@@ -94,13 +95,13 @@ __global__ __launch_bounds__(256) void stack_act_kernel(ActParams p) {
 
 // rocBLAS handles, one per (device, stream), used under the lock.
 std::mutex g_blas_mu;
-std::map<std::pair<int, uintptr_t>, rocblas_handle> g_blas;
+std::map<StreamKey, rocblas_handle> g_blas;
 
 hipError_t blas_handle(hipStream_t stream, rocblas_handle* out) {
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
-  auto key = std::make_pair(dev, reinterpret_cast<uintptr_t>(stream));
+  const StreamKey key = stream_key(dev, stream, hipStreamPerThread);
   auto it = g_blas.find(key);
   if (it == g_blas.end()) {
     rocblas_handle h = nullptr;
