@@ -4,6 +4,8 @@ Function names match the C ABI in include/rwkv7_wkv.h. Each takes torch tensors
 (device memory owned by the caller) or None, passes their addresses, sizes and
 dtype to the library, launches on the current torch stream unless a stream is
 given, and raises RuntimeError with the library's message on a non-zero status.
+The functions without the rwkv7_ prefix allocate their outputs as well, as tensors of the
+stream they launch on (torch.Tensor.record_stream says so where another one uses them).
 Before the call it checks every tensor against the sizes the call takes (shape,
 one input dtype, contiguity, 16-byte alignment, one HIP device) and raises
 ValueError on a mismatch: the C ABI receives bare pointers and cannot.
@@ -34,6 +36,7 @@ RWKV7_ERR_DECAY = -10
 RWKV7_DECAY_HEAD = 0
 RWKV7_DECAY_TOKEN = 1
 RWKV7_NOALLOC_SCRATCH_BYTES = 64 << 20
+_PER_THREAD = 2  # the handle hipStreamPerThread
 
 EXPORTED = ("rwkv7_wkv_prefill", "rwkv7_wkv_step", "rwkv7_wkv_step_q", "rwkv7_wkv_prefill_ex",
             "rwkv7_tmix_prefill", "rwkv7_tmix_prefill_ex", "rwkv7_tmix_step", "rwkv7_wkv_backward",
@@ -153,6 +156,21 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _on_stream_of(stream, like, make):
+    """make(), which allocates, with `stream` current: torch's allocator gives out memory that the current stream has
+    left, so memory for a kernel on another stream has to be of that stream, or work still under way uses it too."""
+    if stream is None or like.device.type != "cuda":
+        return make()
+    import torch
+    if isinstance(stream, int):
+        if stream == _PER_THREAD:
+            raise ValueError("hipStreamPerThread is another stream in every thread, which torch's allocator does not "
+                             "know: allocate the outputs and call the rwkv7_ function")
+        stream = torch.cuda.ExternalStream(stream, device=like.device)
+    with torch.cuda.stream(stream):
+        return make()
 
 
 # ---- argument checks. The C ABI sees raw pointers and cannot check a buffer's size,
@@ -285,10 +303,9 @@ def rwkv7_wkv_prefill_ex(r, w, k, v, a, b, state_in, y, state_out, algo=RWKV7_AL
 
 def wkv7(r, w, k, v, a, b, state_in=None, algo=RWKV7_ALGO_AUTO, want_state=True, stream=None):
     """Allocate y ([B,T,H,64] float32) and the final state, run the prefill, return (y, state_out)."""
-    import torch
     B, T, H, N = r.shape
-    y = torch.empty((B, T, H, N), dtype=torch.float32, device=r.device)
-    s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device) if want_state else None
+    y, s_out = _on_stream_of(stream, r, lambda: (
+        r.new_empty((B, T, H, N), dtype=_T.f32[0]), r.new_empty((B, H, N, N), dtype=_T.f32[0]) if want_state else None))
     rwkv7_wkv_prefill_ex(r, w, k, v, a, b, state_in, y, s_out, algo=algo, stream=stream)
     return y, s_out
 
@@ -335,10 +352,9 @@ def rwkv7_tmix_step(r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, state_o
 def tmix(r, w_raw, k, v, kk, a_lr, ln_w=None, ln_b=None, state_in=None, want_state=True, algo=RWKV7_ALGO_AUTO,
          stream=None):
     """Allocate out ([B,T,H,64] float32) and the final state, run the fused prefill, return (out, state_out)."""
-    import torch
     B, T, H, N = r.shape
-    out = torch.empty((B, T, H, N), dtype=torch.float32, device=r.device)
-    s_out = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device) if want_state else None
+    out, s_out = _on_stream_of(stream, r, lambda: (
+        r.new_empty((B, T, H, N), dtype=_T.f32[0]), r.new_empty((B, H, N, N), dtype=_T.f32[0]) if want_state else None))
     rwkv7_tmix_prefill_ex(r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, s_out, algo=algo, stream=stream)
     return out, s_out
 
@@ -374,11 +390,14 @@ def rwkv7_wkv_backward_ex(r, w, k, v, a, b, state_in, dy, dstate_out, dr, dw, dk
 def wkv7_backward(r, w, k, v, a, b, dy, state_in=None, dstate_out=None, want_dstate=True, stream=None,
                   algo=RWKV7_ALGO_AUTO):
     """Allocate the gradients, run the backward, return dict dr, dw, dk, dv, da, db, dstate_in."""
-    import torch
     B, T, H, N = r.shape
-    out = {n: torch.empty((B, T, H, N), dtype=torch.float32, device=r.device)
-           for n in ("dr", "dw", "dk", "dv", "da", "db")}
-    out["dstate_in"] = torch.empty((B, H, N, N), dtype=torch.float32, device=r.device) if want_dstate else None
+
+    def make():
+        out = {n: r.new_empty((B, T, H, N), dtype=_T.f32[0]) for n in ("dr", "dw", "dk", "dv", "da", "db")}
+        out["dstate_in"] = r.new_empty((B, H, N, N), dtype=_T.f32[0]) if want_dstate else None
+        return out
+
+    out = _on_stream_of(stream, r, make)
     rwkv7_wkv_backward_ex(r, w, k, v, a, b, state_in, dy, dstate_out, *(out[n] for n in
                           ("dr", "dw", "dk", "dv", "da", "db", "dstate_in")), algo=algo, stream=stream)
     return out
@@ -462,8 +481,8 @@ def rwkv7_linattn_step(r, log_w, k, v, state_in, y, state_out, stream=None):
 def linattn(r, log_w, k, v, state_in=None, lens=None, want_state=True, stream=None):
     """Allocate y ([B,T,H,64] in r's dtype) and the final state, run the prompt, return (y, state_out)."""
     B, T, H, N = r.shape
-    y = _T.empty_like(r)
-    s_out = r.new_empty((B, H, N, N), dtype=_T.f32[0]) if want_state else None
+    y, s_out = _on_stream_of(stream, r, lambda: (
+        _T.empty_like(r), r.new_empty((B, H, N, N), dtype=_T.f32[0]) if want_state else None))
     rwkv7_linattn_prefill(r, log_w, k, v, state_in, lens, y, s_out, stream)
     return y, s_out
 
@@ -472,8 +491,7 @@ def linattn_step(r, log_w, k, v, state_in=None, stream=None):
     """Allocate y ([B,1,H,64] in r's dtype) and the new state, run one token, return (y, state_out).
     rwkv7_linattn_step updates a state in place."""
     B, T, H, N = r.shape
-    y = _T.empty_like(r)
-    s_out = r.new_empty((B, H, N, N), dtype=_T.f32[0])
+    y, s_out = _on_stream_of(stream, r, lambda: (_T.empty_like(r), r.new_empty((B, H, N, N), dtype=_T.f32[0])))
     rwkv7_linattn_step(r, log_w, k, v, state_in, y, s_out, stream)
     return y, s_out
 
@@ -499,9 +517,14 @@ def rwkv7_linattn_backward(r, log_w, k, v, state_in, lens, dy, dstate_out, dr, d
 def linattn_backward(r, log_w, k, v, dy, state_in=None, lens=None, dstate_out=None, want_dstate=True, stream=None):
     """Allocate the gradients, run the backward, return dict dr, dlog_w, dk, dv, dstate_in."""
     B, T, H, N = r.shape
-    out = {n: _T.empty_like(r) for n in ("dr", "dk", "dv")}
-    out["dlog_w"] = _T.empty_like(log_w)
-    out["dstate_in"] = r.new_empty((B, H, N, N), dtype=_T.f32[0]) if want_dstate else None
+
+    def make():
+        out = {n: _T.empty_like(r) for n in ("dr", "dk", "dv")}
+        out["dlog_w"] = _T.empty_like(log_w)
+        out["dstate_in"] = r.new_empty((B, H, N, N), dtype=_T.f32[0]) if want_dstate else None
+        return out
+
+    out = _on_stream_of(stream, r, make)
     rwkv7_linattn_backward(r, log_w, k, v, state_in, lens, dy, dstate_out, out["dr"], out["dlog_w"], out["dk"],
                            out["dv"], out["dstate_in"], stream)
     return out
@@ -555,11 +578,12 @@ def rwkv7_layernorm_backward(x, weight, mean, rstd, dy, dx, dweight, dbias, grou
 
 def layernorm(x, weight=None, bias=None, groups=1, eps=1e-5, out_dtype=None, want_stats=True, stream=None):
     """Allocate y (in out_dtype, or x's) and the statistics, run the forward, return (y, mean, rstd)."""
-    y = _T.empty_like(x, dtype=out_dtype)
-    mean = rstd = None
-    if want_stats:
-        mean = x.new_empty(x.shape[:-1] + (groups,), dtype=_T.f32[0])
-        rstd = _T.empty_like(mean)
+    def make():
+        y = _T.empty_like(x, dtype=out_dtype)
+        mean = x.new_empty(x.shape[:-1] + (groups,), dtype=_T.f32[0]) if want_stats else None
+        return y, mean, _T.empty_like(mean) if want_stats else None
+
+    y, mean, rstd = _on_stream_of(stream, x, make)
     rwkv7_layernorm_forward(x, weight, bias, y, mean, rstd, groups, eps, stream)
     return y, mean, rstd
 
@@ -567,9 +591,13 @@ def layernorm(x, weight=None, bias=None, groups=1, eps=1e-5, out_dtype=None, wan
 def layernorm_backward(x, weight, mean, rstd, dy, groups=1, want_dweight=True, stream=None):
     """Allocate the gradients, run the backward, return dict dx, dweight, dbias (the last two None unless
     want_dweight)."""
-    out = {"dx": _T.empty_like(x), "dweight": None, "dbias": None}
-    if want_dweight:
-        out["dweight"] = x.new_empty(x.shape[-1:], dtype=_T.f32[0])
-        out["dbias"] = _T.empty_like(out["dweight"])
+    def make():
+        out = {"dx": _T.empty_like(x), "dweight": None, "dbias": None}
+        if want_dweight:
+            out["dweight"] = x.new_empty(x.shape[-1:], dtype=_T.f32[0])
+            out["dbias"] = _T.empty_like(out["dweight"])
+        return out
+
+    out = _on_stream_of(stream, x, make)
     rwkv7_layernorm_backward(x, weight, mean, rstd, dy, out["dx"], out["dweight"], out["dbias"], groups, stream)
     return out

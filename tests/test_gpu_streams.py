@@ -1,4 +1,4 @@
-"""Streams that the other tests do not pass: each thread's own (hipStreamPerThread)."""
+"""Streams: each thread's own (hipStreamPerThread), and whose memory the allocating functions return."""
 import threading
 
 import pytest
@@ -50,3 +50,44 @@ def test_two_threads_on_their_own_streams(torch):
     assert not failed, failed
     for (d, out), w in zip(cases, want):
         assert all(torch.equal(out[n], w[n]) for n in w)
+
+
+def stream_of(torch, t):
+    """The stream that torch's allocator holds a tensor's memory for."""
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+    raise AssertionError("not memory of the allocator")
+
+
+def calls(torch, d, stream):
+    """The tensors that every allocating function returns."""
+    r, k, v, y = d["r"], d["k"], d["v"], d["dy"]
+    w = torch.full_like(r, 0.9)
+    wf = torch.full(r.shape, -1.0, device="cuda")
+    rows = y.view(y.shape[0], y.shape[1], -1)
+    mean, rstd = (torch.ones(rows.shape[:-1] + (r.shape[2],), device="cuda") for _ in range(2))
+    f = torch.zeros(r.shape, device="cuda")
+    one = [t[:, :1].contiguous() for t in (r, d["log_w"], k, v)]
+    torch.cuda.synchronize()
+    out = [wkv.wkv7(r, w, k, v, k, v, stream=stream), wkv.tmix(r, wf, k, v, k, v, stream=stream),
+           tuple(wkv.wkv7_backward(r, w, k, v, k, v, f, stream=stream).values()),
+           wkv.linattn(r, d["log_w"], k, v, stream=stream), wkv.linattn_step(*one, stream=stream),
+           tuple(wkv.linattn_backward(r, d["log_w"], k, v, y, stream=stream).values()),
+           wkv.layernorm(rows, groups=r.shape[2], stream=stream),
+           tuple(wkv.layernorm_backward(rows, None, mean, rstd, rows, groups=r.shape[2], stream=stream).values())]
+    return [t for o in out for t in o]
+
+
+def test_allocated_outputs_are_of_the_stream(torch):
+    say("allocated outputs")
+    d, _ = case(torch, 2, 40, 3, 79)
+    st = torch.cuda.Stream()
+    for stream, owner in ((None, torch.cuda.current_stream().cuda_stream), (st, st.cuda_stream), (st.cuda_stream, st.cuda_stream)):
+        got = calls(torch, d, stream)
+        assert len(got) == 2 + 2 + 7 + 2 + 2 + 5 + 3 + 3
+        assert {stream_of(torch, t) for t in got} == {owner}
+        torch.cuda.synchronize()
+        del got
+    with pytest.raises(ValueError, match="hipStreamPerThread"):
+        wkv.linattn(d["r"], d["log_w"], d["k"], d["v"], stream=PER_THREAD)
