@@ -649,8 +649,9 @@ hipError_t launch(const LinattnCall& c) {
   p.per_token = c.per_token;
   p.nseg = (int32_t)nseg, p.seg_blocks = seg_blocks;
   const void* fn = reinterpret_cast<const void*>(&linattn_grad_kernel<F32>);
-  static const hipError_t a = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, Cfg<F32>::kLds);
-  if (a != hipSuccess) return a;
+  static std::atomic<uint64_t> granted{0};
+  e = allow_lds(granted, fn, Cfg<F32>::kLds);
+  if (e != hipSuccess) return e;
   void* args[] = {&p};
   e = hipLaunchKernel(fn, dim3((uint32_t)(units * nseg)), dim3(64 * Cfg<F32>::kTiles), args, Cfg<F32>::kLds, c.stream);
   if (e != hipSuccess || c.per_token) return e;

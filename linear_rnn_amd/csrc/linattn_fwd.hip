@@ -4,6 +4,7 @@
 
 #include "linattn_internal.hpp"
 #include "linattn_ops.hpp"
+#include "once_per_device.hpp"
 #include "operators_lock.hpp"
 #include "wkv7_internal.hpp"
 
@@ -448,11 +449,11 @@ hipError_t launch_out(const LinattnCall& c) {
   }
   void* args[] = {&p};
   if constexpr (!F32) {
-    static const hipError_t a = hipFuncSetAttribute(reinterpret_cast<const void*>(&linattn_out16_kernel),
-                                                    hipFuncAttributeMaxDynamicSharedMemorySize, kOutLds);
+    static std::atomic<uint64_t> granted{0};
+    const void* fn = reinterpret_cast<const void*>(&linattn_out16_kernel);
+    const hipError_t a = allow_lds(granted, fn, kOutLds);
     if (a != hipSuccess) return a;
-    return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out16_kernel), dim3((uint32_t)(units * p.nseg)),
-                           dim3(512), args, kOutLds, c.stream);
+    return hipLaunchKernel(fn, dim3((uint32_t)(units * p.nseg)), dim3(512), args, kOutLds, c.stream);
   } else {
     return hipLaunchKernel(reinterpret_cast<const void*>(&linattn_out32_kernel), dim3((uint32_t)(units * p.nseg * 2)),
                            dim3(64 * kWaves), args, 0, c.stream);
@@ -529,6 +530,15 @@ int64_t linattn_cus() {
   if (cus == 0 && hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess && cus > 0)
     cached[dev].store(cus, std::memory_order_relaxed);
   return cus > 0 ? cus : 256;
+}
+
+hipError_t allow_lds(std::atomic<uint64_t>& granted, const void* fn, int bytes) {
+  int dev = 0;
+  const hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  return static_cast<hipError_t>(once_per_device(granted, dev, [&] {
+    return static_cast<int>(hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  }));
 }
 
 hipError_t launch_linattn(const LinattnCall& c) { return c.f32 ? launch_out<true>(c) : launch_out<false>(c); }

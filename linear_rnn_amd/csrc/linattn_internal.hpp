@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace rwkv7 {
 
 // One validated call with work to do (B, H, T at least 1).
@@ -57,5 +59,7 @@ struct LinattnPieces {
 hipError_t launch_linattn_states(const LinattnCall& c, int64_t block, const LinattnPieces* forward, const LinattnPieces* backward);
 // Compute units of the current device (256 if it cannot be asked).
 int64_t linattn_cus();
+// Grants kernel `fn` `bytes` of LDS at launch on the current device; `granted` is the kernel's own.
+hipError_t allow_lds(std::atomic<uint64_t>& granted, const void* fn, int bytes);
 
 }  // namespace rwkv7
