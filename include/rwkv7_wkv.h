@@ -198,6 +198,10 @@ int rwkv7_wkv_step_q(const void *r, const void *w, const void *k, const void *v,
  * doubles the buffer, so that retired memory is bounded by the live buffer's
  * size. An allocation failure returns RWKV7_ERR_HIP before any launch, and so
  * does a call that would grow the buffer while its stream is being captured.
+ * A graph uses the workspace of the stream that it was captured on, wherever it
+ * is replayed: its replays may not run at the same time as another replay of a
+ * graph captured on that stream, nor as a call on that stream (they would write
+ * over each other's records). That holds for every entry point with a workspace.
  */
 int rwkv7_wkv_prefill_ex(const void *r, const void *w, const void *k, const void *v, const void *a,
                          const void *b, const float *state_in, float *y, float *state_out, int64_t B,
@@ -458,10 +462,13 @@ int rwkv7_wkv_prefill_algo(int64_t B, int64_t T, int64_t H, int64_t N, int dtype
  * The state and every sum are float32 (sums of log_w float64). bfloat16 inputs
  * are exact matrix-core operands; scaled intermediates and float32 inputs enter
  * as sums of two or three bfloat16 pieces, so a float32 output (the state, every
- * output of a float32 call) is off by about float32 rounding, and a bfloat16 one
- * by its one rounding. Inputs have to be finite in the tokens that count (a
- * float32 infinity becomes a NaN). No result depends on the launch or on other
- * work on the device: the same call gives the same bits.
+ * output of a float32 call) is off by about float32 rounding. A bfloat16 output is
+ * off by its one rounding and, from intermediates of two pieces (16 bits), by up to
+ * 2^-15 of the sum of its terms' magnitudes; that is the larger one where the terms
+ * cancel. Inputs have to be finite in the tokens that count (a float32 infinity
+ * becomes a NaN, and so may a float32 above 3.39e38, which no bfloat16 holds). No
+ * result depends on the launch or on other work on the device: the same call gives
+ * the same bits.
  *
  * Ownership, alignment (every pointer 16 bytes), aliasing, empty work, streams
  * and error codes are as for rwkv7_wkv_prefill; a `decay` not one of
@@ -469,8 +476,9 @@ int rwkv7_wkv_prefill_algo(int64_t B, int64_t T, int64_t H, int64_t N, int dtype
  * prompt is taken in segments; the states at their starts (16 KiB for each head and
  * 512 tokens) live in the per-(device, stream) workspace described for
  * rwkv7_wkv_prefill_ex, and what is said there about growth and graph capture holds.
- * Calls on one stream share that workspace, also from two threads at once; graphs
- * captured on one stream may not be replayed at the same time on two.
+ * Calls on one stream share that workspace, also from two threads at once; what is
+ * said there about the replays of graphs holds for these prompts, for
+ * rwkv7_linattn_backward and for the sums of rwkv7_layernorm_backward.
  */
 #define RWKV7_DECAY_HEAD 0  /* log_w [H] */
 #define RWKV7_DECAY_TOKEN 1 /* log_w [B, T, H] */

@@ -30,8 +30,9 @@
 //  - token 16J + 4q + i is slot (q, e = J, i): the two token tiles of a D column are an operand of
 //    a product over the 32 tokens.
 // The only layout change left is to turn a token-row operand into a channel-row one: bfloat16 rows
-// are read from LDS turned, float32 rows, which have no room there, go through products with a 0/1
-// matrix (exact).
+// are read from LDS turned, and so are float32 rows in the gradients' kernel, which keeps their pieces
+// there; in the prompt and state kernels float32 rows go by registers, and through products with a
+// 0/1 matrix (exact).
 #pragma once
 
 #include "lane_sums.hpp"
