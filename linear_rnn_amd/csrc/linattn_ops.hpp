@@ -132,7 +132,7 @@ __device__ __forceinline__ u32x4 descriptor(const void* base, uint32_t bytes) {
 }
 __device__ __forceinline__ void to_lds16(u32x4 b, uint32_t off, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(off), "s"(b), "s"(__builtin_amdgcn_readfirstlane((int)lds))
-               : "memory", "m0");
+               : "memory");
 }
 // Without temporal hint, for what no later kernel of the call reads.
 __device__ __forceinline__ void to_lds16_last(u32x4 b, uint32_t off, uint32_t lds) {
