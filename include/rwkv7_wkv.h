@@ -517,7 +517,8 @@ int rwkv7_linattn_step(const void *r, const float *log_w, const void *k, const v
  * RWKV7_DECAY_HEAD is zeros and dstate_in is dstate_out. The states are formed
  * again from the inputs: those before each 128 tokens (float32: 64) and their
  * gradients, 40 KiB in all for each head, live in the workspace as those of
- * rwkv7_linattn_prefill.
+ * rwkv7_linattn_prefill; at most about 1 GiB (or one head's, where that is more),
+ * since the heads of a larger call are taken in slabs that fit.
  */
 int rwkv7_linattn_backward(const void *r, const float *log_w, const void *k, const void *v, const float *state_in,
                            const int32_t *lens, const void *dy, const float *dstate_out, void *dr, float *dlog_w,

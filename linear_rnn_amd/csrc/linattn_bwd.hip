@@ -77,6 +77,7 @@ struct GradParams {
   void* dk;
   void* dv;
   Seq seq;
+  int64_t first;  // number of the first head; states, gradients and marks begin with it
   int32_t per_token;
   int32_t nseg;
   int64_t seg_blocks;
@@ -151,8 +152,8 @@ __global__ __launch_bounds__(64 * Cfg<F32>::kTiles, F32 ? 1 : 2) void linattn_gr
   // i and i + 4 share a SIMD: tiles w and 7 - w together have the same work on every one. (float32: tile w is wave w's.)
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), w = wave < 4 ? wave : 11 - wave;
   const int64_t unit = blockIdx.x / p.nseg, seg = blockIdx.x % p.nseg;
-  const int64_t b = unit / p.seq.H;
-  const int32_t h = unit % p.seq.H;
+  const int64_t b = (p.first + unit) / p.seq.H;
+  const int32_t h = (p.first + unit) % p.seq.H;
   const int64_t T = p.seq.T, len = seq_len(p.seq, b);
   constexpr int kRowBytes = kN * kEsz<F32>;  // a token's, in memory
   const uint32_t row_bytes = p.seq.H * kRowBytes;
@@ -592,34 +593,47 @@ __global__ __launch_bounds__(256) void linattn_zero_kernel(float* x, int64_t n) 
   if (i < n) x[i] = 0.f;
 }
 
+// Workspace of a call for what its heads have between their blocks, or one head's where that is more: the heads are taken
+// in slabs that fit. Smaller slabs cost time, since less is under way at once: B=4 T=16384 H=64 bfloat16 (1.3 GB) 2.11 ms in one
+// slab, 2.14 in two of this size, 2.37 at 512 MiB, 2.47 at 256; B=8 T=4096 H=32 (420 MB) 0.54, 0.54, 0.54, 0.56.
+constexpr size_t kSlabBytes = size_t(1) << 30;
+
 template <bool F32>
 hipError_t launch(const LinattnCall& c) {
-  constexpr int64_t kTokens = Cfg<F32>::kTokens;
+  constexpr int64_t kTokens = Cfg<F32>::kTokens, kStateFloats = kLinattnStateBytes / 4;
   const int64_t units = c.B * c.H, nblk = (c.T + kTokens - 1) / kTokens,
                 pieces = (nblk + kPieceBlocks - 1) / kPieceBlocks, cus = linattn_cus();
+  const bool border = nblk > 1;            // blocks whose state is not the caller's
+  const bool states = border || c.ds_in;  // one block: its state is the caller's, and so is its gradient; a copy where
+                                          // dstate_in is written over it
+  // bytes of a head: its pieces' states and gradients, the marks, and their decays
+  const size_t head = (size_t)(border ? pieces + 2 * nblk : 0) * kLinattnStateBytes +
+                      (size_t)(states ? pieces : 0) * kLinattnStateBytes + (size_t)(pieces + nblk) * 8;
+  const int64_t fit = kSlabBytes / head > 0 ? (int64_t)(kSlabBytes / head) : 1;
+  const int64_t slabs = (units + fit - 1) / fit, slab = (units + slabs - 1) / slabs;
+
   // Segments: as many workgroups as fill the compute units in whole rounds best, each with its first loads to wait for.
   // B=8 T=4096 H=12 bfloat16 210 us in 8 segments of 4 blocks, 371 in one, 247 in 32; B=4 T=4096 H=64 540 in one, 557 in 8.
   int64_t nseg = 1;
   double best = 0;
-  for (int64_t n = 1; n <= nblk && (n == 1 || units * n <= 4 * cus); ++n) {
-    const int64_t length = (nblk + n - 1) / n, rounds = (units * n + cus - 1) / cus;
+  for (int64_t n = 1; n <= nblk && (n == 1 || slab * n <= 4 * cus); ++n) {
+    const int64_t length = (nblk + n - 1) / n, rounds = (slab * n + cus - 1) / cus;
     const double us = rounds * (length * (F32 ? 10.0 : 5.0) + 3.0);
     if (n == 1 || us < best) best = us, nseg = n;
   }
   const int64_t seg_blocks = (nblk + nseg - 1) / nseg;
   nseg = (nblk + seg_blocks - 1) / seg_blocks;
 
-  const bool border = nblk > 1;  // blocks whose state is not the caller's
   size_t need = 0;
   auto room = [&](size_t bytes) {
     const size_t at = need;
     need += (bytes + 255) / 256 * 256;
     return at;
   };
-  const size_t o_states = room(border ? units * pieces * kLinattnStateBytes : 0), o_decay = room(units * pieces * 4);
-  const size_t o_marks = room(border ? units * nblk * kLinattnStateBytes : 0), o_mdecay = room(units * nblk * 4);
-  const size_t o_grads = room(units * pieces * kLinattnStateBytes), o_gdecay = room(units * pieces * 4);
-  const size_t o_gmarks = room(border ? units * nblk * kLinattnStateBytes : 0), o_gmdecay = room(units * nblk * 4);
+  const size_t o_states = room(border ? slab * pieces * kLinattnStateBytes : 0), o_decay = room(slab * pieces * 4);
+  const size_t o_marks = room(border ? slab * nblk * kLinattnStateBytes : 0), o_mdecay = room(slab * nblk * 4);
+  const size_t o_grads = room(states ? slab * pieces * kLinattnStateBytes : 0), o_gdecay = room(slab * pieces * 4);
+  const size_t o_gmarks = room(border ? slab * nblk * kLinattnStateBytes : 0), o_gmdecay = room(slab * nblk * 4);
   const size_t o_parts = room(c.per_token ? 0 : units * nseg * 4);
   std::lock_guard<std::mutex> lock(operators_mutex());
   void* ws = nullptr;
@@ -627,34 +641,45 @@ hipError_t launch(const LinattnCall& c) {
   if (e != hipSuccess) return e;
   char* base = static_cast<char*>(ws);
   auto at = [&](size_t o) { return reinterpret_cast<float*>(base + o); };
+  const void* fn = reinterpret_cast<const void*>(&linattn_grad_kernel<F32>);
+  static std::atomic<uint64_t> granted{0};
+  e = allow_lds(granted, fn, Cfg<F32>::kLds);
+  if (e != hipSuccess) return e;
 
   LinattnPieces f{}, g{};
   f.pieces = g.pieces = f.stride = g.stride = pieces;
   f.every = g.every = 1;
   f.states = at(o_states), f.decay = at(o_decay), f.marks = border ? at(o_marks) : nullptr, f.mark_decay = at(o_mdecay);
   g.states = at(o_grads), g.decay = at(o_gdecay), g.marks = border ? at(o_gmarks) : nullptr, g.mark_decay = at(o_gmdecay);
-  g.end = c.ds_in, g.end_stride = 1;
+  g.end_stride = 1;
   GradParams p{};
   p.r = c.r, p.log_w = c.log_w, p.k = c.k, p.v = c.v, p.dy = c.dy;
-  // one block: its state is the caller's, and so is its gradient; a copy where dstate_in is written over it
-  p.states = border ? f.states : c.s_in, p.marks = f.marks, p.mark_decay = f.mark_decay;
-  p.grads = border || c.ds_in ? g.states : c.ds_out, p.grad_marks = g.marks, p.grad_mark_decay = g.mark_decay;
+  // the state before a block: of its piece (or the caller's), decayed since, and the piece's sum up to the block
+  p.marks = f.marks, p.mark_decay = f.mark_decay;
+  p.grad_marks = g.marks, p.grad_mark_decay = g.mark_decay;
   p.state_stride = p.grad_stride = border ? pieces : 1;
-  if (border || c.ds_in) {
-    e = launch_linattn_states(c, kTokens, border ? &f : nullptr, &g);
-    if (e != hipSuccess) return e;
-  }
-  p.dr = c.dr, p.dlog_w = c.per_token ? c.dlog_w : at(o_parts), p.dk = c.dk, p.dv = c.dv;
+  p.dr = c.dr, p.dk = c.dk, p.dv = c.dv;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
   p.nseg = (int32_t)nseg, p.seg_blocks = seg_blocks;
-  const void* fn = reinterpret_cast<const void*>(&linattn_grad_kernel<F32>);
-  static std::atomic<uint64_t> granted{0};
-  e = allow_lds(granted, fn, Cfg<F32>::kLds);
-  if (e != hipSuccess) return e;
-  void* args[] = {&p};
-  e = hipLaunchKernel(fn, dim3((uint32_t)(units * nseg)), dim3(64 * Cfg<F32>::kTiles), args, Cfg<F32>::kLds, c.stream);
-  if (e != hipSuccess || c.per_token) return e;
+  for (int64_t first = 0; first < units; first += slab) {
+    const int64_t some = units - first < slab ? units - first : slab;
+    auto of = [&](auto* x) { return x ? x + first * kStateFloats : x; };  // the caller's states from the first head on
+    f.first = g.first = p.first = first;
+    f.units = g.units = some;
+    f.start = of(c.s_in), g.start = of(c.ds_out), g.end = of(c.ds_in);
+    p.states = border ? f.states : f.start;
+    p.grads = states ? g.states : g.start;
+    p.dlog_w = c.per_token ? c.dlog_w : at(o_parts) + first * nseg;
+    if (states) {
+      e = launch_linattn_states(c, kTokens, border ? &f : nullptr, &g);
+      if (e != hipSuccess) return e;
+    }
+    void* args[] = {&p};
+    e = hipLaunchKernel(fn, dim3((uint32_t)(some * nseg)), dim3(64 * Cfg<F32>::kTiles), args, Cfg<F32>::kLds, c.stream);
+    if (e != hipSuccess) return e;
+  }
+  if (c.per_token) return hipSuccess;
   const float* parts = at(o_parts);
   float* dlog_w = c.dlog_w;
   int64_t B = c.B;

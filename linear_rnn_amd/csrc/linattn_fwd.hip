@@ -434,7 +434,8 @@ hipError_t launch_out(const LinattnCall& c) {
     lock.lock();
     // what the last segment adds nobody asks for here
     LinattnPieces q{};
-    q.pieces = (p.nseg - 1) * every, q.every = (int32_t)every;
+    q.units = units, q.pieces = (p.nseg - 1) * every, q.every = (int32_t)every;
+    q.start = c.s_in;
     p.stride = q.stride = q.end_stride = q.pieces + 1;
     const size_t states = (size_t)units * q.stride * kLinattnStateBytes;
     void* ws = nullptr;

@@ -43,6 +43,7 @@ constexpr int64_t kPieceBlocks = 4;
 inline int64_t linattn_blocks(int64_t T, int64_t block) { return (T + block - 1) / block; }
 inline int64_t linattn_pieces(int64_t T, int64_t block) { return (linattn_blocks(T, block) + kPieceBlocks - 1) / kPieceBlocks; }
 struct LinattnPieces {
+  int64_t first, units;  // the heads (b H + h) of this launch; every array but the call's tensors begins with the first of them
   int64_t pieces;     // of a sequence, from its start on (backward: all of them)
   int32_t every;      // keep the state before every every-th piece
   float* states;      // [units][stride] states, stride at least pieces; the kept ones come first in a sequence's
@@ -50,6 +51,7 @@ struct LinattnPieces {
   float* decay;       // [units][stride]
   float* marks;       // may be null; [units][blocks] states
   float* mark_decay;  // [units][blocks]
+  const float* start; // may be null (zeros); the state before the first piece (backward: the gradient behind the last), [units]
   float* end;         // may be null; the state behind the last piece (backward: the gradient before the first), [units] with
   int64_t end_stride; // that many states from one to the next
 };

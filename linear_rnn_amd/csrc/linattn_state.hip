@@ -41,6 +41,7 @@ struct StateParams {
   Seq seq;
   int32_t per_token;
   int32_t block;  // tokens
+  int64_t first;  // number of the first head; the arrays of a side begin with it
   int64_t pieces, stride;
 };
 
@@ -84,8 +85,8 @@ __global__ __launch_bounds__(256, 2) void linattn_state_kernel(StateParams p) {
   const int lane = threadIdx.x & 63, li = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t unit = blockIdx.x / p.pieces, piece = blockIdx.x % p.pieces;
-  const int64_t b = unit / p.seq.H;
-  const int32_t h = unit % p.seq.H;
+  const int64_t b = (p.first + unit) / p.seq.H;
+  const int32_t h = (p.first + unit) % p.seq.H;
   const int64_t len = seq_len(p.seq, b);
   const uint32_t row_bytes = p.seq.H * kN * kEsz<F32>;
   const int64_t nblk = (p.seq.T + p.block - 1) / p.block;
@@ -250,18 +251,18 @@ hipError_t launch_linattn_states(const LinattnCall& c, int64_t block, const Lina
   StateParams p{};
   int sides = 0;
   if (forward)
-    p.side[sides++] = Side{c.k, c.v, forward->states, forward->decay, forward->marks, forward->mark_decay, c.s_in, forward->end,
+    p.side[sides++] = Side{c.k, c.v, forward->states, forward->decay, forward->marks, forward->mark_decay, forward->start, forward->end,
                            forward->end_stride, 0, forward->every};
   if (backward)
-    p.side[sides++] = Side{c.r, c.dy, backward->states, backward->decay, backward->marks, backward->mark_decay, c.ds_out,
+    p.side[sides++] = Side{c.r, c.dy, backward->states, backward->decay, backward->marks, backward->mark_decay, backward->start,
                            backward->end, backward->end_stride, 1, backward->every};
   p.log_w = c.log_w;
   p.seq = Seq{c.T, (int32_t)c.H, c.lens};
   p.per_token = c.per_token;
   p.block = (int32_t)block;
   const LinattnPieces& any = forward ? *forward : *backward;
-  p.pieces = any.pieces, p.stride = any.stride;
-  const int64_t units = c.B * c.H;
+  p.first = any.first, p.pieces = any.pieces, p.stride = any.stride;
+  const int64_t units = any.units;
   const void* fn = c.f32 ? reinterpret_cast<const void*>(&linattn_state_kernel<true>)
                          : reinterpret_cast<const void*>(&linattn_state_kernel<false>);
   void* args[] = {&p};
