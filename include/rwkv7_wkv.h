@@ -45,8 +45,9 @@
  *
  * Errors: every entry point returns RWKV7_OK or a negative code, never throws,
  * prints or aborts, and validates every argument before its first HIP call.
- * Entry points are thread-safe; concurrent calls on different streams are
- * independent.
+ * Entry points are thread-safe, also on one stream (each call's kernels stay
+ * together; rwkv7_wkv_prefill_noalloc excepted); concurrent calls on different
+ * streams are independent.
  */
 #ifndef RWKV7_WKV_H
 #define RWKV7_WKV_H

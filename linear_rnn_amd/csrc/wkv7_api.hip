@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "api_checks.hpp"
 #include "rwkv7_wkv.h"
@@ -41,6 +42,10 @@ using rwkv7::WkvCall;
 using rwkv7::overlap;
 using rwkv7::Range;
 using rwkv7::range_of;
+
+// Held while a call of several kernels launches them: what passes from one to the next lives in a workspace that all
+// calls on a stream share, so the kernels of two threads' calls on one stream may not fall between each other.
+std::mutex launch_mu;
 
 int validate(const void* const in[6], const void* s_in, const float* y, const void* s_out, int64_t B,
              int64_t T, int64_t H, int64_t N, int dtype, int sdtype) {
@@ -104,6 +109,7 @@ int run(const void* r, const void* w, const void* k, const void* v, const void* 
   if (step) {
     e = rwkv7::launch_sequential(c, /*decode_shape=*/true);
   } else {
+    std::lock_guard<std::mutex> lock(launch_mu);
     if (algo == RWKV7_ALGO_AUTO) algo = rwkv7::auto_prefill_algo(B, T, H, dtype);
     e = algo == RWKV7_ALGO_CHUNKED         ? rwkv7::launch_chunked(c)
         : algo == RWKV7_ALGO_CHUNKED_SPLIT ? rwkv7::launch_chunked_split(c)
@@ -170,7 +176,12 @@ int run_tmix(const void* r, const float* w_raw, const void* k, const void* v, co
   }
   rwkv7::TmixCall c{{r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, state_out, T, (int32_t)H}, B, H, dtype, s};
   c.algo = algo;
-  e = rwkv7::launch_tmix(c);
+  if (step) {
+    e = rwkv7::launch_tmix(c);
+  } else {
+    std::lock_guard<std::mutex> lock(launch_mu);
+    e = rwkv7::launch_tmix(c);
+  }
   if (e == hipErrorNotSupported) return RWKV7_ERR_ALGO;
   return e == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
 }
@@ -257,6 +268,7 @@ int rwkv7_stack_forward(const void* w_in, const void* w_out, const float* vecs, 
   if (st != RWKV7_OK) return st;
   if (L == 0 || B * T * H == 0) return RWKV7_OK;
   rwkv7::StackCall c{w_in, w_out, vecs, x, states, L, B, T, H, dtype, static_cast<hipStream_t>(stream)};
+  std::lock_guard<std::mutex> lock(launch_mu);
   const hipError_t e = rwkv7::launch_stack(c);
   return e == hipSuccess ? RWKV7_OK : RWKV7_ERR_HIP;
 }
@@ -293,6 +305,7 @@ int rwkv7_wkv_backward_ex(const void* r, const void* w, const void* k, const voi
   // the float32 token-by-token one otherwise
   if (algo == RWKV7_ALGO_AUTO && dtype == RWKV7_DTYPE_BF16 && T * H * 64 < (int64_t(1) << 31))
     algo = RWKV7_ALGO_CHUNKED;
+  std::lock_guard<std::mutex> lock(launch_mu);
   if (algo == RWKV7_ALGO_CHUNKED) {
     e = rwkv7::launch_backward_chunked(c);
     if (e == hipErrorNotSupported) return RWKV7_ERR_ALGO;

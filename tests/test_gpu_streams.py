@@ -4,7 +4,8 @@ import threading
 import pytest
 
 from linear_rnn_amd import wkv
-from tests.gpu_util import say
+from linear_rnn_amd.inputs import CONFIGS, make_cotangents, make_inputs, make_stack_inputs
+from tests.gpu_util import say, to_dev
 from tests.test_gpu_operator_limits import case, chain, clones
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +92,50 @@ def test_allocated_outputs_are_of_the_stream(torch):
         del got
     with pytest.raises(ValueError, match="hipStreamPerThread"):
         wkv.linattn(d["r"], d["log_w"], d["k"], d["v"], stream=PER_THREAD)
+
+
+def test_two_threads_of_the_recurrence_on_one_stream(torch):
+    """The split prefill, the gradients and the stack pass records from kernel to kernel in the stream's workspace."""
+    say("recurrence, two threads on one stream")
+    st = torch.cuda.Stream()
+    cases = []
+    for n, (B, T, H) in enumerate(((1, 700, 3), (2, 450, 2))):
+        x = make_inputs(CONFIGS["L12-D768-prefill"], B=B, T=T, H=H, seed=30 + n, with_state=True)
+        d = to_dev(x)
+        k = make_stack_inputs(2, B, 60, H, "bf16", seed=40 + n)
+        d["w_in"], d["w_out"] = (torch.from_numpy(k[i].view("int16")).cuda().view(torch.bfloat16) for i in ("w_in", "w_out"))
+        d["vecs"], d["x"], d["states"] = (torch.from_numpy(k[i]).cuda() for i in ("vecs", "x", "states"))
+        d["dy"] = torch.from_numpy(make_cotangents(B, T, H, seed=n)["dy"]).cuda()
+        cases.append(d)
+    torch.cuda.synchronize()
+
+    def call(d):
+        a = [d[n] for n in "rwkvab"]
+        with torch.cuda.stream(st):
+            out = {"y": wkv.wkv7(*a, state_in=d["state_in"], algo=wkv.RWKV7_ALGO_CHUNKED_SPLIT)}
+            for algo in (wkv.RWKV7_ALGO_CHUNKED, wkv.RWKV7_ALGO_SEQUENTIAL):
+                out[algo] = tuple(wkv.wkv7_backward(*a, d["dy"], d["state_in"], None, algo=algo).values())
+            x, s = d["x"].clone(), d["states"].clone()
+            wkv.rwkv7_stack_forward(d["w_in"], d["w_out"], d["vecs"], x, s)
+            out["stack"] = (x, s)
+        return [t for o in out.values() for t in o]
+
+    want = [call(d) for d in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(n):
+        try:
+            got = [call(cases[n]) for _ in range(10)]
+            st.synchronize()
+            bad.extend((n, i) for g in got for i, (t, w) in enumerate(zip(g, want[n])) if not torch.equal(t, w))
+        except Exception as e:  # shown by the assertion below
+            bad.append((n, e))
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad, bad
