@@ -467,7 +467,8 @@ int rwkv7_wkv_prefill_algo(int64_t B, int64_t T, int64_t H, int64_t N, int dtype
  * off by its one rounding and, from intermediates of two pieces (16 bits), by up to
  * 2^-15 of the sum of its terms' magnitudes; that is the larger one where the terms
  * cancel. Inputs have to be finite in the tokens that count (a float32 infinity
- * becomes a NaN, and so may a float32 above 3.39e38, which no bfloat16 holds). No
+ * becomes a NaN, and so may a float32 above 3.39e38, which no bfloat16 holds; one
+ * under 2^-102 may lose digits of its pieces). No
  * result depends on the launch or on other work on the device: the same call gives
  * the same bits.
  *

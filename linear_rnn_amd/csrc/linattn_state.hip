@@ -10,7 +10,7 @@
 //
 // Memory bounds it. bfloat16 rows come to LDS whole, by direct loads that each wave keeps 32 tokens ahead of itself in the
 // place where its sum goes at the end, and leave it turned: B=8 T=4096 H=12 with both directions and the states of
-// every block (300 MB) 61 to 66 us; 74 with loads to registers in operand order and turns by matrix products. They are
+// every block (300 MB) 64 us; 74 with loads to registers in operand order and turns by matrix products. They are
 // loaded to stay in the caches, since the kernel that follows reads them again (with a hint against that it takes 4 us
 // longer at B=1 T=8191 H=32). float32 rows, three pieces each, still go by registers.
 #include "linattn_internal.hpp"

@@ -109,5 +109,5 @@ def test_workspace_is_bounded(torch):
 
     call(1)  # code and kernel arguments
     assert call(T) <= (1 << 30) + (64 << 20)
-    assert call(T) == 0
+    assert call(T) <= 0
     assert not dlog_w.any()
