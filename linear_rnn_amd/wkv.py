@@ -221,6 +221,22 @@ def _on_gpu(like, stream):
     if stream is None and like.device.index != _T.current_device():
         raise ValueError("tensors are on %s but the current device is cuda:%d; pass a stream of that device or "
                          "select it" % (like.device, _T.current_device()))
+    where = getattr(stream, "device", None)  # a bare handle does not say
+    if where is not None and where != like.device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (where, like.device))
+
+
+def _launch(name, args, like, stream):
+    """Call the library with `like`'s device current (a stream given by the caller may be another device's)."""
+    index = like.get_device()
+    if index < 0 or stream is not None or index != _T.current_device():
+        _on_gpu(like, stream)  # says what is wrong
+    fn = getattr(lib(), name)
+    if index == _T.current_device():
+        _check(fn(*args, _T.raw_stream(index) if stream is None else _stream(stream)))
+    else:
+        with _T.module.cuda.device(index):
+            _check(fn(*args, _stream(stream)))
 
 
 def _input_dtypes():
@@ -256,20 +272,20 @@ def _check(status: int):
 def rwkv7_wkv_prefill(r, w, k, v, a, b, state_in, y, state_out, stream=None):
     """Whole-sequence prefill. Tensors as in include/rwkv7_wkv.h ([B,T,H,64] inputs, float32 y and state)."""
     args = _args(r, w, k, v, a, b, state_in, y, state_out, stream)
-    _check(lib().rwkv7_wkv_prefill(*args, _stream(stream)))
+    _launch("rwkv7_wkv_prefill", args, r, stream)
 
 
 def rwkv7_wkv_prefill_noalloc(r, w, k, v, a, b, state_in, y, state_out, stream=None):
     """The split chunked prefill with its records in the library's static device array (allocates nothing;
     bfloat16 inputs; calls on one device must not overlap)."""
     args = _args(r, w, k, v, a, b, state_in, y, state_out, stream)
-    _check(lib().rwkv7_wkv_prefill_noalloc(*args, _stream(stream)))
+    _launch("rwkv7_wkv_prefill_noalloc", args, r, stream)
 
 
 def rwkv7_wkv_step(r, w, k, v, a, b, state_in, y, state_out, stream=None):
     """Single-token step (T == 1); state_out may be state_in for an in-place update."""
     args = _args(r, w, k, v, a, b, state_in, y, state_out, stream)
-    _check(lib().rwkv7_wkv_step(*args, _stream(stream)))
+    _launch("rwkv7_wkv_step", args, r, stream)
 
 
 def _state_code(*states) -> int:
@@ -292,13 +308,13 @@ def rwkv7_wkv_step_q(r, w, k, v, a, b, state_in, y, state_out, state_dtype=None,
     if sd not in tdt:
         raise ValueError("state_dtype must be one of RWKV7_STATE_F32 / _BF16 / _F16")
     args = _args(r, w, k, v, a, b, state_in, y, state_out, stream, state_dtypes=(tdt[sd],))
-    _check(lib().rwkv7_wkv_step_q(*args, sd, _stream(stream)))
+    _launch("rwkv7_wkv_step_q", args + [sd], r, stream)
 
 
 def rwkv7_wkv_prefill_ex(r, w, k, v, a, b, state_in, y, state_out, algo=RWKV7_ALGO_AUTO, stream=None):
     """Prefill with an explicit algorithm (RWKV7_ALGO_*)."""
     args = _args(r, w, k, v, a, b, state_in, y, state_out, stream)
-    _check(lib().rwkv7_wkv_prefill_ex(*args, int(algo), _stream(stream)))
+    _launch("rwkv7_wkv_prefill_ex", args + [int(algo)], r, stream)
 
 
 def wkv7(r, w, k, v, a, b, state_in=None, algo=RWKV7_ALGO_AUTO, want_state=True, stream=None):
@@ -332,7 +348,7 @@ def _tmix_args(r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, state_out, s
 def rwkv7_tmix_prefill(r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, state_out, stream=None):
     """Fused time-mix prefill: prologue (decay, normalised removal key, slots), recurrence, ln_x."""
     args = _tmix_args(r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, state_out, stream)
-    _check(lib().rwkv7_tmix_prefill(*args, _stream(stream)))
+    _launch("rwkv7_tmix_prefill", args, r, stream)
 
 
 def rwkv7_tmix_prefill_ex(r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, state_out, algo=RWKV7_ALGO_AUTO,
@@ -340,13 +356,13 @@ def rwkv7_tmix_prefill_ex(r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, s
     """Fused time-mix prefill with an explicit algorithm (RWKV7_ALGO_AUTO / _SEQUENTIAL / _CHUNKED /
     _CHUNKED_SPLIT)."""
     args = _tmix_args(r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, state_out, stream)
-    _check(lib().rwkv7_tmix_prefill_ex(*args, int(algo), _stream(stream)))
+    _launch("rwkv7_tmix_prefill_ex", args + [int(algo)], r, stream)
 
 
 def rwkv7_tmix_step(r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, state_out, stream=None):
     """Fused time-mix single-token step (T == 1); state_out may be state_in."""
     args = _tmix_args(r, w_raw, k, v, kk, a_lr, ln_w, ln_b, state_in, out, state_out, stream)
-    _check(lib().rwkv7_tmix_step(*args, _stream(stream)))
+    _launch("rwkv7_tmix_step", args, r, stream)
 
 
 def tmix(r, w_raw, k, v, kk, a_lr, ln_w=None, ln_b=None, state_in=None, want_state=True, algo=RWKV7_ALGO_AUTO,
@@ -384,7 +400,7 @@ def rwkv7_wkv_backward_ex(r, w, k, v, a, b, state_in, dy, dstate_out, dr, dw, dk
     _expect(dstate_in, "dstate_in", (B, H, N, N), _f32(), r, optional=True)
     _on_gpu(r, stream)
     args = [_ptr(x) for x in (r, w, k, v, a, b, state_in, dy, dstate_out, dr, dw, dk, dv, da, db, dstate_in)]
-    _check(lib().rwkv7_wkv_backward_ex(*args, B, T, H, N, _dtype_code(r), int(algo), _stream(stream)))
+    _launch("rwkv7_wkv_backward_ex", args + [B, T, H, N, _dtype_code(r), int(algo)], r, stream)
 
 
 def wkv7_backward(r, w, k, v, a, b, dy, state_in=None, dstate_out=None, want_dstate=True, stream=None,
@@ -420,23 +436,10 @@ def rwkv7_stack_forward(w_in, w_out, vecs, x, states, stream=None):
     _expect(vecs, "vecs", (L, 5, D), _f32(), states)
     _on_gpu(states, stream)
     args = [_ptr(w_in), _ptr(w_out), _ptr(vecs), _ptr(x), _ptr(states), L, B, T, H, N, _dtype_code(w_in)]
-    _check(lib().rwkv7_stack_forward(*args, _stream(stream)))
+    _launch("rwkv7_stack_forward", args, states, stream)
 
 
 # ---- linear attention with a decay for each head
-
-def _launch(name, args, like, stream):
-    """Call the library with `like`'s device current (a stream given by the caller may be another device's)."""
-    index = like.get_device()
-    if index < 0 or (stream is None and index != _T.current_device()):
-        _on_gpu(like, stream)  # says what is wrong
-    fn = getattr(lib(), name)
-    if index == _T.current_device():
-        _check(fn(*args, _T.raw_stream(index) if stream is None else _stream(stream)))
-    else:
-        with _T.module.cuda.device(index):
-            _check(fn(*args, _stream(stream)))
-
 
 def _linattn_inputs(r, log_w, k, v, state_in):
     """The addresses of the inputs that the linear attention's calls share, the sizes and log_w's layout."""
