@@ -70,6 +70,7 @@ extern "C" {
 #define RWKV7_ERR_HIP (-8)       /* a HIP runtime call or kernel launch failed */
 #define RWKV7_ERR_SCRATCH (-9)   /* rwkv7_wkv_prefill_noalloc: the call does not fit its static scratch array */
 #define RWKV7_ERR_DECAY (-10)    /* linear attention: decay not one of RWKV7_DECAY_* */
+#define RWKV7_ERR_MODE (-11)     /* input not one of RWKV7_INPUT_*, or act not one of RWKV7_ACT_* */
 
 /* Input dtype of r, w, k, v, a, b. y is always float32; so is the state except in rwkv7_wkv_step_q. */
 #define RWKV7_DTYPE_F32 0
@@ -571,6 +572,83 @@ int rwkv7_layernorm_forward(const void *x, const float *weight, const float *bia
 int rwkv7_layernorm_backward(const void *x, const float *weight, const float *mean, const float *rstd, const void *dy,
                              void *dx, float *dweight, float *dbias, int64_t M, int64_t D, int64_t G, int x_dtype,
                              int y_dtype, void *stream);
+
+/*
+ * Gated linear recurrence: a decay for each token and channel, as in the models whose
+ * time mixing has no heads. Per batch b and channel d, with w_t = exp(log_w_t):
+ *
+ *     h_t = w_t h_{t-1} + s(w_t) x_t
+ *     y_t = h_t
+ *
+ * rwkv7_gscan_prefill takes a prompt, rwkv7_gscan_step one token, rwkv7_gscan_backward
+ * the gradients.
+ *
+ *   x          input [B,T,D] in `dtype` (RWKV7_DTYPE_F32 or _BF16)
+ *   log_w      [B,T,D] float32 natural logs of the decays, at most 0; -infinity is a
+ *              decay of 0 (the state is reset before this token, e.g. where packed
+ *              sequences meet)
+ *   state_in   [B,D] float32 initial state, or NULL for zeros
+ *   lens       [B] int32 lengths of the sequences in device memory, or NULL, as for
+ *              rwkv7_linattn_prefill: the tokens from lens[b] on are left out whatever
+ *              they hold, y there is 0 and the state is that after token lens[b] - 1
+ *   y          [B,T,D] output in `dtype`
+ *   state_out  [B,D] float32 final state, or NULL; may equal state_in
+ *   B, T, D    batch, tokens, channels (>= 0); D at most 2^20, B*D at most 2^27 and
+ *              B*T*ceil(D/64) at most 2^35
+ *   input      the input's scale s(w): RWKV7_INPUT_PLAIN 1, RWKV7_INPUT_MIX 1 - w (h is
+ *              a running mean), RWKV7_INPUT_NORM sqrt(1 - w^2) (h keeps the size of x).
+ *              Both are formed from log_w without the cancellation near w = 1.
+ *
+ * The state and all arithmetic are float32, a bfloat16 output is rounded once. No result
+ * depends on the launch or on other work on the device. Inputs have to be finite in the
+ * tokens that count (log_w may be -infinity).
+ *
+ * Ownership, alignment (every pointer 16 bytes), aliasing, empty work, streams and error
+ * codes are as for rwkv7_wkv_prefill; an `input` not one of RWKV7_INPUT_* is
+ * RWKV7_ERR_MODE. Where there are few channels for the device a prompt is taken in
+ * segments, whose maps of the state (at most 16 KiB for each 64 channels) live in the
+ * workspace as the states of rwkv7_linattn_prefill do.
+ */
+#define RWKV7_INPUT_PLAIN 0 /* s = 1 */
+#define RWKV7_INPUT_MIX 1   /* s = 1 - w */
+#define RWKV7_INPUT_NORM 2  /* s = sqrt(1 - w^2) */
+
+int rwkv7_gscan_prefill(const void *x, const float *log_w, const float *state_in, const int32_t *lens, void *y,
+                        float *state_out, int64_t B, int64_t T, int64_t D, int dtype, int input, void *stream);
+
+/*
+ * Single-token step of the gated linear recurrence (T == 1, else RWKV7_ERR_SHAPE): reads
+ * the state, writes y and the new state (state_out may be state_in).
+ */
+int rwkv7_gscan_step(const void *x, const float *log_w, const float *state_in, void *y, float *state_out, int64_t B,
+                     int64_t T, int64_t D, int dtype, int input, void *stream);
+
+/*
+ * Gradients of rwkv7_gscan_prefill. With dy = dL/dy, dstate_out = dL/dh_T and g = dL/dh_t
+ * accumulated from the last token back:
+ *
+ *     g += dy_t
+ *     dx_t = s(w_t) g,  dlog_w_t = (w_t h_{t-1} + s'_t x_t) g
+ *     g <- w_t g                             and finally dstate_in = g
+ *
+ * s' is the derivative of s to log w: 0, -w or -w^2 / sqrt(1 - w^2), and for the last, which
+ * has none at w = 1, 0 there.
+ *
+ *   x, log_w, state_in, lens   the forward call's inputs
+ *   dy          [B,T,D] in `dtype`
+ *   dstate_out  [B,D] float32, or NULL (the final state is not used)
+ *   dx          [B,T,D] output in `dtype`; 0 behind a sequence's length
+ *   dlog_w      [B,T,D] float32 output; 0 behind a sequence's length and where log_w is
+ *               -infinity
+ *   dstate_in   [B,D] float32 output, or NULL; may equal dstate_out
+ *
+ * dx and dlog_w are required. With no tokens dstate_in is dstate_out. The states are formed
+ * again from the inputs; the maps of runs of 128 tokens (32 where D is no multiple of 4),
+ * 12 bytes a run and channel, live in the workspace.
+ */
+int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_in, const int32_t *lens, const void *dy,
+                         const float *dstate_out, void *dx, float *dlog_w, float *dstate_in, int64_t B, int64_t T,
+                         int64_t D, int dtype, int input, void *stream);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *rwkv7_wkv_strerror(int status);

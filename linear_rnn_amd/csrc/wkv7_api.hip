@@ -415,6 +415,7 @@ const char* rwkv7_wkv_strerror(int status) {
     case RWKV7_ERR_HIP: return "HIP runtime error";
     case RWKV7_ERR_SCRATCH: return "the call needs more than the static scratch array of rwkv7_wkv_prefill_noalloc";
     case RWKV7_ERR_DECAY: return "unknown kind of decay (one per head or one per token and head)";
+    case RWKV7_ERR_MODE: return "unknown kind of input scale or activation";
     default: return "unknown status";
   }
 }

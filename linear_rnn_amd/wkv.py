@@ -33,8 +33,12 @@ RWKV7_ALGO_CHUNKED = 2
 RWKV7_ALGO_CHUNKED_SPLIT = 3
 RWKV7_ERR_SCRATCH = -9
 RWKV7_ERR_DECAY = -10
+RWKV7_ERR_MODE = -11
 RWKV7_DECAY_HEAD = 0
 RWKV7_DECAY_TOKEN = 1
+RWKV7_INPUT_PLAIN = 0
+RWKV7_INPUT_MIX = 1
+RWKV7_INPUT_NORM = 2
 RWKV7_NOALLOC_SCRATCH_BYTES = 64 << 20
 _PER_THREAD = 2  # the handle hipStreamPerThread
 
@@ -44,6 +48,7 @@ EXPORTED = ("rwkv7_wkv_prefill", "rwkv7_wkv_step", "rwkv7_wkv_step_q", "rwkv7_wk
             "rwkv7_stack_forward", "rwkv7_wkv_prefill_algo", "rwkv7_wkv_prefill_noalloc",
             "rwkv7_linattn_prefill", "rwkv7_linattn_step", "rwkv7_linattn_backward",
             "rwkv7_layernorm_forward", "rwkv7_layernorm_backward",
+            "rwkv7_gscan_prefill", "rwkv7_gscan_step", "rwkv7_gscan_backward",
             "rwkv7_wkv_strerror")
 
 _lib = None
@@ -99,6 +104,12 @@ def lib() -> ctypes.CDLL:
             L.rwkv7_layernorm_forward.argtypes = [vp] * 6 + [i64] * 3 + [cf, ci, ci, vp]
             L.rwkv7_layernorm_backward.restype = ci
             L.rwkv7_layernorm_backward.argtypes = [vp] * 8 + [i64] * 3 + [ci, ci, vp]
+            L.rwkv7_gscan_prefill.restype = ci
+            L.rwkv7_gscan_prefill.argtypes = [vp] * 6 + [i64] * 3 + [ci, ci, vp]
+            L.rwkv7_gscan_step.restype = ci
+            L.rwkv7_gscan_step.argtypes = [vp] * 5 + [i64] * 3 + [ci, ci, vp]
+            L.rwkv7_gscan_backward.restype = ci
+            L.rwkv7_gscan_backward.argtypes = [vp] * 9 + [i64] * 3 + [ci, ci, vp]
             L.rwkv7_wkv_prefill_algo.restype = ci
             L.rwkv7_wkv_prefill_algo.argtypes = [i64] * 4 + [ci]
             L.rwkv7_wkv_strerror.restype = ctypes.c_char_p
@@ -603,4 +614,94 @@ def layernorm_backward(x, weight, mean, rstd, dy, groups=1, want_dweight=True, s
 
     out = _on_stream_of(stream, x, make)
     rwkv7_layernorm_backward(x, weight, mean, rstd, dy, out["dx"], out["dweight"], out["dbias"], groups, stream)
+    return out
+
+
+# ---- gated linear recurrence: a decay for each token and channel
+
+def _gscan_inputs(x, log_w, state_in):
+    """The addresses of the inputs that the gated recurrence's calls share, and the sizes."""
+    if not isinstance(x, _T.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a [B, T, D] tensor")
+    shape = x.shape
+    B, T, D = shape
+    at = [_at(x, "x", shape, _T.inputs, x), _at(log_w, "log_w", shape, _T.f32, x),
+          None if state_in is None else _at(state_in, "state_in", (B, D), _T.f32, x)]
+    return at, shape, (x.dtype,)
+
+
+def rwkv7_gscan_prefill(x, log_w, state_in, lens, y, state_out, input=RWKV7_INPUT_PLAIN, stream=None):
+    """Gated linear recurrence over a prompt. x, y [B,T,D] in one dtype; log_w float32 [B,T,D]; lens int32 [B] or
+    None; states float32 [B,D] or None; input one of RWKV7_INPUT_*."""
+    at, shape, same = _gscan_inputs(x, log_w, state_in)
+    B, T, D = shape
+    at.append(None if lens is None else _at(lens, "lens", (B,), _T.i32, x))
+    at.append(_at(y, "y", shape, same, x))
+    at.append(None if state_out is None else _at(state_out, "state_out", (B, D), _T.f32, x))
+    at += (B, T, D, _dtype_code(x), int(input))
+    _launch("rwkv7_gscan_prefill", at, x, stream)
+
+
+def rwkv7_gscan_step(x, log_w, state_in, y, state_out, input=RWKV7_INPUT_PLAIN, stream=None):
+    """Single-token step (T == 1) of the gated linear recurrence; state_out may be state_in."""
+    at, shape, same = _gscan_inputs(x, log_w, state_in)
+    B, T, D = shape
+    at.append(_at(y, "y", shape, same, x))
+    at.append(None if state_out is None else _at(state_out, "state_out", (B, D), _T.f32, x))
+    at += (B, T, D, _dtype_code(x), int(input))
+    _launch("rwkv7_gscan_step", at, x, stream)
+
+
+def _three(x):
+    if not isinstance(x, _T.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a [B, T, D] tensor")
+    return x.shape
+
+
+def gscan(x, log_w, state_in=None, lens=None, input=RWKV7_INPUT_PLAIN, want_state=True, stream=None):
+    """Allocate y ([B,T,D] in x's dtype) and the final state, run the prompt, return (y, state_out)."""
+    B, T, D = _three(x)
+    y, s_out = _on_stream_of(stream, x, lambda: (
+        _T.empty_like(x), x.new_empty((B, D), dtype=_T.f32[0]) if want_state else None))
+    rwkv7_gscan_prefill(x, log_w, state_in, lens, y, s_out, input, stream)
+    return y, s_out
+
+
+def gscan_step(x, log_w, state_in=None, input=RWKV7_INPUT_PLAIN, stream=None):
+    """Allocate y ([B,1,D] in x's dtype) and the new state, run one token, return (y, state_out).
+    rwkv7_gscan_step updates a state in place."""
+    B, T, D = _three(x)
+    y, s_out = _on_stream_of(stream, x, lambda: (_T.empty_like(x), x.new_empty((B, D), dtype=_T.f32[0])))
+    rwkv7_gscan_step(x, log_w, state_in, y, s_out, input, stream)
+    return y, s_out
+
+
+def rwkv7_gscan_backward(x, log_w, state_in, lens, dy, dstate_out, dx, dlog_w, dstate_in, input=RWKV7_INPUT_PLAIN,
+                         stream=None):
+    """Gradients of the gated linear recurrence: dx in x's dtype, dlog_w float32, dstate_in float32 or None (may be
+    dstate_out)."""
+    at, shape, same = _gscan_inputs(x, log_w, state_in)
+    B, T, D = shape
+    at.append(None if lens is None else _at(lens, "lens", (B,), _T.i32, x))
+    at.append(_at(dy, "dy", shape, same, x))
+    at.append(None if dstate_out is None else _at(dstate_out, "dstate_out", (B, D), _T.f32, x))
+    at.append(_at(dx, "dx", shape, same, x))
+    at.append(_at(dlog_w, "dlog_w", shape, _T.f32, x))
+    at.append(None if dstate_in is None else _at(dstate_in, "dstate_in", (B, D), _T.f32, x))
+    at += (B, T, D, _dtype_code(x), int(input))
+    _launch("rwkv7_gscan_backward", at, x, stream)
+
+
+def gscan_backward(x, log_w, dy, state_in=None, lens=None, dstate_out=None, input=RWKV7_INPUT_PLAIN, want_dstate=True,
+                   stream=None):
+    """Allocate the gradients, run the backward, return dict dx, dlog_w, dstate_in."""
+    B, T, D = _three(x)
+
+    def make():
+        return {"dx": _T.empty_like(x), "dlog_w": _T.empty_like(x, dtype=_T.f32[0]),
+                "dstate_in": x.new_empty((B, D), dtype=_T.f32[0]) if want_dstate else None}
+
+    out = _on_stream_of(stream, x, make)
+    rwkv7_gscan_backward(x, log_w, state_in, lens, dy, dstate_out, out["dx"], out["dlog_w"], out["dstate_in"], input,
+                         stream)
     return out
