@@ -650,6 +650,59 @@ int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_i
                          const float *dstate_out, void *dx, float *dlog_w, float *dstate_in, int64_t B, int64_t T,
                          int64_t D, int dtype, int input, void *stream);
 
+/*
+ * Gated linear unit: the wide half of a gated feed-forward block, both projections, the
+ * activation and the product in one pass.
+ *
+ *     g = x w_gate,  u = x w_up,  h = act(g) * u
+ *
+ *   x       [M,D] in `dtype` (RWKV7_DTYPE_F32 or _BF16, that of every tensor here)
+ *   w_gate, w_up  [D,F] (row-major, as the projections of rwkv7_stack_forward)
+ *   h       [M,F] output
+ *   gate, up  [M,F] outputs g and u for the backward, or both NULL
+ *   M, D, F rows (at most 2^28), channels (1 to 2^20), hidden channels (at most 2^20); the
+ *           tiles of 256 by 128 of [M,F], of [M,D] and of [D,F] at most 2^22 each
+ *   act     RWKV7_ACT_*
+ *
+ * Sums are float32; each output is rounded once. A float32 call's products are formed from
+ * three bfloat16 pieces of each operand, with errors of about float32 rounding, and the
+ * limits of those pieces that rwkv7_linattn_prefill states. Inputs have to be finite. No
+ * result depends on the launch or on other work on the device.
+ *
+ * Contiguous row-major layouts, 16-byte aligned pointers, outputs that overlap nothing,
+ * streams and error codes as for rwkv7_wkv_prefill; an unknown `act` is RWKV7_ERR_MODE; no
+ * rows or no hidden channels do nothing. float32 operands, and bfloat16 ones whose rows are
+ * no multiple of 8, are copied into the workspace described for rwkv7_wkv_prefill_ex first
+ * (6 or 2 bytes an element); what is said there about growth and graphs holds.
+ */
+#define RWKV7_ACT_SIGMOID 0 /* 1 / (1 + exp(-g)) */
+#define RWKV7_ACT_SILU 1    /* g / (1 + exp(-g)) */
+#define RWKV7_ACT_GELU 2    /* g (1 + erf(g / sqrt 2)) / 2 */
+#define RWKV7_ACT_RELU2 3   /* max(g, 0)^2, as in RWKV's channel mix */
+
+int rwkv7_glu_forward(const void *x, const void *w_gate, const void *w_up, void *h, void *gate, void *up, int64_t M,
+                      int64_t D, int64_t F, int dtype, int act, void *stream);
+
+/*
+ * Gradients of rwkv7_glu_forward from its x, weights and pre-activations:
+ *
+ *     dg = dh * u * act'(g),  du = dh * act(g)
+ *     dx = dg w_gate^T + du w_up^T,  dw_gate = x^T dg,  dw_up = x^T du
+ *
+ *   gate, up  [M,F] what the forward left;  dh  [M,F]
+ *   dx      [M,D] output, or NULL (not computed)
+ *   dw_gate, dw_up  [D,F] outputs, or both NULL (not computed)
+ *
+ * All in `dtype`. In a bfloat16 call dg and du are rounded to bfloat16 where they enter the
+ * products. They live in the workspace (4 bytes for each element of h, float32: 12) with the
+ * copies that rwkv7_glu_forward makes and, where the weights are small, parts of their
+ * gradients (at most 256 tiles of 256 KiB). With no rows dw_gate and dw_up are zeros, with
+ * no hidden channels dx is.
+ */
+int rwkv7_glu_backward(const void *x, const void *w_gate, const void *w_up, const void *gate, const void *up,
+                       const void *dh, void *dx, void *dw_gate, void *dw_up, int64_t M, int64_t D, int64_t F, int dtype,
+                       int act, void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *rwkv7_wkv_strerror(int status);
 

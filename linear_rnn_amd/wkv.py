@@ -39,6 +39,10 @@ RWKV7_DECAY_TOKEN = 1
 RWKV7_INPUT_PLAIN = 0
 RWKV7_INPUT_MIX = 1
 RWKV7_INPUT_NORM = 2
+RWKV7_ACT_SIGMOID = 0
+RWKV7_ACT_SILU = 1
+RWKV7_ACT_GELU = 2
+RWKV7_ACT_RELU2 = 3
 RWKV7_NOALLOC_SCRATCH_BYTES = 64 << 20
 _PER_THREAD = 2  # the handle hipStreamPerThread
 
@@ -49,6 +53,7 @@ EXPORTED = ("rwkv7_wkv_prefill", "rwkv7_wkv_step", "rwkv7_wkv_step_q", "rwkv7_wk
             "rwkv7_linattn_prefill", "rwkv7_linattn_step", "rwkv7_linattn_backward",
             "rwkv7_layernorm_forward", "rwkv7_layernorm_backward",
             "rwkv7_gscan_prefill", "rwkv7_gscan_step", "rwkv7_gscan_backward",
+            "rwkv7_glu_forward", "rwkv7_glu_backward",
             "rwkv7_wkv_strerror")
 
 _lib = None
@@ -110,6 +115,10 @@ def lib() -> ctypes.CDLL:
             L.rwkv7_gscan_step.argtypes = [vp] * 5 + [i64] * 3 + [ci, ci, vp]
             L.rwkv7_gscan_backward.restype = ci
             L.rwkv7_gscan_backward.argtypes = [vp] * 9 + [i64] * 3 + [ci, ci, vp]
+            L.rwkv7_glu_forward.restype = ci
+            L.rwkv7_glu_forward.argtypes = [vp] * 6 + [i64] * 3 + [ci, ci, vp]
+            L.rwkv7_glu_backward.restype = ci
+            L.rwkv7_glu_backward.argtypes = [vp] * 9 + [i64] * 3 + [ci, ci, vp]
             L.rwkv7_wkv_prefill_algo.restype = ci
             L.rwkv7_wkv_prefill_algo.argtypes = [i64] * 4 + [ci]
             L.rwkv7_wkv_strerror.restype = ctypes.c_char_p
@@ -704,4 +713,69 @@ def gscan_backward(x, log_w, dy, state_in=None, lens=None, dstate_out=None, inpu
     out = _on_stream_of(stream, x, make)
     rwkv7_gscan_backward(x, log_w, state_in, lens, dy, dstate_out, out["dx"], out["dlog_w"], out["dstate_in"], input,
                          stream)
+    return out
+
+
+# ---- gated linear unit
+
+def _glu_inputs(x, w_gate, w_up):
+    """The addresses of x and the weights, x's leading sizes, the rows, channels and hidden channels."""
+    if not isinstance(x, _T.Tensor) or x.dim() < 1:
+        raise ValueError("x must be a tensor with the channels in its last dimension")
+    if not isinstance(w_gate, _T.Tensor) or w_gate.dim() != 2:
+        raise ValueError("w_gate must be a [D, F] tensor")
+    shape = x.shape
+    D, F = shape[-1], w_gate.shape[1]
+    at = [_at(x, "x", shape, _T.inputs, x), _at(w_gate, "w_gate", (D, F), (x.dtype,), x),
+          _at(w_up, "w_up", (D, F), (x.dtype,), x)]
+    M = shape[0] if len(shape) == 2 else shape[:-1].numel()
+    return at, shape[:-1] + (F,), M, D, F
+
+
+def rwkv7_glu_forward(x, w_gate, w_up, h, gate, up, act=RWKV7_ACT_SILU, stream=None):
+    """h = act(x w_gate) * (x w_up). x [..., D], weights [D, F], h [..., F] in one dtype; gate and up (the two products)
+    like h, or both None; act one of RWKV7_ACT_*."""
+    at, wide, M, D, F = _glu_inputs(x, w_gate, w_up)
+    same = (x.dtype,)
+    at.append(_at(h, "h", wide, same, x))
+    at.append(None if gate is None else _at(gate, "gate", wide, same, x))
+    at.append(None if up is None else _at(up, "up", wide, same, x))
+    at += (M, D, F, _dtype_code(x), int(act))
+    _launch("rwkv7_glu_forward", at, x, stream)
+
+
+def rwkv7_glu_backward(x, w_gate, w_up, gate, up, dh, dx, dw_gate, dw_up, act=RWKV7_ACT_SILU, stream=None):
+    """Gradients of the gated linear unit from the forward's gate and up; dx like x or None, dw_gate and dw_up like the
+    weights or both None."""
+    at, wide, M, D, F = _glu_inputs(x, w_gate, w_up)
+    same = (x.dtype,)
+    for name, t in (("gate", gate), ("up", up), ("dh", dh)):
+        at.append(_at(t, name, wide, same, x))
+    at.append(None if dx is None else _at(dx, "dx", x.shape, same, x))
+    at.append(None if dw_gate is None else _at(dw_gate, "dw_gate", (D, F), same, x))
+    at.append(None if dw_up is None else _at(dw_up, "dw_up", (D, F), same, x))
+    at += (M, D, F, _dtype_code(x), int(act))
+    _launch("rwkv7_glu_backward", at, x, stream)
+
+
+def glu(x, w_gate, w_up, act=RWKV7_ACT_SILU, want_pre=False, stream=None):
+    """Allocate h (and, with want_pre, the pre-activations for the backward), run the forward, return (h, gate, up)."""
+    shape = _glu_inputs(x, w_gate, w_up)[1]
+
+    def make():
+        return [x.new_empty(shape) if n == 0 or want_pre else None for n in range(3)]
+
+    h, gate, up = _on_stream_of(stream, x, make)
+    rwkv7_glu_forward(x, w_gate, w_up, h, gate, up, act, stream)
+    return h, gate, up
+
+
+def glu_backward(x, w_gate, w_up, gate, up, dh, act=RWKV7_ACT_SILU, want_dx=True, want_dw=True, stream=None):
+    """Allocate the gradients, run the backward, return dict dx, dw_gate, dw_up (None where not wanted)."""
+    def make():
+        return {"dx": _T.empty_like(x) if want_dx else None, "dw_gate": _T.empty_like(w_gate) if want_dw else None,
+                "dw_up": _T.empty_like(w_up) if want_dw else None}
+
+    out = _on_stream_of(stream, x, make)
+    rwkv7_glu_backward(x, w_gate, w_up, gate, up, dh, out["dx"], out["dw_gate"], out["dw_up"], act, stream)
     return out
