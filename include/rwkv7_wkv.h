@@ -661,7 +661,8 @@ int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_i
  *   h       [M,F] output
  *   gate, up  [M,F] outputs g and u for the backward, or both NULL
  *   M, D, F rows (at most 2^28), channels (1 to 2^20), hidden channels (at most 2^20); the
- *           tiles of 256 by 128 of [M,F], of [M,D] and of [D,F] at most 2^22 each
+ *           tiles of 256 by 128 of [M,F], of [M,D] and of [D,F] at most 2^22 each, and
+ *           their elements 2^34
  *   act     RWKV7_ACT_*
  *
  * Sums are float32; each output is rounded once. A float32 call's products are formed from

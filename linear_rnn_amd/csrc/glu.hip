@@ -26,11 +26,24 @@ using namespace glu;
 
 // ---- operands in the form that the products take: bfloat16 pieces in planes of padded rows
 
-// [rows][cols] in the caller's type to NP planes [rows][ld] of pieces, zeros behind the columns. Eight columns a thread.
-struct StageParams {
+// A matrix [rows][cols] in the caller's type, to planes [rows][ld] of pieces, zeros behind the columns.
+struct StageJob {
   const void* src;
   uint16_t* dst;
   int64_t rows, cols, ld;
+};
+// dg and du from g, u and dh, to planes [rows][ld] of pieces.
+struct GradJob {
+  const void *gate, *up, *dh;
+  uint16_t *dg, *du;
+  int64_t rows, cols, ld;
+  int act;
+};
+// What a call prepares, in one launch: workgroups first[i] .. first[i + 1] - 1 do job i (the gradients are the last).
+struct StageParams {
+  StageJob job[3];
+  GradJob grad;
+  uint32_t first[5];
 };
 template <bool F32>
 __device__ __forceinline__ void load8(const void* src, int64_t at, int64_t left, bool wide, float (&v)[8]) {
@@ -63,24 +76,6 @@ __device__ __forceinline__ void store_pieces(uint16_t* dst, int64_t at, int64_t 
 #pragma unroll
   for (int p = 0; p < NP; ++p) *reinterpret_cast<bf16x8*>(dst + p * plane + at) = o.p[p];
 }
-template <bool F32>
-__global__ __launch_bounds__(256) void glu_stage_kernel(StageParams p) {
-  const int64_t per_row = p.ld / 8, plane = p.rows * p.ld;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.rows * per_row; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / per_row, c = i % per_row * 8;
-    float v[8];
-    load8<F32>(p.src, row * p.cols + c, p.cols - c, p.cols % 8 == 0, v);
-    store_pieces<F32 ? 3 : 1>(p.dst, row * p.ld + c, plane, v);
-  }
-}
-
-// dg and du, in pieces.
-struct GradParams {
-  const void *gate, *up, *dh;
-  uint16_t *dg, *du;  // planes [M][ld]
-  int64_t M, F, ld;
-  int act;
-};
 __device__ __forceinline__ void act_and_slope(float g, int act, float& a, float& s) {
   if (act == RWKV7_ACT_GELU) {
     const float c = 0.5f * (1.f + erff(g * 0.70710678f));
@@ -101,44 +96,79 @@ __device__ __forceinline__ void act_and_slope(float g, int act, float& a, float&
     }
   }
 }
+// Eight columns a thread.
 template <bool F32>
-__global__ __launch_bounds__(256) void glu_grad_kernel(GradParams p) {
-  const int64_t per_row = p.ld / 8, plane = p.M * p.ld;
-  const bool wide = p.F % 8 == 0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.M * per_row; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / per_row, c = i % per_row * 8, at = row * p.F + c;
-    float g[8], u[8], d[8], dg[8], du[8];
-    load8<F32>(p.gate, at, p.F - c, wide, g);
-    load8<F32>(p.up, at, p.F - c, wide, u);
-    load8<F32>(p.dh, at, p.F - c, wide, d);
+__device__ __forceinline__ void stage(const StageJob& j, int64_t i) {
+  const int64_t per_row = j.ld / 8, row = i / per_row, c = i % per_row * 8;
+  if (row >= j.rows) return;
+  float v[8];
+  load8<F32>(j.src, row * j.cols + c, j.cols - c, j.cols % 8 == 0, v);
+  store_pieces<F32 ? 3 : 1>(j.dst, row * j.ld + c, j.rows * j.ld, v);
+}
+template <bool F32>
+__device__ __forceinline__ void stage(const GradJob& j, int64_t i) {
+  const int64_t per_row = j.ld / 8, row = i / per_row, c = i % per_row * 8, at = row * j.cols + c;
+  if (row >= j.rows) return;
+  const bool wide = j.cols % 8 == 0;
+  float g[8], u[8], d[8], dg[8], du[8];
+  load8<F32>(j.gate, at, j.cols - c, wide, g);
+  load8<F32>(j.up, at, j.cols - c, wide, u);
+  load8<F32>(j.dh, at, j.cols - c, wide, d);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float a, s;
-      act_and_slope(g[e], p.act, a, s);
-      dg[e] = d[e] * u[e] * s;
-      du[e] = d[e] * a;
-    }
-    store_pieces<F32 ? 3 : 1>(p.dg, row * p.ld + c, plane, dg);
-    store_pieces<F32 ? 3 : 1>(p.du, row * p.ld + c, plane, du);
+  for (int e = 0; e < 8; ++e) {
+    float a, s;
+    act_and_slope(g[e], j.act, a, s);
+    dg[e] = d[e] * u[e] * s;
+    du[e] = d[e] * a;
   }
+  store_pieces<F32 ? 3 : 1>(j.dg, row * j.ld + c, j.rows * j.ld, dg);
+  store_pieces<F32 ? 3 : 1>(j.du, row * j.ld + c, j.rows * j.ld, du);
+}
+template <bool F32>
+__global__ __launch_bounds__(256) void glu_stage_kernel(StageParams p) {
+  const uint32_t block = blockIdx.x;
+  if (block >= p.first[3]) stage<F32>(p.grad, (int64_t)(block - p.first[3]) * 256 + threadIdx.x);
+  else if (block >= p.first[2]) stage<F32>(p.job[2], (int64_t)(block - p.first[2]) * 256 + threadIdx.x);
+  else if (block >= p.first[1]) stage<F32>(p.job[1], (int64_t)(block - p.first[1]) * 256 + threadIdx.x);
+  else stage<F32>(p.job[0], (int64_t)block * 256 + threadIdx.x);
 }
 
-// The sums of the parts, in their order.
-struct JoinParams {
-  const float* partial;  // [splits][products][n]
-  void* out[2];
+// The sums of the parts of a product, in their order: [splits][products][rows * cols] to one or two outputs, or, of
+// g and u, to h (and g and u themselves). Workgroups first .. of the grid's.
+struct JoinJob {
+  const float* partial;
+  void *out, *out2;  // the products; with `h` they may be null
+  void* h;
   int64_t n;
   int32_t splits, products;
   bool f32;
+  int act;
 };
-__global__ __launch_bounds__(256) void glu_join_kernel(JoinParams p) {
-  const int which = blockIdx.y;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.n; i += (int64_t)gridDim.x * 256) {
-    float s = 0.f;
-    for (int k = 0; k < p.splits; ++k) s += p.partial[((int64_t)k * p.products + which) * p.n + i];
-    if (p.f32) static_cast<float*>(p.out[which])[i] = s;
-    else static_cast<uint16_t*>(p.out[which])[i] = __builtin_bit_cast(uint16_t, (__bf16)s);
+struct JoinParams {
+  JoinJob job[2];
+  uint32_t second;  // first workgroup of the second job
+};
+__device__ __forceinline__ void put_out(void* out, bool f32, int64_t i, float v) {
+  if (f32) static_cast<float*>(out)[i] = v;
+  else static_cast<uint16_t*>(out)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
+}
+__device__ __forceinline__ void join(const JoinJob& j, int64_t i) {
+  if (i >= j.n) return;
+  float a = 0.f, b = 0.f;
+  const float* at = j.partial + i;
+#pragma unroll 4
+  for (int s = 0; s < j.splits; ++s) {
+    a += at[0];
+    if (j.products == 2) b += at[j.n];
+    at += j.products * j.n;
   }
+  if (j.h) put_out(j.h, j.f32, i, activation(a, j.act) * b);
+  if (j.out) put_out(j.out, j.f32, i, a);
+  if (j.out2) put_out(j.out2, j.f32, i, b);
+}
+__global__ __launch_bounds__(256) void glu_join_kernel(JoinParams p) {
+  if (blockIdx.x < p.second) join(p.job[0], (int64_t)blockIdx.x * 256 + threadIdx.x);
+  else join(p.job[1], (int64_t)(blockIdx.x - p.second) * 256 + threadIdx.x);
 }
 template <typename T>
 __global__ __launch_bounds__(256) void glu_zero_kernel(T* p, int64_t n) {
@@ -151,9 +181,51 @@ hipError_t start(const void* fn, dim3 blocks, int threads, int lds, const P& par
   void* args[] = {&p};
   return hipLaunchKernel(fn, blocks, dim3(threads), args, lds, stream);
 }
-uint32_t blocks_for(int64_t threads) {
-  const int64_t n = (threads + 255) / 256;
-  return (uint32_t)(n < 1 ? 1 : n < 16384 ? n : 16384);
+uint32_t blocks_for(int64_t threads) { return (uint32_t)((threads + 255) / 256); }
+
+// ---- tiles: which, and how many workgroups share a sum
+
+// Waves side by side over m and n, and 16 x 16 tiles of a wave.
+enum Shape { kLarge, kHalf, kSmall, kShapes };
+// Workgroups that share a compute unit, and the time of a step of 64 k with that many there, in us: from products whose
+// tiles fill the compute units evenly.
+struct ShapeInfo {
+  int bm, bn;
+  int per_cu;
+  float step_us, ends_us;
+};
+struct Plan {
+  Shape shape;
+  int splits;
+};
+
+int compute_units() {
+  int dev = 0, n = 0;
+  if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+      n <= 0)
+    n = 256;
+  return n;
+}
+
+// The shape and the number of parts of the sum with the least estimated time: rounds of workgroups, each its share of
+// the steps, and for parts the second kernel that adds them.
+Plan plan(const ShapeInfo (&shapes)[kShapes], int64_t M, int64_t N, int products, int64_t steps) {
+  const int cus = compute_units();
+  Plan best{kLarge, 1};
+  float least = 0.f;
+  for (int s = 0; s < kShapes; ++s) {
+    const ShapeInfo& f = shapes[s];
+    if (f.bm == 0) continue;
+    const int64_t tiles = (M + f.bm - 1) / f.bm * ((N + f.bn - 1) / f.bn) * products, slots = (int64_t)cus * f.per_cu;
+    for (int splits = 1; splits <= 32; ++splits) {
+      if (splits > 1 && (tiles * splits > 4 * slots || steps / splits < 4)) break;
+      const int64_t rounds = (tiles * splits + slots - 1) / slots, share = (steps + splits - 1) / splits;
+      float us = rounds * (share * f.step_us + f.ends_us);
+      if (splits > 1) us += 4.f + (splits * 8.f + 4.f) * products * M * N * 2e-7f;  // written, read at 5 TB/s
+      if ((s == 0 && splits == 1) || us < least) least = us, best = Plan{(Shape)s, splits};
+    }
+  }
+  return best;
 }
 
 // More than 64 KB of LDS has to be asked for on every device.
@@ -171,8 +243,22 @@ hipError_t gemm(GemmParams p, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const int per_tile = EPI == kGlu ? BN / 2 : BN;
   p.tiles_m = (p.M + BM - 1) / BM;
-  p.tiles_n = (p.N + per_tile - 1) / per_tile * (EPI == kProduct && p.out2 ? 2 : 1);
+  p.tiles_n = (p.N + per_tile - 1) / per_tile * (EPI == kProduct && p.two ? 2 : 1);
   return start(fn, dim3((uint32_t)p.tiles_m * p.tiles_n * p.splits), 64 * WM * WN, lds, p, stream);
+}
+constexpr ShapeInfo kForwardShapes[kShapes] = {{256, 128, 1, 1.8f, 4.f}, {128, 128, 1, 1.0f, 3.f}, {64, 128, 2, 1.0f, 3.f}};
+constexpr ShapeInfo kRowShapes[kShapes] = {{256, 256, 1, 1.8f, 4.f}, {128, 256, 1, 1.0f, 3.f}, {128, 128, 2, 1.0f, 3.f}};
+constexpr ShapeInfo kColumnShapes[kShapes] = {{256, 256, 1, 1.8f, 4.f}, {128, 256, 1, 1.0f, 3.f}, {128, 128, 2, 1.0f, 3.f}};
+hipError_t forward_gemm(const GemmParams& p, Shape s, hipStream_t stream) {
+  if (s == kLarge) return gemm<false, true, 2, 4, 8, 4, kGlu>(p, stream);
+  if (s == kHalf) return gemm<false, true, 2, 4, 4, 4, kGlu>(p, stream);
+  return gemm<false, true, 1, 4, 4, 4, kGlu>(p, stream);
+}
+template <bool COLS>
+hipError_t product_gemm(const GemmParams& p, Shape s, hipStream_t stream) {
+  if (s == kLarge) return gemm<COLS, COLS, 2, 4, 8, 4, kProduct>(p, stream);
+  if (s == kHalf) return gemm<COLS, COLS, 2, 4, 4, 4, kProduct>(p, stream);
+  return gemm<COLS, COLS, 2, 2, 4, 4, kProduct>(p, stream);
 }
 
 // ---- the workspace of a call, in parts
@@ -200,12 +286,30 @@ struct Matrix {
   const uint16_t* piece(char* ws, int i) const {
     return copied() ? reinterpret_cast<const uint16_t*>(ws + at) + i * rows * ld() : static_cast<const uint16_t*>(src);
   }
-  hipError_t stage(char* ws, hipStream_t stream) const {
-    if (!copied()) return hipSuccess;
-    const StageParams p{src, reinterpret_cast<uint16_t*>(ws + at), rows, cols, ld()};
+};
+
+// The launch that prepares a call's operands.
+struct Stage {
+  StageParams p{};
+  int jobs = 0;
+  uint32_t blocks = 0;
+  void add(const Matrix& m, char* ws) {
+    if (!m.copied()) return;
+    p.job[jobs] = StageJob{m.src, reinterpret_cast<uint16_t*>(ws + m.at), m.rows, m.cols, m.ld()};
+    p.first[jobs++] = blocks;
+    blocks += blocks_for(m.rows * m.ld() / 8);
+  }
+  hipError_t launch(const GradJob* grad, bool f32, hipStream_t stream) {
+    // a job that is not there has no workgroups: the one before it ends where the next begins
+    for (int i = jobs; i < 5; ++i) p.first[i] = blocks;
+    if (grad) {
+      p.grad = *grad;
+      blocks += blocks_for(grad->rows * grad->ld / 8);
+    }
+    if (blocks == 0) return hipSuccess;
     const void* fn = f32 ? reinterpret_cast<const void*>(&glu_stage_kernel<true>)
                          : reinterpret_cast<const void*>(&glu_stage_kernel<false>);
-    return start(fn, dim3(blocks_for(rows * ld() / 8)), 256, 0, p, stream);
+    return start(fn, dim3(blocks), 256, 0, p, stream);
   }
 };
 
@@ -215,22 +319,26 @@ int pairs(bool f32) { return f32 ? 6 : 1; }
 int first_of(bool f32, int s) { return f32 ? kPairs[s][0] : 0; }
 int second_of(bool f32, int s) { return f32 ? kPairs[s][1] : 0; }
 
+int64_t steps_of(int64_t K, int segments) { return (K + kBK - 1) / kBK * segments; }
+
 hipError_t forward(const GluCall& c) {
   Matrix x{c.x, c.M, c.D, c.f32}, wg{c.w_gate, c.D, c.F, c.f32}, wu{c.w_up, c.D, c.F, c.f32};
+  const Plan how = plan(kForwardShapes, c.M, c.F, 1, steps_of(c.D, pairs(c.f32)));
   Parts parts;
   for (Matrix* m : {&x, &wg, &wu}) m->place(parts);
+  const size_t partial_at = how.splits > 1 ? parts.add((size_t)how.splits * 2 * c.M * c.F * 4) : 0;
   std::unique_lock<std::mutex> lock(operators_mutex(), std::defer_lock);
   char* ws = nullptr;
   if (parts.bytes) {
     lock.lock();
-    void* p = nullptr;
-    const hipError_t e = device_workspace(c.stream, parts.bytes, &p, kWorkspaceOperators);
+    void* space = nullptr;
+    hipError_t e = device_workspace(c.stream, parts.bytes, &space, kWorkspaceOperators);
     if (e != hipSuccess) return e;
-    ws = static_cast<char*>(p);
-    for (Matrix* m : {&x, &wg, &wu}) {
-      const hipError_t e2 = m->stage(ws, c.stream);
-      if (e2 != hipSuccess) return e2;
-    }
+    ws = static_cast<char*>(space);
+    Stage stage;
+    for (Matrix* m : {&x, &wg, &wu}) stage.add(*m, ws);
+    e = stage.launch(nullptr, c.f32, c.stream);
+    if (e != hipSuccess) return e;
   }
   GemmParams p{};
   p.nseg = pairs(c.f32);
@@ -239,9 +347,15 @@ hipError_t forward(const GluCall& c) {
     p.b[s] = wg.piece(ws, second_of(c.f32, s));
     p.b2[s] = wu.piece(ws, second_of(c.f32, s));
   }
-  p.lda = x.ld(), p.ldb = wg.ld(), p.M = (int32_t)c.M, p.N = (int32_t)c.F, p.K = (int32_t)c.D, p.splits = 1;
+  p.lda = x.ld(), p.ldb = wg.ld(), p.M = (int32_t)c.M, p.N = (int32_t)c.F, p.K = (int32_t)c.D, p.splits = how.splits;
   p.out = c.h, p.gate = c.gate, p.up = c.up, p.f32 = c.f32, p.act = c.act;
-  return gemm<false, true, 2, 4, 8, 4, kGlu>(p, c.stream);
+  p.partial = reinterpret_cast<float*>(ws + partial_at);
+  const hipError_t e = forward_gemm(p, how.shape, c.stream);
+  if (e != hipSuccess || how.splits == 1) return e;
+  JoinParams j{};
+  j.job[0] = JoinJob{p.partial, c.gate, c.up, c.h, c.M * c.F, how.splits, 2, c.f32, c.act};
+  j.second = blocks_for(j.job[0].n);
+  return start(reinterpret_cast<const void*>(&glu_join_kernel), dim3(j.second), 256, 0, j, c.stream);
 }
 
 hipError_t backward(const GluCall& c) {
@@ -249,60 +363,69 @@ hipError_t backward(const GluCall& c) {
   if (!dx && !dw) return hipSuccess;
   Matrix x{c.x, c.M, c.D, c.f32}, wg{c.w_gate, c.D, c.F, c.f32}, wu{c.w_up, c.D, c.F, c.f32};
   const int np = c.f32 ? 3 : 1;
-  const int64_t ldf = padded(c.F);
+  const int64_t ldf = padded(c.F), plane = c.M * ldf;
+  const Plan for_x = plan(kRowShapes, c.M, c.D, 1, steps_of(ldf, 2 * pairs(c.f32)));
+  const Plan for_w = plan(kColumnShapes, c.D, c.F, 2, steps_of(c.M, pairs(c.f32)));
   Parts parts;
   if (dw) x.place(parts);
   if (dx) wg.place(parts), wu.place(parts);
-  const size_t dg_at = parts.add((size_t)np * c.M * ldf * 2), du_at = parts.add((size_t)np * c.M * ldf * 2);
-  // parts of the weights' gradients, where their tiles are too few for the compute units
-  const int64_t wtiles = (c.D + 255) / 256 * ((c.F + 255) / 256) * 2, steps = (c.M + kBK - 1) / kBK * pairs(c.f32);
-  int64_t splits = 256 / wtiles;
-  splits = splits < steps / 8 ? splits : steps / 8;
-  splits = splits < 1 ? 1 : splits;
-  const size_t partial_at = dw && splits > 1 ? parts.add((size_t)splits * 2 * c.D * c.F * 4) : 0;
+  const size_t dg_at = parts.add((size_t)np * plane * 2), du_at = parts.add((size_t)np * plane * 2);
+  const size_t px_at = dx && for_x.splits > 1 ? parts.add((size_t)for_x.splits * c.M * c.D * 4) : 0;
+  const size_t pw_at = dw && for_w.splits > 1 ? parts.add((size_t)for_w.splits * 2 * c.D * c.F * 4) : 0;
 
   std::lock_guard<std::mutex> lock(operators_mutex());
   void* space = nullptr;
   hipError_t e = device_workspace(c.stream, parts.bytes, &space, kWorkspaceOperators);
   if (e != hipSuccess) return e;
   char* ws = static_cast<char*>(space);
-  if (dw && (e = x.stage(ws, c.stream)) != hipSuccess) return e;
-  if (dx && ((e = wg.stage(ws, c.stream)) != hipSuccess || (e = wu.stage(ws, c.stream)) != hipSuccess)) return e;
   uint16_t *dg = reinterpret_cast<uint16_t*>(ws + dg_at), *du = reinterpret_cast<uint16_t*>(ws + du_at);
-  const int64_t plane = c.M * ldf;
-  const GradParams gp{c.gate, c.up, c.dh, dg, du, c.M, c.F, ldf, c.act};
-  e = start(c.f32 ? reinterpret_cast<const void*>(&glu_grad_kernel<true>) : reinterpret_cast<const void*>(&glu_grad_kernel<false>),
-            dim3(blocks_for(plane / 8)), 256, 0, gp, c.stream);
+  Stage stage;
+  if (dw) stage.add(x, ws);
+  if (dx) stage.add(wg, ws), stage.add(wu, ws);
+  const GradJob grad{c.gate, c.up, c.dh, dg, du, c.M, c.F, ldf, c.act};
+  e = stage.launch(&grad, c.f32, c.stream);
   if (e != hipSuccess) return e;
+
+  JoinParams j{};
+  int joins = 0;
+  uint32_t blocks = 0;
   if (dx) {
     GemmParams p{};
     for (int s = 0; s < pairs(c.f32); ++s) {
-      const int i = first_of(c.f32, s), j = second_of(c.f32, s);
-      p.a[2 * s] = dg + i * plane, p.b[2 * s] = wg.piece(ws, j);
-      p.a[2 * s + 1] = du + i * plane, p.b[2 * s + 1] = wu.piece(ws, j);
+      const int f = first_of(c.f32, s), t = second_of(c.f32, s);
+      p.a[2 * s] = dg + f * plane, p.b[2 * s] = wg.piece(ws, t);
+      p.a[2 * s + 1] = du + f * plane, p.b[2 * s + 1] = wu.piece(ws, t);
     }
     p.nseg = 2 * pairs(c.f32);
-    p.lda = ldf, p.ldb = ldf, p.M = (int32_t)c.M, p.N = (int32_t)c.D, p.K = (int32_t)ldf, p.splits = 1;
-    p.out = c.dx, p.f32 = c.f32;
-    e = gemm<false, false, 2, 4, 8, 4, kProduct>(p, c.stream);
+    p.lda = ldf, p.ldb = ldf, p.M = (int32_t)c.M, p.N = (int32_t)c.D, p.K = (int32_t)ldf, p.splits = for_x.splits;
+    p.out = c.dx, p.f32 = c.f32, p.partial = reinterpret_cast<float*>(ws + px_at);
+    e = product_gemm<false>(p, for_x.shape, c.stream);
     if (e != hipSuccess) return e;
+    if (p.splits > 1) {
+      j.job[joins++] = JoinJob{p.partial, c.dx, nullptr, nullptr, c.M * c.D, p.splits, 1, c.f32, 0};
+      blocks += blocks_for(c.M * c.D);
+    }
   }
+  j.second = blocks;
   if (dw) {
     GemmParams p{};
     p.nseg = pairs(c.f32);
     for (int s = 0; s < p.nseg; ++s) {
-      const int i = first_of(c.f32, s), j = second_of(c.f32, s);
-      p.a[s] = x.piece(ws, i), p.b[s] = dg + j * plane, p.b2[s] = du + j * plane;
+      const int f = first_of(c.f32, s), t = second_of(c.f32, s);
+      p.a[s] = x.piece(ws, f), p.b[s] = dg + t * plane, p.b2[s] = du + t * plane;
     }
-    p.lda = x.ld(), p.ldb = ldf, p.M = (int32_t)c.D, p.N = (int32_t)c.F, p.K = (int32_t)c.M, p.splits = (int32_t)splits;
-    p.out = c.dw_gate, p.out2 = c.dw_up, p.f32 = c.f32;
-    p.partial = reinterpret_cast<float*>(ws + partial_at);
-    e = gemm<true, true, 2, 4, 8, 4, kProduct>(p, c.stream);
-    if (e != hipSuccess || splits == 1) return e;
-    const JoinParams jp{p.partial, {c.dw_gate, c.dw_up}, c.D * c.F, (int32_t)splits, 2, c.f32};
-    e = start(reinterpret_cast<const void*>(&glu_join_kernel), dim3(blocks_for(c.D * c.F), 2), 256, 0, jp, c.stream);
+    p.lda = x.ld(), p.ldb = ldf, p.M = (int32_t)c.D, p.N = (int32_t)c.F, p.K = (int32_t)c.M, p.splits = for_w.splits;
+    p.out = c.dw_gate, p.out2 = c.dw_up, p.two = true, p.f32 = c.f32, p.partial = reinterpret_cast<float*>(ws + pw_at);
+    e = product_gemm<true>(p, for_w.shape, c.stream);
+    if (e != hipSuccess) return e;
+    if (p.splits > 1) {
+      j.job[joins++] = JoinJob{p.partial, c.dw_gate, c.dw_up, nullptr, c.D * c.F, p.splits, 2, c.f32, 0};
+      if (joins == 1) j.second = blocks_for(c.D * c.F);  // the only job
+      blocks += blocks_for(c.D * c.F);
+    }
   }
-  return e;
+  if (joins == 0) return e;
+  return start(reinterpret_cast<const void*>(&glu_join_kernel), dim3(blocks), 256, 0, j, c.stream);
 }
 
 }  // namespace
@@ -314,7 +437,8 @@ hipError_t launch_glu_zero(void* p, int64_t n, bool f32, hipStream_t stream) {
   void* args[] = {&p, &n};
   const void* fn = f32 ? reinterpret_cast<const void*>(&glu_zero_kernel<uint32_t>)
                        : reinterpret_cast<const void*>(&glu_zero_kernel<uint16_t>);
-  return hipLaunchKernel(fn, dim3(blocks_for(n)), dim3(256), args, 0, stream);
+  const uint32_t blocks = n < (int64_t(1) << 22) ? blocks_for(n) : 1 << 14;
+  return hipLaunchKernel(fn, dim3(blocks), dim3(256), args, 0, stream);
 }
 
 }  // namespace rwkv7

@@ -20,12 +20,13 @@ int check_sizes(int64_t M, int64_t D, int64_t F, int dtype, int act, Sizes* out)
   if (dtype != RWKV7_DTYPE_F32 && dtype != RWKV7_DTYPE_BF16) return RWKV7_ERR_DTYPE;
   if (act != RWKV7_ACT_SIGMOID && act != RWKV7_ACT_SILU && act != RWKV7_ACT_GELU && act != RWKV7_ACT_RELU2)
     return RWKV7_ERR_MODE;
-  // row numbers and the offsets inside a tile are 32-bit, and the tiles fit a grid
-  constexpr int64_t kMost = int64_t(1) << 20;
+  // row numbers and the offsets inside a tile are 32-bit, and the tiles and threads of 8 elements fit a grid
+  constexpr int64_t kMost = int64_t(1) << 20, kElems = int64_t(1) << 34;
   if (M < 0 || M > (int64_t(1) << 28) || D < 1 || D > kMost || F < 0 || F > kMost) return RWKV7_ERR_SHAPE;
   if (((M + 255) / 256) * ((F + 127) / 128) > (int64_t(1) << 22) || ((M + 255) / 256) * ((D + 127) / 128) > (int64_t(1) << 22) ||
       ((D + 255) / 256) * ((F + 127) / 128) > (int64_t(1) << 22))
     return RWKV7_ERR_SHAPE;
+  if (M * D > kElems || M * F > kElems || D * F > kElems) return RWKV7_ERR_SHAPE;
   const int64_t e = dtype == RWKV7_DTYPE_BF16 ? 2 : 4;
   out->x = M * D * e, out->w = D * F * e, out->h = M * F * e;
   return RWKV7_OK;

@@ -41,9 +41,10 @@ struct GemmParams {
   int32_t splits;                // workgroups that share the sum over segments and k
   void* out;                     // [M, N]
   void* out2;                    // of the second product
+  bool two;                      // kProduct: there is a second one
   void* gate;                    // pre-activations, may be null
   void* up;
-  float* partial;                // [splits][products][M][N], with splits > 1
+  float* partial;                // [splits][products][M][N] with splits > 1, in place of the outputs
   bool f32;                      // element type of the outputs
   int act;
 };
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
   const uint32_t high = p.tiles_m - group * 8 < 8 ? p.tiles_m - group * 8 : 8;
   const uint32_t tm0 = group * 8 + in % high;
   uint32_t tn0 = in / high;
-  const bool second = EPI == kProduct && p.out2 && tn0 >= (uint32_t)p.tiles_n / 2;
+  const bool second = EPI == kProduct && p.two && tn0 >= (uint32_t)p.tiles_n / 2;
   if (second) tn0 -= p.tiles_n / 2;
   const int64_t m0 = (int64_t)tm0 * BM;
   const int n0 = tn0 * BNp;
@@ -211,7 +212,15 @@ __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
   for (int i = 0; i < TM; ++i) {
     const int64_t m = m0 + wm * (TM * 16) + i * 16 + li;
     if (m >= p.M) continue;
-    if constexpr (EPI == kGlu) {
+    if (EPI == kGlu && p.splits > 1) {
+      float* out = p.partial + (int64_t)split * 2 * p.M * p.N;
+#pragma unroll
+      for (int j = 0; j < TN / 2; ++j) {
+        const int n = n0 + wn * (TN / 2 * 16) + j * 16 + 4 * q;
+        store4(out, true, p.N, m, n, p.N, acc[i][j]);
+        store4(out + (int64_t)p.M * p.N, true, p.N, m, n, p.N, acc[i][j + TN / 2]);
+      }
+    } else if constexpr (EPI == kGlu) {
 #pragma unroll
       for (int j = 0; j < TN / 2; ++j) {
         const int n = n0 + wn * (TN / 2 * 16) + j * 16 + 4 * q;
@@ -229,7 +238,7 @@ __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
       void* out = second ? p.out2 : p.out;
       bool f32 = p.f32;
       if (p.splits > 1) {
-        const int64_t number = split * (p.out2 ? 2 : 1) + (second ? 1 : 0);
+        const int64_t number = split * (p.two ? 2 : 1) + (second ? 1 : 0);
         out = p.partial + number * p.M * p.N;
         f32 = true;
       }

@@ -71,7 +71,8 @@ def test_bad_kinds_and_sizes(L, call):
     assert "activation" in wkv.rwkv7_wkv_strerror(E_MODE)
     for bad in (dict(M=-1), dict(D=0), dict(D=-1), dict(F=-1), dict(M=(1 << 28) + 1), dict(D=(1 << 20) + 1),
                 dict(F=(1 << 20) + 1), dict(M=1 << 28, F=1024), dict(M=1 << 28, D=1024), dict(D=1 << 20, F=1 << 20),
-                dict(M=1 << 62)):
+                dict(M=1 << 62),
+                dict(M=1 << 27, D=129)):
         assert call(L, **bad) == E_SHAPE, bad
 
 
