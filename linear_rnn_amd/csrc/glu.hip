@@ -17,6 +17,7 @@
 #include "rwkv7_wkv.h"
 #include "wkv7_internal.hpp"
 
+#include "glu_few.hpp"
 #include "glu_gemm.hpp"
 
 namespace rwkv7 {
@@ -45,17 +46,20 @@ struct StageParams {
   GradJob grad;
   uint32_t first[5];
 };
+// Rows need not begin on 16 bytes here.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 template <bool F32>
-__device__ __forceinline__ void load8(const void* src, int64_t at, int64_t left, bool wide, float (&v)[8]) {
-  if (wide) {
+__device__ __forceinline__ void load8(const void* src, int64_t at, int64_t left, float (&v)[8]) {
+  if (left >= 8) {
     if constexpr (F32) {
-      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
-      const float4 a = f[0], b = f[1];
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+      const f32x4_any* f = reinterpret_cast<const f32x4_any*>(static_cast<const float*>(src) + at);
+      const f32x4_any a = f[0], b = f[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
     } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + at);
-      v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-      v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+      const u32x4_any u = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(src) + at);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(u[i]), v[2 * i + 1] = bf16_hi(u[i]);
     }
   } else {
 #pragma unroll
@@ -102,18 +106,17 @@ __device__ __forceinline__ void stage(const StageJob& j, int64_t i) {
   const int64_t per_row = j.ld / 8, row = i / per_row, c = i % per_row * 8;
   if (row >= j.rows) return;
   float v[8];
-  load8<F32>(j.src, row * j.cols + c, j.cols - c, j.cols % 8 == 0, v);
+  load8<F32>(j.src, row * j.cols + c, j.cols - c, v);
   store_pieces<F32 ? 3 : 1>(j.dst, row * j.ld + c, j.rows * j.ld, v);
 }
 template <bool F32>
 __device__ __forceinline__ void stage(const GradJob& j, int64_t i) {
   const int64_t per_row = j.ld / 8, row = i / per_row, c = i % per_row * 8, at = row * j.cols + c;
   if (row >= j.rows) return;
-  const bool wide = j.cols % 8 == 0;
   float g[8], u[8], d[8], dg[8], du[8];
-  load8<F32>(j.gate, at, j.cols - c, wide, g);
-  load8<F32>(j.up, at, j.cols - c, wide, u);
-  load8<F32>(j.dh, at, j.cols - c, wide, d);
+  load8<F32>(j.gate, at, j.cols - c, g);
+  load8<F32>(j.up, at, j.cols - c, u);
+  load8<F32>(j.dh, at, j.cols - c, d);
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     float a, s;
@@ -148,23 +151,36 @@ struct JoinParams {
   JoinJob job[2];
   uint32_t second;  // first workgroup of the second job
 };
-__device__ __forceinline__ void put_out(void* out, bool f32, int64_t i, float v) {
-  if (f32) static_cast<float*>(out)[i] = v;
-  else static_cast<uint16_t*>(out)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
-}
+// Four elements a thread.
 __device__ __forceinline__ void join(const JoinJob& j, int64_t i) {
+  i *= 4;
   if (i >= j.n) return;
-  float a = 0.f, b = 0.f;
+  const int n = j.n - i < 4 ? (int)(j.n - i) : 4;
+  f32x4 a = linattn::zero4(), b = linattn::zero4();
   const float* at = j.partial + i;
+  auto add = [&](f32x4& to, const float* from) {
+    if (n == 4) {
+      const f32x4_any x = *reinterpret_cast<const f32x4_any*>(from);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) to[e] += x[e];
+    } else {
+      for (int e = 0; e < n; ++e) to[e] += from[e];
+    }
+  };
 #pragma unroll 4
   for (int s = 0; s < j.splits; ++s) {
-    a += at[0];
-    if (j.products == 2) b += at[j.n];
+    add(a, at);
+    if (j.products == 2) add(b, at + j.n);
     at += j.products * j.n;
   }
-  if (j.h) put_out(j.h, j.f32, i, activation(a, j.act) * b);
-  if (j.out) put_out(j.out, j.f32, i, a);
-  if (j.out2) put_out(j.out2, j.f32, i, b);
+  if (j.h) {
+    f32x4 h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = activation(a[e], j.act) * b[e];
+    store4(j.h, j.f32, i, n, h);
+  }
+  if (j.out) store4(j.out, j.f32, i, n, a);
+  if (j.out2) store4(j.out2, j.f32, i, n, b);
 }
 __global__ __launch_bounds__(256) void glu_join_kernel(JoinParams p) {
   if (blockIdx.x < p.second) join(p.job[0], (int64_t)blockIdx.x * 256 + threadIdx.x);
@@ -229,10 +245,10 @@ Plan plan(const ShapeInfo (&shapes)[kShapes], int64_t M, int64_t N, int products
 }
 
 // More than 64 KB of LDS has to be asked for on every device.
-template <bool AC, bool BC, int WM, int WN, int TM, int TN, int EPI>
+template <bool AC, bool BC, int WM, int WN, int TM, int TN, int NB, int EPI>
 hipError_t gemm(GemmParams p, hipStream_t stream) {
-  constexpr int BM = WM * TM * 16, BN = WN * TN * 16, lds = 2 * (BM + BN) * kBK * 2;
-  const void* fn = reinterpret_cast<const void*>(&glu_gemm_kernel<AC, BC, WM, WN, TM, TN, EPI>);
+  constexpr int BM = WM * TM * 16, BN = WN * TN * 16, lds = NB * (BM + BN) * kBK * 2;
+  const void* fn = reinterpret_cast<const void*>(&glu_gemm_kernel<AC, BC, WM, WN, TM, TN, NB, EPI>);
   static std::atomic<uint64_t> granted{0};
   int dev = 0;
   hipError_t e = hipGetDevice(&dev);
@@ -250,15 +266,15 @@ constexpr ShapeInfo kForwardShapes[kShapes] = {{256, 128, 1, 1.8f, 4.f}, {128, 1
 constexpr ShapeInfo kRowShapes[kShapes] = {{256, 256, 1, 1.8f, 4.f}, {128, 256, 1, 1.0f, 3.f}, {128, 128, 2, 1.0f, 3.f}};
 constexpr ShapeInfo kColumnShapes[kShapes] = {{256, 256, 1, 1.8f, 4.f}, {128, 256, 1, 1.0f, 3.f}, {128, 128, 2, 1.0f, 3.f}};
 hipError_t forward_gemm(const GemmParams& p, Shape s, hipStream_t stream) {
-  if (s == kLarge) return gemm<false, true, 2, 4, 8, 4, kGlu>(p, stream);
-  if (s == kHalf) return gemm<false, true, 2, 4, 4, 4, kGlu>(p, stream);
-  return gemm<false, true, 1, 4, 4, 4, kGlu>(p, stream);
+  if (s == kLarge) return gemm<false, true, 2, 4, 8, 4, 2, kGlu>(p, stream);
+  if (s == kHalf) return gemm<false, true, 2, 4, 4, 4, 3, kGlu>(p, stream);
+  return gemm<false, true, 1, 4, 4, 4, 2, kGlu>(p, stream);
 }
 template <bool COLS>
 hipError_t product_gemm(const GemmParams& p, Shape s, hipStream_t stream) {
-  if (s == kLarge) return gemm<COLS, COLS, 2, 4, 8, 4, kProduct>(p, stream);
-  if (s == kHalf) return gemm<COLS, COLS, 2, 4, 4, 4, kProduct>(p, stream);
-  return gemm<COLS, COLS, 2, 2, 4, 4, kProduct>(p, stream);
+  if (s == kLarge) return gemm<COLS, COLS, 2, 4, 8, 4, 2, kProduct>(p, stream);
+  if (s == kHalf) return gemm<COLS, COLS, 2, 4, 4, 4, 3, kProduct>(p, stream);
+  return gemm<COLS, COLS, 2, 2, 4, 4, 2, kProduct>(p, stream);
 }
 
 // ---- the workspace of a call, in parts
@@ -270,7 +286,9 @@ struct Parts {
     return at;
   }
 };
-int64_t padded(int64_t n) { return (n + 7) / 8 * 8; }
+int64_t whole(int64_t n, int64_t of) { return (n + of - 1) / of * of; }
+// Elements between rows of a copy: whole 128-byte lines, where that adds little.
+int64_t padded(int64_t cols) { return whole(cols, cols >= 256 ? 64 : 8); }
 
 // A matrix as an operand: the caller's own where it is bfloat16 with rows of whole 16 bytes, else a copy.
 struct Matrix {
@@ -279,7 +297,7 @@ struct Matrix {
   bool f32;
   size_t at = 0;
   bool copied() const { return f32 || cols % 8 != 0; }
-  int64_t ld() const { return padded(cols); }
+  int64_t ld() const { return copied() ? padded(cols) : cols; }
   void place(Parts& parts) {
     if (copied()) at = parts.add((size_t)rows * ld() * 2 * (f32 ? 3 : 1));
   }
@@ -321,7 +339,18 @@ int second_of(bool f32, int s) { return f32 ? kPairs[s][1] : 0; }
 
 int64_t steps_of(int64_t K, int segments) { return (K + kBK - 1) / kBK * segments; }
 
+// Few rows, whose weights are read once by a kernel of their own. It wants rows of whole 16 bytes.
+bool few_rows(const GluCall& c) { return c.M <= (c.f32 ? 128 : 32) && c.D % 8 == 0 && c.F % 8 == 0; }
+template <bool F32>
+hipError_t forward_few(const GluCall& c) {
+  const FewParams p{c.x, c.w_gate, c.w_up, c.h, c.gate, c.up, (int32_t)c.M, (int32_t)c.D, (int32_t)c.F, c.act};
+  const void* fn = c.M <= 16 ? reinterpret_cast<const void*>(&glu_few_kernel<F32, 1>)
+                           : reinterpret_cast<const void*>(&glu_few_kernel<F32, 2>);
+  return start(fn, dim3((uint32_t)((c.F + kFewCols - 1) / kFewCols), (uint32_t)((c.M + 31) / 32)), 64 * kFewWaves, 0, p, c.stream);
+}
+
 hipError_t forward(const GluCall& c) {
+  if (few_rows(c)) return c.f32 ? forward_few<true>(c) : forward_few<false>(c);
   Matrix x{c.x, c.M, c.D, c.f32}, wg{c.w_gate, c.D, c.F, c.f32}, wu{c.w_up, c.D, c.F, c.f32};
   const Plan how = plan(kForwardShapes, c.M, c.F, 1, steps_of(c.D, pairs(c.f32)));
   Parts parts;
@@ -354,7 +383,7 @@ hipError_t forward(const GluCall& c) {
   if (e != hipSuccess || how.splits == 1) return e;
   JoinParams j{};
   j.job[0] = JoinJob{p.partial, c.gate, c.up, c.h, c.M * c.F, how.splits, 2, c.f32, c.act};
-  j.second = blocks_for(j.job[0].n);
+  j.second = blocks_for((j.job[0].n + 3) / 4);
   return start(reinterpret_cast<const void*>(&glu_join_kernel), dim3(j.second), 256, 0, j, c.stream);
 }
 
@@ -364,7 +393,8 @@ hipError_t backward(const GluCall& c) {
   Matrix x{c.x, c.M, c.D, c.f32}, wg{c.w_gate, c.D, c.F, c.f32}, wu{c.w_up, c.D, c.F, c.f32};
   const int np = c.f32 ? 3 : 1;
   const int64_t ldf = padded(c.F), plane = c.M * ldf;
-  const Plan for_x = plan(kRowShapes, c.M, c.D, 1, steps_of(ldf, 2 * pairs(c.f32)));
+  const int64_t sum_f = whole(c.F, 8);  // with zeros in the copies' columns behind F
+  const Plan for_x = plan(kRowShapes, c.M, c.D, 1, steps_of(sum_f, 2 * pairs(c.f32)));
   const Plan for_w = plan(kColumnShapes, c.D, c.F, 2, steps_of(c.M, pairs(c.f32)));
   Parts parts;
   if (dw) x.place(parts);
@@ -397,13 +427,13 @@ hipError_t backward(const GluCall& c) {
       p.a[2 * s + 1] = du + f * plane, p.b[2 * s + 1] = wu.piece(ws, t);
     }
     p.nseg = 2 * pairs(c.f32);
-    p.lda = ldf, p.ldb = ldf, p.M = (int32_t)c.M, p.N = (int32_t)c.D, p.K = (int32_t)ldf, p.splits = for_x.splits;
+    p.lda = ldf, p.ldb = wg.ld(), p.M = (int32_t)c.M, p.N = (int32_t)c.D, p.K = (int32_t)sum_f, p.splits = for_x.splits;
     p.out = c.dx, p.f32 = c.f32, p.partial = reinterpret_cast<float*>(ws + px_at);
     e = product_gemm<false>(p, for_x.shape, c.stream);
     if (e != hipSuccess) return e;
     if (p.splits > 1) {
       j.job[joins++] = JoinJob{p.partial, c.dx, nullptr, nullptr, c.M * c.D, p.splits, 1, c.f32, 0};
-      blocks += blocks_for(c.M * c.D);
+      blocks += blocks_for((c.M * c.D + 3) / 4);
     }
   }
   j.second = blocks;
@@ -420,8 +450,8 @@ hipError_t backward(const GluCall& c) {
     if (e != hipSuccess) return e;
     if (p.splits > 1) {
       j.job[joins++] = JoinJob{p.partial, c.dw_gate, c.dw_up, nullptr, c.D * c.F, p.splits, 2, c.f32, 0};
-      if (joins == 1) j.second = blocks_for(c.D * c.F);  // the only job
-      blocks += blocks_for(c.D * c.F);
+      if (joins == 1) j.second = blocks_for((c.D * c.F + 3) / 4);  // the only job
+      blocks += blocks_for((c.D * c.F + 3) / 4);
     }
   }
   if (joins == 0) return e;

@@ -7,7 +7,7 @@
 // operands, or the two products of an input's gradient.
 //
 // A workgroup takes BM x BN of the output, a wave TM x TN tiles of 16 x 16, 64 of k at a time. Both operands' next
-// 64 of k come to LDS by direct loads (no registers) while the present ones are multiplied. LDS holds
+// NB - 1 steps come to LDS by direct loads (no registers) while the present one is multiplied. LDS holds
 //  - rows: [row][64 k], 128 bytes a row, the 16-byte pieces of a row exchanged by row & 7, so that 16 lanes reading one
 //    piece of 16 rows meet every bank as often;
 //  - columns: blocks [64 k][128 columns], 256 bytes a row, runs of 16 columns exchanged by the bits of k that the
@@ -25,6 +25,9 @@ using linattn::bf16x4;
 using linattn::bf16x8;
 using linattn::f32x4;
 using linattn::u32x4;
+
+// Four floats that need not begin on 16 bytes.
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kBK = 64;
 constexpr int kMaxSegs = 12;
@@ -75,20 +78,18 @@ struct Loader {
     }
   }
   // The tile's step k0 .. k0 + 63 of an operand; `first`: its first row or column, `n` how many the operand has.
-  __device__ __forceinline__ void fetch(const uint16_t* p, int64_t ld, int64_t first, int64_t n, int k0, int K, uint32_t to,
-                                        int wave) const {
+  __device__ __forceinline__ static u32x4 source(const uint16_t* p, int64_t ld, int64_t first, int64_t n, int k0, int K) {
     if constexpr (COLS) {
       const int64_t left = (K - k0 < kBK ? K - k0 : kBK) * ld - first;
-      const u32x4 d = linattn::descriptor(p + (int64_t)k0 * ld + first, (uint32_t)(left * 2));
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) linattn::to_lds16(d, off[i], to + (i * NW + wave) * 1024);
+      return linattn::descriptor(p + (int64_t)k0 * ld + first, (uint32_t)(left * 2));
     } else {
       const int64_t rows = n - first < R ? n - first : R;
-      const u32x4 d = linattn::descriptor(p + first * ld + k0, (uint32_t)((rows * ld - k0) * 2));
-      const bool inside = piece8 < K - k0;
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i) linattn::to_lds16(d, inside ? off[i] : kNowhere, to + (i * NW + wave) * 1024);
+      return linattn::descriptor(p + first * ld + k0, (uint32_t)((rows * ld - k0) * 2));
     }
+  }
+  __device__ __forceinline__ void load(int i, u32x4 from, int k0, int K, uint32_t to, int wave) const {
+    const uint32_t o = COLS || piece8 < K - k0 ? off[i] : kNowhere;
+    linattn::to_lds16(from, o, to + (i * NW + wave) * 1024);
   }
 };
 // Operand of 16 rows or columns from `first` on, k = 32 h + 8 q .. + 7.
@@ -115,12 +116,11 @@ __device__ __forceinline__ float activation(float g, int act) {
   return sigmoid(g);
 }
 
-// Four consecutive n of row m.
-__device__ __forceinline__ void store4(void* out, bool f32, int64_t ld, int64_t m, int n, int N, f32x4 x) {
-  const int64_t at = m * ld + n;
-  if (n + 3 < N && (ld & 3) == 0) {
+// The first `count` of four elements from `at` on, together where they begin on a multiple of four.
+__device__ __forceinline__ void store4(void* out, bool f32, int64_t at, int count, f32x4 x) {
+  if (count >= 4 && (at & 3) == 0) {
     if (f32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(out) + at) = make_float4(x[0], x[1], x[2], x[3]);
+      *reinterpret_cast<f32x4_any*>(static_cast<float*>(out) + at) = x;
     } else {
       const bf16x4 o = __builtin_convertvector(x, bf16x4);
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = __builtin_bit_cast(uint2, o);
@@ -128,14 +128,14 @@ __device__ __forceinline__ void store4(void* out, bool f32, int64_t ld, int64_t 
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (n + i < N) {
+      if (i < count) {
         if (f32) static_cast<float*>(out)[at + i] = x[i];
         else static_cast<uint16_t*>(out)[at + i] = __builtin_bit_cast(uint16_t, (__bf16)x[i]);
       }
   }
 }
 
-template <bool ACOLS, bool BCOLS, int WM, int WN, int TM, int TN, int EPI>
+template <bool ACOLS, bool BCOLS, int WM, int WN, int TM, int TN, int NB, int EPI>
 __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
   constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
   constexpr int kProducts = EPI == kGlu ? 2 : 1;  // in one tile
@@ -166,15 +166,33 @@ __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
   Loader<BCOLS, BNp, NW> lb;
   la.init(p.lda, wave, lane);
   lb.init(p.ldb, wave, lane);
-  int seg = s0 / ksteps, kt = s0 % ksteps;  // of the step to be fetched
-  auto fetch = [&](int buf) {
-    const uint32_t to = lds0 + buf * kBuf;
-    const int k0 = kt * kBK;
-    const uint16_t* b = second ? p.b2[seg] : p.b[seg];
-    la.fetch(p.a[seg], p.lda, m0, p.M, k0, p.K, to, wave);
-    lb.fetch(b, p.ldb, n0, p.N, k0, p.K, to + kA, wave);
-    if constexpr (EPI == kGlu) lb.fetch(p.b2[seg], p.ldb, n0, p.N, k0, p.K, to + kA + kB, wave);
-    if (++kt == ksteps) kt = 0, ++seg;
+  int seg = s0 / ksteps, kt = s0 % ksteps;  // of the step to be loaded
+  constexpr int kLoadsA = Loader<ACOLS, BM, NW>::kLoads, kLoadsB = Loader<BCOLS, BNp, NW>::kLoads;
+  constexpr int kLoads = kLoadsA + kProducts * kLoadsB;
+  struct Step {
+    u32x4 a, b, b2;
+    int k0;
+    uint32_t to;
+  };
+  // Steps behind the last load zeros, which nobody reads.
+  auto step_to = [&](int buf, bool any) {
+    Step x;
+    x.k0 = kt * kBK;
+    x.to = lds0 + buf * kBuf;
+    x.a = la.source(p.a[seg], p.lda, m0, p.M, x.k0, p.K);
+    x.b = lb.source(second ? p.b2[seg] : p.b[seg], p.ldb, n0, p.N, x.k0, p.K);
+    if constexpr (EPI == kGlu) x.b2 = lb.source(p.b2[seg], p.ldb, n0, p.N, x.k0, p.K);
+    if (!any) x.a[2] = x.b[2] = x.b2[2] = 0;
+    if (++kt == ksteps) {
+      kt = 0;
+      if (seg + 1 < p.nseg) ++seg;
+    }
+    return x;
+  };
+  auto load = [&](const Step& x, int i) {
+    if (i < kLoadsA) la.load(i, x.a, x.k0, p.K, x.to, wave);
+    else if (i < kLoadsA + kLoadsB) lb.load(i - kLoadsA, x.b, x.k0, p.K, x.to + kA, wave);
+    else lb.load(i - kLoadsA - kLoadsB, x.b2, x.k0, p.K, x.to + kA + kB, wave);
   };
 
   f32x4 acc[TM][TN];
@@ -183,29 +201,62 @@ __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = linattn::zero4();
 
-  if (s0 < s1) fetch(0);
+  // Fragments of a half step are in registers before its products begin: those of the second half are read from LDS
+  // between the first half's products, those of the next step's first half between the second's, and so are the loads
+  // into this step's buffer begun. The barrier stands between the halves: everything of this step has been read then,
+  // and the next step's loads, begun NB - 1 steps ago, are in. All 8 waves read at once otherwise, and multiply at once:
+  // the matrix cores were idle 47% of the cycles.
+  struct Half {
+    bf16x8 a[TM], b[TN];
+  } first, last;
+  auto read_a = [&](Half& f, int buf, int h, int i) {
+    f.a[i] = fragment<ACOLS>(lds + buf * kBuf, wm * (TM * 16) + i * 16, h, lane);
+  };
+  auto read_b = [&](Half& f, int buf, int h, int j) {
+    const int col = EPI == kGlu ? wn * (TN / 2 * 16) + (j % (TN / 2)) * 16 : wn * (TN * 16) + j * 16;
+    f.b[j] = fragment<BCOLS>(lds + buf * kBuf + kA + (EPI == kGlu && j >= TN / 2 ? kB : 0), col, h, lane);
+  };
+  // The products of row i of the wave's tiles, behind what is read for row i of the next half. Two workgroups of the
+  // small shapes share a compute unit and fill each other's gaps: they read all first (4% faster there).
+  constexpr bool kInRows = TM >= 8;
+  auto row = [&](const Half& f, Half& next, int buf, int h, int i) {
+    if (kInRows || i == 0) {
+#pragma unroll
+      for (int j = kInRows ? i * TN / TM : 0; j < (kInRows ? (i + 1) * TN / TM : TN); ++j) read_b(next, buf, h, j);
+#pragma unroll
+      for (int k = i; k < (kInRows ? i + 1 : TM); ++k) read_a(next, buf, h, k);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.b[j], f.a[i], acc[i][j], 0, 0, 0);
+    if (kInRows || i == TM - 1) __builtin_amdgcn_sched_barrier(0);
+  };
+#pragma unroll
+  for (int n = 0; n < NB; ++n) {
+    const Step x = step_to(n, s0 + n < s1);
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) load(x, i);
+  }
+  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"((NB - 1) * kLoads) : "memory");
+#pragma unroll
+  for (int j = 0; j < TN; ++j) read_b(first, 0, 0, j);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) read_a(first, 0, 0, i);
   int buf = 0;
   for (int s = s0; s < s1; ++s) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (s + 1 < s1) fetch(buf ^ 1);
-    const char* at = lds + buf * kBuf;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      bf16x8 a[TM], b[TN];
+    for (int i = 0; i < TM; ++i) row(first, last, buf, 1, i);
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NB - 2) * kLoads) : "memory");
+    const Step x = step_to(buf, s + NB < s1);
+    buf = buf + 1 == NB ? 0 : buf + 1;
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const int col = EPI == kGlu ? wn * (TN / 2 * 16) + (j % (TN / 2)) * 16 : wn * (TN * 16) + j * 16;
-        b[j] = fragment<BCOLS>(at + kA + (EPI == kGlu && j >= TN / 2 ? kB : 0), col, h, lane);
-      }
+    for (int i = 0; i < TM; ++i) {
 #pragma unroll
-      for (int i = 0; i < TM; ++i) a[i] = fragment<ACOLS>(at, wm * (TM * 16) + i * 16, h, lane);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
+      for (int l = kInRows || i == 0 ? i * kLoads / TM : kLoads; l < (kInRows ? (i + 1) * kLoads / TM : kLoads); ++l) load(x, l);
+      row(last, first, buf, 0, i);
     }
-    buf ^= 1;
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // before the workgroup's LDS is another's
 
   const int q = lane >> 4, li = lane & 15;
 #pragma unroll
@@ -217,8 +268,8 @@ __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
 #pragma unroll
       for (int j = 0; j < TN / 2; ++j) {
         const int n = n0 + wn * (TN / 2 * 16) + j * 16 + 4 * q;
-        store4(out, true, p.N, m, n, p.N, acc[i][j]);
-        store4(out + (int64_t)p.M * p.N, true, p.N, m, n, p.N, acc[i][j + TN / 2]);
+        store4(out, true, m * p.N + n, p.N - n, acc[i][j]);
+        store4(out + (int64_t)p.M * p.N, true, m * p.N + n, p.N - n, acc[i][j + TN / 2]);
       }
     } else if constexpr (EPI == kGlu) {
 #pragma unroll
@@ -228,10 +279,10 @@ __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
         f32x4 h;
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] = activation(g[e], p.act) * u[e];
-        store4(p.out, p.f32, p.N, m, n, p.N, h);
+        store4(p.out, p.f32, m * p.N + n, p.N - n, h);
         if (p.gate) {
-          store4(p.gate, p.f32, p.N, m, n, p.N, g);
-          store4(p.up, p.f32, p.N, m, n, p.N, u);
+          store4(p.gate, p.f32, m * p.N + n, p.N - n, g);
+          store4(p.up, p.f32, m * p.N + n, p.N - n, u);
         }
       }
     } else {
@@ -243,7 +294,10 @@ __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
         f32 = true;
       }
 #pragma unroll
-      for (int j = 0; j < TN; ++j) store4(out, f32, p.N, m, n0 + wn * (TN * 16) + j * 16 + 4 * q, p.N, acc[i][j]);
+      for (int j = 0; j < TN; ++j) {
+        const int n = n0 + wn * (TN * 16) + j * 16 + 4 * q;
+        store4(out, f32, m * p.N + n, p.N - n, acc[i][j]);
+      }
     }
   }
 }
