@@ -201,18 +201,29 @@ uint32_t blocks_for(int64_t threads) { return (uint32_t)((threads + 255) / 256);
 
 // ---- tiles: which, and how many workgroups share a sum
 
-// Waves side by side over m and n, and 16 x 16 tiles of a wave.
+// Shapes of a workgroup's tile, and what a step of 64 k and a tile's beginning and end take where as many workgroups as
+// fit share a compute unit, in us: from products of 4096 to 8192 rows and columns, whose tiles fill the compute units
+// evenly. 256 x 256: 1,340 TFLOP/s; 128 x 256: 1,080; two of 128 x 128 (64 x 256 in the forward): 1,050.
 enum Shape { kLarge, kHalf, kSmall, kShapes };
-// Workgroups that share a compute unit, and the time of a step of 64 k with that many there, in us: from products whose
-// tiles fill the compute units evenly.
 struct ShapeInfo {
   int bm, bn;
   int per_cu;
   float step_us, ends_us;
 };
+// bn of the forward: columns of both weights
+constexpr ShapeInfo kForwardShapes[kShapes] = {{256, 128, 1, 1.55f, 5.f}, {128, 128, 1, 0.96f, 4.f}, {64, 128, 2, 1.f, 4.f}};
+constexpr ShapeInfo kGradShapes[kShapes] = {{256, 256, 1, 1.55f, 5.f}, {128, 256, 1, 0.96f, 4.f}, {128, 128, 2, 1.f, 4.f}};
+
+// A product: its sizes, how many of them, and the steps of its sum.
+struct Product {
+  int64_t M, N, count, steps;
+  int64_t tiles(const ShapeInfo& f) const { return (M + f.bm - 1) / f.bm * ((N + f.bn - 1) / f.bn) * count; }
+  // written by each part and read again, at 5 TB/s, with the join's launch
+  float join_us(int splits) const { return splits > 1 ? 4.f + (splits * 8.f + 4.f) * count * M * N * 2e-7f : 0.f; }
+};
 struct Plan {
   Shape shape;
-  int splits;
+  int splits[2];
 };
 
 int compute_units() {
@@ -223,58 +234,100 @@ int compute_units() {
   return n;
 }
 
-// The shape and the number of parts of the sum with the least estimated time: rounds of workgroups, each its share of
-// the steps, and for parts the second kernel that adds them.
-Plan plan(const ShapeInfo (&shapes)[kShapes], int64_t M, int64_t N, int products, int64_t steps) {
+// When the last of two kinds of workgroups is done, of which `slots` run at a time, the first kind before the second:
+// n[i] of them of us[i] each.
+float finish(const int64_t (&n)[2], const float (&us)[2], int64_t slots) {
+  // slots that are free early and late behind the first kind
+  const int64_t late = n[0] % slots;
+  float t[2] = {n[0] / slots * us[0], (n[0] / slots + 1) * us[0]};
+  const int64_t count[2] = {slots - late, late};
+  float end = late ? t[1] : t[0];
+  int64_t left = n[1];
+  if (left > 8 * slots) {  // whole rounds, which both kinds of slots take alike
+    const int64_t rounds = left / slots - 4;
+    left -= rounds * slots;
+    t[0] += rounds * us[1], t[1] += rounds * us[1];
+  }
+  while (left > 0) {
+    const int i = count[1] == 0 || t[0] <= t[1] ? 0 : 1;
+    left -= count[i];
+    t[i] += us[1];
+    end = end > t[i] ? end : t[i];
+  }
+  return end;
+}
+
+// The shape and the numbers of parts of the sums with the least estimated time. Parts fill the compute units where
+// there are few tiles, and level the last round of workgroups; a second kernel adds them.
+Plan plan(const ShapeInfo (&shapes)[kShapes], const Product (&job)[2]) {
+  constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
   const int cus = compute_units();
-  Plan best{kLarge, 1};
+  Plan best{kLarge, {1, 1}};
   float least = 0.f;
+  bool any = false;
   for (int s = 0; s < kShapes; ++s) {
     const ShapeInfo& f = shapes[s];
-    if (f.bm == 0) continue;
-    const int64_t tiles = (M + f.bm - 1) / f.bm * ((N + f.bn - 1) / f.bn) * products, slots = (int64_t)cus * f.per_cu;
-    for (int splits = 1; splits <= 32; ++splits) {
-      if (splits > 1 && (tiles * splits > 4 * slots || steps / splits < 4)) break;
-      const int64_t rounds = (tiles * splits + slots - 1) / slots, share = (steps + splits - 1) / splits;
-      float us = rounds * (share * f.step_us + f.ends_us);
-      if (splits > 1) us += 4.f + (splits * 8.f + 4.f) * products * M * N * 2e-7f;  // written, read at 5 TB/s
-      if ((s == 0 && splits == 1) || us < least) least = us, best = Plan{(Shape)s, splits};
+    const int64_t slots = (int64_t)cus * f.per_cu, tiles[2] = {job[0].tiles(f), job[1].tiles(f)};
+    for (int a : kSplits) {
+      if (a > 1 && (tiles[0] * a > 4 * slots || job[0].steps < 4 * a)) break;
+      for (int b : kSplits) {
+        if (b > 1 && (tiles[1] * b > 4 * slots || job[1].steps < 4 * b)) break;
+        const int64_t n[2] = {tiles[0] * a, tiles[1] * b};
+        const float us[2] = {(job[0].steps + a - 1) / a * f.step_us + f.ends_us, (job[1].steps + b - 1) / b * f.step_us + f.ends_us};
+        const float t = finish(n, us, slots) + job[0].join_us(a) + job[1].join_us(b);
+        if (!any || t < least) any = true, least = t, best = Plan{(Shape)s, {a, b}};
+      }
     }
   }
   return best;
 }
 
 // More than 64 KB of LDS has to be asked for on every device.
-template <bool AC, bool BC, int WM, int WN, int TM, int TN, int NB, int EPI>
-hipError_t gemm(GemmParams p, hipStream_t stream) {
-  constexpr int BM = WM * TM * 16, BN = WN * TN * 16, lds = NB * (BM + BN) * kBK * 2;
-  const void* fn = reinterpret_cast<const void*>(&glu_gemm_kernel<AC, BC, WM, WN, TM, TN, NB, EPI>);
-  static std::atomic<uint64_t> granted{0};
+template <int LDS>
+hipError_t grant(const void* fn, std::atomic<uint64_t>& granted) {
   int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
+  const hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
-  e = static_cast<hipError_t>(once_per_device(granted, dev, [&] {
-    return static_cast<int>(hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, lds));
+  return static_cast<hipError_t>(once_per_device(granted, dev, [&] {
+    return static_cast<int>(hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, LDS));
   }));
-  if (e != hipSuccess) return e;
-  const int per_tile = EPI == kGlu ? BN / 2 : BN;
+}
+template <int BM, int BN>
+uint32_t set_tiles(GemmParams& p) {
   p.tiles_m = (p.M + BM - 1) / BM;
-  p.tiles_n = (p.N + per_tile - 1) / per_tile * (EPI == kProduct && p.two ? 2 : 1);
-  return start(fn, dim3((uint32_t)p.tiles_m * p.tiles_n * p.splits), 64 * WM * WN, lds, p, stream);
+  p.tiles_n = (p.N + BN - 1) / BN * (p.two ? 2 : 1);
+  return (uint32_t)p.tiles_m * p.tiles_n * p.splits;
 }
-constexpr ShapeInfo kForwardShapes[kShapes] = {{256, 128, 1, 1.8f, 4.f}, {128, 128, 1, 1.0f, 3.f}, {64, 128, 2, 1.0f, 3.f}};
-constexpr ShapeInfo kRowShapes[kShapes] = {{256, 256, 1, 1.8f, 4.f}, {128, 256, 1, 1.0f, 3.f}, {128, 128, 2, 1.0f, 3.f}};
-constexpr ShapeInfo kColumnShapes[kShapes] = {{256, 256, 1, 1.8f, 4.f}, {128, 256, 1, 1.0f, 3.f}, {128, 128, 2, 1.0f, 3.f}};
-hipError_t forward_gemm(const GemmParams& p, Shape s, hipStream_t stream) {
-  if (s == kLarge) return gemm<false, true, 2, 4, 8, 4, 2, kGlu>(p, stream);
-  if (s == kHalf) return gemm<false, true, 2, 4, 4, 4, 3, kGlu>(p, stream);
-  return gemm<false, true, 1, 4, 4, 4, 2, kGlu>(p, stream);
+template <int WM, int WN, int TM, int TN, int NB>
+hipError_t forward_product(GemmParams p, hipStream_t stream) {
+  constexpr int BM = WM * TM * 16, BN = WN * TN * 16, lds = NB * (BM + BN) * kBK * 2;
+  const void* fn = reinterpret_cast<const void*>(&glu_forward_kernel<WM, WN, TM, TN, NB>);
+  static std::atomic<uint64_t> granted{0};
+  const hipError_t e = grant<lds>(fn, granted);
+  if (e != hipSuccess) return e;
+  const uint32_t blocks = set_tiles<BM, BN / 2>(p);
+  return start(fn, dim3(blocks), 64 * WM * WN, lds, p, stream);
 }
-template <bool COLS>
-hipError_t product_gemm(const GemmParams& p, Shape s, hipStream_t stream) {
-  if (s == kLarge) return gemm<COLS, COLS, 2, 4, 8, 4, 2, kProduct>(p, stream);
-  if (s == kHalf) return gemm<COLS, COLS, 2, 4, 4, 4, 3, kProduct>(p, stream);
-  return gemm<COLS, COLS, 2, 2, 4, 4, 2, kProduct>(p, stream);
+template <int WM, int WN, int TM, int TN, int NB>
+hipError_t grad_products(GradProducts p, bool x, bool w, hipStream_t stream) {
+  constexpr int BM = WM * TM * 16, BN = WN * TN * 16, lds = NB * (BM + BN) * kBK * 2;
+  const void* fn = reinterpret_cast<const void*>(&glu_backward_kernel<WM, WN, TM, TN, NB>);
+  static std::atomic<uint64_t> granted{0};
+  const hipError_t e = grant<lds>(fn, granted);
+  if (e != hipSuccess) return e;
+  p.first = x ? set_tiles<BM, BN>(p.x) : 0;
+  const uint32_t blocks = p.first + (w ? set_tiles<BM, BN>(p.w) : 0);
+  return start(fn, dim3(blocks), 64 * WM * WN, lds, p, stream);
+}
+hipError_t forward_products(const GemmParams& p, Shape s, hipStream_t stream) {
+  if (s == kLarge) return forward_product<2, 4, 8, 4, 2>(p, stream);
+  if (s == kHalf) return forward_product<2, 4, 4, 4, 3>(p, stream);
+  return forward_product<1, 4, 4, 4, 2>(p, stream);
+}
+hipError_t backward_products(const GradProducts& p, bool x, bool w, Shape s, hipStream_t stream) {
+  if (s == kLarge) return grad_products<2, 4, 8, 4, 2>(p, x, w, stream);
+  if (s == kHalf) return grad_products<2, 4, 4, 4, 3>(p, x, w, stream);
+  return grad_products<2, 2, 4, 4, 2>(p, x, w, stream);
 }
 
 // ---- the workspace of a call, in parts
@@ -352,10 +405,12 @@ hipError_t forward_few(const GluCall& c) {
 hipError_t forward(const GluCall& c) {
   if (few_rows(c)) return c.f32 ? forward_few<true>(c) : forward_few<false>(c);
   Matrix x{c.x, c.M, c.D, c.f32}, wg{c.w_gate, c.D, c.F, c.f32}, wu{c.w_up, c.D, c.F, c.f32};
-  const Plan how = plan(kForwardShapes, c.M, c.F, 1, steps_of(c.D, pairs(c.f32)));
+  const Product job[2] = {{c.M, c.F, 1, steps_of(c.D, pairs(c.f32))}, {0, 0, 0, 0}};
+  const Plan how = plan(kForwardShapes, job);
+  const int splits = how.splits[0];
   Parts parts;
   for (Matrix* m : {&x, &wg, &wu}) m->place(parts);
-  const size_t partial_at = how.splits > 1 ? parts.add((size_t)how.splits * 2 * c.M * c.F * 4) : 0;
+  const size_t partial_at = splits > 1 ? parts.add((size_t)splits * 2 * c.M * c.F * 4) : 0;
   std::unique_lock<std::mutex> lock(operators_mutex(), std::defer_lock);
   char* ws = nullptr;
   if (parts.bytes) {
@@ -376,13 +431,13 @@ hipError_t forward(const GluCall& c) {
     p.b[s] = wg.piece(ws, second_of(c.f32, s));
     p.b2[s] = wu.piece(ws, second_of(c.f32, s));
   }
-  p.lda = x.ld(), p.ldb = wg.ld(), p.M = (int32_t)c.M, p.N = (int32_t)c.F, p.K = (int32_t)c.D, p.splits = how.splits;
+  p.lda = x.ld(), p.ldb = wg.ld(), p.M = (int32_t)c.M, p.N = (int32_t)c.F, p.K = (int32_t)c.D, p.splits = splits;
   p.out = c.h, p.gate = c.gate, p.up = c.up, p.f32 = c.f32, p.act = c.act;
   p.partial = reinterpret_cast<float*>(ws + partial_at);
-  const hipError_t e = forward_gemm(p, how.shape, c.stream);
-  if (e != hipSuccess || how.splits == 1) return e;
+  const hipError_t e = forward_products(p, how.shape, c.stream);
+  if (e != hipSuccess || splits == 1) return e;
   JoinParams j{};
-  j.job[0] = JoinJob{p.partial, c.gate, c.up, c.h, c.M * c.F, how.splits, 2, c.f32, c.act};
+  j.job[0] = JoinJob{p.partial, c.gate, c.up, c.h, c.M * c.F, splits, 2, c.f32, c.act};
   j.second = blocks_for((j.job[0].n + 3) / 4);
   return start(reinterpret_cast<const void*>(&glu_join_kernel), dim3(j.second), 256, 0, j, c.stream);
 }
@@ -394,14 +449,17 @@ hipError_t backward(const GluCall& c) {
   const int np = c.f32 ? 3 : 1;
   const int64_t ldf = padded(c.F), plane = c.M * ldf;
   const int64_t sum_f = whole(c.F, 8);  // with zeros in the copies' columns behind F
-  const Plan for_x = plan(kRowShapes, c.M, c.D, 1, steps_of(sum_f, 2 * pairs(c.f32)));
-  const Plan for_w = plan(kColumnShapes, c.D, c.F, 2, steps_of(c.M, pairs(c.f32)));
+  Product job[2] = {{c.M, c.D, 1, steps_of(sum_f, 2 * pairs(c.f32))}, {c.D, c.F, 2, steps_of(c.M, pairs(c.f32))}};
+  if (!dx) job[0] = Product{0, 0, 0, 0};
+  if (!dw) job[1] = Product{0, 0, 0, 0};
+  const Plan how = plan(kGradShapes, job);
+  const int sx = how.splits[0], sw = how.splits[1];
   Parts parts;
   if (dw) x.place(parts);
   if (dx) wg.place(parts), wu.place(parts);
   const size_t dg_at = parts.add((size_t)np * plane * 2), du_at = parts.add((size_t)np * plane * 2);
-  const size_t px_at = dx && for_x.splits > 1 ? parts.add((size_t)for_x.splits * c.M * c.D * 4) : 0;
-  const size_t pw_at = dw && for_w.splits > 1 ? parts.add((size_t)for_w.splits * 2 * c.D * c.F * 4) : 0;
+  const size_t px_at = dx && sx > 1 ? parts.add((size_t)sx * c.M * c.D * 4) : 0;
+  const size_t pw_at = dw && sw > 1 ? parts.add((size_t)sw * 2 * c.D * c.F * 4) : 0;
 
   std::lock_guard<std::mutex> lock(operators_mutex());
   void* space = nullptr;
@@ -416,45 +474,43 @@ hipError_t backward(const GluCall& c) {
   e = stage.launch(&grad, c.f32, c.stream);
   if (e != hipSuccess) return e;
 
+  GradProducts p{};
   JoinParams j{};
   int joins = 0;
   uint32_t blocks = 0;
   if (dx) {
-    GemmParams p{};
+    GemmParams& o = p.x;
     for (int s = 0; s < pairs(c.f32); ++s) {
       const int f = first_of(c.f32, s), t = second_of(c.f32, s);
-      p.a[2 * s] = dg + f * plane, p.b[2 * s] = wg.piece(ws, t);
-      p.a[2 * s + 1] = du + f * plane, p.b[2 * s + 1] = wu.piece(ws, t);
+      o.a[2 * s] = dg + f * plane, o.b[2 * s] = wg.piece(ws, t);
+      o.a[2 * s + 1] = du + f * plane, o.b[2 * s + 1] = wu.piece(ws, t);
     }
-    p.nseg = 2 * pairs(c.f32);
-    p.lda = ldf, p.ldb = wg.ld(), p.M = (int32_t)c.M, p.N = (int32_t)c.D, p.K = (int32_t)sum_f, p.splits = for_x.splits;
-    p.out = c.dx, p.f32 = c.f32, p.partial = reinterpret_cast<float*>(ws + px_at);
-    e = product_gemm<false>(p, for_x.shape, c.stream);
-    if (e != hipSuccess) return e;
-    if (p.splits > 1) {
-      j.job[joins++] = JoinJob{p.partial, c.dx, nullptr, nullptr, c.M * c.D, p.splits, 1, c.f32, 0};
+    o.nseg = 2 * pairs(c.f32);
+    o.lda = ldf, o.ldb = wg.ld(), o.M = (int32_t)c.M, o.N = (int32_t)c.D, o.K = (int32_t)sum_f, o.splits = sx;
+    o.out = c.dx, o.f32 = c.f32, o.partial = reinterpret_cast<float*>(ws + px_at);
+    if (sx > 1) {
+      j.job[joins++] = JoinJob{o.partial, c.dx, nullptr, nullptr, c.M * c.D, sx, 1, c.f32, 0};
       blocks += blocks_for((c.M * c.D + 3) / 4);
     }
   }
   j.second = blocks;
   if (dw) {
-    GemmParams p{};
-    p.nseg = pairs(c.f32);
-    for (int s = 0; s < p.nseg; ++s) {
+    GemmParams& o = p.w;
+    o.nseg = pairs(c.f32);
+    for (int s = 0; s < o.nseg; ++s) {
       const int f = first_of(c.f32, s), t = second_of(c.f32, s);
-      p.a[s] = x.piece(ws, f), p.b[s] = dg + t * plane, p.b2[s] = du + t * plane;
+      o.a[s] = x.piece(ws, f), o.b[s] = dg + t * plane, o.b2[s] = du + t * plane;
     }
-    p.lda = x.ld(), p.ldb = ldf, p.M = (int32_t)c.D, p.N = (int32_t)c.F, p.K = (int32_t)c.M, p.splits = for_w.splits;
-    p.out = c.dw_gate, p.out2 = c.dw_up, p.two = true, p.f32 = c.f32, p.partial = reinterpret_cast<float*>(ws + pw_at);
-    e = product_gemm<true>(p, for_w.shape, c.stream);
-    if (e != hipSuccess) return e;
-    if (p.splits > 1) {
-      j.job[joins++] = JoinJob{p.partial, c.dw_gate, c.dw_up, nullptr, c.D * c.F, p.splits, 2, c.f32, 0};
-      if (joins == 1) j.second = blocks_for((c.D * c.F + 3) / 4);  // the only job
+    o.lda = x.ld(), o.ldb = ldf, o.M = (int32_t)c.D, o.N = (int32_t)c.F, o.K = (int32_t)c.M, o.splits = sw;
+    o.out = c.dw_gate, o.out2 = c.dw_up, o.two = true, o.f32 = c.f32, o.partial = reinterpret_cast<float*>(ws + pw_at);
+    if (sw > 1) {
+      j.job[joins++] = JoinJob{o.partial, c.dw_gate, c.dw_up, nullptr, c.D * c.F, sw, 2, c.f32, 0};
       blocks += blocks_for((c.D * c.F + 3) / 4);
+      if (joins == 1) j.second = blocks;  // the only job
     }
   }
-  if (joins == 0) return e;
+  e = backward_products(p, dx, dw, how.shape, c.stream);
+  if (e != hipSuccess || joins == 0) return e;
   return start(reinterpret_cast<const void*>(&glu_join_kernel), dim3(blocks), 256, 0, j, c.stream);
 }
 

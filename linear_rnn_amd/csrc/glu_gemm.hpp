@@ -135,8 +135,9 @@ __device__ __forceinline__ void store4(void* out, bool f32, int64_t at, int coun
   }
 }
 
+// Workgroup `block` of a product's tiles_m tiles_n splits.
 template <bool ACOLS, bool BCOLS, int WM, int WN, int TM, int TN, int NB, int EPI>
-__global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
+__device__ __forceinline__ void tile_product(const GemmParams& p, uint32_t block) {
   constexpr int NW = WM * WN, BM = WM * TM * 16, BN = WN * TN * 16;
   constexpr int kProducts = EPI == kGlu ? 2 : 1;  // in one tile
   constexpr int BNp = BN / kProducts;
@@ -148,7 +149,7 @@ __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
 
   // Neighbouring tiles on one die: eight rows of tiles at a time.
   const uint32_t tiles = p.tiles_m * p.tiles_n;
-  const uint32_t id = xcd_swizzle(blockIdx.x, tiles * p.splits);
+  const uint32_t id = xcd_swizzle(block, tiles * p.splits);
   const uint32_t split = id / tiles, t = id % tiles;
   const uint32_t group = t / (8 * p.tiles_n), in = t % (8 * p.tiles_n);
   const uint32_t high = p.tiles_m - group * 8 < 8 ? p.tiles_m - group * 8 : 8;
@@ -300,6 +301,22 @@ __global__ __launch_bounds__(64 * WM * WN) void glu_gemm_kernel(GemmParams p) {
       }
     }
   }
+}
+
+template <int WM, int WN, int TM, int TN, int NB>
+__global__ __launch_bounds__(64 * WM * WN) void glu_forward_kernel(GemmParams p) {
+  tile_product<false, true, WM, WN, TM, TN, NB, kGlu>(p, blockIdx.x);
+}
+// The products of the backward side by side: the input's gradient (operands in rows), and behind `first` the weights'
+// (operands in columns).
+struct GradProducts {
+  GemmParams x, w;
+  uint32_t first;
+};
+template <int WM, int WN, int TM, int TN, int NB>
+__global__ __launch_bounds__(64 * WM * WN) void glu_backward_kernel(GradProducts p) {
+  if (blockIdx.x < p.first) tile_product<false, false, WM, WN, TM, TN, NB, kProduct>(p.x, blockIdx.x);
+  else tile_product<true, true, WM, WN, TM, TN, NB, kProduct>(p.w, blockIdx.x - p.first);
 }
 
 }  // namespace glu
