@@ -17,6 +17,8 @@
 #include "wkv7_device.hpp"
 #include "wkv7_internal.hpp"
 
+#include <atomic>
+
 namespace rwkv7 {
 namespace {
 
@@ -29,8 +31,8 @@ constexpr int kWaves = kThreads / kWave;
 constexpr int kTok = 8;        // tokens in a row of a thread
 template <int VEC>
 constexpr int kLanes = kSlab / VEC;  // threads side by side over the channels
-template <int VEC>
-constexpr int kTile = kThreads / kLanes<VEC> * kTok;  // tokens of a workgroup at a time
+template <int VEC, int W = kWaves>
+constexpr int kTile = W * kWave / kLanes<VEC> * kTok;  // tokens of a workgroup of W waves at a time
 template <bool F32>
 constexpr uint32_t kEsz = F32 ? 4 : 2;
 
@@ -46,13 +48,20 @@ struct ScanParams {
   float* dlog_w;
   const float* ds_out;
   float* ds_in;
-  // Maps of runs of tokens, [run][B][D] each. Forward: run 0 is the initial state (P = 0), run s + 1 segment s.
-  // Backward: run s is tile s; `l` first holds its L, then the state before it, `r` first what it adds to the
-  // gradient of the state, then the gradient that comes back to its last token.
+  // Gradients in two passes: the maps of tiles, [tile][B][D] each; `l` first holds a tile's L, then the state before it,
+  // `r` first what it adds to the gradient of the state, then the gradient that comes back to its last token.
   float *p, *l, *r;
+  // Words that workgroups pass to each other: maps of tiles, [tile][channel of all slabs], P and L (`there`) or P and R
+  // (`back`) in one; the states before every kGroup tiles (`there` again, behind the tiles); numbers of workgroups.
+  uint64_t *there, *back;
+  float *first_state, *last_grad;  // copies of s_in and ds_out (zeros where null), [unit][64]: those may be overwritten
+  uint32_t* ticket;  // number of workgroups that have started
+  uint32_t* left;    // tiles left to the second kernel: how many, which
+  uint32_t tiles, units;
+  uint64_t words;  // to be emptied
+  int polls;
   int64_t T, BD;
-  int64_t seg_tokens;  // a multiple of the tile
-  uint32_t B, D, slabs, segs;
+  uint32_t B, D, slabs;
   uint32_t first;  // number of the launch's first workgroup
 };
 
@@ -107,17 +116,14 @@ __device__ __forceinline__ void store(__amdgpu_buffer_rsrc_t b, uint32_t off, co
 }
 
 __device__ __forceinline__ float decay(float log_w) { return __builtin_amdgcn_exp2f(log_w * 1.44269504f); }
-// 1 - exp(-z) for z >= 0, where w = exp(-z). 1 - w loses the digits of a decay close to 1, so up to 0.35 it is the
-// alternating series, whose ninth term is below 2^-25 of the first there.
+// 1 - exp(-z) for z >= 0, where w = exp(-z). 1 - w loses the digits of a decay close to 1, so up to 0.36 it is z times a
+// polynomial of degree 4: the interpolation of (1 - exp(-z)) / z at that interval's Chebyshev nodes, 2^-25 off.
 __device__ __forceinline__ float one_minus(float z, float w) {
-  float p = fmaf(z, -1.f / 8, 1.f);
-  p = fmaf(z * (-1.f / 7), p, 1.f);
-  p = fmaf(z * (-1.f / 6), p, 1.f);
-  p = fmaf(z * (-1.f / 5), p, 1.f);
-  p = fmaf(z * (-1.f / 4), p, 1.f);
-  p = fmaf(z * (-1.f / 3), p, 1.f);
-  p = fmaf(z * (-1.f / 2), p, 1.f);
-  return z < 0.35f ? z * p : 1.f - w;
+  float p = fmaf(z, 0.0071817646f, -0.041313525f);
+  p = fmaf(z, p, 0.1666218f);
+  p = fmaf(z, p, -0.499998f);
+  p = fmaf(z, p, 1.f);
+  return z < 0.36f ? z * p : 1.f - w;
 }
 template <int KIND>
 __device__ __forceinline__ float scale(float log_w, float w) {
@@ -125,12 +131,13 @@ __device__ __forceinline__ float scale(float log_w, float w) {
   else if constexpr (KIND == RWKV7_INPUT_MIX) return one_minus(-log_w, w);
   else return __builtin_amdgcn_sqrtf(one_minus(-2.f * log_w, w * w));
 }
-// The derivative of s to log w; that of sqrt(1 - w^2) at w = 1, where it has none, counts as 0.
+// dh/dlog w = w h + s' x, with h the state before. The derivative s' of sqrt(1 - w^2) at w = 1, where it has none, counts
+// as 0.
 template <int KIND>
-__device__ __forceinline__ float slope(float w, float s) {
-  if constexpr (KIND == RWKV7_INPUT_PLAIN) return 0.f;
-  else if constexpr (KIND == RWKV7_INPUT_MIX) return -w;
-  else return s > 0.f ? -w * w * __builtin_amdgcn_rcpf(s) : s * 0.f;
+__device__ __forceinline__ float through(float w, float s, float h, float x) {
+  if constexpr (KIND == RWKV7_INPUT_PLAIN) return w * h;
+  else if constexpr (KIND == RWKV7_INPUT_MIX) return w * (h - x);
+  else return w * fmaf(s > 0.f ? -w * __builtin_amdgcn_rcpf(s) : 0.f, x, h);
 }
 
 // Values of the even and the odd row of 16 lanes of a pair, and of the lower and the upper half, in all their lanes.
@@ -149,8 +156,9 @@ __device__ __forceinline__ Two halves(float x) {
 }
 
 // The maps of the other waves: [turn][wave][channel].
+template <int W = kWaves>
 struct Shared {
-  float p[2][kWaves][kSlab], l[2][kWaves][kSlab];
+  float p[2][W][kSlab], l[2][W][kSlab];
 };
 
 // From each thread's map (P, L): the map of the threads before it (REV: behind it) in the wave, in (P, L), and the
@@ -225,51 +233,24 @@ __device__ __forceinline__ int64_t length(const ScanParams& p, uint32_t b) {
   return n < 0 ? 0 : n < p.T ? n : p.T;
 }
 
-// A prompt, segment by segment: each workgroup walks the tiles of one segment of one sequence, the next tile's loads
-// in flight while one is summed. MAPS: only the segment's map (for the workgroups of the segments behind it).
-template <bool F32, int VEC, int KIND, bool MAPS>
-__global__ __launch_bounds__(kThreads) void gscan_kernel(ScanParams p) {
+// A prompt, a workgroup for each unit (64 channels of a sequence): it walks the tiles, the next tile's loads in flight
+// while one is summed.
+template <bool F32, int VEC, int KIND>
+__global__ __launch_bounds__(kThreads) void gscan_walk_kernel(ScanParams p) {
   constexpr uint32_t esz = kEsz<F32>;
   constexpr int tile = kTile<VEC>;
-  __shared__ Shared sh;
-  const uint32_t id = p.first + blockIdx.x;
-  const uint32_t slab = id % p.slabs, seg = id / p.slabs % p.segs, b = id / p.slabs / p.segs;
+  __shared__ Shared<> sh;
+  const uint32_t unit = p.first + blockIdx.x, slab = unit % p.slabs, b = unit / p.slabs;
   const uint32_t c = slab * kSlab + threadIdx.x % kLanes<VEC> * VEC, group = threadIdx.x / kLanes<VEC>;
   const bool on = c < p.D;
-  const int64_t t0 = (int64_t)seg * p.seg_tokens;
-  const int64_t end = p.T - t0 < p.seg_tokens ? p.T - t0 : p.seg_tokens;  // of the segment, from t0
-  int64_t live = length(p, b) - t0;                                      // its tokens that count
-  live = live < 0 ? 0 : live < end ? live : end;
+  const int64_t live = length(p, b);
   const uint32_t at = group * kTok * p.D + c;
   const uint32_t xoff = on ? at * esz : kNowhere, woff = on ? at * 4 : kNowhere;
-  const int64_t base = ((int64_t)b * p.T + t0) * p.D;
+  const int64_t base = (int64_t)b * p.T * p.D;
   const int64_t bd = (int64_t)b * p.D + c;
 
-  float carry[VEC], all[VEC];
-#pragma unroll
-  for (int v = 0; v < VEC; ++v) carry[v] = 0.f, all[v] = 1.f;
-  if constexpr (MAPS) {
-    if (seg == 0 && on && group == 0) {  // run 0: the initial state, which may be overwritten while others start from it
-      float s[VEC] = {}, none[VEC] = {};
-      if (p.s_in) get<VEC>(p.s_in + bd, s);
-      put<VEC>(p.p + bd, none);
-      put<VEC>(p.l + bd, s);
-    }
-  } else if (on) {
-    if (p.segs == 1) {
-      if (p.s_in) get<VEC>(p.s_in + bd, carry);
-    } else {
-#pragma unroll 8
-      for (uint32_t s = 0; s <= seg; ++s) {
-        float mp[VEC], ml[VEC];
-        get<VEC>(p.p + s * p.BD + bd, mp);
-        get<VEC>(p.l + s * p.BD + bd, ml);
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) carry[v] = fmaf(mp[v], carry[v], ml[v]);
-      }
-    }
-  }
-
+  float carry[VEC] = {};
+  if (on && p.s_in) get<VEC>(p.s_in + bd, carry);
   Raw<F32, VEC> rx[kTok];
   Raw<true, VEC> rw[kTok];
   auto fetch = [&](int64_t m) {
@@ -285,9 +266,9 @@ __global__ __launch_bounds__(kThreads) void gscan_kernel(ScanParams p) {
   fetch(0);
   int turn = 0;
   for (int64_t m = 0; m < live; m += tile) {
-    float w[kTok][VEC], a[kTok][VEC], P[VEC], L[VEC], in[VEC];
+    float w[kTok][VEC], a[kTok][VEC], P[VEC], L[VEC], in[VEC], unused[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) P[v] = 1.f, L[v] = 0.f;
+    for (int v = 0; v < VEC; ++v) P[v] = unused[v] = 1.f, L[v] = 0.f;
 #pragma unroll
     for (int k = 0; k < kTok; ++k)
 #pragma unroll
@@ -306,32 +287,92 @@ __global__ __launch_bounds__(kThreads) void gscan_kernel(ScanParams p) {
       }
     maps_of_wave<VEC, false>(P, L, sh.p[turn], sh.l[turn]);
     lds_barrier();
-    enter<VEC, false>(P, L, sh.p[turn], sh.l[turn], carry, in, all);
+    enter<VEC, false>(P, L, sh.p[turn], sh.l[turn], carry, in, unused);
     turn ^= 1;
-    if constexpr (!MAPS) {
-      const int64_t n = live - m < tile ? live - m : tile;
-      const auto by = buffer(static_cast<char*>(p.y) + (base + m * p.D) * esz, (uint32_t)n * p.D * esz);
+    const int64_t n = live - m < tile ? live - m : tile;
+    const auto by = buffer(static_cast<char*>(p.y) + (base + m * p.D) * esz, (uint32_t)n * p.D * esz);
 #pragma unroll
-      for (int k = 0; k < kTok; ++k) {
+    for (int k = 0; k < kTok; ++k) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) in[v] = fmaf(w[k][v], in[v], a[k][v]);
-        store<F32, VEC>(by, xoff + k * p.D * esz, in);
-      }
+      for (int v = 0; v < VEC; ++v) in[v] = fmaf(w[k][v], in[v], a[k][v]);
+      store<F32, VEC>(by, xoff + k * p.D * esz, in);
     }
   }
-  if constexpr (MAPS) {
-    if (on && group == 0) {
-      put<VEC>(p.p + (seg + 1) * p.BD + bd, all);
-      put<VEC>(p.l + (seg + 1) * p.BD + bd, carry);
-    }
-  } else {
-    if (p.s_out && on && group == 0 && seg == p.segs - 1) put<VEC>(p.s_out + bd, carry);
-    const float none[VEC] = {};
-    for (int64_t m = live; m < end; m += tile) {  // behind the sequence's end
-      const int64_t n = end - m < tile ? end - m : tile;
-      const auto by = buffer(static_cast<char*>(p.y) + (base + m * p.D) * esz, (uint32_t)n * p.D * esz);
+  if (p.s_out && on && group == 0) put<VEC>(p.s_out + bd, carry);
+  const float none[VEC] = {};
+  for (int64_t m = live; m < p.T; m += tile) {  // behind the sequence's end
+    const int64_t n = p.T - m < tile ? p.T - m : tile;
+    const auto by = buffer(static_cast<char*>(p.y) + (base + m * p.D) * esz, (uint32_t)n * p.D * esz);
 #pragma unroll
-      for (int k = 0; k < kTok; ++k) store<F32, VEC>(by, xoff + k * p.D * esz, none);
+    for (int k = 0; k < kTok; ++k) store<F32, VEC>(by, xoff + k * p.D * esz, none);
+  }
+}
+
+// One more token in a thread's map of the state (P, L) and that of what comes back to the gradient (P, R).
+template <bool F32, int VEC, int KIND>
+__device__ __forceinline__ void add_token(const Raw<F32, VEC>& rx, const Raw<F32, VEC>& rg, const Raw<true, VEC>& rw,
+                                          float (&w)[VEC], float (&s)[VEC], float (&P)[VEC], float (&L)[VEC], float (&R)[VEC]) {
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const float lw = value<true, VEC>(rw, v);
+    w[v] = decay(lw);
+    s[v] = scale<KIND>(lw, w[v]);
+    L[v] = fmaf(w[v], L[v], s[v] * value<F32, VEC>(rx, v));
+    P[v] *= w[v];
+    R[v] = fmaf(P[v], value<F32, VEC>(rg, v), R[v]);
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void forget(uint32_t (&u)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+v"(u[i]));
+}
+
+// A thread's tokens' gradients from the state before them (h) and the gradient behind them (g): that of the states
+// from the last token, then the rest from the first; zeros behind the sequence's end.
+template <bool F32, int VEC, int KIND>
+__device__ __forceinline__ void write_grads(const ScanParams& p, int64_t base, uint32_t end, uint32_t live, uint32_t group,
+                                            uint32_t xoff, uint32_t woff, Raw<F32, VEC> (&rx)[kTok],
+                                            Raw<F32, VEC> (&rg)[kTok], const float (&w)[kTok][VEC],
+                                            const float (&s)[kTok][VEC], float (&h)[VEC], float (&g)[VEC]) {
+  constexpr uint32_t esz = kEsz<F32>;
+  // What is quickly formed again is not kept in registers since the loads: offsets, widened values, s x.
+  asm volatile("" : "+v"(xoff), "+v"(woff));
+#pragma unroll
+  for (int k = 0; k < kTok; ++k) forget(rx[k].u), forget(rg[k].u);
+  float q[kTok][VEC];
+#pragma unroll
+  for (int k = kTok - 1; k >= 0; --k)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      q[k][v] = value<F32, VEC>(rg[k], v) + g[v];
+      g[v] = w[k][v] * q[k][v];
+    }
+  auto bdx = buffer(static_cast<char*>(p.dx) + base * esz, live * p.D * esz);
+  auto bdw = buffer(p.dlog_w + base, live * p.D * 4);
+#pragma unroll
+  for (int k = 0; k < kTok; ++k) {
+    float dx[VEC], dw[VEC];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      const float x = value<F32, VEC>(rx[k], v);
+      dx[v] = s[k][v] * q[k][v];
+      dw[v] = through<KIND>(w[k][v], s[k][v], h[v], x) * q[k][v];
+      h[v] = fmaf(w[k][v], h[v], s[k][v] * x);
+    }
+    store<F32, VEC>(bdx, xoff + k * p.D * esz, dx);
+    store<true, VEC>(bdw, woff + k * p.D * 4, dw);
+  }
+  if (live < end) {
+    const float none[VEC] = {};
+    bdx = buffer(static_cast<char*>(p.dx) + base * esz, end * p.D * esz);
+    bdw = buffer(p.dlog_w + base, end * p.D * 4);
+#pragma unroll 1
+    for (int k = 0; k < kTok; ++k) {
+      if (group * kTok + k < live) continue;
+      store<F32, VEC>(bdx, xoff + k * p.D * esz, none);
+      store<true, VEC>(bdw, woff + k * p.D * 4, none);
     }
   }
 }
@@ -339,12 +380,12 @@ __global__ __launch_bounds__(kThreads) void gscan_kernel(ScanParams p) {
 // Gradients: a workgroup a tile, which it holds in registers. MAPS: the tile's maps, of the state forward and of its
 // gradient backward (they share P). Else, from the state before the tile and the gradient behind it, the gradients.
 template <bool F32, int VEC, int KIND, bool MAPS>
-__global__ __launch_bounds__(kThreads) void gscan_grad_kernel(ScanParams p) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) void gscan_grad_kernel(ScanParams p) {
   constexpr uint32_t esz = kEsz<F32>;
   constexpr int tile = kTile<VEC>;
-  __shared__ Shared sh[2];
+  __shared__ Shared<> sh[2];
   const uint32_t id = p.first + blockIdx.x;
-  const uint32_t slab = id % p.slabs, seg = id / p.slabs % p.segs, b = id / p.slabs / p.segs;
+  const uint32_t slab = id % p.slabs, seg = id / p.slabs % p.tiles, b = id / p.slabs / p.tiles;
   const uint32_t c = slab * kSlab + threadIdx.x % kLanes<VEC> * VEC, group = threadIdx.x / kLanes<VEC>;
   const bool on = c < p.D;
   const int64_t t0 = (int64_t)seg * tile;
@@ -367,6 +408,7 @@ __global__ __launch_bounds__(kThreads) void gscan_grad_kernel(ScanParams p) {
     rx[k] = load<F32, VEC>(bx, xoff + k * p.D * esz);
     rg[k] = load<F32, VEC>(bg, xoff + k * p.D * esz);
   }
+  __builtin_amdgcn_sched_barrier(0);  // all loads before the first that is waited for
   float state[VEC] = {}, grad[VEC] = {}, all[VEC] = {};
   if (!MAPS && on) {
     get<VEC>(p.l + run, state);
@@ -376,19 +418,7 @@ __global__ __launch_bounds__(kThreads) void gscan_grad_kernel(ScanParams p) {
 #pragma unroll
   for (int v = 0; v < VEC; ++v) P[v] = all[v] = 1.f, L[v] = R[v] = 0.f;
 #pragma unroll
-  for (int k = 0; k < kTok; ++k)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-      const float lw = value<true, VEC>(rw[k], v);
-      w[k][v] = decay(lw);
-      s[k][v] = scale<KIND>(lw, w[k][v]);
-      L[v] = fmaf(w[k][v], L[v], s[k][v] * value<F32, VEC>(rx[k], v));
-      P[v] *= w[k][v];
-    }
-#pragma unroll
-  for (int k = kTok - 1; k >= 0; --k)
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) R[v] = w[k][v] * (value<F32, VEC>(rg[k], v) + R[v]);
+  for (int k = 0; k < kTok; ++k) add_token<F32, VEC, KIND>(rx[k], rg[k], rw[k], w[k], s[k], P, L, R);
 #pragma unroll
   for (int v = 0; v < VEC; ++v) Q[v] = P[v];
   maps_of_wave<VEC, false>(P, L, sh[0].p[0], sh[0].l[0]);
@@ -406,31 +436,352 @@ __global__ __launch_bounds__(kThreads) void gscan_grad_kernel(ScanParams p) {
       put<VEC>(p.r + run, grad);
     }
   } else {
-    float before[kTok][VEC];
+    write_grads<F32, VEC, KIND>(p, base, end, live, group, xoff, woff, rx, rg, w, s, h, g);
+  }
+}
+
+// ---- one pass over the data where the tiles of a sequence are spread over workgroups: each passes its tile's map on
+// to the others of its sequence, in words of memory that hold both numbers of a map, so that a word is valid or empty.
+
+constexpr uint64_t kEmpty = ~uint64_t(0);  // a NaN that no published word has as its P
+constexpr uint32_t kGroup = 32;            // tiles whose maps are composed at once
+constexpr int kChainWaves = 8;
+
+__device__ __forceinline__ void publish(uint64_t* at, float p, float l) {
+  const uint32_t bits = p == p ? __float_as_uint(p) : 0x7fc00000u;
+  __hip_atomic_store(at, (uint64_t)__float_as_uint(l) << 32 | bits, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t peek(const uint64_t* at) {
+  return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Before each call: empties the words and copies the states that the call may overwrite.
+__global__ __launch_bounds__(256) void gscan_empty_kernel(ScanParams p) {
+  const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x, n = (uint64_t)gridDim.x * 256;
+  if (i == 0) *p.ticket = 0, *p.left = 0;
+  for (uint64_t w = i; w < p.words; w += n) p.there[w] = kEmpty;
+  for (uint64_t w = i; w < (uint64_t)p.units * kSlab; w += n) {
+    const uint32_t unit = w / kSlab, c = unit % p.slabs * kSlab + w % kSlab;
+    const int64_t at = (int64_t)(unit / p.slabs) * p.D + c;
+    if (p.first_state) p.first_state[w] = p.s_in && c < p.D ? p.s_in[at] : 0.f;
+    if (p.last_grad) p.last_grad[w] = p.ds_out && c < p.D ? p.ds_out[at] : 0.f;
+  }
+}
+
+// Workgroups take their numbers as they start, so that one waits only for others that have started too.
+__device__ __forceinline__ uint32_t take_ticket(const ScanParams& p, uint32_t* shared) {
+  if (threadIdx.x == 0) *shared = atomicAdd(p.ticket, 1u);
+  __syncthreads();
+  return *shared;
+}
+
+// After a barrier: the map of the wave's tokens before this thread's (REV: behind them) becomes the tile's.
+template <int VEC, bool REV, int W>
+__device__ __forceinline__ void compose(float (&P)[VEC], float (&L)[VEC], const float (*sp)[kSlab], const float (*sl)[kSlab]) {
+  const int wave = threadIdx.x >> 6, c = threadIdx.x % kLanes<VEC> * VEC;
+  float wp[VEC], wl[VEC], ap[VEC], al[VEC], ep[VEC], el[VEC];
 #pragma unroll
-    for (int k = 0; k < kTok; ++k)
+  for (int v = 0; v < VEC; ++v) ap[v] = 1.f, al[v] = 0.f, ep[v] = P[v], el[v] = L[v];
 #pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        before[k][v] = h[v];
-        h[v] = fmaf(w[k][v], h[v], s[k][v] * value<F32, VEC>(rx[k], v));
-      }
-    // zeros behind the sequence's end
-    const auto bdx = buffer(static_cast<char*>(p.dx) + base * esz, end * p.D * esz);
-    const auto bdw = buffer(p.dlog_w + base, end * p.D * 4);
+  for (int i = 0; i < W; ++i) {
+    const int w = REV ? W - 1 - i : i;
+    get<VEC>(&sp[w][c], wp);
+    get<VEC>(&sl[w][c], wl);
 #pragma unroll
-    for (int k = kTok - 1; k >= 0; --k) {
-      float dx[VEC], dw[VEC];
-      const bool counts = group * kTok + k < live;
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const float q = value<F32, VEC>(rg[k], v) + g[v];
-        dx[v] = counts ? s[k][v] * q : 0.f;
-        dw[v] = counts ? fmaf(w[k][v], before[k][v], slope<KIND>(w[k][v], s[k][v]) * value<F32, VEC>(rx[k], v)) * q : 0.f;
-        g[v] = w[k][v] * q;
-      }
-      store<F32, VEC>(bdx, xoff + k * p.D * esz, dx);
-      store<true, VEC>(bdw, woff + k * p.D * 4, dw);
+    for (int v = 0; v < VEC; ++v) {
+      if (w == wave) P[v] = ep[v] * ap[v], L[v] = fmaf(ep[v], al[v], el[v]);
+      al[v] = fmaf(wp[v], al[v], wl[v]);
+      ap[v] *= wp[v];
     }
+  }
+}
+
+// After a barrier: the map of the whole tile of channel `lane`, from the waves' maps.
+template <bool REV, int W>
+__device__ __forceinline__ void whole_map(const float (*sp)[kSlab], const float (*sl)[kSlab], float& p, float& l) {
+  const int lane = threadIdx.x & 63;
+  p = 1.f, l = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const int w = REV ? W - 1 - i : i;
+    l = fmaf(sp[w][lane], l, sl[w][lane]);
+    p *= sp[w][lane];
+  }
+}
+// After a barrier: what the waves' maps make of `v`, the values of the channels from c on at their beginning.
+template <int VEC, bool REV, int W>
+__device__ __forceinline__ void pass(const float (*sp)[kSlab], const float (*sl)[kSlab], int c, float (&v)[VEC]) {
+  float p[VEC], l[VEC];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    get<VEC>(&sp[REV ? W - 1 - i : i][c], p);
+    get<VEC>(&sl[REV ? W - 1 - i : i][c], l);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) v[e] = fmaf(p[e], v[e], l[e]);
+  }
+}
+
+// A prompt: a workgroup a tile, all sequences' first tiles before their second ones. The state before a tile comes
+// from the state before its kGroup tiles, which the last of those before them published, and the maps of those of its
+// kGroup that are before it: the same composition whenever they come. All of them are workgroups that started earlier, and a
+// tile's map waits for nobody.
+template <bool F32, int VEC, int KIND, int W>
+__global__ __launch_bounds__(W * kWave) void gscan_chain_kernel(ScanParams p) {
+  constexpr uint32_t esz = kEsz<F32>;
+  constexpr int tile = kTile<VEC, W>;
+  constexpr uint32_t kEach = kGroup / W;  // tiles whose maps a wave reads, a channel a lane
+  __shared__ Shared<W> sh;
+  __shared__ uint32_t number;
+  const uint32_t id = take_ticket(p, &number), unit = id % p.units, k = id / p.units;
+  const uint32_t slab = unit % p.slabs, b = unit / p.slabs;
+  const uint32_t lc = threadIdx.x % kLanes<VEC> * VEC, c = slab * kSlab + lc, group = threadIdx.x / kLanes<VEC>;
+  const bool on = c < p.D;
+  const int64_t t0 = (int64_t)k * tile;
+  const uint32_t end = (uint32_t)(p.T - t0 < tile ? p.T - t0 : tile);
+  const int64_t here = length(p, b) - t0;
+  const uint32_t live = here < 0 ? 0 : here < end ? (uint32_t)here : end;
+  const uint32_t at = group * kTok * p.D + c;
+  const uint32_t xoff = on ? at * esz : kNowhere, woff = on ? at * 4 : kNowhere;
+  const int64_t base = ((int64_t)b * p.T + t0) * p.D;
+  const uint64_t row = (uint64_t)p.units * kSlab, word = (uint64_t)unit * kSlab;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  const auto bx = buffer(static_cast<const char*>(p.x) + base * esz, live * p.D * esz);
+  const auto bw = buffer(p.log_w + base, live * p.D * 4);
+  Raw<F32, VEC> rx[kTok];
+  Raw<true, VEC> rw[kTok];
+#pragma unroll
+  for (int i = 0; i < kTok; ++i) {
+    rw[i] = load<true, VEC>(bw, woff + i * p.D * 4);
+    rx[i] = load<F32, VEC>(bx, xoff + i * p.D * esz);
+  }
+  __builtin_amdgcn_sched_barrier(0);  // all loads before the first that is waited for
+  float w[kTok][VEC], a[kTok][VEC], P[VEC], L[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) P[v] = 1.f, L[v] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kTok; ++i)
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+      const float lw = value<true, VEC>(rw[i], v);
+      w[i][v] = decay(lw);
+      a[i][v] = scale<KIND>(lw, w[i][v]) * value<F32, VEC>(rx[i], v);
+      L[v] = fmaf(w[i][v], L[v], a[i][v]);
+      P[v] *= w[i][v];
+    }
+  maps_of_wave<VEC, false>(P, L, sh.p[0], sh.l[0]);
+  lds_barrier();
+  if (wave == 0) {
+    float q, l;
+    whole_map<false, W>(sh.p[0], sh.l[0], q, l);
+    publish(p.there + k * row + word + lane, q, l);
+  }
+  compose<VEC, false, W>(P, L, sh.p[0], sh.l[0]);
+
+  // the state before this tile's kGroup tiles in wave 0's map, as a constant
+  const uint32_t before = k / kGroup * kGroup;
+  // (all looked for at once, without a branch between them: this tile's own in the place of those it does not need)
+  const uint64_t* const own = p.there + k * row + word + lane;
+  auto from = [&](uint32_t i) {
+    if (i == kEach) return wave == 0 && before > 0 ? p.there + (p.tiles + before / kGroup - 1) * row + word + lane : own;
+    const uint32_t j = before + wave * kEach + i;
+    return j < k ? p.there + j * row + word + lane : own;
+  };
+  uint64_t m[kEach + 1];
+#pragma unroll
+  for (uint32_t i = 0; i <= kEach; ++i) m[i] = peek(from(i));
+#pragma unroll
+  for (uint32_t i = 0; i <= kEach; ++i)
+    while (from(i) != own && m[i] == kEmpty) {
+      __builtin_amdgcn_s_sleep(1);
+      m[i] = peek(from(i));
+    }
+  float mp = 1.f, ml = 0.f;
+  if (wave == 0) mp = 0.f, ml = before > 0 ? __uint_as_float((uint32_t)(m[kEach] >> 32)) : p.first_state[word + lane];
+#pragma unroll
+  for (uint32_t i = 0; i < kEach; ++i) {
+    const bool counts = before + wave * kEach + i < k;
+    const float q = counts ? __uint_as_float((uint32_t)m[i]) : 1.f;
+    ml = fmaf(q, ml, counts ? __uint_as_float((uint32_t)(m[i] >> 32)) : 0.f);
+    mp *= q;
+  }
+  sh.p[1][wave][lane] = mp;
+  sh.l[1][wave][lane] = ml;
+  lds_barrier();
+  const bool ends = k + 1 == p.tiles;
+  if (wave == 0 && (ends || k % kGroup == kGroup - 1)) {  // the state behind this tile
+    float q, l, next[1] = {0.f};
+    pass<1, false, W>(sh.p[1], sh.l[1], lane, next);
+    whole_map<false, W>(sh.p[0], sh.l[0], q, l);
+    next[0] = fmaf(q, next[0], l);
+    if (!ends) publish(p.there + (p.tiles + k / kGroup) * row + word + lane, 0.f, next[0]);
+    else if (p.s_out && slab * kSlab + lane < p.D) p.s_out[(int64_t)b * p.D + slab * kSlab + lane] = next[0];
+  }
+  float state[VEC] = {};
+  pass<VEC, false, W>(sh.p[1], sh.l[1], lc, state);
+  auto by = buffer(static_cast<char*>(p.y) + base * esz, live * p.D * esz);
+  float h[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) h[v] = fmaf(P[v], state[v], L[v]);
+#pragma unroll
+  for (int i = 0; i < kTok; ++i) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) h[v] = fmaf(w[i][v], h[v], a[i][v]);
+    store<F32, VEC>(by, xoff + i * p.D * esz, h);
+  }
+  if (live < end) {  // zeros behind the sequence's end
+    const float none[VEC] = {};
+    by = buffer(static_cast<char*>(p.y) + base * esz, end * p.D * esz);
+#pragma unroll 1
+    for (int i = 0; i < kTok; ++i)
+      if (group * kTok + i >= live) store<F32, VEC>(by, xoff + i * p.D * esz, none);
+  }
+}
+
+// Gradients in one pass, for at most kAcross tiles a sequence: a workgroup a tile, a sequence's (of 64 channels) tiles
+// in a row. Every tile needs the maps of those before it and, for the gradient, of those behind it, whose workgroups
+// start later. So a workgroup looks for them `polls` times, some 100 us, and where one is not there (other work holds
+// the compute units) leaves its tile to a second kernel, before which all maps are: no wait depends on another
+// workgroup, and the results are the same.
+constexpr uint32_t kAcross = 64;
+template <bool F32, int VEC, int KIND>
+__device__ __forceinline__ void across(const ScanParams& p, uint32_t id, bool again) {
+  constexpr uint32_t esz = kEsz<F32>;
+  constexpr int tile = kTile<VEC>;
+  constexpr uint32_t kAtOnce = 8;  // maps that a wave looks for at once
+  __shared__ Shared<> sh[2];
+  __shared__ float4 parked[VEC][kThreads];
+  const uint32_t unit = id / p.tiles, k = id % p.tiles;
+  const uint32_t slab = unit % p.slabs, b = unit / p.slabs;
+  const uint32_t lc = threadIdx.x % kLanes<VEC> * VEC, c = slab * kSlab + lc, group = threadIdx.x / kLanes<VEC>;
+  const bool on = c < p.D;
+  const uint32_t at = group * kTok * p.D + c;
+  const uint32_t xoff = on ? at * esz : kNowhere, woff = on ? at * 4 : kNowhere;
+  const int64_t len = length(p, b);
+  const uint64_t row = (uint64_t)p.units * kSlab, word = (uint64_t)unit * kSlab;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t each = (p.tiles + kWaves - 1) / kWaves;  // tiles whose maps a wave reads, in a row, a channel a lane
+
+  const int64_t t0 = (int64_t)k * tile, base = ((int64_t)b * p.T + t0) * p.D;
+  const uint32_t end = (uint32_t)(p.T - t0 < tile ? p.T - t0 : tile);
+  const uint32_t live = len - t0 < 0 ? 0 : len - t0 < end ? (uint32_t)(len - t0) : end;
+  const auto bx = buffer(static_cast<const char*>(p.x) + base * esz, live * p.D * esz);
+  const auto bg = buffer(static_cast<const char*>(p.dy) + base * esz, live * p.D * esz);
+  const auto bw = buffer(p.log_w + base, live * p.D * 4);
+  Raw<F32, VEC> rx[kTok], rg[kTok];
+  Raw<true, VEC> rw[kTok];
+#pragma unroll
+  for (int i = 0; i < kTok; ++i) {
+    rw[i] = load<true, VEC>(bw, woff + i * p.D * 4);
+    rx[i] = load<F32, VEC>(bx, xoff + i * p.D * esz);
+    rg[i] = load<F32, VEC>(bg, xoff + i * p.D * esz);
+  }
+  __builtin_amdgcn_sched_barrier(0);  // all loads before the first that is waited for
+  float w[kTok][VEC], s[kTok][VEC], P[VEC], L[VEC], Q[VEC], R[VEC];
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) P[v] = 1.f, L[v] = R[v] = 0.f;
+#pragma unroll
+  for (int i = 0; i < kTok; ++i) add_token<F32, VEC, KIND>(rx[i], rg[i], rw[i], w[i], s[i], P, L, R);
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) Q[v] = P[v];
+  maps_of_wave<VEC, false>(P, L, sh[0].p[0], sh[0].l[0]);
+  maps_of_wave<VEC, true>(Q, R, sh[0].p[1], sh[0].l[1]);
+  lds_barrier();
+  // what this thread's tokens need of the tile's other threads, out of the registers while others' maps are looked for
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) parked[v][threadIdx.x] = make_float4(P[v], L[v], Q[v], R[v]);
+  float fp = 1.f, fl = 0.f, gp = 1.f, gl = 0.f;
+  if (p.tiles > 1) {
+    if (wave < 2 && !again) {
+      float q, l;
+      if (wave == 0) whole_map<false, kWaves>(sh[0].p[0], sh[0].l[0], q, l);
+      else whole_map<true, kWaves>(sh[0].p[1], sh[0].l[1], q, l);
+      publish((wave == 0 ? p.there : p.back) + k * row + word + lane, q, l);
+    }
+    uint32_t missing = 0;
+    int polls = p.polls;  // for all of them together
+#pragma unroll 1
+    for (uint32_t i0 = 0; i0 < each && missing == 0; i0 += kAtOnce) {
+      // all looked for at once, without a branch between them: this tile's own in the place of those it does not need
+      uint64_t m[kAtOnce];
+      auto tile_of = [&](uint32_t i) { return wave * each + i0 + i; };
+      auto other = [&](uint32_t i) { return (uint32_t)(i0 + i < each) & (uint32_t)(tile_of(i) < p.tiles) & (uint32_t)(tile_of(i) != k); };
+      auto from = [&](uint32_t i) {
+        const uint32_t o = other(i) ? tile_of(i) : k;
+        return (o < k ? p.there : p.back) + o * row + word + lane;
+      };
+#pragma unroll 1
+      for (;; --polls) {
+#pragma unroll
+        for (uint32_t i = 0; i < kAtOnce; ++i) m[i] = peek(from(i));
+        missing = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < kAtOnce; ++i) missing = missing | (other(i) & (uint32_t)(m[i] == kEmpty));
+        if (missing == 0 || polls <= 0) break;
+        __builtin_amdgcn_s_sleep(4);
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < kAtOnce; ++i) {
+        const float q = __uint_as_float((uint32_t)m[i]), l = __uint_as_float((uint32_t)(m[i] >> 32));
+        const bool in_front = other(i) & (uint32_t)(tile_of(i) < k), behind = other(i) & (uint32_t)(tile_of(i) > k);
+        fl = fmaf(in_front ? q : 1.f, fl, in_front ? l : 0.f);
+        fp *= in_front ? q : 1.f;
+        gl = fmaf(gp, behind ? l : 0.f, gl);  // what comes back passes the tiles in front last
+        gp *= behind ? q : 1.f;
+      }
+    }
+    if (__syncthreads_or((int)missing)) {
+      if (threadIdx.x == 0) p.left[1 + atomicAdd(p.left, 1u)] = id;
+      return;
+    }
+  }
+
+  sh[1].p[0][wave][lane] = fp;
+  sh[1].l[0][wave][lane] = fl;
+  sh[1].p[1][wave][lane] = gp;
+  sh[1].l[1][wave][lane] = gl;
+  float state[VEC] = {}, grad[VEC] = {}, h[VEC], g[VEC], end_grad = 0.f;
+  const uint32_t lane_c = slab * kSlab + lane;
+  const int64_t of_b = (int64_t)b * p.D;
+  if (p.tiles > 1) {
+    get<VEC>(p.first_state + word + lc, state);
+    get<VEC>(p.last_grad + word + lc, grad);
+    end_grad = p.last_grad[word + lane];
+  } else {
+    if (on && p.s_in) get<VEC>(p.s_in + of_b + c, state);
+    if (on && p.ds_out) get<VEC>(p.ds_out + of_b + c, grad);
+    if (lane_c < p.D && p.ds_out) end_grad = p.ds_out[of_b + lane_c];
+  }
+  __syncthreads();  // ds_out has been read, before ds_in, which it may be, is written
+  if (k == 0 && wave == 0 && p.ds_in && lane_c < p.D) {
+    float q, l, d[1] = {end_grad};
+    pass<1, true, kWaves>(sh[1].p[1], sh[1].l[1], lane, d);
+    whole_map<true, kWaves>(sh[0].p[1], sh[0].l[1], q, l);
+    p.ds_in[of_b + lane_c] = fmaf(q, d[0], l);
+  }
+  pass<VEC, false, kWaves>(sh[1].p[0], sh[1].l[0], lc, state);
+  pass<VEC, true, kWaves>(sh[1].p[1], sh[1].l[1], lc, grad);
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) {
+    const float4 f = parked[v][threadIdx.x];
+    P[v] = f.x, L[v] = f.y, Q[v] = f.z, R[v] = f.w;
+  }
+  compose<VEC, false, kWaves>(P, L, sh[0].p[0], sh[0].l[0]);
+  compose<VEC, true, kWaves>(Q, R, sh[0].p[1], sh[0].l[1]);
+#pragma unroll
+  for (int v = 0; v < VEC; ++v) h[v] = fmaf(P[v], state[v], L[v]), g[v] = fmaf(Q[v], grad[v], R[v]);
+  write_grads<F32, VEC, KIND>(p, base, end, live, group, xoff, woff, rx, rg, w, s, h, g);
+}
+
+template <bool F32, int VEC, int KIND>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) void gscan_across_kernel(ScanParams p) {
+  across<F32, VEC, KIND>(p, p.first + blockIdx.x, false);
+}
+template <bool F32, int VEC, int KIND>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) void gscan_left_kernel(ScanParams p) {
+  for (uint32_t i = blockIdx.x; i < *p.left; i += gridDim.x) {
+    across<F32, VEC, KIND>(p, p.left[1 + i], true);
+    __syncthreads();  // LDS is written again
   }
 }
 
@@ -442,8 +793,8 @@ __global__ __launch_bounds__(1024) void gscan_join_kernel(ScanParams p) {
   const uint32_t b = id / p.slabs, c = id % p.slabs * kSlab + (threadIdx.x & 63), wave = threadIdx.x >> 6;
   const bool on = c < p.D;
   const int64_t bd = (int64_t)b * p.D + (on ? c : 0);
-  const uint32_t each = (p.segs + 15) / 16, s0 = wave * each < p.segs ? wave * each : p.segs;
-  const uint32_t s1 = s0 + each < p.segs ? s0 + each : p.segs;
+  const uint32_t each = (p.tiles + 15) / 16, s0 = wave * each < p.tiles ? wave * each : p.tiles;
+  const uint32_t s1 = s0 + each < p.tiles ? s0 + each : p.tiles;
   float P = 1.f, L = 0.f, R = 0.f, Q = 1.f;
 #pragma unroll 4
   for (uint32_t s = s0; s < s1; ++s) {
@@ -533,7 +884,27 @@ ScanParams params(const GscanCall& c) {
   p.dy = c.dy, p.dx = c.dx, p.dlog_w = c.dlog_w, p.ds_out = c.ds_out, p.ds_in = c.ds_in;
   p.T = c.T, p.BD = c.B * c.D, p.B = (uint32_t)c.B, p.D = (uint32_t)c.D;
   p.slabs = (p.D + kSlab - 1) / kSlab;
+  p.units = p.B * p.slabs;
   return p;
+}
+
+// Polls of a workgroup for the others' maps before it leaves its tile to the second kernel.
+std::atomic<int> g_polls{64};
+
+// The words that workgroups pass on, in the workspace: `rows` of them for each unit's 64 channels, a second array of as
+// many for the gradient, copies of the states, and the number of workgroups. The caller holds the operators' lock.
+hipError_t words(ScanParams& p, const GscanCall& c, uint64_t rows, bool back) {
+  const uint64_t row = (uint64_t)p.units * kSlab, n = rows * row * (back ? 2 : 1);
+  void* ws = nullptr;
+  const size_t list = back ? ((size_t)p.units * p.tiles + 1) * 4 : 4;
+  const hipError_t e = device_workspace(c.stream, n * 8 + 2 * row * 4 + 4 + list, &ws, kWorkspaceOperators);
+  if (e != hipSuccess) return e;
+  p.there = static_cast<uint64_t*>(ws), p.back = back ? p.there + rows * row : nullptr, p.words = n;
+  p.first_state = reinterpret_cast<float*>(p.there + n), p.last_grad = back ? p.first_state + row : nullptr;
+  p.ticket = reinterpret_cast<uint32_t*>(p.first_state + 2 * row), p.left = p.ticket + 1;
+  p.polls = g_polls.load(std::memory_order_relaxed);
+  const uint64_t blocks = (n / 4 + 255) / 256;
+  return start(reinterpret_cast<const void*>(&gscan_empty_kernel), blocks < 1024 ? (blocks ? blocks : 1) : 1024, 256, p, c.stream);
 }
 
 template <bool F32, int VEC, int KIND>
@@ -541,28 +912,19 @@ struct Kernels {
   static constexpr int tile = kTile<VEC>;
   static hipError_t prefill(const GscanCall& c) {
     ScanParams p = params(c);
-    const int64_t tiles = (c.T + tile - 1) / tile, units = c.B * p.slabs;
-    // Segments: a workgroup for each unit leaves compute units idle where there are fewer than 256 of them.
-    int64_t segs = units >= 256 ? 1 : (512 + units - 1) / units;
-    const int64_t most = tiles / 2;
-    segs = segs < most ? segs : most;
-    segs = segs < 1 ? 1 : segs;
-    p.seg_tokens = (tiles + segs - 1) / segs * tile;
-    p.segs = (uint32_t)(tiles == 0 ? 1 : (c.T + p.seg_tokens - 1) / p.seg_tokens);
-    const void* fn = reinterpret_cast<const void*>(&gscan_kernel<F32, VEC, KIND, false>);
-    if (p.segs == 1) return start(fn, (uint64_t)units, kThreads, p, c.stream);
+    const uint32_t tiles = (uint32_t)((c.T + tile - 1) / tile);
+    // Walking takes 2 us a tile or, from 192 units on, the memory's time; passing maps on 3 us for emptying their words
+    // and then the memory's time, at some 5 TB/s with any number of units: B=8 T=4096 D=1024 (128 units) 72 and 54 us,
+    // B=1 T=8192 D=768 (12) 134 and 19, B=16 T=2048 D=768 (192) 41 and 44, B=1 T=256 D=768 7.2 and 9.4, B=8 T=4096
+    // D=4096 (512) 219 and 205.
+    if (tiles <= 3 || (p.units >= 192 && tiles <= 16))
+      return start(reinterpret_cast<const void*>(&gscan_walk_kernel<F32, VEC, KIND>), p.units, kThreads, p, c.stream);
+    p.tiles = (uint32_t)((c.T + kTile<VEC, kChainWaves> - 1) / kTile<VEC, kChainWaves>);
     std::lock_guard<std::mutex> lock(operators_mutex());
-    void* ws = nullptr;
-    const uint32_t nsegs = p.segs;
-    hipError_t e = device_workspace(c.stream, (size_t)2 * nsegs * p.BD * 4, &ws, kWorkspaceOperators);
+    const hipError_t e = words(p, c, (uint64_t)p.tiles + (p.tiles + kGroup - 1) / kGroup, false);
     if (e != hipSuccess) return e;
-    p.p = static_cast<float*>(ws), p.l = p.p + nsegs * p.BD;
-    p.segs = nsegs - 1;  // nothing starts behind the last
-    e = start(reinterpret_cast<const void*>(&gscan_kernel<F32, VEC, KIND, true>), (uint64_t)units * p.segs, kThreads, p,
-              c.stream);
-    if (e != hipSuccess) return e;
-    p.segs = nsegs;
-    return start(fn, (uint64_t)units * p.segs, kThreads, p, c.stream);
+    return start(reinterpret_cast<const void*>(&gscan_chain_kernel<F32, VEC, KIND, kChainWaves>), (uint64_t)p.units * p.tiles,
+                 kChainWaves * kWave, p, c.stream);
   }
   static hipError_t step(const GscanCall& c) {
     const ScanParams p = params(c);
@@ -572,19 +934,29 @@ struct Kernels {
   }
   static hipError_t backward(const GscanCall& c) {
     ScanParams p = params(c);
-    p.segs = (uint32_t)((c.T + tile - 1) / tile);
-    const uint64_t units = (uint64_t)p.B * p.slabs;
+    p.tiles = (uint32_t)((c.T + tile - 1) / tile);
+    const uint64_t blocks = (uint64_t)p.units * p.tiles;
     const void* join = reinterpret_cast<const void*>(&gscan_join_kernel);
-    if (p.segs == 0) return start(join, units, 1024, p, c.stream);
+    const void* one_pass = reinterpret_cast<const void*>(&gscan_across_kernel<F32, VEC, KIND>);
+    if (p.tiles == 0) return start(join, p.units, 1024, p, c.stream);
+    if (p.tiles == 1) return start(one_pass, blocks, kThreads, p, c.stream);
     std::lock_guard<std::mutex> lock(operators_mutex());
+    hipError_t e = hipSuccess;
+    if (p.tiles <= kAcross) {
+      e = words(p, c, p.tiles, true);
+      if (e == hipSuccess) e = start(one_pass, blocks, kThreads, p, c.stream);
+      if (e == hipSuccess)
+        e = start(reinterpret_cast<const void*>(&gscan_left_kernel<F32, VEC, KIND>), blocks < 256 ? blocks : 256, kThreads, p, c.stream);
+      return e;
+    }
     void* ws = nullptr;
-    hipError_t e = device_workspace(c.stream, (size_t)3 * p.segs * p.BD * 4, &ws, kWorkspaceOperators);
+    e = device_workspace(c.stream, (size_t)3 * p.tiles * p.BD * 4, &ws, kWorkspaceOperators);
     if (e != hipSuccess) return e;
-    p.p = static_cast<float*>(ws), p.l = p.p + p.segs * p.BD, p.r = p.l + p.segs * p.BD;
-    e = start(reinterpret_cast<const void*>(&gscan_grad_kernel<F32, VEC, KIND, true>), units * p.segs, kThreads, p, c.stream);
-    if (e == hipSuccess) e = start(join, units, 1024, p, c.stream);
+    p.p = static_cast<float*>(ws), p.l = p.p + p.tiles * p.BD, p.r = p.l + p.tiles * p.BD;
+    e = start(reinterpret_cast<const void*>(&gscan_grad_kernel<F32, VEC, KIND, true>), blocks, kThreads, p, c.stream);
+    if (e == hipSuccess) e = start(join, p.units, 1024, p, c.stream);
     if (e == hipSuccess)
-      e = start(reinterpret_cast<const void*>(&gscan_grad_kernel<F32, VEC, KIND, false>), units * p.segs, kThreads, p, c.stream);
+      e = start(reinterpret_cast<const void*>(&gscan_grad_kernel<F32, VEC, KIND, false>), blocks, kThreads, p, c.stream);
     return e;
   }
 };
@@ -609,6 +981,8 @@ hipError_t dispatch(const GscanCall& c, Op op) {
 }
 
 }  // namespace
+
+void set_gscan_polls(int polls) { g_polls.store(polls, std::memory_order_relaxed); }
 
 hipError_t launch_gscan_prefill(const GscanCall& c) { return dispatch(c, Op::kPrefill); }
 hipError_t launch_gscan_step(const GscanCall& c) { return dispatch(c, Op::kStep); }

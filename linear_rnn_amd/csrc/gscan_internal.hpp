@@ -27,5 +27,8 @@ struct GscanCall {
 hipError_t launch_gscan_prefill(const GscanCall& c);
 hipError_t launch_gscan_step(const GscanCall& c);
 hipError_t launch_gscan_backward(const GscanCall& c);
+// How often a workgroup of the backward looks for the others' maps before it leaves its tile to a second kernel (results
+// are the same).
+void set_gscan_polls(int polls);
 
 }  // namespace rwkv7

@@ -25,7 +25,8 @@ def cuda(x):
 # one token and tile edges (128 tokens; 32 where D is no multiple of 4), widths below, at and behind 64 channels, odd
 # ones, few channels over many tokens (segments), many sequences (none)
 SIZES = [(1, 1, 1), (2, 1, 64), (1, 2, 3), (2, 7, 5), (2, 31, 66), (1, 33, 65), (3, 127, 64), (2, 128, 68), (2, 129, 128),
-         (1, 257, 130), (2, 300, 1000), (1, 3001, 64), (5, 1000, 4), (1, 700, 33), (300, 40, 20), (130, 70, 130), (4, 0, 16)]
+         (1, 257, 130), (2, 300, 1000), (1, 3001, 64), (5, 1000, 4), (1, 700, 33), (300, 40, 20), (130, 70, 130), (1, 4500, 96), (1, 9000, 24), (1, 4500, 33),
+         (4, 0, 16)]
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
@@ -290,3 +291,40 @@ def test_outputs_on_another_stream(torch):
         y1, s1 = wkv.gscan(d["x"], d["log_w"], d["state_in"], stream=stream)
     stream.synchronize()
     assert torch.equal(y, y1) and torch.equal(s, s1)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("B,T,D", [(1, 900, 130), (2, 8192, 64), (1, 600, 7), (40, 4000, 132)])
+def test_gradients_without_waiting(torch, B, T, D, dtype):
+    """A workgroup that looks for the other tiles' maps only once leaves its tile to a second kernel: the same bits."""
+    import ctypes
+    polls = getattr(ctypes.CDLL(wkv.LIB_PATH), "_ZN5rwkv715set_gscan_pollsEi")
+    say("gscan without waiting", B, T, D, dtype)
+    d = cuda(ref.make(B, T, D, getattr(torch, dtype), seed=12))
+    want = wkv.gscan_backward(d["x"], d["log_w"], d["dy"], d["state_in"], dstate_out=d["dstate_out"], input=KIND["mix"])
+    torch.cuda.synchronize()
+    polls(0)
+    try:
+        for _ in range(3):
+            got = wkv.gscan_backward(d["x"], d["log_w"], d["dy"], d["state_in"], dstate_out=d["dstate_out"], input=KIND["mix"])
+            torch.cuda.synchronize()
+            assert all(torch.equal(got[n], want[n]) for n in want)
+    finally:
+        polls(64)
+
+
+def test_the_same_call_gives_the_same_bits(torch):
+    """Whatever order the workgroups come in: many calls, alone and beside other work on the device."""
+    d = cuda(ref.make(3, 5000, 100, torch.bfloat16, seed=13))
+    y, s = wkv.gscan(d["x"], d["log_w"], d["state_in"], input=KIND["norm"])
+    g = wkv.gscan_backward(d["x"], d["log_w"], d["dy"], d["state_in"], dstate_out=d["dstate_out"], input=KIND["norm"])
+    torch.cuda.synchronize()
+    other, a = torch.cuda.Stream(), torch.randn(2048, 2048, device="cuda")
+    for i in range(20):
+        if i % 2:
+            with torch.cuda.stream(other):
+                a @ a
+        y1, s1 = wkv.gscan(d["x"], d["log_w"], d["state_in"], input=KIND["norm"])
+        g1 = wkv.gscan_backward(d["x"], d["log_w"], d["dy"], d["state_in"], dstate_out=d["dstate_out"], input=KIND["norm"])
+        assert torch.equal(y1, y) and torch.equal(s1, s) and all(torch.equal(g1[n], g[n]) for n in g)
+    torch.cuda.synchronize()
