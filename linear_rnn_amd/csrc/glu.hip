@@ -224,6 +224,7 @@ struct Product {
 struct Plan {
   Shape shape;
   int splits[2];
+  float us;
 };
 
 int compute_units() {
@@ -262,8 +263,7 @@ float finish(const int64_t (&n)[2], const float (&us)[2], int64_t slots) {
 Plan plan(const ShapeInfo (&shapes)[kShapes], const Product (&job)[2]) {
   constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
   const int cus = compute_units();
-  Plan best{kLarge, {1, 1}};
-  float least = 0.f;
+  Plan best{kLarge, {1, 1}, 0.f};
   bool any = false;
   for (int s = 0; s < kShapes; ++s) {
     const ShapeInfo& f = shapes[s];
@@ -275,7 +275,7 @@ Plan plan(const ShapeInfo (&shapes)[kShapes], const Product (&job)[2]) {
         const int64_t n[2] = {tiles[0] * a, tiles[1] * b};
         const float us[2] = {(job[0].steps + a - 1) / a * f.step_us + f.ends_us, (job[1].steps + b - 1) / b * f.step_us + f.ends_us};
         const float t = finish(n, us, slots) + job[0].join_us(a) + job[1].join_us(b);
-        if (!any || t < least) any = true, least = t, best = Plan{(Shape)s, {a, b}};
+        if (!any || t < best.us) any = true, best = Plan{(Shape)s, {a, b}, t};
       }
     }
   }
@@ -392,21 +392,37 @@ int second_of(bool f32, int s) { return f32 ? kPairs[s][1] : 0; }
 
 int64_t steps_of(int64_t K, int segments) { return (K + kBK - 1) / kBK * segments; }
 
-// Few rows, whose weights are read once by a kernel of their own. It wants rows of whole 16 bytes.
-bool few_rows(const GluCall& c) { return c.M <= (c.f32 ? 128 : 32) && c.D % 8 == 0 && c.F % 8 == 0; }
-template <bool F32>
+// Few rows go by a kernel that reads the weights once (where rows are of whole 16 bytes): in bfloat16 up to the 32 that
+// it takes at a time (33 rows of D=2048 F=5504 34 us and 21 by tiles, 32 rows 21 and 22, 17 of D=4096 F=10944 30 and
+// 36). In float32 more, 32 at a time by the float32 matrix instructions at some 75 TFLOP/s, as long as that is
+// estimated to take less than tiles and the copies in pieces: D=4096 F=10944 192 rows 406 us and 525 by tiles, 256
+// 502 and 480; D=768 F=2048 256 rows 24 and 35.
+bool few_rows(const GluCall& c, const Plan& tiles) {
+  if (c.D % 8 != 0 || c.F % 8 != 0) return false;
+  if (!c.f32) return c.M <= 32;
+  const float few = 6.f + 4.f * whole(c.M, 32) * c.D * c.F / 75e6f;
+  const float copies = 8.f + (2.f * c.D * c.F + (float)c.M * c.D) * 10 / 4e6f;
+  return few < tiles.us + copies;
+}
+template <bool F32, int C>
 hipError_t forward_few(const GluCall& c) {
   const FewParams p{c.x, c.w_gate, c.w_up, c.h, c.gate, c.up, (int32_t)c.M, (int32_t)c.D, (int32_t)c.F, c.act};
-  const void* fn = c.M <= 16 ? reinterpret_cast<const void*>(&glu_few_kernel<F32, 1>)
-                           : reinterpret_cast<const void*>(&glu_few_kernel<F32, 2>);
-  return start(fn, dim3((uint32_t)((c.F + kFewCols - 1) / kFewCols), (uint32_t)((c.M + 31) / 32)), 64 * kFewWaves, 0, p, c.stream);
+  const void* fn = c.M <= 16 ? reinterpret_cast<const void*>(&glu_few_kernel<F32, C, 1>)
+                             : reinterpret_cast<const void*>(&glu_few_kernel<F32, C, 2>);
+  return start(fn, dim3((uint32_t)((c.F + 16 * C - 1) / (16 * C)), (uint32_t)((c.M + 31) / 32)), 64 * kFewWaves, 0, p, c.stream);
+}
+// 64 columns a workgroup; float32 half as many up to F=8192, where there are too few workgroups else (1 row of D=2048
+// F=5504 23 us and 17, of D=4096 F=10944 65 and 76; in bfloat16 that makes half lines of a row, 12.6 and 21).
+hipError_t forward_few(const GluCall& c) {
+  if (!c.f32) return forward_few<false, 4>(c);
+  return c.F <= 8192 ? forward_few<true, 2>(c) : forward_few<true, 4>(c);
 }
 
 hipError_t forward(const GluCall& c) {
-  if (few_rows(c)) return c.f32 ? forward_few<true>(c) : forward_few<false>(c);
   Matrix x{c.x, c.M, c.D, c.f32}, wg{c.w_gate, c.D, c.F, c.f32}, wu{c.w_up, c.D, c.F, c.f32};
   const Product job[2] = {{c.M, c.F, 1, steps_of(c.D, pairs(c.f32))}, {0, 0, 0, 0}};
   const Plan how = plan(kForwardShapes, job);
+  if (few_rows(c, how)) return forward_few(c);
   const int splits = how.splits[0];
   Parts parts;
   for (Matrix* m : {&x, &wg, &wu}) m->place(parts);

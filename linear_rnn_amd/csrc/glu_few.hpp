@@ -1,9 +1,9 @@
 // The gated linear unit of a few rows (a decode step): the weights are read once, which is all that counts.
 //
-// A workgroup takes 64 columns of both weights, its waves the blocks of k in turn. Weights go from memory to registers
-// and from there to the matrix cores, the rows of x as the other operand (up to 16 a tile): a lane reads 4 columns of
-// the rows of k that are its part of an operand, so column c of its 4 is an operand whose 16 rows are the columns
-// 4 li + c. No LDS until the waves' sums meet there.
+// A workgroup takes 16 C columns of both weights, its waves the blocks of k in turn. Weights go from memory to registers
+// and from there to the matrix cores, the rows of x as the other operand (up to 16 a tile): a lane reads C columns of
+// the rows of k that are its part of an operand, so column c of its C is an operand whose 16 rows are the columns
+// C li + c. No LDS until the waves' sums meet there.
 #pragma once
 
 #include "glu_gemm.hpp"
@@ -12,7 +12,6 @@ namespace rwkv7 {
 namespace glu {
 
 constexpr int kFewWaves = 8;
-constexpr int kFewCols = 64;  // of a workgroup
 
 struct FewParams {
   const void* x;  // [M, D]
@@ -25,13 +24,25 @@ struct FewParams {
   int act;
 };
 
-// acc[weights][c] += columns 4 li + c (rows of the result) times rows m of x (its columns), over k0 .. k0 + kBlock - 1.
-template <bool F32, int MT>
+// C columns of a row as loaded.
+template <int BYTES>
+struct Words {
+  uint32_t u[BYTES / 4];
+};
+template <int BYTES>
+__device__ __forceinline__ Words<BYTES> load_words(__amdgpu_buffer_rsrc_t b, uint32_t off) {
+  if constexpr (BYTES == 16) return __builtin_bit_cast(Words<16>, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+  else if constexpr (BYTES == 8) return __builtin_bit_cast(Words<8>, __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0));
+  else return __builtin_bit_cast(Words<4>, __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0));
+}
+
+// acc[weights][c] += columns C li + c (rows of the result) times rows m of x (its columns), over k0 .. k0 + kBlock - 1.
+template <bool F32, int C, int MT>
 struct FewBlock;
-template <int MT>
-struct FewBlock<false, MT> {
+template <int C, int MT>
+struct FewBlock<false, C, MT> {
   static constexpr int kBlock = 32;
-  uint2 w[2][8];  // rows k0 + 8 q + j
+  Words<2 * C> w[2][8];  // rows k0 + 8 q + j
   bf16x8 x[MT];
   __device__ __forceinline__ void load(const FewParams& p, int k0, int col, int lane) {
     const int q = lane >> 4, li = lane & 15;
@@ -41,9 +52,9 @@ struct FewBlock<false, MT> {
     const auto bu = linattn::buffer(static_cast<const uint16_t*>(p.w_up) + at, bytes);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t off = ((uint32_t)(8 * q + j) * p.F + col + 4 * li) * 2;
-      w[0][j] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(bg, off, 0, 0));
-      w[1][j] = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(bu, off, 0, 0));
+      const uint32_t off = ((uint32_t)(8 * q + j) * p.F + col + C * li) * 2;
+      w[0][j] = load_words<2 * C>(bg, off);
+      w[1][j] = load_words<2 * C>(bu, off);
     }
     const int k = k0 + 8 * q;
 #pragma unroll
@@ -54,15 +65,15 @@ struct FewBlock<false, MT> {
       x[t] = __builtin_bit_cast(bf16x8, v);
     }
   }
-  __device__ __forceinline__ void multiply(f32x4 (&acc)[2][4][MT]) const {
+  __device__ __forceinline__ void multiply(f32x4 (&acc)[2][C][MT]) const {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < C; ++c) {
         u32x4 a;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t lo = c < 2 ? w[i][2 * j].x : w[i][2 * j].y, hi = c < 2 ? w[i][2 * j + 1].x : w[i][2 * j + 1].y;
+          const uint32_t lo = w[i][2 * j].u[c >> 1], hi = w[i][2 * j + 1].u[c >> 1];
           a[j] = __builtin_amdgcn_perm(hi, lo, c & 1 ? 0x07060302u : 0x05040100u);
         }
 #pragma unroll
@@ -71,10 +82,10 @@ struct FewBlock<false, MT> {
       }
   }
 };
-template <int MT>
-struct FewBlock<true, MT> {
+template <int C, int MT>
+struct FewBlock<true, C, MT> {
   static constexpr int kBlock = 16;
-  f32x4 w[2][4];  // rows k0 + 4 q + j
+  Words<4 * C> w[2][4];  // rows k0 + 4 q + j
   f32x4 x[MT];
   __device__ __forceinline__ void load(const FewParams& p, int k0, int col, int lane) {
     const int q = lane >> 4, li = lane & 15;
@@ -84,9 +95,9 @@ struct FewBlock<true, MT> {
     const auto bu = linattn::buffer(static_cast<const float*>(p.w_up) + at, bytes);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t off = ((uint32_t)(4 * q + j) * p.F + col + 4 * li) * 4;
-      w[0][j] = __builtin_bit_cast(f32x4, linattn::load16(bg, off));
-      w[1][j] = __builtin_bit_cast(f32x4, linattn::load16(bu, off));
+      const uint32_t off = ((uint32_t)(4 * q + j) * p.F + col + C * li) * 4;
+      w[0][j] = load_words<4 * C>(bg, off);
+      w[1][j] = load_words<4 * C>(bu, off);
     }
     const int k = k0 + 4 * q;
 #pragma unroll
@@ -96,26 +107,26 @@ struct FewBlock<true, MT> {
       if (m < p.M && k < p.D) x[t] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.x) + (int64_t)m * p.D + k);
     }
   }
-  __device__ __forceinline__ void multiply(f32x4 (&acc)[2][4][MT]) const {
+  __device__ __forceinline__ void multiply(f32x4 (&acc)[2][C][MT]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < C; ++c)
 #pragma unroll
           for (int t = 0; t < MT; ++t)
-            acc[i][c][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(w[i][j][c], x[t][j], acc[i][c][t], 0, 0, 0);
+            acc[i][c][t] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[i][j].u[c]), x[t][j], acc[i][c][t], 0, 0, 0);
   }
 };
 
-// A lane's element i of acc[..][c]: column 4 (4 q + i) + c, row m = li of x.
-template <bool F32, int MT>
+// A lane's element i of acc[..][c]: column C (4 q + i) + c, row m = li of x.
+template <bool F32, int C, int MT>
 __global__ __launch_bounds__(64 * kFewWaves) void glu_few_kernel(FewParams p) {
-  constexpr int kRow = kFewCols + 4;  // floats, so that lanes of different rows meet different banks
+  constexpr int kCols = 16 * C, kRow = kCols + 4;  // floats, so that lanes of different rows meet different banks
   __shared__ float sums[kFewWaves][16][kRow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = blockIdx.x * kFewCols;
+  const int col = blockIdx.x * kCols;
   const int64_t m0 = (int64_t)blockIdx.y * 16 * MT;  // its rows
   {
     constexpr int esz = F32 ? 4 : 2;
@@ -124,14 +135,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void glu_few_kernel(FewParams p) {
     if (p.gate) p.gate = static_cast<char*>(p.gate) + m0 * p.F * esz, p.up = static_cast<char*>(p.up) + m0 * p.F * esz;
     p.M = p.M - (int)m0 < 16 * MT ? p.M - (int)m0 : 16 * MT;
   }
-  f32x4 acc[2][4][MT];
+  f32x4 acc[2][C][MT];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[i][c][t] = linattn::zero4();
-  using Block = FewBlock<F32, MT>;
+  using Block = FewBlock<F32, C, MT>;
   constexpr int kStride = kFewWaves * Block::kBlock;
   Block now, next;
   int k = wave * Block::kBlock;
@@ -149,30 +160,29 @@ __global__ __launch_bounds__(64 * kFewWaves) void glu_few_kernel(FewParams p) {
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     if (16 * t >= p.M) break;
-    // up to two (row, column) pairs a thread: threads 0 .. 63 the columns of a row
-    constexpr int kEach = 16 * kFewCols / (64 * kFewWaves);
+    // (row, column) pairs, threads side by side the columns of a row
+    constexpr int kEach = 16 * kCols / (64 * kFewWaves), kRows = 16 / kEach;
+    const int mine = threadIdx.x / kCols, n0 = threadIdx.x % kCols;
     float v[2][kEach];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       __syncthreads();
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const f32x4 o = {acc[i][0][t][r], acc[i][1][t][r], acc[i][2][t][r], acc[i][3][t][r]};
-        *reinterpret_cast<f32x4*>(&sums[wave][li][4 * (4 * q + r)]) = o;
-      }
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c) sums[wave][li][C * (4 * q + r) + c] = acc[i][c][t][r];
       __syncthreads();
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
-        const int m = (threadIdx.x >> 6) + e * kFewWaves, n = threadIdx.x & 63;
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kFewWaves; ++w) s += sums[w][m][n];
+        for (int w = 0; w < kFewWaves; ++w) s += sums[w][mine + e * kRows][n0];
         v[i][e] = s;
       }
     }
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
-      const int m = 16 * t + (threadIdx.x >> 6) + e * kFewWaves, n = col + (threadIdx.x & 63);
+      const int m = 16 * t + mine + e * kRows, n = col + n0;
       if (m >= p.M || n >= p.F) continue;
       const int64_t at = (int64_t)m * p.F + n;
       const float h = activation(v[0][e], p.act) * v[1][e];

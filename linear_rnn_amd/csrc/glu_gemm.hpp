@@ -218,8 +218,9 @@ __device__ __forceinline__ void tile_product(const GemmParams& p, uint32_t block
     f.b[j] = fragment<BCOLS>(lds + buf * kBuf + kA + (EPI == kGlu && j >= TN / 2 ? kB : 0), col, h, lane);
   };
   // The products of row i of the wave's tiles, behind what is read for row i of the next half. Two workgroups of the
-  // small shapes share a compute unit and fill each other's gaps: they read all first (4% faster there).
-  constexpr bool kInRows = TM >= 8;
+  // small shape share a compute unit and fill each other's gaps: they read all first (4% faster there, 4 to 8% slower
+  // with a workgroup of 8 waves).
+  constexpr bool kInRows = NW >= 8;
   auto row = [&](const Half& f, Half& next, int buf, int h, int i) {
     if (kInRows || i == 0) {
 #pragma unroll

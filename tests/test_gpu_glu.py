@@ -34,7 +34,8 @@ def backward(d, act, **kw):
 # below, at and behind a tile, odd
 SIZES = [(1, 8, 8), (1, 1, 1), (3, 7, 5), (1, 768, 2048), (5, 64, 136), (16, 40, 24), (17, 200, 264), (33, 64, 100), (64, 96, 130),
          (65, 72, 256), (128, 128, 128), (129, 1000, 136), (255, 200, 129), (256, 256, 512), (257, 264, 520), (300, 33, 1000),
-         (1000, 512, 1365), (2000, 16, 72)]
+         (1000, 512, 1365), (2000, 16, 72), (20, 72, 8200),
+         (100, 768, 2048), (400, 768, 1000)]
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
