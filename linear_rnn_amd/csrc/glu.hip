@@ -235,9 +235,15 @@ int compute_units() {
   return n;
 }
 
-// When the last of two kinds of workgroups is done, of which `slots` run at a time, the first kind before the second:
+// When the last of two kinds of workgroups is done, of which `slots` run at a time, the longer kind before the other:
 // n[i] of them of us[i] each.
-float finish(const int64_t (&n)[2], const float (&us)[2], int64_t slots) {
+float finish(int64_t (&n)[2], float (&us)[2], int64_t slots) {
+  if (us[1] > us[0]) {
+    const int64_t k = n[0];
+    n[0] = n[1], n[1] = k;
+    const float t = us[0];
+    us[0] = us[1], us[1] = t;
+  }
   // slots that are free early and late behind the first kind
   const int64_t late = n[0] % slots;
   float t[2] = {n[0] / slots * us[0], (n[0] / slots + 1) * us[0]};
@@ -272,8 +278,8 @@ Plan plan(const ShapeInfo (&shapes)[kShapes], const Product (&job)[2]) {
       if (a > 1 && (tiles[0] * a > 4 * slots || job[0].steps < 4 * a)) break;
       for (int b : kSplits) {
         if (b > 1 && (tiles[1] * b > 4 * slots || job[1].steps < 4 * b)) break;
-        const int64_t n[2] = {tiles[0] * a, tiles[1] * b};
-        const float us[2] = {(job[0].steps + a - 1) / a * f.step_us + f.ends_us, (job[1].steps + b - 1) / b * f.step_us + f.ends_us};
+        int64_t n[2] = {tiles[0] * a, tiles[1] * b};
+        float us[2] = {(job[0].steps + a - 1) / a * f.step_us + f.ends_us, (job[1].steps + b - 1) / b * f.step_us + f.ends_us};
         const float t = finish(n, us, slots) + job[0].join_us(a) + job[1].join_us(b);
         if (!any || t < best.us) any = true, best = Plan{(Shape)s, {a, b}, t};
       }
@@ -315,8 +321,9 @@ hipError_t grad_products(GradProducts p, bool x, bool w, hipStream_t stream) {
   static std::atomic<uint64_t> granted{0};
   const hipError_t e = grant<lds>(fn, granted);
   if (e != hipSuccess) return e;
-  p.first = x ? set_tiles<BM, BN>(p.x) : 0;
-  const uint32_t blocks = p.first + (w ? set_tiles<BM, BN>(p.w) : 0);
+  const uint32_t nx = x ? set_tiles<BM, BN>(p.x) : 0, nw = w ? set_tiles<BM, BN>(p.w) : 0;
+  p.first = p.w_first ? nw : nx;
+  const uint32_t blocks = nx + nw;
   return start(fn, dim3(blocks), 64 * WM * WN, lds, p, stream);
 }
 hipError_t forward_products(const GemmParams& p, Shape s, hipStream_t stream) {
@@ -491,6 +498,7 @@ hipError_t backward(const GluCall& c) {
   if (e != hipSuccess) return e;
 
   GradProducts p{};
+  p.w_first = (job[1].steps + sw - 1) / sw > (job[0].steps + sx - 1) / sx;
   JoinParams j{};
   int joins = 0;
   uint32_t blocks = 0;

@@ -308,16 +308,19 @@ template <int WM, int WN, int TM, int TN, int NB>
 __global__ __launch_bounds__(64 * WM * WN) void glu_forward_kernel(GemmParams p) {
   tile_product<false, true, WM, WN, TM, TN, NB, kGlu>(p, blockIdx.x);
 }
-// The products of the backward side by side: the input's gradient (operands in rows), and behind `first` the weights'
-// (operands in columns).
+// The products of the backward side by side: the input's gradient (operands in rows) and the weights' (in columns), the
+// one with the longer sums first, so that the last workgroups to start are the short ones. `first`: its workgroups.
 struct GradProducts {
   GemmParams x, w;
   uint32_t first;
+  bool w_first;
 };
 template <int WM, int WN, int TM, int TN, int NB>
 __global__ __launch_bounds__(64 * WM * WN) void glu_backward_kernel(GradProducts p) {
-  if (blockIdx.x < p.first) tile_product<false, false, WM, WN, TM, TN, NB, kProduct>(p.x, blockIdx.x);
-  else tile_product<true, true, WM, WN, TM, TN, NB, kProduct>(p.w, blockIdx.x - p.first);
+  const bool early = blockIdx.x < p.first;
+  const uint32_t block = early ? blockIdx.x : blockIdx.x - p.first;
+  if (early != p.w_first) tile_product<false, false, WM, WN, TM, TN, NB, kProduct>(p.x, block);
+  else tile_product<true, true, WM, WN, TM, TN, NB, kProduct>(p.w, block);
 }
 
 }  // namespace glu

@@ -661,27 +661,28 @@ def rwkv7_gscan_step(x, log_w, state_in, y, state_out, input=RWKV7_INPUT_PLAIN, 
     _launch("rwkv7_gscan_step", at, x, stream)
 
 
-def _three(x):
-    if not isinstance(x, _T.Tensor) or x.dim() != 3:
-        raise ValueError("x must be a [B, T, D] tensor")
-    return x.shape
-
+# Outputs that the functions below allocate themselves are as they have to be, and are not looked at again.
 
 def gscan(x, log_w, state_in=None, lens=None, input=RWKV7_INPUT_PLAIN, want_state=True, stream=None):
     """Allocate y ([B,T,D] in x's dtype) and the final state, run the prompt, return (y, state_out)."""
-    B, T, D = _three(x)
+    at, shape, same = _gscan_inputs(x, log_w, state_in)
+    B, T, D = shape
+    at.append(None if lens is None else _at(lens, "lens", (B,), _T.i32, x))
     y, s_out = _on_stream_of(stream, x, lambda: (
         _T.empty_like(x), x.new_empty((B, D), dtype=_T.f32[0]) if want_state else None))
-    rwkv7_gscan_prefill(x, log_w, state_in, lens, y, s_out, input, stream)
+    at += (_ptr(y), _ptr(s_out), B, T, D, _T.codes[x.dtype], int(input))
+    _launch("rwkv7_gscan_prefill", at, x, stream)
     return y, s_out
 
 
 def gscan_step(x, log_w, state_in=None, input=RWKV7_INPUT_PLAIN, stream=None):
     """Allocate y ([B,1,D] in x's dtype) and the new state, run one token, return (y, state_out).
     rwkv7_gscan_step updates a state in place."""
-    B, T, D = _three(x)
+    at, shape, same = _gscan_inputs(x, log_w, state_in)
+    B, T, D = shape
     y, s_out = _on_stream_of(stream, x, lambda: (_T.empty_like(x), x.new_empty((B, D), dtype=_T.f32[0])))
-    rwkv7_gscan_step(x, log_w, state_in, y, s_out, input, stream)
+    at += (_ptr(y), _ptr(s_out), B, T, D, _T.codes[x.dtype], int(input))
+    _launch("rwkv7_gscan_step", at, x, stream)
     return y, s_out
 
 
@@ -704,15 +705,19 @@ def rwkv7_gscan_backward(x, log_w, state_in, lens, dy, dstate_out, dx, dlog_w, d
 def gscan_backward(x, log_w, dy, state_in=None, lens=None, dstate_out=None, input=RWKV7_INPUT_PLAIN, want_dstate=True,
                    stream=None):
     """Allocate the gradients, run the backward, return dict dx, dlog_w, dstate_in."""
-    B, T, D = _three(x)
+    at, shape, same = _gscan_inputs(x, log_w, state_in)
+    B, T, D = shape
+    at.append(None if lens is None else _at(lens, "lens", (B,), _T.i32, x))
+    at.append(_at(dy, "dy", shape, same, x))
+    at.append(None if dstate_out is None else _at(dstate_out, "dstate_out", (B, D), _T.f32, x))
 
     def make():
-        return {"dx": _T.empty_like(x), "dlog_w": _T.empty_like(x, dtype=_T.f32[0]),
+        return {"dx": _T.empty_like(x), "dlog_w": _T.empty_like(log_w),
                 "dstate_in": x.new_empty((B, D), dtype=_T.f32[0]) if want_dstate else None}
 
     out = _on_stream_of(stream, x, make)
-    rwkv7_gscan_backward(x, log_w, state_in, lens, dy, dstate_out, out["dx"], out["dlog_w"], out["dstate_in"], input,
-                         stream)
+    at += (_ptr(out["dx"]), _ptr(out["dlog_w"]), _ptr(out["dstate_in"]), B, T, D, _T.codes[x.dtype], int(input))
+    _launch("rwkv7_gscan_backward", at, x, stream)
     return out
 
 
@@ -760,22 +765,25 @@ def rwkv7_glu_backward(x, w_gate, w_up, gate, up, dh, dx, dw_gate, dw_up, act=RW
 
 def glu(x, w_gate, w_up, act=RWKV7_ACT_SILU, want_pre=False, stream=None):
     """Allocate h (and, with want_pre, the pre-activations for the backward), run the forward, return (h, gate, up)."""
-    shape = _glu_inputs(x, w_gate, w_up)[1]
-
-    def make():
-        return [x.new_empty(shape) if n == 0 or want_pre else None for n in range(3)]
-
-    h, gate, up = _on_stream_of(stream, x, make)
-    rwkv7_glu_forward(x, w_gate, w_up, h, gate, up, act, stream)
+    at, wide, M, D, F = _glu_inputs(x, w_gate, w_up)
+    h, gate, up = _on_stream_of(stream, x, lambda: (
+        x.new_empty(wide), x.new_empty(wide) if want_pre else None, x.new_empty(wide) if want_pre else None))
+    at += (_ptr(h), _ptr(gate), _ptr(up), M, D, F, _T.codes[x.dtype], int(act))
+    _launch("rwkv7_glu_forward", at, x, stream)
     return h, gate, up
 
 
 def glu_backward(x, w_gate, w_up, gate, up, dh, act=RWKV7_ACT_SILU, want_dx=True, want_dw=True, stream=None):
     """Allocate the gradients, run the backward, return dict dx, dw_gate, dw_up (None where not wanted)."""
+    at, wide, M, D, F = _glu_inputs(x, w_gate, w_up)
+    for name, t in (("gate", gate), ("up", up), ("dh", dh)):
+        at.append(_at(t, name, wide, (x.dtype,), x))
+
     def make():
         return {"dx": _T.empty_like(x) if want_dx else None, "dw_gate": _T.empty_like(w_gate) if want_dw else None,
                 "dw_up": _T.empty_like(w_up) if want_dw else None}
 
     out = _on_stream_of(stream, x, make)
-    rwkv7_glu_backward(x, w_gate, w_up, gate, up, dh, out["dx"], out["dw_gate"], out["dw_up"], act, stream)
+    at += (_ptr(out["dx"]), _ptr(out["dw_gate"]), _ptr(out["dw_up"]), M, D, F, _T.codes[x.dtype], int(act))
+    _launch("rwkv7_glu_backward", at, x, stream)
     return out
