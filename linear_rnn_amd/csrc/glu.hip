@@ -280,7 +280,9 @@ Plan plan(const ShapeInfo (&shapes)[kShapes], const Product (&job)[2]) {
         if (b > 1 && (tiles[1] * b > 4 * slots || job[1].steps < 4 * b)) break;
         int64_t n[2] = {tiles[0] * a, tiles[1] * b};
         float us[2] = {(job[0].steps + a - 1) / a * f.step_us + f.ends_us, (job[1].steps + b - 1) / b * f.step_us + f.ends_us};
-        const float t = finish(n, us, slots) + job[0].join_us(a) + job[1].join_us(b);
+        const float joins = job[0].join_us(a) + job[1].join_us(b);
+        if (any && (n[0] * us[0] + n[1] * us[1]) / slots + joins >= best.us) continue;  // at least that
+        const float t = finish(n, us, slots) + joins;
         if (!any || t < best.us) any = true, best = Plan{(Shape)s, {a, b}, t};
       }
     }
@@ -405,7 +407,7 @@ int64_t steps_of(int64_t K, int segments) { return (K + kBK - 1) / kBK * segment
 // estimated to take less than tiles and the copies in pieces: D=4096 F=10944 192 rows 406 us and 525 by tiles, 256
 // 502 and 480; D=768 F=2048 256 rows 24 and 35.
 bool few_rows(const GluCall& c, const Plan& tiles) {
-  if (c.D % 8 != 0 || c.F % 8 != 0) return false;
+  if (c.D % 8 != 0 || c.F % 8 != 0 || c.M > 4096) return false;
   if (!c.f32) return c.M <= 32;
   const float few = 6.f + 4.f * whole(c.M, 32) * c.D * c.F / 75e6f;
   const float copies = 8.f + (2.f * c.D * c.F + (float)c.M * c.D) * 10 / 4e6f;

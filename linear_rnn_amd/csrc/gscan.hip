@@ -590,9 +590,12 @@ __global__ __launch_bounds__(W * kWave) void gscan_chain_kernel(ScanParams p) {
   uint64_t m[kEach + 1];
 #pragma unroll
   for (uint32_t i = 0; i <= kEach; ++i) m[i] = peek(from(i));
+  // Some seconds at most: what two calls that share a workspace against the rules may wait for never comes (an empty
+  // word is a NaN, and so are the results).
+  uint32_t polls = 1 << 21;
 #pragma unroll
   for (uint32_t i = 0; i <= kEach; ++i)
-    while (from(i) != own && m[i] == kEmpty) {
+    while (from(i) != own && m[i] == kEmpty && --polls != 0) {
       __builtin_amdgcn_s_sleep(1);
       m[i] = peek(from(i));
     }
@@ -942,7 +945,8 @@ struct Kernels {
     if (p.tiles == 1) return start(one_pass, blocks, kThreads, p, c.stream);
     std::lock_guard<std::mutex> lock(operators_mutex());
     hipError_t e = hipSuccess;
-    if (p.tiles <= kAcross) {
+    // (words are of 64 channels: they would outgrow the data of a few)
+    if (p.tiles <= kAcross && p.D >= 16) {
       e = words(p, c, p.tiles, true);
       if (e == hipSuccess) e = start(one_pass, blocks, kThreads, p, c.stream);
       if (e == hipSuccess)

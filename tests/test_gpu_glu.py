@@ -250,3 +250,31 @@ def test_outputs_on_another_stream(torch):
         h1, g1, u1 = forward(d, "silu", want_pre=True, stream=stream)
     stream.synchronize()
     assert torch.equal(h, h1) and torch.equal(gate, g1) and torch.equal(up, u1)
+
+
+def test_growth_during_capture_is_refused(torch):
+    stream = torch.cuda.Stream()
+    d, out = case(torch, 3000, 130, 1001, torch.float32, 10)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        with pytest.raises(wkv.Rwkv7Error):
+            wkv.rwkv7_glu_forward(d["x"], d["w_gate"], d["w_up"], out["h"], None, None, stream=stream)
+        with pytest.raises(wkv.Rwkv7Error):
+            wkv.rwkv7_glu_backward(d["x"], d["w_gate"], d["w_up"], d["gate"], d["up"], d["dh"], out["dx"], None, None,
+                                   stream=stream)
+    chain(d, out, stream)
+    stream.synchronize()
+
+
+def test_many_rows_of_few_channels(torch):
+    """More rows than a grid's second dimension has, in products of one tile of columns."""
+    for dtype in (torch.float32, torch.bfloat16):
+        x = ref.make(2_200_000, 8, 8, dtype, seed=11)
+        d = cuda(x)
+        h = forward(d, "silu")[0]
+        part = slice(2_199_000, 2_200_000)
+        ref.check("h", h[part], ref.forward(x["x"][part], x["w_gate"], x["w_up"], "silu")["h"])
+        g = backward(d, "silu", want_dw=False)
+        want = ref.backward(x["x"][part], x["w_gate"], x["w_up"], x["gate"][part], x["up"][part], x["dh"][part], "silu")
+        ref.check("dx", g["dx"][part], want["dx"])

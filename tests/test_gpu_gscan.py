@@ -159,9 +159,10 @@ def test_no_tokens(torch):
     assert not wkv.gscan_backward(d["x"], d["log_w"], d["dy"])["dstate_in"].any()
 
 
-def test_sequences_and_channels_are_their_own(torch):
-    """The largest width, whose tiles reach past 2^28 bytes: a part of the channels, and one sequence, bit for bit."""
-    B, T, D = 2, 130, 1 << 20
+@pytest.mark.parametrize("B,T", [(2, 130), (1, 600)])
+def test_sequences_and_channels_are_their_own(torch, B, T):
+    """The largest width, whose tiles reach past 2^29 bytes: a part of the channels, and one sequence, bit for bit."""
+    D = 1 << 20
     say("gscan widest", B, T, D)
     g = torch.Generator(device="cuda").manual_seed(1)
     x = torch.empty(B, T, D, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
@@ -169,11 +170,11 @@ def test_sequences_and_channels_are_their_own(torch):
     y, s = wkv.gscan(x, lw)
     grads = wkv.gscan_backward(x, lw, x)
     part = slice(D - 16384, D)
-    x1, lw1 = x[1:, :, part].contiguous(), lw[1:, :, part].contiguous()
+    x1, lw1 = x[-1:, :, part].contiguous(), lw[-1:, :, part].contiguous()
     y1, s1 = wkv.gscan(x1, lw1)
-    assert torch.equal(y[1:, :, part], y1) and torch.equal(s[1:, part], s1)
+    assert torch.equal(y[-1:, :, part], y1) and torch.equal(s[-1:, part], s1)
     g1 = wkv.gscan_backward(x1, lw1, x1)
-    assert torch.equal(grads["dx"][1:, :, part], g1["dx"]) and torch.equal(grads["dlog_w"][1:, :, part], g1["dlog_w"])
+    assert torch.equal(grads["dx"][-1:, :, part], g1["dx"]) and torch.equal(grads["dlog_w"][-1:, :, part], g1["dlog_w"])
 
 
 def test_offsets_past_32_bits(torch):
@@ -328,3 +329,25 @@ def test_the_same_call_gives_the_same_bits(torch):
         g1 = wkv.gscan_backward(d["x"], d["log_w"], d["dy"], d["state_in"], dstate_out=d["dstate_out"], input=KIND["norm"])
         assert torch.equal(y1, y) and torch.equal(s1, s) and all(torch.equal(g1[n], g[n]) for n in g)
     torch.cuda.synchronize()
+
+
+def test_growth_during_capture_is_refused(torch):
+    """A stream whose workspace is too small: the call fails before any launch, and works after an eager one."""
+    stream = torch.cuda.Stream()
+    d, out = case(torch, 1, 3000, 192, 14)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        with pytest.raises(wkv.Rwkv7Error):
+            wkv.rwkv7_gscan_prefill(d["x"], d["log_w"], None, None, out["y"], None, stream=stream)
+        with pytest.raises(wkv.Rwkv7Error):
+            wkv.rwkv7_gscan_backward(d["x"], d["log_w"], None, None, d["dy"], None, out["dx"], out["dw"], None, stream=stream)
+    chain(d, out, stream)
+    stream.synchronize()
+    want = clones(out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        chain(d, out, stream)
+    g.replay()
+    torch.cuda.synchronize()
+    same(torch, out, want)
