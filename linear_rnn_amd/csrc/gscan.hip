@@ -380,7 +380,7 @@ __device__ __forceinline__ void write_grads(const ScanParams& p, int64_t base, u
 // Gradients: a workgroup a tile, which it holds in registers. MAPS: the tile's maps, of the state forward and of its
 // gradient backward (they share P). Else, from the state before the tile and the gradient behind it, the gradients.
 template <bool F32, int VEC, int KIND, bool MAPS>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) void gscan_grad_kernel(ScanParams p) {
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(F32 ? 2 : 3))) void gscan_grad_kernel(ScanParams p) {
   constexpr uint32_t esz = kEsz<F32>;
   constexpr int tile = kTile<VEC>;
   __shared__ Shared<> sh[2];
@@ -475,14 +475,17 @@ __device__ __forceinline__ uint32_t take_ticket(const ScanParams& p, uint32_t* s
   return *shared;
 }
 
-// After a barrier: the map of the wave's tokens before this thread's (REV: behind them) becomes the tile's.
-template <int VEC, bool REV, int W>
+// After a barrier: the map of the wave's tokens before this thread's (REV: behind them) becomes the tile's. ROLLED: the
+// waves' maps are read from LDS one by one; at once they would take the registers of a third of the workgroups of the
+// bfloat16 gradients (213 registers and 161), while the other kernels gain nothing by fewer.
+template <int VEC, bool REV, int W, bool ROLLED>
 __device__ __forceinline__ void compose(float (&P)[VEC], float (&L)[VEC], const float (*sp)[kSlab], const float (*sl)[kSlab]) {
+  constexpr int kTurns = ROLLED ? 1 : W;
   const int wave = threadIdx.x >> 6, c = threadIdx.x % kLanes<VEC> * VEC;
   float wp[VEC], wl[VEC], ap[VEC], al[VEC], ep[VEC], el[VEC];
 #pragma unroll
   for (int v = 0; v < VEC; ++v) ap[v] = 1.f, al[v] = 0.f, ep[v] = P[v], el[v] = L[v];
-#pragma unroll
+#pragma unroll kTurns
   for (int i = 0; i < W; ++i) {
     const int w = REV ? W - 1 - i : i;
     get<VEC>(&sp[w][c], wp);
@@ -509,10 +512,11 @@ __device__ __forceinline__ void whole_map(const float (*sp)[kSlab], const float 
   }
 }
 // After a barrier: what the waves' maps make of `v`, the values of the channels from c on at their beginning.
-template <int VEC, bool REV, int W>
+template <int VEC, bool REV, int W, bool ROLLED>
 __device__ __forceinline__ void pass(const float (*sp)[kSlab], const float (*sl)[kSlab], int c, float (&v)[VEC]) {
+  constexpr int kTurns = ROLLED ? 1 : W;
   float p[VEC], l[VEC];
-#pragma unroll
+#pragma unroll kTurns
   for (int i = 0; i < W; ++i) {
     get<VEC>(&sp[REV ? W - 1 - i : i][c], p);
     get<VEC>(&sl[REV ? W - 1 - i : i][c], l);
@@ -576,7 +580,7 @@ __global__ __launch_bounds__(W * kWave) void gscan_chain_kernel(ScanParams p) {
     whole_map<false, W>(sh.p[0], sh.l[0], q, l);
     publish(p.there + k * row + word + lane, q, l);
   }
-  compose<VEC, false, W>(P, L, sh.p[0], sh.l[0]);
+  compose<VEC, false, W, false>(P, L, sh.p[0], sh.l[0]);
 
   // the state before this tile's kGroup tiles in wave 0's map, as a constant
   const uint32_t before = k / kGroup * kGroup;
@@ -587,18 +591,19 @@ __global__ __launch_bounds__(W * kWave) void gscan_chain_kernel(ScanParams p) {
     const uint32_t j = before + wave * kEach + i;
     return j < k ? p.there + j * row + word + lane : own;
   };
-  uint64_t m[kEach + 1];
-#pragma unroll
-  for (uint32_t i = 0; i <= kEach; ++i) m[i] = peek(from(i));
   // Some seconds at most: what two calls that share a workspace against the rules may wait for never comes (an empty
   // word is a NaN, and so are the results).
-  uint32_t polls = 1 << 21;
+  uint64_t m[kEach + 1];
+#pragma unroll 1
+  for (uint32_t polls = 0; polls < 1u << 21; ++polls) {
 #pragma unroll
-  for (uint32_t i = 0; i <= kEach; ++i)
-    while (from(i) != own && m[i] == kEmpty && --polls != 0) {
-      __builtin_amdgcn_s_sleep(1);
-      m[i] = peek(from(i));
-    }
+    for (uint32_t i = 0; i <= kEach; ++i) m[i] = peek(from(i));
+    uint32_t missing = 0;
+#pragma unroll
+    for (uint32_t i = 0; i <= kEach; ++i) missing = missing | ((uint32_t)(from(i) != own) & (uint32_t)(m[i] == kEmpty));
+    if (missing == 0) break;
+    __builtin_amdgcn_s_sleep(1);
+  }
   float mp = 1.f, ml = 0.f;
   if (wave == 0) mp = 0.f, ml = before > 0 ? __uint_as_float((uint32_t)(m[kEach] >> 32)) : p.first_state[word + lane];
 #pragma unroll
@@ -614,14 +619,14 @@ __global__ __launch_bounds__(W * kWave) void gscan_chain_kernel(ScanParams p) {
   const bool ends = k + 1 == p.tiles;
   if (wave == 0 && (ends || k % kGroup == kGroup - 1)) {  // the state behind this tile
     float q, l, next[1] = {0.f};
-    pass<1, false, W>(sh.p[1], sh.l[1], lane, next);
+    pass<1, false, W, false>(sh.p[1], sh.l[1], lane, next);
     whole_map<false, W>(sh.p[0], sh.l[0], q, l);
     next[0] = fmaf(q, next[0], l);
     if (!ends) publish(p.there + (p.tiles + k / kGroup) * row + word + lane, 0.f, next[0]);
     else if (p.s_out && slab * kSlab + lane < p.D) p.s_out[(int64_t)b * p.D + slab * kSlab + lane] = next[0];
   }
   float state[VEC] = {};
-  pass<VEC, false, W>(sh.p[1], sh.l[1], lc, state);
+  pass<VEC, false, W, false>(sh.p[1], sh.l[1], lc, state);
   auto by = buffer(static_cast<char*>(p.y) + base * esz, live * p.D * esz);
   float h[VEC];
 #pragma unroll
@@ -758,19 +763,19 @@ __device__ __forceinline__ void across(const ScanParams& p, uint32_t id, bool ag
   __syncthreads();  // ds_out has been read, before ds_in, which it may be, is written
   if (k == 0 && wave == 0 && p.ds_in && lane_c < p.D) {
     float q, l, d[1] = {end_grad};
-    pass<1, true, kWaves>(sh[1].p[1], sh[1].l[1], lane, d);
+    pass<1, true, kWaves, !F32>(sh[1].p[1], sh[1].l[1], lane, d);
     whole_map<true, kWaves>(sh[0].p[1], sh[0].l[1], q, l);
     p.ds_in[of_b + lane_c] = fmaf(q, d[0], l);
   }
-  pass<VEC, false, kWaves>(sh[1].p[0], sh[1].l[0], lc, state);
-  pass<VEC, true, kWaves>(sh[1].p[1], sh[1].l[1], lc, grad);
+  pass<VEC, false, kWaves, !F32>(sh[1].p[0], sh[1].l[0], lc, state);
+  pass<VEC, true, kWaves, !F32>(sh[1].p[1], sh[1].l[1], lc, grad);
 #pragma unroll
   for (int v = 0; v < VEC; ++v) {
     const float4 f = parked[v][threadIdx.x];
     P[v] = f.x, L[v] = f.y, Q[v] = f.z, R[v] = f.w;
   }
-  compose<VEC, false, kWaves>(P, L, sh[0].p[0], sh[0].l[0]);
-  compose<VEC, true, kWaves>(Q, R, sh[0].p[1], sh[0].l[1]);
+  compose<VEC, false, kWaves, !F32>(P, L, sh[0].p[0], sh[0].l[0]);
+  compose<VEC, true, kWaves, !F32>(Q, R, sh[0].p[1], sh[0].l[1]);
 #pragma unroll
   for (int v = 0; v < VEC; ++v) h[v] = fmaf(P[v], state[v], L[v]), g[v] = fmaf(Q[v], grad[v], R[v]);
   write_grads<F32, VEC, KIND>(p, base, end, live, group, xoff, woff, rx, rg, w, s, h, g);
