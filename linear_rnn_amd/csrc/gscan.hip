@@ -537,6 +537,7 @@ __global__ __launch_bounds__(W * kWave) void gscan_chain_kernel(ScanParams p) {
   __shared__ Shared<W> sh;
   __shared__ uint32_t number;
   const uint32_t id = take_ticket(p, &number), unit = id % p.units, k = id / p.units;
+  if (k >= p.tiles) return;  // only where two calls share a workspace against the rules
   const uint32_t slab = unit % p.slabs, b = unit / p.slabs;
   const uint32_t lc = threadIdx.x % kLanes<VEC> * VEC, c = slab * kSlab + lc, group = threadIdx.x / kLanes<VEC>;
   const bool on = c < p.D;
@@ -738,8 +739,11 @@ __device__ __forceinline__ void across(const ScanParams& p, uint32_t id, bool ag
         gp *= behind ? q : 1.f;
       }
     }
-    if (__syncthreads_or((int)missing)) {
-      if (threadIdx.x == 0) p.left[1 + atomicAdd(p.left, 1u)] = id;
+    if (!again && __syncthreads_or((int)missing)) {
+      if (threadIdx.x == 0) {
+        const uint32_t n = atomicAdd(p.left, 1u);
+        if (n < p.units * p.tiles) p.left[1 + n] = id;  // (always, but for calls that share a workspace against the rules)
+      }
       return;
     }
   }
@@ -787,8 +791,10 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) v
 }
 template <bool F32, int VEC, int KIND>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2))) void gscan_left_kernel(ScanParams p) {
-  for (uint32_t i = blockIdx.x; i < *p.left; i += gridDim.x) {
-    across<F32, VEC, KIND>(p, p.left[1 + i], true);
+  const uint32_t all = p.units * p.tiles, listed = *p.left, n = listed < all ? listed : all;
+  for (uint32_t i = blockIdx.x; i < n; i += gridDim.x) {
+    const uint32_t id = p.left[1 + i];
+    if (id < all) across<F32, VEC, KIND>(p, id, true);
     __syncthreads();  // LDS is written again
   }
 }
