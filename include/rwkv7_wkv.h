@@ -605,8 +605,9 @@ int rwkv7_layernorm_backward(const void *x, const float *weight, const float *me
  *
  * Ownership, alignment (every pointer 16 bytes), aliasing, empty work, streams and error
  * codes are as for rwkv7_wkv_prefill; an `input` not one of RWKV7_INPUT_* is
- * RWKV7_ERR_MODE. Where there are few channels for the device a prompt is taken in
- * segments, whose maps of the state (at most 16 KiB for each 64 channels) live in the
+ * RWKV7_ERR_MODE. Where there are few channels for the device a prompt is taken in tiles
+ * of 256 tokens (64 where D is no multiple of 4), whose maps of the state, 8 bytes a tile
+ * and channel (channels rounded up to 64 for each sequence) and a little more, live in the
  * workspace as the states of rwkv7_linattn_prefill do.
  */
 #define RWKV7_INPUT_PLAIN 0 /* s = 1 */
@@ -643,8 +644,9 @@ int rwkv7_gscan_step(const void *x, const float *log_w, const float *state_in, v
  *   dstate_in   [B,D] float32 output, or NULL; may equal dstate_out
  *
  * dx and dlog_w are required. With no tokens dstate_in is dstate_out. The states are formed
- * again from the inputs; the maps of runs of 128 tokens (32 where D is no multiple of 4),
- * 12 bytes a run and channel, live in the workspace.
+ * again from the inputs; the maps of tiles of 128 tokens (32 where D is no multiple of 4),
+ * 16 bytes a tile and channel (channels rounded up to 64; 12 bytes and D as it is with more
+ * than 64 tiles or D below 16), live in the workspace.
  */
 int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_in, const int32_t *lens, const void *dy,
                          const float *dstate_out, void *dx, float *dlog_w, float *dstate_in, int64_t B, int64_t T,
@@ -674,7 +676,9 @@ int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_i
  * streams and error codes as for rwkv7_wkv_prefill; an unknown `act` is RWKV7_ERR_MODE; no
  * rows or no hidden channels do nothing. float32 operands, and bfloat16 ones whose rows are
  * no multiple of 8, are copied into the workspace described for rwkv7_wkv_prefill_ex first
- * (6 or 2 bytes an element); what is said there about growth and graphs holds.
+ * (6 or 2 bytes an element; not where M is small), and where there are few tiles for the
+ * device, parts of the sums live there (at most 4 tiles a compute unit, of 256 KiB); what is
+ * said there about growth and graphs holds.
  */
 #define RWKV7_ACT_SIGMOID 0 /* 1 / (1 + exp(-g)) */
 #define RWKV7_ACT_SILU 1    /* g / (1 + exp(-g)) */
@@ -696,9 +700,8 @@ int rwkv7_glu_forward(const void *x, const void *w_gate, const void *w_up, void 
  *
  * All in `dtype`. In a bfloat16 call dg and du are rounded to bfloat16 where they enter the
  * products. They live in the workspace (4 bytes for each element of h, float32: 12) with the
- * copies that rwkv7_glu_forward makes and, where the weights are small, parts of their
- * gradients (at most 256 tiles of 256 KiB). With no rows dw_gate and dw_up are zeros, with
- * no hidden channels dx is.
+ * copies that rwkv7_glu_forward makes and parts of the sums as there. With no rows dw_gate
+ * and dw_up are zeros, with no hidden channels dx is.
  */
 int rwkv7_glu_backward(const void *x, const void *w_gate, const void *w_up, const void *gate, const void *up,
                        const void *dh, void *dx, void *dw_gate, void *dw_up, int64_t M, int64_t D, int64_t F, int dtype,
