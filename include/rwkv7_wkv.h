@@ -667,18 +667,19 @@ int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_i
  *           their elements 2^34
  *   act     RWKV7_ACT_*
  *
- * Sums are float32; each output is rounded once. A float32 call's products are formed from
- * three bfloat16 pieces of each operand, with errors of about float32 rounding, and the
- * limits of those pieces that rwkv7_linattn_prefill states. Inputs have to be finite. No
- * result depends on the launch or on other work on the device.
+ * Sums are float32; each output is rounded once. The products of a large float32 call, and
+ * those of float32 gradients, are formed from three bfloat16 pieces of each operand, with
+ * errors of about float32 rounding, and the limits of those pieces that
+ * rwkv7_linattn_prefill states. Inputs have to be finite. No result depends on the launch
+ * or on other work on the device.
  *
  * Contiguous row-major layouts, 16-byte aligned pointers, outputs that overlap nothing,
  * streams and error codes as for rwkv7_wkv_prefill; an unknown `act` is RWKV7_ERR_MODE; no
- * rows or no hidden channels do nothing. float32 operands, and bfloat16 ones whose rows are
- * no multiple of 8, are copied into the workspace described for rwkv7_wkv_prefill_ex first
- * (6 or 2 bytes an element; not where M is small), and where there are few tiles for the
- * device, parts of the sums live there (at most 4 tiles a compute unit, of 256 KiB); what is
- * said there about growth and graphs holds.
+ * rows or no hidden channels do nothing. The pieces of a large float32 call, and bfloat16
+ * operands whose rows are no multiple of 8, are copied into the workspace described for
+ * rwkv7_wkv_prefill_ex first (6 or 2 bytes an element), and where there are few tiles for
+ * the device, parts of the sums live there (at most 4 tiles a compute unit, of 256 KiB);
+ * what is said there about growth and graphs holds.
  */
 #define RWKV7_ACT_SIGMOID 0 /* 1 / (1 + exp(-g)) */
 #define RWKV7_ACT_SILU 1    /* g / (1 + exp(-g)) */

@@ -8,15 +8,17 @@
 //
 // Numbers. Sums are float32. A bfloat16 call's operands are its inputs, exact; dg and du are rounded to bfloat16
 // where they enter the products (2^-8 of each at most, half a step, as a bfloat16 program that keeps them in memory
-// rounds them). A float32 call's operands are sums of three bfloat16 pieces, of whose nine products the six whose
-// orders add to at most 2 are kept, the smallest first: errors of about 2^-24, at 1/6 of the bfloat16 rate, which is
-// more than the float32 matrix instructions' 1/16.
+// rounds them). A large float32 call's operands, and those of the gradients, are sums of three bfloat16 pieces, of whose
+// nine products the six whose orders add to at most 2 are kept, the smallest first: errors of about 2^-24, at 1/6 of
+// the bfloat16 rate, which is more than the float32 matrix instructions' 1/16. Other float32 forwards take these
+// (glu_f32.hpp), without pieces, workspace and sums in parts.
 #include "glu_internal.hpp"
 #include "once_per_device.hpp"
 #include "operators_lock.hpp"
 #include "rwkv7_wkv.h"
 #include "wkv7_internal.hpp"
 
+#include "glu_f32.hpp"
 #include "glu_few.hpp"
 #include "glu_gemm.hpp"
 
@@ -401,24 +403,16 @@ int second_of(bool f32, int s) { return f32 ? kPairs[s][1] : 0; }
 
 int64_t steps_of(int64_t K, int segments) { return (K + kBK - 1) / kBK * segments; }
 
-// Few rows go by a kernel that reads the weights once (where rows are of whole 16 bytes): in bfloat16 up to the 32 that
-// it takes at a time (33 rows of D=2048 F=5504 34 us and 21 by tiles, 32 rows 21 and 22, 17 of D=4096 F=10944 30 and
-// 36). In float32 more, 32 at a time by the float32 matrix instructions at some 75 TFLOP/s, as long as that is
-// estimated to take less than tiles and the copies in pieces: D=4096 F=10944 192 rows 406 us and 525 by tiles, 256
-// 502 and 480; D=768 F=2048 256 rows 24 and 35.
-bool few_rows(const GluCall& c, const Plan& tiles) {
-  if (c.D % 8 != 0 || c.F % 8 != 0 || c.M > 4096) return false;
-  if (!c.f32) return c.M <= 32;
-  const float few = 6.f + 4.f * whole(c.M, 32) * c.D * c.F / 75e6f;
-  const float copies = 8.f + (2.f * c.D * c.F + (float)c.M * c.D) * 10 / 4e6f;
-  return few < tiles.us + copies;
-}
+// Up to 32 rows (of whole 16 bytes) go by a kernel that reads the weights once: bfloat16, 33 rows of D=2048 F=5504 34 us
+// and 21 by tiles, 32 rows 21 and 22, 17 of D=4096 F=10944 30 and 36; float32, 64 rows of D=2048 F=5504 53 us and 43 by
+// tiles, 32 rows 29 and 34.
+bool few_rows(const GluCall& c) { return c.D % 8 == 0 && c.F % 8 == 0 && c.M <= 32; }
 template <bool F32, int C>
 hipError_t forward_few(const GluCall& c) {
   const FewParams p{c.x, c.w_gate, c.w_up, c.h, c.gate, c.up, (int32_t)c.M, (int32_t)c.D, (int32_t)c.F, c.act};
   const void* fn = c.M <= 16 ? reinterpret_cast<const void*>(&glu_few_kernel<F32, C, 1>)
                              : reinterpret_cast<const void*>(&glu_few_kernel<F32, C, 2>);
-  return start(fn, dim3((uint32_t)((c.F + 16 * C - 1) / (16 * C)), (uint32_t)((c.M + 31) / 32)), 64 * kFewWaves, 0, p, c.stream);
+  return start(fn, dim3((uint32_t)((c.F + 16 * C - 1) / (16 * C))), 64 * kFewWaves, 0, p, c.stream);
 }
 // 64 columns a workgroup; float32 half as many up to F=8192, where there are too few workgroups else (1 row of D=2048
 // F=5504 23 us and 17, of D=4096 F=10944 65 and 76; in bfloat16 that makes half lines of a row, 12.6 and 21).
@@ -427,11 +421,49 @@ hipError_t forward_few(const GluCall& c) {
   return c.F <= 8192 ? forward_few<true, 2>(c) : forward_few<true, 4>(c);
 }
 
+template <int TM>
+hipError_t forward_f32(const GluCall& c) {
+  F32Params p{static_cast<const float*>(c.x), static_cast<const float*>(c.w_gate), static_cast<const float*>(c.w_up),
+              static_cast<float*>(c.h), static_cast<float*>(c.gate), static_cast<float*>(c.up), (int32_t)c.M, (int32_t)c.D,
+              (int32_t)c.F, 0, 0, c.act};
+  p.tiles_m = (int32_t)((c.M + 16 * TM - 1) / (16 * TM)), p.tiles_n = (int32_t)((c.F + kCols32 - 1) / kCols32);
+  return start(reinterpret_cast<const void*>(&glu_forward32_kernel<TM>), dim3((uint32_t)p.tiles_m * p.tiles_n), 64 * kWaves32, 0, p,
+               c.stream);
+}
+constexpr hipError_t (*kForwardF32[kMostTM32])(const GluCall&) = {&forward_f32<1>, &forward_f32<2>, &forward_f32<3>,
+                                                                  &forward_f32<4>, &forward_f32<5>};
+// The float32 instructions' tile with the least estimated time: of its steps, by rows, on the compute unit with the most
+// tiles (1 to 64 rows of tiles, of sizes 40 x 64 x 96 to 4096 x 4096 x 4096: within 10%). It is taken where that is less
+// than the estimate for pieces: 515 x 770 x 2049 43 us and 55, 700 x 768 x 2048 41 and 54, 7 x 770 x 2049 13 and 42;
+// 2048 x 768 x 2048 102 and 81, 4096 x 4096 x 4096 1,950 and 1,255.
+struct F32Plan {
+  int tm = 0;
+  float us = 1e30f;
+};
+F32Plan plan_f32(const GluCall& c) {
+  constexpr float kStepUs[kMostTM32] = {0.29f, 0.49f, 0.725f, 0.96f, 1.21f}, kWaitUs = 0.1f, kEndsUs = 7.f;
+  const int cus = compute_units();
+  F32Plan best;
+  for (int tm = 1; tm <= kMostTM32; ++tm) {
+    const int64_t tiles = (c.M + 16 * tm - 1) / (16 * tm) * ((c.F + kCols32 - 1) / kCols32);
+    if (tiles > (int64_t(1) << 22)) continue;  // a grid's threads are counted in 32 bits
+    const float us = kEndsUs + (c.D + kStep32 - 1) / kStep32 * ((tiles + cus - 1) / cus * kStepUs[tm - 1] + kWaitUs);
+    if (us < best.us) best.tm = tm, best.us = us;
+  }
+  return best;
+}
+
 hipError_t forward(const GluCall& c) {
+  if (few_rows(c)) return forward_few(c);
   Matrix x{c.x, c.M, c.D, c.f32}, wg{c.w_gate, c.D, c.F, c.f32}, wu{c.w_up, c.D, c.F, c.f32};
   const Product job[2] = {{c.M, c.F, 1, steps_of(c.D, pairs(c.f32))}, {0, 0, 0, 0}};
   const Plan how = plan(kForwardShapes, job);
-  if (few_rows(c, how)) return forward_few(c);
+  if (c.f32) {
+    // the pieces come first: 4 bytes read and 6 written an element
+    const float pieces = 8.f + (2.f * c.D * c.F + (float)c.M * c.D) * 10 / 6e6f;
+    const F32Plan f32 = plan_f32(c);
+    if (f32.us < how.us + pieces) return kForwardF32[f32.tm - 1](c);
+  }
   const int splits = how.splits[0];
   Parts parts;
   for (Matrix* m : {&x, &wg, &wu}) m->place(parts);

@@ -127,14 +127,6 @@ __global__ __launch_bounds__(64 * kFewWaves) void glu_few_kernel(FewParams p) {
   __shared__ float sums[kFewWaves][16][kRow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = blockIdx.x * kCols;
-  const int64_t m0 = (int64_t)blockIdx.y * 16 * MT;  // its rows
-  {
-    constexpr int esz = F32 ? 4 : 2;
-    p.x = static_cast<const char*>(p.x) + m0 * p.D * esz;
-    p.h = static_cast<char*>(p.h) + m0 * p.F * esz;
-    if (p.gate) p.gate = static_cast<char*>(p.gate) + m0 * p.F * esz, p.up = static_cast<char*>(p.up) + m0 * p.F * esz;
-    p.M = p.M - (int)m0 < 16 * MT ? p.M - (int)m0 : 16 * MT;
-  }
   f32x4 acc[2][C][MT];
 #pragma unroll
   for (int i = 0; i < 2; ++i)

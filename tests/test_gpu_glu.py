@@ -254,7 +254,7 @@ def test_outputs_on_another_stream(torch):
 
 def test_growth_during_capture_is_refused(torch):
     stream = torch.cuda.Stream()
-    d, out = case(torch, 3000, 130, 1001, torch.float32, 10)
+    d, out = case(torch, 3000, 130, 1001, torch.bfloat16, 10)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g, stream=stream):
@@ -278,3 +278,26 @@ def test_many_rows_of_few_channels(torch):
         g = backward(d, "silu", want_dw=False)
         want = ref.backward(x["x"][part], x["w_gate"], x["w_up"], x["gate"][part], x["up"][part], x["dh"][part], "silu")
         ref.check("dx", g["dx"][part], want["dx"])
+
+
+# each height of the float32 instructions' tiles (16 to 80 rows), then pieces
+@pytest.mark.parametrize("act,M,D,F", [("gelu", 7, 770, 2049), ("silu", 200, 770, 2049), ("relu2", 515, 333, 1001),
+                                       ("sigmoid", 1000, 333, 1001), ("gelu", 515, 770, 2049), ("silu", 3000, 770, 2049)])
+def test_float32_tiles(torch, act, M, D, F):
+    """Operands in the middle of larger buffers of NaN, outputs next to what has to stay."""
+    say("glu", M, D, F, act)
+    x = ref.make(M, D, F, torch.float32, seed=M + 1)
+    d = {}
+    for n in ("x", "w_gate", "w_up"):
+        big = torch.full((x[n].numel() + 4096,), float("nan"), device="cuda")
+        d[n] = big[2048:2048 + x[n].numel()].view(x[n].shape)
+        d[n].copy_(x[n])
+    whole = [torch.full((M * F + 4096,), 7.0, device="cuda") for _ in range(3)]
+    got = [t[2048:2048 + M * F].view(M, F) for t in whole]
+    wkv.rwkv7_glu_forward(d["x"], d["w_gate"], d["w_up"], *got, act=ACT[act])
+    want = ref.forward(x["x"], x["w_gate"], x["w_up"], act)
+    for n, t in zip(("h", "gate", "up"), got):
+        ref.check(n, t, want[n])
+        ref.norm(n, t, want[n], D)
+    for t in whole:
+        assert (t[:2048] == 7).all() and (t[2048 + M * F:] == 7).all()
