@@ -403,22 +403,31 @@ int second_of(bool f32, int s) { return f32 ? kPairs[s][1] : 0; }
 
 int64_t steps_of(int64_t K, int segments) { return (K + kBK - 1) / kBK * segments; }
 
-// Up to 32 rows (of whole 16 bytes) go by a kernel that reads the weights once: bfloat16, 33 rows of D=2048 F=5504 34 us
-// and 21 by tiles, 32 rows 21 and 22, 17 of D=4096 F=10944 30 and 36; float32, 64 rows of D=2048 F=5504 53 us and 43 by
-// tiles, 32 rows 29 and 34.
-bool few_rows(const GluCall& c) { return c.D % 8 == 0 && c.F % 8 == 0 && c.M <= 32; }
+// Few rows (of whole 4 bytes, which a lane loads at least) go by a kernel that reads the weights once for 32 of them.
+bool few_rows(const GluCall& c) { return c.M <= 32 && (c.f32 || (c.D % 2 == 0 && c.F % 2 == 0)); }
+// 64 columns a workgroup; float32 half as many up to F=8192, where there are too few workgroups else (1 row of D=2048
+// F=5504 23 us and 17, of D=4096 F=10944 65 and 76; in bfloat16 that makes half lines of a row, 12.6 and 21).
+int few_columns(const GluCall& c) { return c.f32 && c.F <= 8192 ? 32 : 64; }
+// More rows do too where the workgroups of 32 rows each fit side by side and each takes less time (its k one after the
+// other) than tiles are estimated to: 64 rows of D=2048 F=5504 19 us and 25 by tiles, 256 of D=768 F=2048 10 and 20; 96 of
+// D=2048 F=5504, more workgroups than compute units, 35 and 25, 64 of D=16384 F=1024 88 and 38; float32 128 of D=768
+// F=2048 13 and 14.
+bool few_rows_each(const GluCall& c, float tiles_us) {
+  if (!c.f32 && (c.D % 2 != 0 || c.F % 2 != 0)) return false;
+  const int64_t groups = (c.M + 31) / 32 * ((c.F + few_columns(c) - 1) / few_columns(c));
+  const float us = 6.f + c.D * (c.f32 ? 0.0003f * few_columns(c) : 0.0051f);
+  return groups <= compute_units() && us < tiles_us;
+}
 template <bool F32, int C>
 hipError_t forward_few(const GluCall& c) {
   const FewParams p{c.x, c.w_gate, c.w_up, c.h, c.gate, c.up, (int32_t)c.M, (int32_t)c.D, (int32_t)c.F, c.act};
   const void* fn = c.M <= 16 ? reinterpret_cast<const void*>(&glu_few_kernel<F32, C, 1>)
                              : reinterpret_cast<const void*>(&glu_few_kernel<F32, C, 2>);
-  return start(fn, dim3((uint32_t)((c.F + 16 * C - 1) / (16 * C))), 64 * kFewWaves, 0, p, c.stream);
+  return start(fn, dim3((uint32_t)((c.F + 16 * C - 1) / (16 * C)), (uint32_t)((c.M + 31) / 32)), 64 * kFewWaves, 0, p, c.stream);
 }
-// 64 columns a workgroup; float32 half as many up to F=8192, where there are too few workgroups else (1 row of D=2048
-// F=5504 23 us and 17, of D=4096 F=10944 65 and 76; in bfloat16 that makes half lines of a row, 12.6 and 21).
 hipError_t forward_few(const GluCall& c) {
   if (!c.f32) return forward_few<false, 4>(c);
-  return c.F <= 8192 ? forward_few<true, 2>(c) : forward_few<true, 4>(c);
+  return few_columns(c) == 32 ? forward_few<true, 2>(c) : forward_few<true, 4>(c);
 }
 
 template <int TM>
@@ -462,7 +471,11 @@ hipError_t forward(const GluCall& c) {
     // the pieces come first: 4 bytes read and 6 written an element
     const float pieces = 8.f + (2.f * c.D * c.F + (float)c.M * c.D) * 10 / 6e6f;
     const F32Plan f32 = plan_f32(c);
-    if (f32.us < how.us + pieces) return kForwardF32[f32.tm - 1](c);
+    const float us = how.us + pieces;
+    if (few_rows_each(c, f32.us < us ? f32.us : us)) return forward_few(c);
+    if (f32.us < us) return kForwardF32[f32.tm - 1](c);
+  } else if (few_rows_each(c, how.us + 10.f)) {  // products this small take some 10 us more than estimated
+    return forward_few(c);
   }
   const int splits = how.splits[0];
   Parts parts;

@@ -57,11 +57,12 @@ struct FewBlock<false, C, MT> {
       w[1][j] = load_words<2 * C>(bu, off);
     }
     const int k = k0 + 8 * q;
+    const auto bx = linattn::buffer(p.x, (uint32_t)p.M * p.D * 2);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const int m = 16 * t + li;
-      u32x4 v = {0, 0, 0, 0};
-      if (m < p.M && k < p.D) v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.x) + (int64_t)m * p.D + k);
+      u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(bx, ((uint32_t)(16 * t + li) * p.D + k) * 2, 0, 0));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = k + 2 * i < p.D ? v[i] : 0;  // not the next row's
       x[t] = __builtin_bit_cast(bf16x8, v);
     }
   }
@@ -100,11 +101,12 @@ struct FewBlock<true, C, MT> {
       w[1][j] = load_words<4 * C>(bu, off);
     }
     const int k = k0 + 4 * q;
+    const auto bx = linattn::buffer(p.x, (uint32_t)p.M * p.D * 4);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const int m = 16 * t + li;
-      x[t] = linattn::zero4();
-      if (m < p.M && k < p.D) x[t] = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p.x) + (int64_t)m * p.D + k);
+      x[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(bx, ((uint32_t)(16 * t + li) * p.D + k) * 4, 0, 0));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[t][i] = k + i < p.D ? x[t][i] : 0.f;  // not the next row's
     }
   }
   __device__ __forceinline__ void multiply(f32x4 (&acc)[2][C][MT]) const {
@@ -127,6 +129,14 @@ __global__ __launch_bounds__(64 * kFewWaves) void glu_few_kernel(FewParams p) {
   __shared__ float sums[kFewWaves][16][kRow];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = blockIdx.x * kCols;
+  const int64_t m0 = (int64_t)blockIdx.y * 16 * MT;  // its rows
+  {
+    constexpr int esz = F32 ? 4 : 2;
+    p.x = static_cast<const char*>(p.x) + m0 * p.D * esz;
+    p.h = static_cast<char*>(p.h) + m0 * p.F * esz;
+    if (p.gate) p.gate = static_cast<char*>(p.gate) + m0 * p.F * esz, p.up = static_cast<char*>(p.up) + m0 * p.F * esz;
+    p.M = p.M - (int)m0 < 16 * MT ? p.M - (int)m0 : 16 * MT;
+  }
   f32x4 acc[2][C][MT];
 #pragma unroll
   for (int i = 0; i < 2; ++i)

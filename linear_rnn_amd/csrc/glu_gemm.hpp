@@ -116,14 +116,15 @@ __device__ __forceinline__ float activation(float g, int act) {
   return sigmoid(g);
 }
 
-// The first `count` of four elements from `at` on, together where they begin on a multiple of four.
+// The first `count` of four elements from `at` on, which may begin anywhere.
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
 __device__ __forceinline__ void store4(void* out, bool f32, int64_t at, int count, f32x4 x) {
-  if (count >= 4 && (at & 3) == 0) {
+  if (count >= 4) {
     if (f32) {
       *reinterpret_cast<f32x4_any*>(static_cast<float*>(out) + at) = x;
     } else {
       const bf16x4 o = __builtin_convertvector(x, bf16x4);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = __builtin_bit_cast(uint2, o);
+      *reinterpret_cast<u32x2_any*>(static_cast<uint16_t*>(out) + at) = __builtin_bit_cast(u32x2_any, o);
     }
   } else {
 #pragma unroll
