@@ -606,7 +606,7 @@ int rwkv7_layernorm_backward(const void *x, const float *weight, const float *me
  * Ownership, alignment (every pointer 16 bytes), aliasing, empty work, streams and error
  * codes are as for rwkv7_wkv_prefill; an `input` not one of RWKV7_INPUT_* is
  * RWKV7_ERR_MODE. Where there are few channels for the device a prompt is taken in tiles
- * of 256 tokens (64 where D is no multiple of 4), whose maps of the state, 8 bytes a tile
+ * of 256 tokens (64 where D mod 64 is 1, 2 or 3), whose maps of the state, 8 bytes a tile
  * and channel (channels rounded up to 64 for each sequence) and a little more, live in the
  * workspace as the states of rwkv7_linattn_prefill do.
  */
@@ -644,7 +644,7 @@ int rwkv7_gscan_step(const void *x, const float *log_w, const float *state_in, v
  *   dstate_in   [B,D] float32 output, or NULL; may equal dstate_out
  *
  * dx and dlog_w are required. With no tokens dstate_in is dstate_out. The states are formed
- * again from the inputs; the maps of tiles of 128 tokens (32 where D is no multiple of 4),
+ * again from the inputs; the maps of tiles of 128 tokens (32 where D mod 64 is 1 to 3),
  * 16 bytes a tile and channel (channels rounded up to 64; 12 bytes and D as it is with more
  * than 64 tiles or D below 16), live in the workspace.
  */

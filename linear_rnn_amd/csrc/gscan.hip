@@ -10,7 +10,10 @@
 // element is read once and h is the recurrence's own: no quotient of cumulative decays, which would overflow.
 // The state, the maps and all sums are float32; a bfloat16 output is rounded once.
 //
-// Memory bounds all of it (8 bytes an element of a bfloat16 prompt, 14 of the gradients, and some ten operations).
+// Memory bounds all of it (8 bytes an element of a bfloat16 prompt, 14 of the gradients, and some ten operations), at
+// the rate of a large copy (4.9 to 5.5 TB/s): B=8 T=4096 D=4096 bfloat16 205 us (5.25 TB/s), B=1 T=32767 D=1024 float32 88 us
+// (4.6, with 4 us for emptying words), gradients of B=8 T=4096 D=1024 bfloat16 102 us (4.6, the words they pass on
+// not counted), float32 122 us (5.5). A step of B=512 D=4096 takes 5.9 us (5.7 TB/s, from the last-level cache).
 #include "gscan_internal.hpp"
 #include "operators_lock.hpp"
 #include "rwkv7_wkv.h"
@@ -24,6 +27,7 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr int kSlab = 64;      // channels of a workgroup
 constexpr int kThreads = 256;
@@ -71,6 +75,23 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer(const void* base, uint3
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00027000);
 }
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset behind the end of every tile
+
+// The channels of a thread's place c (a multiple of VEC) among all slabs': where D is no multiple of four the last place has
+// the last four channels, some of them the place's before it too (of the same workgroup), and both compute and write the
+// same. A place from D on has none. So rows of nearly any width are loaded in fours (B=1 T=20000 D=333 bfloat16 23 us,
+// by single channels 36; B=8 T=4096 D=1023 69 us, D=1025, by single channels, 123).
+template <int VEC>
+__device__ __forceinline__ uint32_t channel(uint32_t c, uint32_t D) {
+  return VEC == 4 && c < D && c + 4 > D ? D - 4 : c;
+}
+// That of a place of a single channel.
+template <int VEC>
+__device__ __forceinline__ uint32_t channel_at(uint32_t c, uint32_t D) {
+  return VEC == 4 ? channel<4>(c & ~3u, D) + (c & 3) : c;
+}
+// Not where a slab has one to three channels: its places would share some with another workgroup, which may have
+// overwritten their states.
+__host__ __device__ constexpr bool in_fours(uint32_t D) { return D % kSlab == 0 || D % kSlab >= 4; }
 
 // VEC values as loaded.
 template <bool F32, int VEC>
@@ -192,6 +213,7 @@ __device__ __forceinline__ void maps_of_wave(float (&P)[VEC], float (&L)[VEC], f
     }
   }
 }
+// In LDS or in a workspace, where four channels begin on 16 bytes.
 template <int VEC>
 __device__ __forceinline__ void get(const float* at, float (&o)[VEC]) {
   if constexpr (VEC == 4) {
@@ -201,9 +223,19 @@ __device__ __forceinline__ void get(const float* at, float (&o)[VEC]) {
     o[0] = *at;
   }
 }
+// In a [B, D] tensor, where they may begin on any channel.
 template <int VEC>
-__device__ __forceinline__ void put(float* at, const float (&o)[VEC]) {
-  if constexpr (VEC == 4) *reinterpret_cast<float4*>(at) = make_float4(o[0], o[1], o[2], o[3]);
+__device__ __forceinline__ void get_any(const float* at, float (&o)[VEC]) {
+  if constexpr (VEC == 4) {
+    const f32x4_any f = *reinterpret_cast<const f32x4_any*>(at);
+    o[0] = f[0], o[1] = f[1], o[2] = f[2], o[3] = f[3];
+  } else {
+    o[0] = *at;
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void put_any(float* at, const float (&o)[VEC]) {
+  if constexpr (VEC == 4) *reinterpret_cast<f32x4_any*>(at) = f32x4_any{o[0], o[1], o[2], o[3]};
   else *at = o[0];
 }
 // After a barrier: `in` is the state before this thread's tokens (REV: the gradient behind them), from that before
@@ -241,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void gscan_walk_kernel(ScanParams p) {
   constexpr int tile = kTile<VEC>;
   __shared__ Shared<> sh;
   const uint32_t unit = p.first + blockIdx.x, slab = unit % p.slabs, b = unit / p.slabs;
-  const uint32_t c = slab * kSlab + threadIdx.x % kLanes<VEC> * VEC, group = threadIdx.x / kLanes<VEC>;
+  const uint32_t c = channel<VEC>(slab * kSlab + threadIdx.x % kLanes<VEC> * VEC, p.D), group = threadIdx.x / kLanes<VEC>;
   const bool on = c < p.D;
   const int64_t live = length(p, b);
   const uint32_t at = group * kTok * p.D + c;
@@ -250,7 +282,7 @@ __global__ __launch_bounds__(kThreads) void gscan_walk_kernel(ScanParams p) {
   const int64_t bd = (int64_t)b * p.D + c;
 
   float carry[VEC] = {};
-  if (on && p.s_in) get<VEC>(p.s_in + bd, carry);
+  if (on && p.s_in) get_any<VEC>(p.s_in + bd, carry);
   Raw<F32, VEC> rx[kTok];
   Raw<true, VEC> rw[kTok];
   auto fetch = [&](int64_t m) {
@@ -298,7 +330,7 @@ __global__ __launch_bounds__(kThreads) void gscan_walk_kernel(ScanParams p) {
       store<F32, VEC>(by, xoff + k * p.D * esz, in);
     }
   }
-  if (p.s_out && on && group == 0) put<VEC>(p.s_out + bd, carry);
+  if (p.s_out && on && group == 0) put_any<VEC>(p.s_out + bd, carry);
   const float none[VEC] = {};
   for (int64_t m = live; m < p.T; m += tile) {  // behind the sequence's end
     const int64_t n = p.T - m < tile ? p.T - m : tile;
@@ -386,7 +418,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(F32 ? 
   __shared__ Shared<> sh[2];
   const uint32_t id = p.first + blockIdx.x;
   const uint32_t slab = id % p.slabs, seg = id / p.slabs % p.tiles, b = id / p.slabs / p.tiles;
-  const uint32_t c = slab * kSlab + threadIdx.x % kLanes<VEC> * VEC, group = threadIdx.x / kLanes<VEC>;
+  const uint32_t c = channel<VEC>(slab * kSlab + threadIdx.x % kLanes<VEC> * VEC, p.D), group = threadIdx.x / kLanes<VEC>;
   const bool on = c < p.D;
   const int64_t t0 = (int64_t)seg * tile;
   const uint32_t end = (uint32_t)(p.T - t0 < tile ? p.T - t0 : tile);
@@ -411,8 +443,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(F32 ? 
   __builtin_amdgcn_sched_barrier(0);  // all loads before the first that is waited for
   float state[VEC] = {}, grad[VEC] = {}, all[VEC] = {};
   if (!MAPS && on) {
-    get<VEC>(p.l + run, state);
-    get<VEC>(p.r + run, grad);
+    get_any<VEC>(p.l + run, state);
+    get_any<VEC>(p.r + run, grad);
   }
   float w[kTok][VEC], s[kTok][VEC], P[VEC], L[VEC], Q[VEC], R[VEC];
 #pragma unroll
@@ -431,9 +463,9 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(F32 ? 
   enter<VEC, true>(Q, R, sh[1].p[0], sh[1].l[0], grad, g, unused);
   if constexpr (MAPS) {
     if (on && group == 0) {
-      put<VEC>(p.p + run, all);
-      put<VEC>(p.l + run, state);
-      put<VEC>(p.r + run, grad);
+      put_any<VEC>(p.p + run, all);
+      put_any<VEC>(p.l + run, state);
+      put_any<VEC>(p.r + run, grad);
     }
   } else {
     write_grads<F32, VEC, KIND>(p, base, end, live, group, xoff, woff, rx, rg, w, s, h, g);
@@ -461,7 +493,8 @@ __global__ __launch_bounds__(256) void gscan_empty_kernel(ScanParams p) {
   if (i == 0) *p.ticket = 0, *p.left = 0;
   for (uint64_t w = i; w < p.words; w += n) p.there[w] = kEmpty;
   for (uint64_t w = i; w < (uint64_t)p.units * kSlab; w += n) {
-    const uint32_t unit = w / kSlab, c = unit % p.slabs * kSlab + w % kSlab;
+    const uint32_t unit = w / kSlab, at_c = unit % p.slabs * kSlab + w % kSlab;
+    const uint32_t c = in_fours(p.D) ? channel_at<4>(at_c, p.D) : at_c;
     const int64_t at = (int64_t)(unit / p.slabs) * p.D + c;
     if (p.first_state) p.first_state[w] = p.s_in && c < p.D ? p.s_in[at] : 0.f;
     if (p.last_grad) p.last_grad[w] = p.ds_out && c < p.D ? p.ds_out[at] : 0.f;
@@ -539,7 +572,7 @@ __global__ __launch_bounds__(W * kWave) void gscan_chain_kernel(ScanParams p) {
   const uint32_t id = take_ticket(p, &number), unit = id % p.units, k = id / p.units;
   if (k >= p.tiles) return;  // only where two calls share a workspace against the rules
   const uint32_t slab = unit % p.slabs, b = unit / p.slabs;
-  const uint32_t lc = threadIdx.x % kLanes<VEC> * VEC, c = slab * kSlab + lc, group = threadIdx.x / kLanes<VEC>;
+  const uint32_t lc = threadIdx.x % kLanes<VEC> * VEC, c = channel<VEC>(slab * kSlab + lc, p.D), group = threadIdx.x / kLanes<VEC>;
   const bool on = c < p.D;
   const int64_t t0 = (int64_t)k * tile;
   const uint32_t end = (uint32_t)(p.T - t0 < tile ? p.T - t0 : tile);
@@ -618,13 +651,14 @@ __global__ __launch_bounds__(W * kWave) void gscan_chain_kernel(ScanParams p) {
   sh.l[1][wave][lane] = ml;
   lds_barrier();
   const bool ends = k + 1 == p.tiles;
+  const uint32_t lane_c = channel_at<VEC>(slab * kSlab + lane, p.D);
   if (wave == 0 && (ends || k % kGroup == kGroup - 1)) {  // the state behind this tile
     float q, l, next[1] = {0.f};
     pass<1, false, W, false>(sh.p[1], sh.l[1], lane, next);
     whole_map<false, W>(sh.p[0], sh.l[0], q, l);
     next[0] = fmaf(q, next[0], l);
     if (!ends) publish(p.there + (p.tiles + k / kGroup) * row + word + lane, 0.f, next[0]);
-    else if (p.s_out && slab * kSlab + lane < p.D) p.s_out[(int64_t)b * p.D + slab * kSlab + lane] = next[0];
+    else if (p.s_out && lane_c < p.D) p.s_out[(int64_t)b * p.D + lane_c] = next[0];
   }
   float state[VEC] = {};
   pass<VEC, false, W, false>(sh.p[1], sh.l[1], lc, state);
@@ -662,7 +696,7 @@ __device__ __forceinline__ void across(const ScanParams& p, uint32_t id, bool ag
   __shared__ float4 parked[VEC][kThreads];
   const uint32_t unit = id / p.tiles, k = id % p.tiles;
   const uint32_t slab = unit % p.slabs, b = unit / p.slabs;
-  const uint32_t lc = threadIdx.x % kLanes<VEC> * VEC, c = slab * kSlab + lc, group = threadIdx.x / kLanes<VEC>;
+  const uint32_t lc = threadIdx.x % kLanes<VEC> * VEC, c = channel<VEC>(slab * kSlab + lc, p.D), group = threadIdx.x / kLanes<VEC>;
   const bool on = c < p.D;
   const uint32_t at = group * kTok * p.D + c;
   const uint32_t xoff = on ? at * esz : kNowhere, woff = on ? at * 4 : kNowhere;
@@ -753,15 +787,15 @@ __device__ __forceinline__ void across(const ScanParams& p, uint32_t id, bool ag
   sh[1].p[1][wave][lane] = gp;
   sh[1].l[1][wave][lane] = gl;
   float state[VEC] = {}, grad[VEC] = {}, h[VEC], g[VEC], end_grad = 0.f;
-  const uint32_t lane_c = slab * kSlab + lane;
+  const uint32_t lane_c = channel_at<VEC>(slab * kSlab + lane, p.D);
   const int64_t of_b = (int64_t)b * p.D;
   if (p.tiles > 1) {
     get<VEC>(p.first_state + word + lc, state);
     get<VEC>(p.last_grad + word + lc, grad);
     end_grad = p.last_grad[word + lane];
   } else {
-    if (on && p.s_in) get<VEC>(p.s_in + of_b + c, state);
-    if (on && p.ds_out) get<VEC>(p.ds_out + of_b + c, grad);
+    if (on && p.s_in) get_any<VEC>(p.s_in + of_b + c, state);
+    if (on && p.ds_out) get_any<VEC>(p.ds_out + of_b + c, grad);
     if (lane_c < p.D && p.ds_out) end_grad = p.ds_out[of_b + lane_c];
   }
   __syncthreads();  // ds_out has been read, before ds_in, which it may be, is written
@@ -847,7 +881,7 @@ __global__ __launch_bounds__(kThreads) void gscan_step_kernel(ScanParams p) {
   const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * VEC;
   if (i >= p.BD) return;
   float s[VEC] = {}, lw[VEC];
-  if (p.s_in) get<VEC>(p.s_in + i, s);
+  if (p.s_in) get<VEC>(p.s_in + i, s);  // here four channels begin on 16 bytes
   get<VEC>(p.log_w + i, lw);
   const char* x = static_cast<const char*>(p.x) + i * kEsz<F32>;
   char* y = static_cast<char*>(p.y) + i * kEsz<F32>;
@@ -868,7 +902,7 @@ __global__ __launch_bounds__(kThreads) void gscan_step_kernel(ScanParams p) {
     const float w = decay(lw[v]);
     s[v] = fmaf(w, s[v], scale<KIND>(lw[v], w) * value<F32, VEC>(rx, v));
   }
-  if (p.s_out) put<VEC>(p.s_out + i, s);
+  if (p.s_out) put_any<VEC>(p.s_out + i, s);
   if constexpr (VEC == 4 && F32) {
     *reinterpret_cast<float4*>(y) = make_float4(s[0], s[1], s[2], s[3]);
   } else if constexpr (VEC == 4) {
@@ -988,9 +1022,10 @@ hipError_t by_kind(const GscanCall& c, Op op) {
   if (c.input == RWKV7_INPUT_MIX) return run<F32, VEC, RWKV7_INPUT_MIX>(c, op);
   return run<F32, VEC, RWKV7_INPUT_NORM>(c, op);
 }
-// Four channels a thread where every row starts on four of them, else one.
+// Four channels a thread, or one: also in a step whose states are no multiple of four (no two threads may have the same
+// channel there, as it may be updated in place).
 hipError_t dispatch(const GscanCall& c, Op op) {
-  const bool four = (op == Op::kStep ? c.B * c.D : c.D) % 4 == 0;
+  const bool four = op == Op::kStep ? c.B * c.D % 4 == 0 : in_fours((uint32_t)c.D);
   if (c.f32) return four ? by_kind<true, 4>(c, op) : by_kind<true, 1>(c, op);
   return four ? by_kind<false, 4>(c, op) : by_kind<false, 1>(c, op);
 }

@@ -22,7 +22,7 @@ def cuda(x):
     return {n: None if t is None else t.cuda() for n, t in x.items()}
 
 
-# one token and tile edges (128 tokens; 32 where D is no multiple of 4), widths below, at and behind 64 channels, odd
+# one token and tile edges (128 tokens; 32 where D leaves one to three of 64 channels over), widths below, at and behind 64 channels, odd
 # ones, few channels over many tokens (segments), many sequences (none)
 SIZES = [(1, 1, 1), (2, 1, 64), (1, 2, 3), (2, 7, 5), (2, 31, 66), (1, 33, 65), (3, 127, 64), (2, 128, 68), (2, 129, 128),
          (1, 257, 130), (2, 300, 1000), (1, 3001, 64), (5, 1000, 4), (1, 700, 33), (300, 40, 20), (130, 70, 130), (1, 4500, 96), (1, 9000, 24), (1, 4500, 33),
@@ -147,6 +147,38 @@ def test_in_place_and_left_out_states(torch, B, T, D):
         ga = wkv.gscan_backward(d["x"], d["log_w"], d["dy"], a, dstate_out=a)
         gb = wkv.gscan_backward(d["x"], d["log_w"], d["dy"], b, dstate_out=b)
         assert all(torch.equal(ga[n], gb[n]) for n in ga)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("T", [1, 5, 300, 1500, 9000])
+@pytest.mark.parametrize("D", [4, 5, 7, 37, 63, 67, 126, 129])
+def test_odd_widths(torch, D, T, dtype):
+    """Rows that begin anywhere, states in place, next to values that have to stay."""
+    B, kind = (2, "norm") if T < 1000 else (1, "mix")
+    say("gscan", B, T, D, kind, dtype)
+    x = ref.make(B, T, D, getattr(torch, dtype), seed=T + D)
+    outs, rooms = {}, []
+
+    def place(like):
+        room = torch.full((like.numel() + 512,), 7.0, dtype=like.dtype, device="cuda")
+        rooms.append((room, like.numel()))
+        out = room[256:256 + like.numel()].view(like.shape)
+        out.copy_(like)
+        return out
+
+    d = {n: place(t) for n, t in x.items()}
+    for n, like in (("y", "x"), ("dx", "x"), ("dlog_w", "log_w")):
+        outs[n] = place(x[like])
+    outs["state"], outs["dstate_in"] = place(x["state_in"]), place(x["dstate_out"])
+    wkv.rwkv7_gscan_prefill(d["x"], d["log_w"], outs["state"], None, outs["y"], outs["state"], input=KIND[kind])
+    wkv.rwkv7_gscan_backward(d["x"], d["log_w"], d["state_in"], None, d["dy"], outs["dstate_in"], outs["dx"], outs["dlog_w"],
+                             outs["dstate_in"], input=KIND[kind])
+    want = {**ref.forward(x["x"], x["log_w"], x["state_in"], None, kind),
+            **ref.backward(x["x"], x["log_w"], x["state_in"], None, x["dy"], x["dstate_out"], kind)}
+    for n, t in outs.items():
+        ref.check(n, t, want[n])
+    for room, n in rooms:
+        assert (room[:256] == 7).all() and (room[256 + n:] == 7).all()
 
 
 def test_no_tokens(torch):
