@@ -491,7 +491,8 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* at) {
 __global__ __launch_bounds__(256) void gscan_empty_kernel(ScanParams p) {
   const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x, n = (uint64_t)gridDim.x * 256;
   if (i == 0) *p.ticket = 0, *p.left = 0;
-  for (uint64_t w = i; w < p.words; w += n) p.there[w] = kEmpty;
+  for (uint64_t w = 2 * i; w < p.words; w += 2 * n)
+    *reinterpret_cast<ulonglong2*>(p.there + w) = make_ulonglong2(kEmpty, kEmpty);
   for (uint64_t w = i; w < (uint64_t)p.units * kSlab; w += n) {
     const uint32_t unit = w / kSlab, at_c = unit % p.slabs * kSlab + w % kSlab;
     const uint32_t c = in_fours(p.D) ? channel_at<4>(at_c, p.D) : at_c;
