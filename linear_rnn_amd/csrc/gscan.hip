@@ -991,7 +991,9 @@ struct Kernels {
     if (p.tiles == 1) return start(one_pass, blocks, kThreads, p, c.stream);
     std::lock_guard<std::mutex> lock(operators_mutex());
     hipError_t e = hipSuccess;
-    // (words are of 64 channels: they would outgrow the data of a few)
+    // In one pass or two, bfloat16: B=8 T=4096 D=1024 (32 tiles) 100 and 112 us, B=4 T=8192 D=2048 (64) 213 and 240, B=2
+    // T=16384 D=2048 (128) 253 and 241, B=1 T=32768 D=2048 309 and 242: every tile reads all others' maps. (Words are of
+    // 64 channels and would outgrow the data of one to three; of 8 B=512 T=4096 takes 194 and 204.)
     if (p.tiles <= kAcross && p.D >= 16) {
       e = words(p, c, p.tiles, true);
       if (e == hipSuccess) e = start(one_pass, blocks, kThreads, p, c.stream);
