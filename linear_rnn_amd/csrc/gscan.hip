@@ -15,6 +15,7 @@
 // (4.6, with 4 us for emptying words), gradients of B=8 T=4096 D=1024 bfloat16 102 us (4.6, the words they pass on
 // not counted), float32 122 us (5.5). A step of B=512 D=4096 takes 5.9 us (5.7 TB/s, from the last-level cache).
 #include "gscan_internal.hpp"
+#include "launch_chunks.hpp"
 #include "operators_lock.hpp"
 #include "rwkv7_wkv.h"
 #include "wkv7_device.hpp"
@@ -918,16 +919,12 @@ __global__ __launch_bounds__(kThreads) void gscan_step_kernel(ScanParams p) {
   }
 }
 
-// In launches of at most 2^22 workgroups: a grid's threads are counted in 32 bits.
 hipError_t start(const void* fn, uint64_t blocks, int threads, ScanParams p, hipStream_t stream) {
-  for (uint64_t first = 0; first < blocks; first += 1u << 22) {
-    const uint64_t n = blocks - first < (1u << 22) ? blocks - first : (1u << 22);
-    p.first = (uint32_t)first;
+  return static_cast<hipError_t>(in_chunks(blocks, threads, [&](uint32_t first, uint32_t n) {
+    p.first = first;
     void* args[] = {&p};
-    const hipError_t e = hipLaunchKernel(fn, dim3((uint32_t)n), dim3(threads), args, 0, stream);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+    return static_cast<int>(hipLaunchKernel(fn, dim3(n), dim3(threads), args, 0, stream));
+  }));
 }
 
 ScanParams params(const GscanCall& c) {
