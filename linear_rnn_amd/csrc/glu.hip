@@ -84,7 +84,7 @@ __device__ __forceinline__ void store_pieces(uint16_t* dst, int64_t at, int64_t 
 }
 __device__ __forceinline__ void act_and_slope(float g, int act, float& a, float& s) {
   if (act == RWKV7_ACT_GELU) {
-    const float c = 0.5f * (1.f + erff(g * 0.70710678f));
+    const float c = 0.5f * erfcf(g * -0.70710678f);
     a = g * c;
     s = fmaf(g * 0.39894228f, __builtin_amdgcn_exp2f(g * g * -0.72134752f), c);
   } else if (act == RWKV7_ACT_RELU2) {

@@ -111,7 +111,7 @@ __device__ __forceinline__ float sigmoid(float g) {
 }
 __device__ __forceinline__ float activation(float g, int act) {
   if (act == RWKV7_ACT_SILU) return g * sigmoid(g);
-  if (act == RWKV7_ACT_GELU) return 0.5f * g * (1.f + erff(g * 0.70710678f));
+  if (act == RWKV7_ACT_GELU) return 0.5f * g * erfcf(g * -0.70710678f);  // 1 + erf would cancel below 0
   if (act == RWKV7_ACT_RELU2) return g > 0.f ? g * g : 0.f;
   return sigmoid(g);
 }
