@@ -959,16 +959,26 @@ hipError_t words(ScanParams& p, const GscanCall& c, uint64_t rows, bool back) {
 template <bool F32, int VEC, int KIND>
 struct Kernels {
   static constexpr int tile = kTile<VEC>;
+  // Whether a prompt of so many units is walked, in `tiles`, or passes maps on, in `chain_tiles`.
+  // In fours walking takes 2 us a tile (128 tokens) or, from 192 units on, the memory's time; passing maps on 3 us for
+  // emptying their words and then the memory's time, at some 5 TB/s with any number of units: B=8 T=4096 D=1024 (128 units)
+  // 72 and 54 us, B=1 T=8192 D=768 (12) 134 and 19, B=16 T=2048 D=768 (192) 41 and 44, B=1 T=256 D=768 7.2 and 9.4, B=8
+  // T=4096 D=4096 (512) 219 and 205.
+  // By single channels a tile has 32 tokens and takes 0.6 us to walk, one after the other; a tile of 64 that passes its maps
+  // on 0.014 us of the device's time, after 6 us: D=65 bfloat16 with 2 units T=256 6.8 and 6.2 us, T=1024 22 and 6.3; 64
+  // units T=512 12 and 13, T=2048 43 and 35; 128 units T=2048 43 and 60; 512 units T=1024 35 and 109; D=1025 float32, 136
+  // units T=4096 163 and 131, the one size measured where the rule loses more than a tenth.
+  static bool walks(uint32_t units, uint32_t tiles, uint32_t chain_tiles) {
+    if (VEC == 4) return tiles <= 3 || (units >= 192 && tiles <= 16);
+    return 40 * ((int64_t)tiles - 7) <= (int64_t)units * chain_tiles;
+  }
   static hipError_t prefill(const GscanCall& c) {
     ScanParams p = params(c);
     const uint32_t tiles = (uint32_t)((c.T + tile - 1) / tile);
-    // Walking takes 2 us a tile or, from 192 units on, the memory's time; passing maps on 3 us for emptying their words
-    // and then the memory's time, at some 5 TB/s with any number of units: B=8 T=4096 D=1024 (128 units) 72 and 54 us,
-    // B=1 T=8192 D=768 (12) 134 and 19, B=16 T=2048 D=768 (192) 41 and 44, B=1 T=256 D=768 7.2 and 9.4, B=8 T=4096
-    // D=4096 (512) 219 and 205.
-    if (tiles <= 3 || (p.units >= 192 && tiles <= 16))
+    const uint32_t chain_tiles = (uint32_t)((c.T + kTile<VEC, kChainWaves> - 1) / kTile<VEC, kChainWaves>);
+    if (walks(p.units, tiles, chain_tiles))
       return start(reinterpret_cast<const void*>(&gscan_walk_kernel<F32, VEC, KIND>), p.units, kThreads, p, c.stream);
-    p.tiles = (uint32_t)((c.T + kTile<VEC, kChainWaves> - 1) / kTile<VEC, kChainWaves>);
+    p.tiles = chain_tiles;
     std::lock_guard<std::mutex> lock(operators_mutex());
     const hipError_t e = words(p, c, (uint64_t)p.tiles + (p.tiles + kGroup - 1) / kGroup, false);
     if (e != hipSuccess) return e;
