@@ -605,10 +605,13 @@ int rwkv7_layernorm_backward(const void *x, const float *weight, const float *me
  *
  * Ownership, alignment (every pointer 16 bytes), aliasing, empty work, streams and error
  * codes are as for rwkv7_wkv_prefill; an `input` not one of RWKV7_INPUT_* is
- * RWKV7_ERR_MODE. Where there are few channels for the device a prompt is taken in tiles
- * of 256 tokens (64 where D mod 64 is 1, 2 or 3), whose maps of the state, 8 bytes a tile
- * and channel (channels rounded up to 64 for each sequence) and a little more, live in the
- * workspace as the states of rwkv7_linattn_prefill do.
+ * RWKV7_ERR_MODE. A prompt needs no workspace up to 384 tokens, and none up to 2048 where
+ * B*ceil(D/64) is 192 or more; where D mod 64 is 1, 2 or 3 none up to 224 tokens, and none
+ * at any length where B*ceil(D/64) is 80 or more. Other prompts are taken in tiles of 256
+ * tokens (64 where D mod 64 is 1, 2 or 3), whose maps of the state, 8 bytes a tile and channel
+ * (channels rounded up to 64 for each sequence) and a little more, live in the workspace as
+ * the states of rwkv7_linattn_prefill do; what is said there about growth and graphs holds
+ * for wide prompts too.
  */
 #define RWKV7_INPUT_PLAIN 0 /* s = 1 */
 #define RWKV7_INPUT_MIX 1   /* s = 1 - w */
@@ -678,8 +681,8 @@ int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_i
  * rows or no hidden channels do nothing. The pieces of a large float32 call, and bfloat16
  * operands whose rows are no multiple of 8, are copied into the workspace described for
  * rwkv7_wkv_prefill_ex first (6 or 2 bytes an element), and where there are few tiles for
- * the device, parts of the sums live there (at most 4 tiles a compute unit, of 256 KiB);
- * what is said there about growth and graphs holds.
+ * the device, parts of the sums live there (at most 4 tiles a compute unit, of 256 KiB, for
+ * each sum); what is said there about growth and graphs holds.
  */
 #define RWKV7_ACT_SIGMOID 0 /* 1 / (1 + exp(-g)) */
 #define RWKV7_ACT_SILU 1    /* g / (1 + exp(-g)) */
@@ -701,8 +704,9 @@ int rwkv7_glu_forward(const void *x, const void *w_gate, const void *w_up, void 
  *
  * All in `dtype`. In a bfloat16 call dg and du are rounded to bfloat16 where they enter the
  * products. They live in the workspace (4 bytes for each element of h, float32: 12) with the
- * copies that rwkv7_glu_forward makes and parts of the sums as there. With no rows dw_gate
- * and dw_up are zeros, with no hidden channels dx is.
+ * copies that rwkv7_glu_forward makes and parts of its two sums, dx's and the weights', each as
+ * large as there at most. With no rows dw_gate and dw_up are zeros, with no hidden channels dx
+ * is.
  */
 int rwkv7_glu_backward(const void *x, const void *w_gate, const void *w_up, const void *gate, const void *up,
                        const void *dh, void *dx, void *dw_gate, void *dw_up, int64_t M, int64_t D, int64_t F, int dtype,
