@@ -21,6 +21,7 @@
 #include "glu_f32.hpp"
 #include "glu_few.hpp"
 #include "glu_gemm.hpp"
+#include "glu_rules.hpp"
 
 namespace rwkv7 {
 namespace {
@@ -201,33 +202,7 @@ hipError_t start(const void* fn, dim3 blocks, int threads, int lds, const P& par
 }
 uint32_t blocks_for(int64_t threads) { return (uint32_t)((threads + 255) / 256); }
 
-// ---- tiles: which, and how many workgroups share a sum
-
-// Shapes of a workgroup's tile, and what a step of 64 k and a tile's beginning and end take where as many workgroups as
-// fit share a compute unit, in us: from products of 4096 to 8192 rows and columns, whose tiles fill the compute units
-// evenly. 256 x 256: 1,340 TFLOP/s; 128 x 256: 1,080; two of 128 x 128 (64 x 256 in the forward): 1,050.
-enum Shape { kLarge, kHalf, kSmall, kShapes };
-struct ShapeInfo {
-  int bm, bn;
-  int per_cu;
-  float step_us, ends_us;
-};
-// bn of the forward: columns of both weights
-constexpr ShapeInfo kForwardShapes[kShapes] = {{256, 128, 1, 1.55f, 5.f}, {128, 128, 1, 0.96f, 4.f}, {64, 128, 2, 1.f, 4.f}};
-constexpr ShapeInfo kGradShapes[kShapes] = {{256, 256, 1, 1.55f, 5.f}, {128, 256, 1, 0.96f, 4.f}, {128, 128, 2, 1.f, 4.f}};
-
-// A product: its sizes, how many of them, and the steps of its sum.
-struct Product {
-  int64_t M, N, count, steps;
-  int64_t tiles(const ShapeInfo& f) const { return (M + f.bm - 1) / f.bm * ((N + f.bn - 1) / f.bn) * count; }
-  // written by each part and read again, at 5 TB/s, with the join's launch
-  float join_us(int splits) const { return splits > 1 ? 4.f + (splits * 8.f + 4.f) * count * M * N * 2e-7f : 0.f; }
-};
-struct Plan {
-  Shape shape;
-  int splits[2];
-  float us;
-};
+// ---- tiles (which, and how many workgroups share a sum: glu_rules.hpp)
 
 int compute_units() {
   int dev = 0, n = 0;
@@ -235,61 +210,6 @@ int compute_units() {
       n <= 0)
     n = 256;
   return n;
-}
-
-// When the last of two kinds of workgroups is done, of which `slots` run at a time, the longer kind before the other:
-// n[i] of them of us[i] each.
-float finish(int64_t (&n)[2], float (&us)[2], int64_t slots) {
-  if (us[1] > us[0]) {
-    const int64_t k = n[0];
-    n[0] = n[1], n[1] = k;
-    const float t = us[0];
-    us[0] = us[1], us[1] = t;
-  }
-  // slots that are free early and late behind the first kind
-  const int64_t late = n[0] % slots;
-  float t[2] = {n[0] / slots * us[0], (n[0] / slots + 1) * us[0]};
-  const int64_t count[2] = {slots - late, late};
-  float end = late ? t[1] : t[0];
-  int64_t left = n[1];
-  if (left > 8 * slots) {  // whole rounds, which both kinds of slots take alike
-    const int64_t rounds = left / slots - 4;
-    left -= rounds * slots;
-    t[0] += rounds * us[1], t[1] += rounds * us[1];
-  }
-  while (left > 0) {
-    const int i = count[1] == 0 || t[0] <= t[1] ? 0 : 1;
-    left -= count[i];
-    t[i] += us[1];
-    end = end > t[i] ? end : t[i];
-  }
-  return end;
-}
-
-// The shape and the numbers of parts of the sums with the least estimated time. Parts fill the compute units where
-// there are few tiles, and level the last round of workgroups; a second kernel adds them.
-Plan plan(const ShapeInfo (&shapes)[kShapes], const Product (&job)[2]) {
-  constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32};
-  const int cus = compute_units();
-  Plan best{kLarge, {1, 1}, 0.f};
-  bool any = false;
-  for (int s = 0; s < kShapes; ++s) {
-    const ShapeInfo& f = shapes[s];
-    const int64_t slots = (int64_t)cus * f.per_cu, tiles[2] = {job[0].tiles(f), job[1].tiles(f)};
-    for (int a : kSplits) {
-      if (a > 1 && (tiles[0] * a > 4 * slots || job[0].steps < 4 * a)) break;
-      for (int b : kSplits) {
-        if (b > 1 && (tiles[1] * b > 4 * slots || job[1].steps < 4 * b)) break;
-        int64_t n[2] = {tiles[0] * a, tiles[1] * b};
-        float us[2] = {(job[0].steps + a - 1) / a * f.step_us + f.ends_us, (job[1].steps + b - 1) / b * f.step_us + f.ends_us};
-        const float joins = job[0].join_us(a) + job[1].join_us(b);
-        if (any && (n[0] * us[0] + n[1] * us[1]) / slots + joins >= best.us) continue;  // at least that
-        const float t = finish(n, us, slots) + joins;
-        if (!any || t < best.us) any = true, best = Plan{(Shape)s, {a, b}, t};
-      }
-    }
-  }
-  return best;
 }
 
 // More than 64 KB of LDS has to be asked for on every device.
@@ -397,27 +317,9 @@ struct Stage {
 
 // The pairs of pieces of two operands, the smallest products first.
 constexpr int kPairs[6][2] = {{2, 0}, {1, 1}, {0, 2}, {1, 0}, {0, 1}, {0, 0}};
-int pairs(bool f32) { return f32 ? 6 : 1; }
 int first_of(bool f32, int s) { return f32 ? kPairs[s][0] : 0; }
 int second_of(bool f32, int s) { return f32 ? kPairs[s][1] : 0; }
 
-int64_t steps_of(int64_t K, int segments) { return (K + kBK - 1) / kBK * segments; }
-
-// Few rows (of whole 4 bytes, which a lane loads at least) go by a kernel that reads the weights once for 32 of them.
-bool few_rows(const GluCall& c) { return c.M <= 32 && (c.f32 || (c.D % 2 == 0 && c.F % 2 == 0)); }
-// 64 columns a workgroup; float32 half as many up to F=8192, where there are too few workgroups else (1 row of D=2048
-// F=5504 23 us and 17, of D=4096 F=10944 65 and 76; in bfloat16 that makes half lines of a row, 12.6 and 21).
-int few_columns(const GluCall& c) { return c.f32 && c.F <= 8192 ? 32 : 64; }
-// More rows do too where the workgroups of 32 rows each fit side by side and each takes less time (its k one after the
-// other) than tiles are estimated to: 64 rows of D=2048 F=5504 19 us and 25 by tiles, 256 of D=768 F=2048 10 and 20; 96 of
-// D=2048 F=5504, more workgroups than compute units, 35 and 25, 64 of D=16384 F=1024 88 and 38; float32 128 of D=768
-// F=2048 13 and 14.
-bool few_rows_each(const GluCall& c, float tiles_us) {
-  if (!c.f32 && (c.D % 2 != 0 || c.F % 2 != 0)) return false;
-  const int64_t groups = (c.M + 31) / 32 * ((c.F + few_columns(c) - 1) / few_columns(c));
-  const float us = 6.f + c.D * (c.f32 ? 0.0003f * few_columns(c) : 0.0051f);
-  return groups <= compute_units() && us < tiles_us;
-}
 template <bool F32, int C>
 hipError_t forward_few(const GluCall& c) {
   const FewParams p{c.x, c.w_gate, c.w_up, c.h, c.gate, c.up, (int32_t)c.M, (int32_t)c.D, (int32_t)c.F, c.act};
@@ -427,7 +329,7 @@ hipError_t forward_few(const GluCall& c) {
 }
 hipError_t forward_few(const GluCall& c) {
   if (!c.f32) return forward_few<false, 4>(c);
-  return few_columns(c) == 32 ? forward_few<true, 2>(c) : forward_few<true, 4>(c);
+  return few_columns(Sizes{c.M, c.D, c.F, c.f32}, compute_units()) == 32 ? forward_few<true, 2>(c) : forward_few<true, 4>(c);
 }
 
 template <int TM>
@@ -441,43 +343,12 @@ hipError_t forward_f32(const GluCall& c) {
 }
 constexpr hipError_t (*kForwardF32[kMostTM32])(const GluCall&) = {&forward_f32<1>, &forward_f32<2>, &forward_f32<3>,
                                                                   &forward_f32<4>, &forward_f32<5>};
-// The float32 instructions' tile with the least estimated time: of its steps, by rows, on the compute unit with the most
-// tiles (1 to 64 rows of tiles, of sizes 40 x 64 x 96 to 4096 x 4096 x 4096: within 10%). It is taken where that is less
-// than the estimate for pieces: 515 x 770 x 2049 43 us and 55, 700 x 768 x 2048 41 and 54, 7 x 770 x 2049 13 and 42;
-// 2048 x 768 x 2048 102 and 81, 4096 x 4096 x 4096 1,950 and 1,255.
-struct F32Plan {
-  int tm = 0;
-  float us = 1e30f;
-};
-F32Plan plan_f32(const GluCall& c) {
-  constexpr float kStepUs[kMostTM32] = {0.29f, 0.49f, 0.725f, 0.96f, 1.21f}, kWaitUs = 0.1f, kEndsUs = 7.f;
-  const int cus = compute_units();
-  F32Plan best;
-  for (int tm = 1; tm <= kMostTM32; ++tm) {
-    const int64_t tiles = (c.M + 16 * tm - 1) / (16 * tm) * ((c.F + kCols32 - 1) / kCols32);
-    if (tiles > (int64_t(1) << 22)) continue;  // a grid's threads are counted in 32 bits
-    const float us = kEndsUs + (c.D + kStep32 - 1) / kStep32 * ((tiles + cus - 1) / cus * kStepUs[tm - 1] + kWaitUs);
-    if (us < best.us) best.tm = tm, best.us = us;
-  }
-  return best;
-}
-
 hipError_t forward(const GluCall& c) {
-  if (few_rows(c)) return forward_few(c);
+  const ForwardPlan how = plan_forward(Sizes{c.M, c.D, c.F, c.f32}, compute_units());
+  if (how.way == kFew) return forward_few(c);
+  if (how.way == kInstructions) return kForwardF32[how.tm - 1](c);
   Matrix x{c.x, c.M, c.D, c.f32}, wg{c.w_gate, c.D, c.F, c.f32}, wu{c.w_up, c.D, c.F, c.f32};
-  const Product job[2] = {{c.M, c.F, 1, steps_of(c.D, pairs(c.f32))}, {0, 0, 0, 0}};
-  const Plan how = plan(kForwardShapes, job);
-  if (c.f32) {
-    // the pieces come first: 4 bytes read and 6 written an element
-    const float pieces = 8.f + (2.f * c.D * c.F + (float)c.M * c.D) * 10 / 6e6f;
-    const F32Plan f32 = plan_f32(c);
-    const float us = how.us + pieces;
-    if (few_rows_each(c, f32.us < us ? f32.us : us)) return forward_few(c);
-    if (f32.us < us) return kForwardF32[f32.tm - 1](c);
-  } else if (few_rows_each(c, how.us + 10.f)) {  // products this small take some 10 us more than estimated
-    return forward_few(c);
-  }
-  const int splits = how.splits[0];
+  const int splits = how.tiles.splits[0];
   Parts parts;
   for (Matrix* m : {&x, &wg, &wu}) m->place(parts);
   const size_t partial_at = splits > 1 ? parts.add((size_t)splits * 2 * c.M * c.F * 4) : 0;
@@ -504,7 +375,7 @@ hipError_t forward(const GluCall& c) {
   p.lda = x.ld(), p.ldb = wg.ld(), p.M = (int32_t)c.M, p.N = (int32_t)c.F, p.K = (int32_t)c.D, p.splits = splits;
   p.out = c.h, p.gate = c.gate, p.up = c.up, p.f32 = c.f32, p.act = c.act;
   p.partial = reinterpret_cast<float*>(ws + partial_at);
-  const hipError_t e = forward_products(p, how.shape, c.stream);
+  const hipError_t e = forward_products(p, how.tiles.shape, c.stream);
   if (e != hipSuccess || splits == 1) return e;
   JoinParams j{};
   j.job[0] = JoinJob{p.partial, c.gate, c.up, c.h, c.M * c.F, splits, 2, c.f32, c.act};
@@ -522,7 +393,7 @@ hipError_t backward(const GluCall& c) {
   Product job[2] = {{c.M, c.D, 1, steps_of(sum_f, 2 * pairs(c.f32))}, {c.D, c.F, 2, steps_of(c.M, pairs(c.f32))}};
   if (!dx) job[0] = Product{0, 0, 0, 0};
   if (!dw) job[1] = Product{0, 0, 0, 0};
-  const Plan how = plan(kGradShapes, job);
+  const Plan how = plan(kGradShapes, job, compute_units());
   const int sx = how.splits[0], sw = how.splits[1];
   Parts parts;
   if (dw) x.place(parts);

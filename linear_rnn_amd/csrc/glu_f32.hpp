@@ -15,11 +15,8 @@
 namespace rwkv7 {
 namespace glu {
 
-constexpr int kCols32 = 64;   // columns of a tile, of each weight
-constexpr int kStep32 = 32;   // of k
 constexpr int kRow32 = kStep32 + 4;
 constexpr int kWaves32 = 8;
-constexpr int kMostTM32 = 5;  // two workgroups on a compute unit: 128 registers a thread, 60 KB of LDS
 
 struct F32Params {
   const float* x;  // [M, D]
@@ -33,7 +30,7 @@ struct F32Params {
 
 template <int TM>
 __global__ __launch_bounds__(64 * kWaves32) __attribute__((amdgpu_waves_per_eu(4))) void glu_forward32_kernel(F32Params p) {
-  constexpr int BM = 16 * TM, kThreads = 64 * kWaves32, kRows = 2 * kCols32 + BM;
+  constexpr int BM = 16 * TM, kRows = 2 * kCols32 + BM;
   constexpr int kSum = 2 * kCols32 + 4;  // floats between rows of the sums
   constexpr int kFloats = 2 * kRows * kRow32 > BM * kSum ? 2 * kRows * kRow32 : BM * kSum;
   __shared__ __attribute__((aligned(16))) float lds[kFloats];

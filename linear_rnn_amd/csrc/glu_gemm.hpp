@@ -16,6 +16,7 @@
 // The product is formed turned (rows of a D tile are n, columns m), so that a lane has four consecutive n of one m.
 #pragma once
 
+#include "glu_rules.hpp"
 #include "linattn_ops.hpp"
 
 namespace rwkv7 {
@@ -29,7 +30,6 @@ using linattn::u32x4;
 // Four floats that need not begin on 16 bytes.
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
-constexpr int kBK = 64;
 constexpr int kMaxSegs = 12;
 constexpr uint32_t kNowhere = 0x80000000u;
 
