@@ -13,6 +13,7 @@
 // the bfloat16 rate, which is more than the float32 matrix instructions' 1/16. Other float32 forwards take these
 // (glu_f32.hpp), without pieces, workspace and sums in parts.
 #include "glu_internal.hpp"
+#include "launch_chunks.hpp"
 #include "once_per_device.hpp"
 #include "operators_lock.hpp"
 #include "rwkv7_wkv.h"
@@ -48,6 +49,7 @@ struct StageParams {
   StageJob job[3];
   GradJob grad;
   uint32_t first[5];
+  uint32_t begin;  // number of the launch's first workgroup
 };
 // Rows need not begin on 16 bytes here.
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
@@ -132,7 +134,7 @@ __device__ __forceinline__ void stage(const GradJob& j, int64_t i) {
 }
 template <bool F32>
 __global__ __launch_bounds__(256) void glu_stage_kernel(StageParams p) {
-  const uint32_t block = blockIdx.x;
+  const uint32_t block = p.begin + blockIdx.x;
   if (block >= p.first[3]) stage<F32>(p.grad, (int64_t)(block - p.first[3]) * 256 + threadIdx.x);
   else if (block >= p.first[2]) stage<F32>(p.job[2], (int64_t)(block - p.first[2]) * 256 + threadIdx.x);
   else if (block >= p.first[1]) stage<F32>(p.job[1], (int64_t)(block - p.first[1]) * 256 + threadIdx.x);
@@ -308,10 +310,12 @@ struct Stage {
       p.grad = *grad;
       blocks += blocks_for(grad->rows * grad->ld / 8);
     }
-    if (blocks == 0) return hipSuccess;
     const void* fn = f32 ? reinterpret_cast<const void*>(&glu_stage_kernel<true>)
                          : reinterpret_cast<const void*>(&glu_stage_kernel<false>);
-    return start(fn, dim3(blocks), 256, 0, p, stream);
+    return static_cast<hipError_t>(in_chunks(blocks, 256, [&](uint32_t first, uint32_t n) {
+      p.begin = first;
+      return static_cast<int>(start(fn, dim3(n), 256, 0, p, stream));
+    }));
   }
 };
 

@@ -44,3 +44,14 @@ def test_the_gated_recurrence_launches_so():
     """All its kernels, of 256, 512 and 1024 threads, are launched by the one function that cuts into such chunks."""
     text = open(os.path.join(build.CSRC, "gscan.hip")).read()
     assert text.count("hipLaunchKernel(") == 1 and "in_chunks(blocks, threads," in text
+
+
+def test_the_gated_unit_prepares_its_operands_so():
+    """The one launch of the gated linear unit that may have more threads: weights of 2^34 elements, the most that is
+    taken, are 2^31 threads of 8 each, and there are two; its tiles, of at least 64 x 128 for 256 threads, fit."""
+    assert 2 * (1 << 34) // 8 >= 1 << 32
+    # tiles: 2^28 rows of one column of tiles, or 2^34 elements in both directions
+    assert (1 << 28) // 64 * 256 < 1 << 32 and (1 << 34) // (64 * 128) * 256 < 1 << 32
+    text = open(os.path.join(build.CSRC, "glu.hip")).read()
+    stage = text[text.index("struct Stage {"):]
+    assert "in_chunks(blocks, 256," in stage[:stage.index("\n};")]
