@@ -680,7 +680,8 @@ int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_i
  * streams and error codes as for rwkv7_wkv_prefill; an unknown `act` is RWKV7_ERR_MODE; no
  * rows or no hidden channels do nothing. The pieces of a large float32 call, and bfloat16
  * operands whose rows are no multiple of 8, are copied into the workspace described for
- * rwkv7_wkv_prefill_ex first (6 or 2 bytes an element), and where there are few tiles for
+ * rwkv7_wkv_prefill_ex first (6 or 2 bytes an element; of x at most 4 GiB at once, as larger
+ * calls take their rows in slabs), and where there are few tiles for
  * the device, parts of the sums live there (at most 4 tiles a compute unit, of 256 KiB, for
  * each sum); what is said there about growth and graphs holds.
  */
@@ -705,8 +706,10 @@ int rwkv7_glu_forward(const void *x, const void *w_gate, const void *w_up, void 
  * All in `dtype`. In a bfloat16 call dg and du are rounded to bfloat16 where they enter the
  * products. They live in the workspace (4 bytes for each element of h, float32: 12) with the
  * copies that rwkv7_glu_forward makes and parts of its two sums, dx's and the weights', each as
- * large as there at most. With no rows dw_gate and dw_up are zeros, with no hidden channels dx
- * is.
+ * large as there at most. Calls whose dg, du and copy of x pass 4 GiB take their rows in slabs
+ * that do not (of at least 128 rows), and the weights' gradients are added up over those in the
+ * workspace, with 8 bytes more for each element of dw_gate, and 8 for a slab's own. With no
+ * rows dw_gate and dw_up are zeros, with no hidden channels dx is.
  */
 int rwkv7_glu_backward(const void *x, const void *w_gate, const void *w_up, const void *gate, const void *up,
                        const void *dh, void *dx, void *dw_gate, void *dw_up, int64_t M, int64_t D, int64_t F, int dtype,

@@ -347,44 +347,73 @@ hipError_t forward_f32(const GluCall& c) {
 }
 constexpr hipError_t (*kForwardF32[kMostTM32])(const GluCall&) = {&forward_f32<1>, &forward_f32<2>, &forward_f32<3>,
                                                                   &forward_f32<4>, &forward_f32<5>};
+// Rows that are in the workspace at once: what lives there for each of them (copies of x, dg and du) is at most 4 GiB, or 128
+// rows. Gradients of larger calls add up the weights' from one slab of rows to the next, in float32: 131072 x 4096 x 10944 bfloat16
+// in two slabs 39.7 ms, at once 39.0; float32 32768 x 64 x 10944 4.5 and 5.0.
+constexpr size_t kSlabBytes = size_t(1) << 32;
+int64_t slab_rows(int64_t M, size_t row_bytes) {
+  const int64_t fit = row_bytes ? (int64_t)(kSlabBytes / row_bytes / 128 * 128) : M, most = fit > 128 ? fit : 128;
+  if (M <= most) return M;
+  const int64_t slabs = (M + most - 1) / most;
+  return whole((M + slabs - 1) / slabs, 128);
+}
+// Row `row` of a caller's matrix (null stays null).
+const void* at_row(const void* p, int64_t row, int64_t cols, bool f32) {
+  return p ? static_cast<const char*>(p) + row * cols * (f32 ? 4 : 2) : nullptr;
+}
+void* at_row(void* p, int64_t row, int64_t cols, bool f32) {
+  return const_cast<void*>(at_row(static_cast<const void*>(p), row, cols, f32));
+}
+
 hipError_t forward(const GluCall& c) {
   const ForwardPlan how = plan_forward(Sizes{c.M, c.D, c.F, c.f32}, compute_units());
   if (how.way == kFew) return forward_few(c);
   if (how.way == kInstructions) return kForwardF32[how.tm - 1](c);
   Matrix x{c.x, c.M, c.D, c.f32}, wg{c.w_gate, c.D, c.F, c.f32}, wu{c.w_up, c.D, c.F, c.f32};
   const int splits = how.tiles.splits[0];
+  const int64_t rows = slab_rows(c.M, x.copied() ? x.ld() * 2 * (c.f32 ? 3 : 1) : 0);
+  x.rows = rows;
   Parts parts;
   for (Matrix* m : {&x, &wg, &wu}) m->place(parts);
-  const size_t partial_at = splits > 1 ? parts.add((size_t)splits * 2 * c.M * c.F * 4) : 0;
+  const size_t partial_at = splits > 1 ? parts.add((size_t)splits * 2 * rows * c.F * 4) : 0;
   std::unique_lock<std::mutex> lock(operators_mutex(), std::defer_lock);
   char* ws = nullptr;
   if (parts.bytes) {
     lock.lock();
     void* space = nullptr;
-    hipError_t e = device_workspace(c.stream, parts.bytes, &space, kWorkspaceOperators);
+    const hipError_t e = device_workspace(c.stream, parts.bytes, &space, kWorkspaceOperators);
     if (e != hipSuccess) return e;
     ws = static_cast<char*>(space);
+  }
+  for (int64_t first = 0; first < c.M; first += rows) {
+    const int64_t here = c.M - first < rows ? c.M - first : rows;
+    x.src = at_row(c.x, first, c.D, c.f32), x.rows = here;
     Stage stage;
-    for (Matrix* m : {&x, &wg, &wu}) stage.add(*m, ws);
-    e = stage.launch(nullptr, c.f32, c.stream);
+    stage.add(x, ws);
+    if (first == 0) stage.add(wg, ws), stage.add(wu, ws);
+    hipError_t e = stage.launch(nullptr, c.f32, c.stream);
+    if (e != hipSuccess) return e;
+    GemmParams p{};
+    p.nseg = pairs(c.f32);
+    for (int s = 0; s < p.nseg; ++s) {
+      p.a[s] = x.piece(ws, first_of(c.f32, s));
+      p.b[s] = wg.piece(ws, second_of(c.f32, s));
+      p.b2[s] = wu.piece(ws, second_of(c.f32, s));
+    }
+    p.lda = x.ld(), p.ldb = wg.ld(), p.M = (int32_t)here, p.N = (int32_t)c.F, p.K = (int32_t)c.D, p.splits = splits;
+    p.out = at_row(c.h, first, c.F, c.f32), p.gate = at_row(c.gate, first, c.F, c.f32), p.up = at_row(c.up, first, c.F, c.f32);
+    p.f32 = c.f32, p.act = c.act;
+    p.partial = reinterpret_cast<float*>(ws + partial_at);
+    e = forward_products(p, how.tiles.shape, c.stream);
+    if (e != hipSuccess) return e;
+    if (splits == 1) continue;
+    JoinParams j{};
+    j.job[0] = JoinJob{p.partial, p.gate, p.up, p.out, here * c.F, splits, 2, c.f32, c.act};
+    j.second = blocks_for((j.job[0].n + 3) / 4);
+    e = start(reinterpret_cast<const void*>(&glu_join_kernel), dim3(j.second), 256, 0, j, c.stream);
     if (e != hipSuccess) return e;
   }
-  GemmParams p{};
-  p.nseg = pairs(c.f32);
-  for (int s = 0; s < p.nseg; ++s) {
-    p.a[s] = x.piece(ws, first_of(c.f32, s));
-    p.b[s] = wg.piece(ws, second_of(c.f32, s));
-    p.b2[s] = wu.piece(ws, second_of(c.f32, s));
-  }
-  p.lda = x.ld(), p.ldb = wg.ld(), p.M = (int32_t)c.M, p.N = (int32_t)c.F, p.K = (int32_t)c.D, p.splits = splits;
-  p.out = c.h, p.gate = c.gate, p.up = c.up, p.f32 = c.f32, p.act = c.act;
-  p.partial = reinterpret_cast<float*>(ws + partial_at);
-  const hipError_t e = forward_products(p, how.tiles.shape, c.stream);
-  if (e != hipSuccess || splits == 1) return e;
-  JoinParams j{};
-  j.job[0] = JoinJob{p.partial, c.gate, c.up, c.h, c.M * c.F, splits, 2, c.f32, c.act};
-  j.second = blocks_for((j.job[0].n + 3) / 4);
-  return start(reinterpret_cast<const void*>(&glu_join_kernel), dim3(j.second), 256, 0, j, c.stream);
+  return hipSuccess;
 }
 
 hipError_t backward(const GluCall& c) {
@@ -392,19 +421,25 @@ hipError_t backward(const GluCall& c) {
   if (!dx && !dw) return hipSuccess;
   Matrix x{c.x, c.M, c.D, c.f32}, wg{c.w_gate, c.D, c.F, c.f32}, wu{c.w_up, c.D, c.F, c.f32};
   const int np = c.f32 ? 3 : 1;
-  const int64_t ldf = padded(c.F), plane = c.M * ldf;
+  const int64_t ldf = padded(c.F);
   const int64_t sum_f = whole(c.F, 8);  // with zeros in the copies' columns behind F
-  Product job[2] = {{c.M, c.D, 1, steps_of(sum_f, 2 * pairs(c.f32))}, {c.D, c.F, 2, steps_of(c.M, pairs(c.f32))}};
+  const int64_t rows = slab_rows(c.M, (size_t)np * 2 * (2 * ldf + (dw && x.copied() ? x.ld() : 0)));
+  const bool slabs = rows < c.M;
+  Product job[2] = {{rows, c.D, 1, steps_of(sum_f, 2 * pairs(c.f32))}, {c.D, c.F, 2, steps_of(rows, pairs(c.f32))}};
   if (!dx) job[0] = Product{0, 0, 0, 0};
   if (!dw) job[1] = Product{0, 0, 0, 0};
   const Plan how = plan(kGradShapes, job, compute_units());
   const int sx = how.splits[0], sw = how.splits[1];
   Parts parts;
+  x.rows = rows;
   if (dw) x.place(parts);
   if (dx) wg.place(parts), wu.place(parts);
-  const size_t dg_at = parts.add((size_t)np * plane * 2), du_at = parts.add((size_t)np * plane * 2);
-  const size_t px_at = dx && sx > 1 ? parts.add((size_t)sx * c.M * c.D * 4) : 0;
-  const size_t pw_at = dw && sw > 1 ? parts.add((size_t)sw * 2 * c.D * c.F * 4) : 0;
+  const size_t dg_at = parts.add((size_t)np * rows * ldf * 2), du_at = parts.add((size_t)np * rows * ldf * 2);
+  const size_t px_at = dx && sx > 1 ? parts.add((size_t)sx * rows * c.D * 4) : 0;
+  // with slabs the weights' gradients are parts too, behind their sum over the slabs before
+  const bool join_w = dw && (sw > 1 || slabs);
+  const int64_t weights = c.D * c.F;
+  const size_t pw_at = join_w ? parts.add((size_t)(sw + slabs) * 2 * weights * 4) : 0;
 
   std::lock_guard<std::mutex> lock(operators_mutex());
   void* space = nullptr;
@@ -412,52 +447,66 @@ hipError_t backward(const GluCall& c) {
   if (e != hipSuccess) return e;
   char* ws = static_cast<char*>(space);
   uint16_t *dg = reinterpret_cast<uint16_t*>(ws + dg_at), *du = reinterpret_cast<uint16_t*>(ws + du_at);
-  Stage stage;
-  if (dw) stage.add(x, ws);
-  if (dx) stage.add(wg, ws), stage.add(wu, ws);
-  const GradJob grad{c.gate, c.up, c.dh, dg, du, c.M, c.F, ldf, c.act};
-  e = stage.launch(&grad, c.f32, c.stream);
-  if (e != hipSuccess) return e;
+  float* const sum_w = reinterpret_cast<float*>(ws + pw_at);
+  float* const parts_w = sum_w + (slabs ? 2 * weights : 0);
+  for (int64_t first = 0; first < c.M; first += rows) {
+    const int64_t here = c.M - first < rows ? c.M - first : rows, plane = here * ldf;
+    const bool last = first + here == c.M;
+    x.src = at_row(c.x, first, c.D, c.f32), x.rows = here;
+    Stage stage;
+    if (dw) stage.add(x, ws);
+    if (dx && first == 0) stage.add(wg, ws), stage.add(wu, ws);
+    const GradJob grad{at_row(c.gate, first, c.F, c.f32), at_row(c.up, first, c.F, c.f32), at_row(c.dh, first, c.F, c.f32),
+                       dg, du, here, c.F, ldf, c.act};
+    e = stage.launch(&grad, c.f32, c.stream);
+    if (e != hipSuccess) return e;
 
-  GradProducts p{};
-  p.w_first = (job[1].steps + sw - 1) / sw > (job[0].steps + sx - 1) / sx;
-  JoinParams j{};
-  int joins = 0;
-  uint32_t blocks = 0;
-  if (dx) {
-    GemmParams& o = p.x;
-    for (int s = 0; s < pairs(c.f32); ++s) {
-      const int f = first_of(c.f32, s), t = second_of(c.f32, s);
-      o.a[2 * s] = dg + f * plane, o.b[2 * s] = wg.piece(ws, t);
-      o.a[2 * s + 1] = du + f * plane, o.b[2 * s + 1] = wu.piece(ws, t);
+    GradProducts p{};
+    p.w_first = (job[1].steps + sw - 1) / sw > (job[0].steps + sx - 1) / sx;
+    JoinParams j{};
+    int joins = 0;
+    uint32_t blocks = 0;
+    if (dx) {
+      GemmParams& o = p.x;
+      for (int s = 0; s < pairs(c.f32); ++s) {
+        const int f = first_of(c.f32, s), t = second_of(c.f32, s);
+        o.a[2 * s] = dg + f * plane, o.b[2 * s] = wg.piece(ws, t);
+        o.a[2 * s + 1] = du + f * plane, o.b[2 * s + 1] = wu.piece(ws, t);
+      }
+      o.nseg = 2 * pairs(c.f32);
+      o.lda = ldf, o.ldb = wg.ld(), o.M = (int32_t)here, o.N = (int32_t)c.D, o.K = (int32_t)sum_f, o.splits = sx;
+      o.out = at_row(c.dx, first, c.D, c.f32), o.f32 = c.f32, o.partial = reinterpret_cast<float*>(ws + px_at);
+      if (sx > 1) {
+        j.job[joins++] = JoinJob{o.partial, o.out, nullptr, nullptr, here * c.D, sx, 1, c.f32, 0};
+        blocks += blocks_for((here * c.D + 3) / 4);
+      }
     }
-    o.nseg = 2 * pairs(c.f32);
-    o.lda = ldf, o.ldb = wg.ld(), o.M = (int32_t)c.M, o.N = (int32_t)c.D, o.K = (int32_t)sum_f, o.splits = sx;
-    o.out = c.dx, o.f32 = c.f32, o.partial = reinterpret_cast<float*>(ws + px_at);
-    if (sx > 1) {
-      j.job[joins++] = JoinJob{o.partial, c.dx, nullptr, nullptr, c.M * c.D, sx, 1, c.f32, 0};
-      blocks += blocks_for((c.M * c.D + 3) / 4);
+    j.second = blocks;
+    if (dw) {
+      GemmParams& o = p.w;
+      o.nseg = pairs(c.f32);
+      for (int s = 0; s < o.nseg; ++s) {
+        const int f = first_of(c.f32, s), t = second_of(c.f32, s);
+        o.a[s] = x.piece(ws, f), o.b[s] = dg + t * plane, o.b2[s] = du + t * plane;
+      }
+      o.lda = x.ld(), o.ldb = ldf, o.M = (int32_t)c.D, o.N = (int32_t)c.F, o.K = (int32_t)here, o.splits = sw;
+      o.out = c.dw_gate, o.out2 = c.dw_up, o.two = true, o.f32 = c.f32, o.partial = parts_w;
+      const bool more = first > 0;  // there is a sum already
+      if (join_w && sw == 1 && !more) {
+        o.out = sum_w, o.out2 = sum_w + weights, o.f32 = true;  // the product is the sum
+      } else if (join_w) {
+        if (sw == 1) o.out = parts_w, o.out2 = parts_w + weights, o.f32 = true;
+        j.job[joins++] = JoinJob{more ? sum_w : parts_w, last ? c.dw_gate : sum_w, last ? c.dw_up : sum_w + weights, nullptr,
+                                 weights, sw + more, 2, c.f32 || !last, 0};
+        blocks += blocks_for((weights + 3) / 4);
+        if (joins == 1) j.second = blocks;  // the only job
+      }
     }
+    e = backward_products(p, dx, dw, how.shape, c.stream);
+    if (e == hipSuccess && joins > 0) e = start(reinterpret_cast<const void*>(&glu_join_kernel), dim3(blocks), 256, 0, j, c.stream);
+    if (e != hipSuccess) return e;
   }
-  j.second = blocks;
-  if (dw) {
-    GemmParams& o = p.w;
-    o.nseg = pairs(c.f32);
-    for (int s = 0; s < o.nseg; ++s) {
-      const int f = first_of(c.f32, s), t = second_of(c.f32, s);
-      o.a[s] = x.piece(ws, f), o.b[s] = dg + t * plane, o.b2[s] = du + t * plane;
-    }
-    o.lda = x.ld(), o.ldb = ldf, o.M = (int32_t)c.D, o.N = (int32_t)c.F, o.K = (int32_t)c.M, o.splits = sw;
-    o.out = c.dw_gate, o.out2 = c.dw_up, o.two = true, o.f32 = c.f32, o.partial = reinterpret_cast<float*>(ws + pw_at);
-    if (sw > 1) {
-      j.job[joins++] = JoinJob{o.partial, c.dw_gate, c.dw_up, nullptr, c.D * c.F, sw, 2, c.f32, 0};
-      blocks += blocks_for((c.D * c.F + 3) / 4);
-      if (joins == 1) j.second = blocks;  // the only job
-    }
-  }
-  e = backward_products(p, dx, dw, how.shape, c.stream);
-  if (e != hipSuccess || joins == 0) return e;
-  return start(reinterpret_cast<const void*>(&glu_join_kernel), dim3(blocks), 256, 0, j, c.stream);
+  return hipSuccess;
 }
 
 }  // namespace
