@@ -1003,7 +1003,9 @@ struct Kernels {
     hipError_t e = hipSuccess;
     // In one pass or two, bfloat16: B=8 T=4096 D=1024 (32 tiles) 100 and 112 us, B=4 T=8192 D=2048 (64) 213 and 240, B=2
     // T=16384 D=2048 (128) 253 and 241, B=1 T=32768 D=2048 309 and 242: every tile reads all others' maps. (Words are of
-    // 64 channels and would outgrow the data of one to three; of 8 B=512 T=4096 takes 194 and 204.)
+    // 64 channels and would outgrow the data of one to three; of 8 B=512 T=4096 takes 194 and 204.) Single channels, with
+    // tiles of 32 tokens, alike: B=8 T=1024 D=1025 (32) 38 and 52, B=4 T=2048 (64) 45 and 52, float32 50 and 64; a few units of
+    // a few tiles 9.6 and 8.6; D=65 B=128 T=2048 125 and 101, the most that the rule loses there.
     if (p.tiles <= kAcross && p.D >= 16) {
       e = words(p, c, p.tiles, true);
       if (e == hipSuccess) e = start(one_pass, blocks, kThreads, p, c.stream);
