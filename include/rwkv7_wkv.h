@@ -607,7 +607,7 @@ int rwkv7_layernorm_backward(const void *x, const float *weight, const float *me
  * codes are as for rwkv7_wkv_prefill; an `input` not one of RWKV7_INPUT_* is
  * RWKV7_ERR_MODE. A prompt needs no workspace up to 384 tokens, and none up to 2048 where
  * B*ceil(D/64) is 192 or more; where D mod 64 is 1, 2 or 3 none up to 224 tokens, and none
- * at any length where B*ceil(D/64) is 80 or more. Other prompts are taken in tiles of 256
+ * at any length where B*ceil(D/64) is 160 or more. Other prompts are taken in tiles of 256
  * tokens (64 where D mod 64 is 1, 2 or 3), whose maps of the state, 8 bytes a tile and channel
  * (channels rounded up to 64 for each sequence) and a little more, live in the workspace as
  * the states of rwkv7_linattn_prefill do; what is said there about growth and graphs holds

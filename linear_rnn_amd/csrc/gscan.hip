@@ -964,13 +964,14 @@ struct Kernels {
   // emptying their words and then the memory's time, at some 5 TB/s with any number of units: B=8 T=4096 D=1024 (128 units)
   // 72 and 54 us, B=1 T=8192 D=768 (12) 134 and 19, B=16 T=2048 D=768 (192) 41 and 44, B=1 T=256 D=768 7.2 and 9.4, B=8
   // T=4096 D=4096 (512) 219 and 205.
-  // By single channels a tile has 32 tokens and takes 0.6 us to walk, one after the other; a tile of 64 that passes its maps
-  // on 0.014 us of the device's time, after 6 us: D=65 bfloat16 with 2 units T=256 6.8 and 6.2 us, T=1024 22 and 6.3; 64
-  // units T=512 12 and 13, T=2048 43 and 35; 128 units T=2048 43 and 60; 512 units T=1024 35 and 109; D=1025 float32, 136
-  // units T=4096 163 and 131, the one size measured where the rule loses more than a tenth.
+  // By single channels a tile has 32 tokens and takes 0.6 us to walk, one after the other, 1.0 to 1.2 where the inputs come from
+  // memory and not from the last-level cache; a tile of 64 that passes its maps on takes 0.014 us of the device's time,
+  // after 6 us. From memory, MIX, bfloat16: D=65 with 16 units T=512 14 and 8 us, 64 units T=2048 67 and 37, 128 units T=512
+  // 20 and 23, T=4096 138 and 112, 192 units T=4096 148 and 162, 512 units T=1024 54 and 112; float32 D=1025 B=8 (136)
+  // T=1024 44 and 46, T=4096 167 and 135, from the cache T=2048 44 and 70.
   static bool walks(uint32_t units, uint32_t tiles, uint32_t chain_tiles) {
     if (VEC == 4) return tiles <= 3 || (units >= 192 && tiles <= 16);
-    return 40 * ((int64_t)tiles - 7) <= (int64_t)units * chain_tiles;
+    return 80 * ((int64_t)tiles - 7) <= (int64_t)units * chain_tiles;
   }
   static hipError_t prefill(const GscanCall& c) {
     ScanParams p = params(c);

@@ -20,7 +20,7 @@ def cuda(x):
     return {n: t.cuda() for n, t in x.items()}
 
 
-@pytest.mark.parametrize("B,T,D", [(90, 700, 1), (64, 700, 65), (40, 1300, 66), (27, 700, 131), (2, 220, 65)])
+@pytest.mark.parametrize("B,T,D", [(160, 700, 1), (80, 700, 65), (82, 1300, 66), (54, 700, 131), (2, 220, 65)])
 def test_many_units_need_no_workspace(torch, B, T, D):
     """On a stream without a workspace, under capture, where one cannot be had."""
     say("gscan single channels, capture", B, T, D)
@@ -44,7 +44,7 @@ def test_many_units_need_no_workspace(torch, B, T, D):
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
-@pytest.mark.parametrize("B,T,D", [(79, 9000, 1), (80, 9000, 1), (1, 9000, 65), (3, 225, 65), (3, 257, 65), (40, 1500, 65)])
+@pytest.mark.parametrize("B,T,D", [(159, 9000, 1), (160, 9000, 1), (1, 9000, 65), (3, 225, 65), (3, 257, 65), (64, 700, 65), (64, 1500, 65)])
 def test_both_sides_of_the_rule(torch, B, T, D, dtype):
     say("gscan single channels", B, T, D, dtype)
     x = ref.make(B, T, D, getattr(torch, dtype), seed=B + T)
