@@ -649,7 +649,7 @@ int rwkv7_gscan_step(const void *x, const float *log_w, const float *state_in, v
  * dx and dlog_w are required. With no tokens dstate_in is dstate_out. The states are formed
  * again from the inputs; the maps of tiles of 128 tokens (32 where D mod 64 is 1 to 3),
  * 16 bytes a tile and channel (channels rounded up to 64; 12 bytes and D as it is with more
- * than 64 tiles or D below 16), live in the workspace.
+ * than 160 tiles, or 64 of 32 tokens, or D below 16), live in the workspace.
  */
 int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_in, const int32_t *lens, const void *dy,
                          const float *dstate_out, void *dx, float *dlog_w, float *dstate_in, int64_t B, int64_t T,

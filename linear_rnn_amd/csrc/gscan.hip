@@ -515,7 +515,7 @@ __device__ __forceinline__ uint32_t take_ticket(const ScanParams& p, uint32_t* s
 
 // After a barrier: the map of the wave's tokens before this thread's (REV: behind them) becomes the tile's. ROLLED: the
 // waves' maps are read from LDS one by one; at once they would take the registers of a third of the workgroups of the
-// bfloat16 gradients (213 registers and 161), while the other kernels gain nothing by fewer.
+// bfloat16 gradients (213 registers and 161; B=8 T=4096 D=1024 114 and 107 us, B=4 D=4096 230 and 213), while the other kernels gain nothing by fewer.
 template <int VEC, bool REV, int W, bool ROLLED>
 __device__ __forceinline__ void compose(float (&P)[VEC], float (&L)[VEC], const float (*sp)[kSlab], const float (*sl)[kSlab]) {
   constexpr int kTurns = ROLLED ? 1 : W;
@@ -686,12 +686,13 @@ __global__ __launch_bounds__(W * kWave) void gscan_chain_kernel(ScanParams p) {
   }
 }
 
-// Gradients in one pass, for at most kAcross tiles a sequence: a workgroup a tile, a sequence's (of 64 channels) tiles
+// Gradients in one pass, for at most kAcross<VEC> tiles a sequence: a workgroup a tile, a sequence's (of 64 channels) tiles
 // in a row. Every tile needs the maps of those before it and, for the gradient, of those behind it, whose workgroups
 // start later. So a workgroup looks for them `polls` times, some 100 us, and where one is not there (other work holds
 // the compute units) leaves its tile to a second kernel, before which all maps are: no wait depends on another
 // workgroup, and the results are the same.
-constexpr uint32_t kAcross = 64;
+template <int VEC>
+constexpr uint32_t kAcross = VEC == 4 ? 160 : 64;
 template <bool F32, int VEC, int KIND>
 __device__ __forceinline__ void across(const ScanParams& p, uint32_t id, bool again) {
   constexpr uint32_t esz = kEsz<F32>;
@@ -1002,12 +1003,13 @@ struct Kernels {
     if (p.tiles == 1) return start(one_pass, blocks, kThreads, p, c.stream);
     std::lock_guard<std::mutex> lock(operators_mutex());
     hipError_t e = hipSuccess;
-    // In one pass or two, bfloat16: B=8 T=4096 D=1024 (32 tiles) 100 and 112 us, B=4 T=8192 D=2048 (64) 213 and 240, B=2
-    // T=16384 D=2048 (128) 253 and 241, B=1 T=32768 D=2048 309 and 242: every tile reads all others' maps. (Words are of
-    // 64 channels and would outgrow the data of one to three; of 8 B=512 T=4096 takes 194 and 204.) Single channels, with
-    // tiles of 32 tokens, alike: B=8 T=1024 D=1025 (32) 38 and 52, B=4 T=2048 (64) 45 and 52, float32 50 and 64; a few units of
-    // a few tiles 9.6 and 8.6; D=65 B=128 T=2048 125 and 101, the most that the rule loses there.
-    if (p.tiles <= kAcross && p.D >= 16) {
+    // In one pass or two, bfloat16: B=8 T=4096 D=1024 (32 tiles) 107 and 146 us, B=4 T=8192 D=2048 (64) 224 and 290, B=4 T=16384
+    // D=1024 (128) 283 and 306, T=20480 (160) 340 and 371, T=32768 (256) 623 and 588; B=1 D=1024 T=16384 63 and 69, T=20480 93
+    // and 86, T=24576 118 and 101; float32 B=4 D=1024 (96) 244 and 325, (160) 455 and 529, (192) 664 and 627: every tile
+    // reads all others' maps. (Words are of 64 channels and would outgrow the data of one to three; of 8 B=512 T=4096 takes
+    // 184 and 158.) Single channels, with tiles of 32 tokens: B=8 T=1024 D=1025 (32) 38 and 52, B=4 T=2048 (64) 45 and 52,
+    // float32 50 and 64; a few units of a few tiles 9.6 and 8.6; D=65 B=128 T=2048 125 and 101, the most that the rule loses there.
+    if (p.tiles <= kAcross<VEC> && p.D >= 16) {
       e = words(p, c, p.tiles, true);
       if (e == hipSuccess) e = start(one_pass, blocks, kThreads, p, c.stream);
       if (e == hipSuccess)
