@@ -114,11 +114,13 @@ inline int few_columns(const Sizes& c, int cus) { return c.f32 && (c.F + 31) / 3
 
 // Up to 32 rows. A workgroup's k come one after the other, or the weights' bytes count (7.2 TB/s), which tiles have to read
 // too. Tiles of so few rows take their steps, or the bytes, and for each part of the sums that the join adds half a us.
-constexpr float kFewStart = 3.5f, kFewTilesStart = 6.f, kFewTilesPart = 0.55f;
+// The constants lie between what weights from the last-level cache take and what those from memory do, so that no call measured
+// of either kind is more than 11% slower than by few rows.
+constexpr float kFewStart = 5.f, kFewTilesStart = 6.f, kFewTilesPart = 0.55f;
 inline float weights_us(const Sizes& c) { return 2.f * c.D * c.F * (c.f32 ? 4 : 2) / 7.2e6f; }
 inline float few_us(const Sizes& c, int cus) {
   const bool one = c.M <= 16;  // tile of 16 rows
-  const float k = c.f32 ? (one ? 0.0050f : 0.0095f) * (few_columns(c, cus) / 32) : one ? 0.0038f : 0.0046f;
+  const float k = c.f32 ? (one ? 0.0065f : 0.0095f) * (few_columns(c, cus) / 32) : one ? 0.0045f : 0.0046f;
   const float walk = kFewStart + c.D * k, read = 3.f + weights_us(c);
   return walk > read ? walk : read;
 }
@@ -130,9 +132,11 @@ inline bool few_at_once(const Sizes& c, int cus) {
   const float n = (float)steps_of(c.D, 1), more = few - kFewTilesStart;
   return more <= weights_us(c) || more * more <= 4.f * kFewTilesPart * n;
 }
-// Both ways in us (bfloat16, a graph's calls): 1 x 2048 x 5504 11.3 and 18.6, 32 x 2048 x 512 14.9 and 14.7, 1 x 4096 x 2048
-// 18.7 and 19.0, 32 x 4096 x 2048 26 and 23, 32 x 4096 x 4096 27 and 29, 1 x 8192 x 512 33 and 26, 32 x 8192 x 4096 48 and 38, 32
-// x 8192 x 8192 55 and 62, 1 x 16384 x 256 62 and 29, 32 x 16384 x 512 89 and 32.
+// Both ways in us, bfloat16 in a graph, weights from the cache: 1 x 2048 x 5504 11.3 and 18.6, 32 x 2048 x 2048 14.9 and 15.5, 8 x
+// 4096 x 2048 19.8 and 21.7, 32 x 4096 x 2048 26 and 23, 32 x 4096 x 4096 27 and 29, 1 x 8192 x 512 33 and 26, 32 x 8192 x 4096 48
+// and 38, 32 x 8192 x 8192 55 and 62, 1 x 16384 x 256 62 and 29, 32 x 16384 x 512 89 and 32; from memory: 1 x 2048 x 5504 17 and 21,
+// 32 x 2048 x 2048 23 and 18, 16 x 4096 x 2048 38 and 23, 32 x 4096 x 4096 44 and 32, 32 x 8192 x 8192 87 and 74, 32 x 16384 x 512
+// 156 and 34.
 inline bool few_rows(const Sizes& c, const Plan& how, int cus) {
   const int p = how.splits[0];
   const float steps = (float)((steps_of(c.D, 1) + p - 1) / p), bytes = weights_us(c);
