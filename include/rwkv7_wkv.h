@@ -688,7 +688,7 @@ int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_i
 #define RWKV7_ACT_SIGMOID 0 /* 1 / (1 + exp(-g)) */
 #define RWKV7_ACT_SILU 1    /* g / (1 + exp(-g)) */
 #define RWKV7_ACT_GELU 2    /* g (1 + erf(g / sqrt 2)) / 2 */
-#define RWKV7_ACT_RELU2 3   /* max(g, 0)^2, as in RWKV's channel mix */
+#define RWKV7_ACT_RELU2 3   /* max(g, 0)^2 (RWKV's channel mix squares so, but has no second projection) */
 
 int rwkv7_glu_forward(const void *x, const void *w_gate, const void *w_up, void *h, void *gate, void *up, int64_t M,
                       int64_t D, int64_t F, int dtype, int act, void *stream);

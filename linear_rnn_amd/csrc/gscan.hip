@@ -12,8 +12,8 @@
 //
 // Memory bounds all of it (8 bytes an element of a bfloat16 prompt, 14 of the gradients, and some ten operations), at
 // the rate of a large copy (4.9 to 5.5 TB/s): B=8 T=4096 D=4096 bfloat16 205 us (5.25 TB/s), B=1 T=32767 D=1024 float32 88 us
-// (4.6, with 4 us for emptying words), gradients of B=8 T=4096 D=1024 bfloat16 102 us (4.6, the words they pass on
-// not counted), float32 122 us (5.5). A step of B=512 D=4096 takes 5.9 us (5.7 TB/s, from the last-level cache).
+// (4.6, with 4 us for emptying words), gradients of B=8 T=4096 D=1024 bfloat16 107 us (4.4, the words they pass on
+// not counted), float32 137 us (4.9). A step of B=512 D=4096 takes 5.3 us (6.3 TB/s, from the last-level cache).
 #include "gscan_internal.hpp"
 #include "launch_chunks.hpp"
 #include "operators_lock.hpp"
@@ -80,7 +80,7 @@ constexpr uint32_t kNowhere = 0x80000000u;  // an offset behind the end of every
 // The channels of a thread's place c (a multiple of VEC) among all slabs': where D is no multiple of four the last place has
 // the last four channels, some of them the place's before it too (of the same workgroup), and both compute and write the
 // same. A place from D on has none. So rows of nearly any width are loaded in fours (B=1 T=20000 D=333 bfloat16 23 us,
-// by single channels 36; B=8 T=4096 D=1023 69 us, D=1025, by single channels, 123).
+// by single channels 36; B=8 T=4096 D=1023 71 us, D=1025, by single channels, 123).
 template <int VEC>
 __device__ __forceinline__ uint32_t channel(uint32_t c, uint32_t D) {
   return VEC == 4 && c < D && c + 4 > D ? D - 4 : c;
