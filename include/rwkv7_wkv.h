@@ -683,7 +683,8 @@ int rwkv7_gscan_backward(const void *x, const float *log_w, const float *state_i
  * rwkv7_wkv_prefill_ex first (6 or 2 bytes an element; of x at most 4 GiB at once, as larger
  * calls take their rows in slabs), and where there are few tiles for
  * the device, parts of the sums live there (at most 4 tiles a compute unit, of 256 KiB, for
- * each sum); what is said there about growth and graphs holds.
+ * each sum); what is said there about growth and graphs holds. Up to 32 rows of up to 1024
+ * channels need no workspace (in bfloat16 with an even D and F).
  */
 #define RWKV7_ACT_SIGMOID 0 /* 1 / (1 + exp(-g)) */
 #define RWKV7_ACT_SILU 1    /* g / (1 + exp(-g)) */

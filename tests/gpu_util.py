@@ -57,3 +57,16 @@ def sample_units(B, H, n, seed=0):
     while len(units) < min(n, B * H):
         units.add((int(rng.integers(B)), int(rng.integers(H))))
     return sorted(units)
+
+
+def new_stream():
+    """A stream that no other test has used: torch gives out the same ones again, with what the library keeps for them.
+    It is not destroyed, so that its handle stays its own."""
+    import ctypes
+
+    import torch
+
+    hip, handle = ctypes.CDLL("libamdhip64.so"), ctypes.c_void_p()
+    hip.hipStreamCreateWithFlags.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_uint]
+    assert hip.hipStreamCreateWithFlags(ctypes.byref(handle), 1) == 0  # hipStreamNonBlocking, as torch's are
+    return torch.cuda.ExternalStream(handle.value)

@@ -80,3 +80,10 @@ def test_rows_that_begin_anywhere(choose):
     """A bfloat16 row of an odd width begins on two bytes: not for the kernel of few rows."""
     for M, D, F in ((1, 769, 2048), (32, 768, 2049), (100, 33, 21)):
         assert choose([(0, M, D, F)])[0][0] == TILES and choose([(1, M, D, F)])[0][0] != TILES
+
+
+def test_few_rows_that_need_no_workspace(choose):
+    """Up to 32 rows of up to 1024 channels, as the header says, whatever the hidden channels."""
+    sizes = [(f32, M, D, F) for f32 in (0, 1) for M in (1, 16, 17, 32) for D in (2, 66, 512, 1000, 1024)
+             for F in (2, 64, 1000, 8192, 8194, 100_000, 1 << 20)]
+    assert all(way == FEW for way, _ in choose(sizes))

@@ -4,7 +4,7 @@ import pytest
 
 from linear_rnn_amd import wkv
 from tests import glu_ref as ref
-from tests.gpu_util import say
+from tests.gpu_util import new_stream, say
 
 pytestmark = pytest.mark.gpu
 ACT = {"sigmoid": wkv.RWKV7_ACT_SIGMOID, "silu": wkv.RWKV7_ACT_SILU, "gelu": wkv.RWKV7_ACT_GELU, "relu2": wkv.RWKV7_ACT_RELU2}
@@ -43,3 +43,42 @@ def test_few_rows_of_many_channels(torch, M, D, F, dtype):
     h = torch.empty_like(got[0])
     wkv.rwkv7_glu_forward(d["x"], d["w_gate"], d["w_up"], h, None, None, act=ACT[act])
     assert torch.equal(h, got[0])
+
+
+# no workspace, as the header says, and with one
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("M,D,F,none", [(1, 1024, 8, True), (32, 1024, 2, True), (32, 1024, 5504, True), (17, 768, 16384, True), (32, 2, 100, True),
+                                        (32, 16384, 256, False), (32, 8192, 512, False)])
+def test_capture(torch, M, D, F, none, dtype):
+    """On a stream without a workspace; a call that needs one is refused there and can be captured behind an eager one."""
+    say("glu few rows, capture", M, D, F, dtype)
+    x = ref.make(M, D, F, getattr(torch, dtype), seed=5)
+    d = {n: x[n].cuda() for n in ("x", "w_gate", "w_up")}
+    h = torch.empty(M, F, dtype=d["x"].dtype, device="cuda")
+    want, stream = ref.forward(x["x"], x["w_gate"], x["w_up"], "silu")["h"], new_stream()
+    torch.cuda.synchronize()
+
+    def call():
+        wkv.rwkv7_glu_forward(d["x"], d["w_gate"], d["w_up"], h, None, None, act=ACT["silu"], stream=stream)
+
+    g, refused = torch.cuda.CUDAGraph(), False
+    with torch.cuda.graph(g, stream=stream):
+        try:
+            call()
+        except wkv.Rwkv7Error:
+            refused = True
+    assert refused == (not none)
+    if refused:
+        call()
+        stream.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            call()
+    eager = wkv.glu(d["x"], d["w_gate"], d["w_up"], act=ACT["silu"])[0]
+    for _ in range(3):
+        h.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        ref.check("h", h, want)
+        assert torch.equal(h, eager)

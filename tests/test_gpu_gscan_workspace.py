@@ -1,12 +1,11 @@
 """Which prompts of the gated linear recurrence need the workspace, as the header says: a call that needs none can be
 captured on a stream that has none, one that needs it is refused there."""
-import ctypes
 import re
 
 import pytest
 
 from linear_rnn_amd import wkv
-from tests.gpu_util import say
+from tests.gpu_util import new_stream, say
 
 pytestmark = pytest.mark.gpu
 
@@ -16,15 +15,6 @@ def torch():
     import torch as t
     wkv.lib()
     return t
-
-
-def new_stream(torch):
-    """A stream that no other test has used: torch gives out the same ones again, with what the library keeps for them.
-    It is not destroyed, so that its handle stays its own."""
-    hip, handle = ctypes.CDLL("libamdhip64.so"), ctypes.c_void_p()
-    hip.hipStreamCreateWithFlags.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_uint]
-    assert hip.hipStreamCreateWithFlags(ctypes.byref(handle), 1) == 0  # hipStreamNonBlocking, as torch's are
-    return torch.cuda.ExternalStream(handle.value)
 
 
 def stated(B, T, D):
@@ -49,7 +39,7 @@ def test_workspace_of_a_prompt(torch, B, T, D):
     say("gscan workspace", B, T, D)
     x = torch.zeros(B, T, D, dtype=torch.bfloat16, device="cuda")
     lw, y = torch.zeros(B, T, D, device="cuda"), torch.empty_like(x)
-    stream, g, refused = new_stream(torch), torch.cuda.CUDAGraph(), False
+    stream, g, refused = new_stream(), torch.cuda.CUDAGraph(), False
     torch.cuda.synchronize()
     with torch.cuda.graph(g, stream=stream):
         try:
